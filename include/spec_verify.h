@@ -353,6 +353,131 @@ sv_status spec_verify_run_noalloc(const void* target_logits, sv_dtype tdt,
                                   int8_t* flags, uint64_t* counters,
                                   void* cuda_stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around a verifying call.  They take no handle and no workspace,
+ * allocate nothing and keep nothing from one call to the next, so calls may
+ * overlap and may be captured.  Every pointer is device memory on `device`
+ * (made current for the call, whatever device is current before it); strides
+ * count elements.  Host errors as spec_verify_run, before any launch. */
+
+/* Grouped matrix products with bias, activation and residual in the epilogue:
+ *   y[g, m, n] = act(sum_k x[g, m, k] * w[g, n, k] + bias[g, n]) + residual[g, m, n]
+ * for groups g, e.g. the heads of a draft model: blocks h + silu(W h + b) (one
+ * group per head, x shared by a group stride of 0), or an output head whose
+ * rows land in the verifier's logits layout ([B, k, V]: y_row = k * V, y_group
+ * = V).
+ *   x, w: bfloat16, the K entries of a row contiguous; row (g, m) of x starts
+ *     at element g * x_group + m * x_row, row (g, n) of w at g * w_group + n *
+ *     w_row.  Strides may be 0 or overlap.
+ *   bias (NULL = none): row g starts at g * bias_group.  residual (NULL =
+ *     none): row (g, m) starts at g * residual_group + m * residual_row.
+ *   y: rows at g * y_group + m * y_row, which must not overlap each other
+ *     (SV_EINVAL); it may be the residual itself, with the same strides and
+ *     type, and must not overlap any other input.
+ *   bias_dt, residual_dt, y_dt: SV_F32 or SV_BF16 each.
+ *   Products are summed in fp32, the epilogue is fp32, and y is rounded once.
+ *   cap: the bound of SV_ACT_SOFTCAP (cap * tanh(z / cap)), finite and > 0;
+ *     otherwise not used.
+ * groups, M or N = 0 is a no-op; K = 0 sums nothing.  Any size, stride and
+ * alignment of the element is taken; rows of x and w that start at multiples
+ * of 16 bytes take the fast path.  SV_EUNSUPPORTED: a stride of 2^40 or more. */
+typedef enum {
+  SV_ACT_NONE = 0,
+  SV_ACT_RELU = 1,
+  SV_ACT_SILU = 2,
+  SV_ACT_GELU = 3,      /* z * (1 + erf(z / sqrt 2)) / 2 */
+  SV_ACT_GELU_TANH = 4, /* z * (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  SV_ACT_SOFTCAP = 5    /* cap * tanh(z / cap) */
+} sv_activation;
+
+sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_group,
+                             const void* w, int64_t w_row, int64_t w_group,
+                             const void* bias, sv_dtype bias_dt, int64_t bias_group,
+                             const void* residual, sv_dtype residual_dt, int64_t residual_row,
+                             int64_t residual_group,
+                             void* y, sv_dtype y_dt, int64_t y_row, int64_t y_group,
+                             int groups, int M, int N, int K, sv_activation act, float cap,
+                             int device, void* cuda_stream);
+
+/* The probabilities of logits rows, as spec_verify_tree reads them:
+ *   probs[r, v] = softmax(logits[r, :] / T_r)[v], fp32.
+ *   logits: rows of V entries of dtype dt, row r at r * logits_stride.
+ *   T_r = temperature_per_row[r] (device, [rows]) or, where that is NULL,
+ *     temperature: finite, >= 0.  0 puts 1 on the row's first largest logit.
+ *   probs: rows at r * probs_stride >= V apart; it may be fp32 logits
+ *     themselves with the same stride, and must not overlap them otherwise.
+ * A row with a NaN or +inf logit, with every logit -inf, or with a temperature
+ * of its own that is negative or not finite becomes NaN throughout (a verifying
+ * call that reads it fails closed).  V up to SV_MAX_V; rows = 0 is a no-op. */
+sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_t logits_stride,
+                              int rows, int V, float temperature, const float* temperature_per_row,
+                              float* probs, int64_t probs_stride, int device, void* cuda_stream);
+
+/* Verify drafted trees against the target's PROBABILITIES from given uniforms,
+ * with the accept test and the residual rule of this header, for batches whose
+ * sequences differ in how many tokens were drafted and how they branch.
+ *
+ * Sequence b has the nodes node_start[b] .. node_start[b+1] - 1 of the node
+ * arrays, n_b of them (0 is allowed: a plain sample).  Node i (counted within
+ * its sequence) offers token node_tokens[i] behind node parent[i] < i, -1 being
+ * the committed prefix (the root).  A chain is parent[i] = i - 1; candidates
+ * for one place are nodes with one parent, offered in index order until one is
+ * accepted.
+ *
+ * Rows: target_probs has total_nodes + B rows of V entries, fp32, at r *
+ * target_stride: the root's row of sequence b is node_start[b] + b, node i's
+ * row, the target's distribution behind it, the (1 + i)-th after that.
+ * draft_row, of the same total_nodes + B entries, says for each of these rows
+ * which of the draft_rows rows of draft_probs (at i * draft_stride) the
+ * children of that node were drawn from; -1: the children are certain
+ * proposals without a distribution (rows of nodes without children are not
+ * used, and say -1).
+ *
+ * At a node with rows p and q, with rest = p and Z = 1 at first, a child x is
+ * accepted iff rest(x) > 0 and u * mu(x) <= rest(x) / Z, where u = u_accept of
+ * that child, and mu = q (SV_WITH_REPLACEMENT: siblings drawn independently), q
+ * renormalised without the siblings offered before (SV_WITHOUT_REPLACEMENT), or
+ * 1 (certain).  A refusal leaves rest = the positive part of rest / Z - mu and Z
+ * its sum.  Behind the last child refused (or where a node has none) the token
+ * comes from rest by inverse CDF in token order: the smallest v whose inclusive
+ * prefix sum exceeds u_pick[b] * Z; a rest with no mass falls back to p.  p and
+ * q are taken as they stand, with a mass of 1 each.  Sums are accurate to
+ * about 1e-14, so the token is the one that exact sums give, and does not
+ * depend on how the work is split.
+ *
+ * Outputs: accepted_len [B] = accepted drafts; tokens [B, max_depth + 1] = the
+ * accepted drafts, the sampled token, then -1; path [B, max_depth] = the
+ * accepted nodes, then -1 (the rows of a cache to keep); accept_prob
+ * [total_nodes] = min(1, rest / (Z mu)) of the nodes offered, 0 elsewhere;
+ * flags [total_nodes] = SV_FLAG_ACCEPT, _REJECT or _UNREACHED; counters as
+ * spec_verify_run (TESTED, ACCEPTED, REJECTED, BONUS: stopped at a node
+ * without children, INVALID and DEGENERATE; the others are left).  path,
+ * accept_prob, flags and counters are optional (NULL = skip).
+ *
+ * max_nodes bounds every n_b and max_depth <= max_nodes the depth of every
+ * tree.  A sequence whose node range leaves [0, total_nodes] or holds more
+ * nodes, with a token outside [0, V), a parent outside [-1, i), a draft_row
+ * outside [-1, draft_rows) or a deeper node, or for which a probability read
+ * is NaN, infinite or (at a node offered) negative, fails closed as invalid
+ * input: accepted_len, tokens and path -1, and for nodes of a valid range
+ * accept_prob 0 and SV_FLAG_INVALID.  Of a row only what the walk needs is read: single entries, and
+ * whole rows where a sum over them is.  Uniforms are expected in [0, 1).
+ * SV_EUNSUPPORTED beyond SV_MAX_V or SV_MAX_NODES; B = 0 is a no-op. */
+#define SV_MAX_NODES 256
+
+typedef enum { SV_WITH_REPLACEMENT = 0, SV_WITHOUT_REPLACEMENT = 1 } sv_siblings;
+
+sv_status spec_verify_tree(const float* target_probs, int64_t target_stride,
+                           const float* draft_probs, int64_t draft_stride, int draft_rows,
+                           const int32_t* node_start, const int32_t* node_tokens,
+                           const int32_t* parent, const int32_t* draft_row,
+                           const float* u_accept, const float* u_pick,
+                           int B, int total_nodes, int max_nodes, int max_depth, int V,
+                           sv_siblings siblings,
+                           int32_t* accepted_len, int32_t* tokens, int32_t* path,
+                           float* accept_prob, int8_t* flags, uint64_t* counters,
+                           int device, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,5 +13,7 @@ from .spec_verify import (  # noqa: F401
     spec_verify_diagnostics, spec_verify_free, spec_verify_init, spec_verify_launches_per_run, spec_verify_mark_next,
     spec_verify_run, spec_verify_run_ex, spec_verify_run_host, spec_verify_run_noalloc,
     spec_verify_set_filters, spec_verify_set_gate_policy, spec_verify_status_string, run_noalloc,
-    spec_verify_launches_per_filtered_run)
+    spec_verify_launches_per_filtered_run, ACTIVATIONS, SV_MAX_NODES, SV_WITH_REPLACEMENT, SV_WITHOUT_REPLACEMENT,
+    SV_ACT_GELU, SV_ACT_GELU_TANH, SV_ACT_NONE, SV_ACT_RELU, SV_ACT_SILU, SV_ACT_SOFTCAP,
+    linear, softmax, verify_tree, spec_verify_linear, spec_verify_softmax, spec_verify_tree)
 from .metrics import acceptance_summary, rule_id, summary_line  # noqa: F401,E402

@@ -12,12 +12,14 @@
 #include <mutex>
 #include <new>
 
+#include "device_guard.cuh"
 #include "handle.h"
 
 
 namespace {
 
 using sv::align_up;
+using sv::DeviceGuard;
 using sv::filter_on;
 
 size_t elem_size(sv_dtype d) { return d == SV_BF16 ? 2 : 4; }
@@ -32,22 +34,6 @@ cudaError_t configure_all(int (*blocks_per_sm)[2], int fin_spread_smem) {
   if (e == cudaSuccess) e = sv::ops_bf16_bf16.configure(&blocks_per_sm[1][1], fin_spread_smem);
   return e;
 }
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) {
-      ok = false;
-      return;
-    }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
 
 }  // namespace
 

@@ -26,6 +26,11 @@ COUNTER_NAMES = ("tested", "accepted", "null", "rejected", "bonus", "boundary", 
                  "degenerate")
 SV_MAX_K = 32
 SV_MAX_V = 1 << 22
+SV_MAX_NODES = 256
+(SV_ACT_NONE, SV_ACT_RELU, SV_ACT_SILU, SV_ACT_GELU, SV_ACT_GELU_TANH, SV_ACT_SOFTCAP) = range(6)
+ACTIVATIONS = {"none": SV_ACT_NONE, "relu": SV_ACT_RELU, "silu": SV_ACT_SILU, "gelu": SV_ACT_GELU,
+               "gelu_tanh": SV_ACT_GELU_TANH, "softcap": SV_ACT_SOFTCAP}
+SV_WITH_REPLACEMENT, SV_WITHOUT_REPLACEMENT = 0, 1
 
 _lib = None
 
@@ -72,6 +77,14 @@ def load() -> ctypes.CDLL:
     L.spec_verify_set_filters.restype = I
     L.spec_verify_launches_per_filtered_run.argtypes = []
     L.spec_verify_launches_per_filtered_run.restype = I
+    I64 = ctypes.c_int64
+    L.spec_verify_linear.argtypes = [P, I64, I64, P, I64, I64, P, I, I64, P, I, I64, I64, P, I, I64, I64, I, I, I, I, I,
+                                     F, I, P]
+    L.spec_verify_linear.restype = I
+    L.spec_verify_softmax.argtypes = [P, I, I64, I, I, F, P, P, I64, I, P]
+    L.spec_verify_softmax.restype = I
+    L.spec_verify_tree.argtypes = [P, I64, P, I64, I, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, P, P, I, P]
+    L.spec_verify_tree.restype = I
     _lib = L
     return L
 
@@ -161,6 +174,31 @@ def spec_verify_run_noalloc(Lt, tdt, Ld, ddt, D, B, k, V, temperature, gate_mode
                                           stream)
 
 
+def spec_verify_linear(x, x_row, x_group, w, w_row, w_group, bias, bias_dt, bias_group, residual, residual_dt,
+                       residual_row, residual_group, y, y_dt, y_row, y_group, groups, M, N, K, act, cap, device,
+                       stream) -> int:
+    """Raw call of the grouped matrix product; returns the status."""
+    return load().spec_verify_linear(x, x_row, x_group, w, w_row, w_group, bias, bias_dt, bias_group, residual,
+                                     residual_dt, residual_row, residual_group, y, y_dt, y_row, y_group, groups, M, N,
+                                     K, act, cap, device, stream)
+
+
+def spec_verify_softmax(logits, dt, logits_stride, rows, V, temperature, temperature_per_row, probs, probs_stride,
+                        device, stream) -> int:
+    """Raw call of the logits rows' probabilities; returns the status."""
+    return load().spec_verify_softmax(logits, dt, logits_stride, rows, V, temperature, temperature_per_row, probs,
+                                      probs_stride, device, stream)
+
+
+def spec_verify_tree(p, p_stride, q, q_stride, draft_rows, node_start, tokens, parent, draft_row, u_accept, u_pick, B,
+                     total_nodes, max_nodes, max_depth, V, siblings, accepted_len, out_tokens, path, accept_prob,
+                     flags, counters, device, stream) -> int:
+    """Raw call of the tree verification; returns the status."""
+    return load().spec_verify_tree(p, p_stride, q, q_stride, draft_rows, node_start, tokens, parent, draft_row,
+                                   u_accept, u_pick, B, total_nodes, max_nodes, max_depth, V, siblings, accepted_len,
+                                   out_tokens, path, accept_prob, flags, counters, device, stream)
+
+
 # ------------------------------------------------------ torch marshalling
 
 def _dt(t: torch.Tensor) -> int:
@@ -184,6 +222,167 @@ def _check(t: torch.Tensor, name: str, shape, dtype=None, device=None):
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _check_rows(t: torch.Tensor, name: str, dim: int, dtype=None, device=None):
+    """A tensor of ``dim`` dimensions whose rows are contiguous, the other strides being free."""
+    if t.dim() != dim:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dim}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1 and 0 not in t.shape:
+        raise ValueError(f"{name}: rows must be contiguous")
+
+
+def _cuda_device(t: torch.Tensor, name: str):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}, expected a CUDA device")
+    return t.device
+
+
+def _stream(dev: torch.device, stream):
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+
+
+def linear(x, weight, bias=None, residual=None, activation="none", cap=0.0, out=None, out_dtype=None, stream=None):
+    """act(x @ weight.T + bias) + residual, with the sums and the epilogue in fp32 and one rounding.
+
+    ``x`` [M, K] and ``weight`` [N, K] give [M, N]; ``weight`` [G, N, K] (one
+    matrix per head) with ``x`` [G, M, K], or [M, K] shared by the heads, gives
+    [G, M, N].  ``x`` and ``weight`` are bfloat16; ``bias`` [N] / [G, N],
+    ``residual`` and ``out`` (shaped as the result) bfloat16 or float32.  Only
+    rows have to be contiguous: ``out=logits.transpose(0, 1)`` writes heads
+    straight into [M, G, N].  ``activation``: none, relu, silu, gelu, gelu_tanh,
+    or softcap (``cap`` * tanh(z / ``cap``)).  ``out`` may be ``residual``
+    itself.  A new result takes ``out_dtype`` (default bfloat16).  No gradient
+    is recorded."""
+    dev = _cuda_device(x, "x")
+    bf16 = torch.bfloat16
+    if weight.dim() not in (2, 3):
+        raise ValueError(f"weight: {weight.dim()} dimensions, expected 2 or 3")
+    grouped = weight.dim() == 3
+    _check_rows(weight, "weight", weight.dim(), bf16, dev)
+    G = weight.shape[0] if grouped else 1
+    N, K = weight.shape[-2:]
+    shared = x.dim() == 2
+    _check_rows(x, "x", 2 if shared else 3, bf16, dev)
+    if not shared and (not grouped or x.shape[0] != G):
+        raise ValueError(f"x: shape {tuple(x.shape)} does not go with weight {tuple(weight.shape)}")
+    M = x.shape[-2]
+    if x.shape[-1] != K:
+        raise ValueError(f"x: rows of {x.shape[-1]}, weight has rows of {K}")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
+    shape = (G, M, N) if grouped else (M, N)
+    dim = len(shape)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or bf16, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out: dtype {out.dtype} != {out_dtype}")
+    for t, name, shp in ((out, "out", shape), (residual, "residual", shape), (bias, "bias", (G, N) if grouped else (N,))):
+        if t is not None:
+            _check_rows(t, name, len(shp), None, dev)
+            if t.shape != shp:
+                raise ValueError(f"{name}: shape {tuple(t.shape)} != {shp}")
+    r = residual
+    rc = spec_verify_linear(
+        x.data_ptr(), x.stride(-2), 0 if shared else x.stride(0), weight.data_ptr(), weight.stride(-2),
+        weight.stride(0) if grouped else 0, _ptr(bias), 0 if bias is None else _dt(bias),
+        bias.stride(0) if grouped and bias is not None else 0, _ptr(r), 0 if r is None else _dt(r),
+        0 if r is None else r.stride(-2), r.stride(0) if grouped and r is not None else 0, out.data_ptr(), _dt(out),
+        out.stride(-2), out.stride(0) if dim == 3 else 0, G, M, N, K, act, float(cap), dev.index, _stream(dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_linear")
+    return out
+
+
+def softmax(logits, temperature, out=None, stream=None):
+    """Probabilities of logits rows [rows, V] (bfloat16 or float32, rows contiguous) as fp32 [rows, V].
+
+    ``temperature``: a float, or a float32 tensor [rows] on the device; 0 puts 1
+    on a row's first largest logit.  Rows without a distribution (a NaN or +inf
+    logit, every logit -inf, a bad temperature of their own) become NaN."""
+    dev = _cuda_device(logits, "logits")
+    _check_rows(logits, "logits", 2, None, dev)
+    rows, V = logits.shape
+    per_row = None
+    if isinstance(temperature, torch.Tensor):
+        _check(temperature, "temperature", (rows,), torch.float32, dev)
+        per_row, temperature = temperature.data_ptr(), 1.0
+    if out is None:
+        out = torch.empty(rows, V, dtype=torch.float32, device=dev)
+    else:
+        _check_rows(out, "out", 2, torch.float32, dev)
+        if out.shape != logits.shape:
+            raise ValueError(f"out: shape {tuple(out.shape)} != {tuple(logits.shape)}")
+    rc = spec_verify_softmax(logits.data_ptr(), _dt(logits), logits.stride(0), rows, V, float(temperature), per_row,
+                             out.data_ptr(), out.stride(0), dev.index, _stream(dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_softmax")
+    return out
+
+
+def verify_tree(target_probs, draft_probs, tokens, parent, draft_row, node_start, u_accept, u_pick, max_nodes=None,
+                max_depth=None, replacement=True, counters=None, out=None, stream=None):
+    """Verify drafted trees (ragged batches, several candidates per place) from probabilities and given uniforms.
+
+    ``node_start`` [B + 1], ``tokens``, ``parent`` [nodes] and ``draft_row``
+    [nodes + B] are int32, ``u_accept`` [nodes] and ``u_pick`` [B] float32;
+    ``target_probs`` [nodes + B, V] holds each sequence's root row, then its
+    nodes' rows; ``draft_probs`` [draft rows, V] (or None) the distributions
+    that ``draft_row`` names, -1 for certain proposals (see
+    ``spec_verify_tree`` in include/spec_verify.h).  ``max_nodes`` and
+    ``max_depth`` bound a sequence's nodes and its depth (default: the number
+    of nodes, as far as SV_MAX_NODES).  ``replacement``: whether siblings were
+    drawn with replacement.  Returns accepted_len [B], tokens [B, max_depth + 1],
+    path [B, max_depth], accept_prob and flags [nodes]."""
+    dev = _cuda_device(target_probs, "target_probs")
+    f32, i32 = torch.float32, torch.int32
+    _check_rows(target_probs, "target_probs", 2, f32, dev)
+    V = target_probs.shape[1]
+    B, total = u_pick.shape[0], tokens.shape[0]
+    if target_probs.shape[0] != total + B:
+        raise ValueError(f"target_probs: {target_probs.shape[0]} rows, expected {total + B}")
+    rows_q, q_stride = 0, 0
+    if draft_probs is not None:
+        _check_rows(draft_probs, "draft_probs", 2, f32, dev)
+        if draft_probs.shape[1] != V:
+            raise ValueError(f"draft_probs: rows of {draft_probs.shape[1]}, expected {V}")
+        rows_q, q_stride = draft_probs.shape[0], draft_probs.stride(0)
+    for t, name, n, dtype in ((tokens, "tokens", total, i32), (parent, "parent", total, i32),
+                              (draft_row, "draft_row", total + B, i32), (node_start, "node_start", B + 1, i32),
+                              (u_accept, "u_accept", total, f32), (u_pick, "u_pick", B, f32)):
+        _check(t, name, (n,), dtype, dev)
+    if counters is not None:
+        _check(counters, "counters", (8,), torch.int64, dev)
+    if max_nodes is None:
+        max_nodes = min(total, SV_MAX_NODES)
+    if max_depth is None:
+        max_depth = max_nodes
+    if out is None:
+        out = dict(accepted_len=torch.empty(B, dtype=i32, device=dev),
+                   tokens=torch.empty(B, max_depth + 1, dtype=i32, device=dev),
+                   path=torch.empty(B, max_depth, dtype=i32, device=dev),
+                   accept_prob=torch.empty(total, dtype=f32, device=dev),
+                   flags=torch.empty(total, dtype=torch.int8, device=dev))
+    else:
+        for name, shp, dtype in (("accepted_len", (B,), i32), ("tokens", (B, max_depth + 1), i32),
+                                 ("path", (B, max_depth), i32), ("accept_prob", (total,), f32),
+                                 ("flags", (total,), torch.int8)):
+            if name in out:
+                _check(out[name], name, shp, dtype, dev)
+    rc = spec_verify_tree(
+        target_probs.data_ptr(), target_probs.stride(0), _ptr(draft_probs), q_stride, rows_q, node_start.data_ptr(),
+        tokens.data_ptr(), parent.data_ptr(), draft_row.data_ptr(), u_accept.data_ptr(), u_pick.data_ptr(), B, total,
+        max_nodes, max_depth, V, SV_WITH_REPLACEMENT if replacement else SV_WITHOUT_REPLACEMENT,
+        out["accepted_len"].data_ptr(), out["tokens"].data_ptr(), _ptr(out.get("path")), _ptr(out.get("accept_prob")),
+        _ptr(out.get("flags")), _ptr(counters), dev.index, _stream(dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_tree")
+    return out
 
 
 class SpecVerifier:
@@ -279,6 +478,32 @@ class SpecVerifier:
         if rs is not None:
             o["row_stats"] = rs
         return o
+
+    def run_hidden(self, target_hidden, target_head, draft_hidden, draft_head, D, temperature, target_bias=None,
+                   draft_bias=None, cap=None, logits_dtype=torch.bfloat16, **kw):
+        """Verify from hidden states: the output heads' products, then ``run``.
+
+        ``target_hidden`` [B, k+1, H] with ``target_head`` [V, H];
+        ``draft_hidden`` [B, k, H'] with ``draft_head`` [V, H'], or [k, V, H']
+        for a head per position (all bfloat16), and biases [V] (or [k, V]).
+        ``cap`` bounds both sides' logits (cap * tanh(z / cap)).  ``kw`` goes to
+        ``run``; the result also holds target_logits and draft_logits."""
+        B, k, V, dev = target_hidden.shape[0], self.k, self.V, self.device
+        _check(target_hidden, "target_hidden", (B, k + 1, target_hidden.shape[-1]), torch.bfloat16, dev)
+        _check(draft_hidden, "draft_hidden", (B, k, draft_hidden.shape[-1]), torch.bfloat16, dev)
+        Lt = torch.empty(B, k + 1, V, dtype=logits_dtype, device=dev)
+        Ld = torch.empty(B, k, V, dtype=logits_dtype, device=dev)
+        act = dict(activation="none" if cap is None else "softcap", cap=cap or 0.0, stream=kw.get("stream"))
+        linear(target_hidden.view(B * (k + 1), target_hidden.shape[-1]), target_head, bias=target_bias,
+               out=Lt.view(B * (k + 1), V), **act)
+        if draft_head.dim() == 3:
+            linear(draft_hidden.transpose(0, 1), draft_head, bias=draft_bias, out=Ld.transpose(0, 1), **act)
+        else:
+            linear(draft_hidden.view(B * k, draft_hidden.shape[-1]), draft_head, bias=draft_bias,
+                   out=Ld.view(B * k, V), **act)
+        out = self.run(Lt, Ld, D, temperature, **kw)
+        out["target_logits"], out["draft_logits"] = Lt, Ld
+        return out
 
     def diagnostics(self, Lt, Ld, D, temperature, gate_mode=SV_PLAIN, threshold=0.5,
                     gate_per_seq=None, threshold_per_seq=None, out=None, stream=None):

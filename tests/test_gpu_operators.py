@@ -1,0 +1,537 @@
+"""The operators around a verifying call on the GPU: matrix products, row
+probabilities and tree verification against 64-bit implementations, and a run
+of them together.  Token ids have to be equal, everything else within bounds
+derived beside it."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import oracle as O
+from tests import operators_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import speculative_decoding_verification_online_gb300 as pkg
+    from speculative_decoding_verification_online_gb300 import build as B
+    B.build()
+    pkg.load()
+    return pkg
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+# ------------------------------------------------------------- linear
+
+def _operands(seed, G, M, N, K, shared=False, pad=0, offset=0):
+    g = _gen(seed)
+
+    def rows(n_rows, k):
+        store = torch.full((offset + n_rows * (k + pad),), float("nan"), dtype=torch.bfloat16, device="cuda")
+        v = store[offset:].view(n_rows, k + pad)[:, :k]
+        v.copy_(torch.randn(n_rows, k, generator=g, device="cuda"))
+        return v
+
+    x = rows((1 if shared else G) * M, K)
+    w = rows(G * N, K)
+    x = x if shared else x.unflatten(0, (G, M))
+    return x, w.unflatten(0, (G, N)), g
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 1), (1, 128, 64), (1, 4096, 512), (2, 130, 72), (5, 127, 63), (16, 256, 128), (17, 129, 200),
+    (33, 384, 1024), (64, 1000, 320), (77, 515, 1001), (96, 640, 136), (128, 128, 4096), (129, 257, 65), (200, 300, 96),
+    (256, 512, 512), (257, 513, 520), (384, 1280, 256), (511, 100, 48), (640, 2048, 384)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_sizes(sv, M, N, K, out):
+    x, w, g = _operands(M * 7 + N, 1, M, N, K)
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    y = sv.linear(x[0], w[0], out_dtype=dt)
+    assert y.dtype == dt and y.shape == (M, N)
+    ref.assert_linear(y, x[0], w[0], None, None, "none", 0.0, f"{M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh", "softcap"])
+@pytest.mark.parametrize("M,N,K", [(3, 200, 64), (70, 333, 257), (300, 512, 128)])
+def test_linear_epilogues(sv, act, M, N, K):
+    x, w, g = _operands(M + len(act), 1, M, N, K)
+    x, w = x[0], w[0]
+    for bdt, rdt, ydt in ((torch.bfloat16, torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16, torch.float32),
+                          (torch.bfloat16, torch.float32, torch.bfloat16), (None, torch.float32, torch.float32),
+                          (torch.float32, None, torch.bfloat16)):
+        bias = None if bdt is None else torch.randn(N, generator=g, device="cuda").to(bdt) * 3
+        res = None if rdt is None else torch.randn(M, N, generator=g, device="cuda").to(rdt)
+        y = sv.linear(x, w, bias=bias, residual=res, activation=act, cap=5.0, out_dtype=ydt)
+        ref.assert_linear(y, x, w, bias, res, act, 5.0, f"{act} {bdt} {rdt} {ydt}")
+
+
+@pytest.mark.parametrize("G,M,N,K,shared,pad,offset", [
+    (4, 1, 512, 256, True, 0, 0), (5, 6, 384, 512, True, 8, 0), (3, 17, 200, 100, False, 0, 0),
+    (2, 77, 321, 129, False, 3, 1), (5, 64, 256, 320, False, 8, 8), (2, 130, 140, 72, True, 1, 0),
+    (7, 300, 128, 64, False, 0, 4)])
+def test_linear_groups_strides_and_layouts(sv, G, M, N, K, shared, pad, offset):
+    x, w, g = _operands(G * 100 + M, G, M, N, K, shared, pad, offset)
+    bias = torch.randn(G, N + 5, generator=g, device="cuda")[:, 2:2 + N]
+    res = torch.randn(M, G, N, generator=g, device="cuda").to(torch.bfloat16).transpose(0, 1)
+    store = torch.full((M, G, N + 2), 7.0, device="cuda")
+    out = store[:, :, 1:N + 1].transpose(0, 1)
+    y = sv.linear(x, w, bias=bias, residual=res, activation="silu", out=out)
+    assert y is out
+    ref.assert_linear(out, x, w, bias, res, "silu", 0.0)
+    assert bool((store[:, :, 0] == 7).all()) and bool((store[:, :, -1] == 7).all())  # nothing beside the rows
+
+
+def test_linear_into_its_own_residual(sv):
+    x, w, g = _operands(3, 1, 70, 260, 192)
+    res = torch.randn(70, 260, generator=g, device="cuda").to(torch.bfloat16)
+    out = res.clone()
+    sv.linear(x[0], w[0], residual=out, activation="silu", out=out)
+    ref.assert_linear(out, x[0], w[0], None, res, "silu", 0.0)
+
+
+def test_linear_empty_sizes(sv):
+    x, w, g = _operands(3, 2, 5, 40, 16)
+    bias, res = torch.randn(2, 40, device="cuda"), torch.randn(2, 5, 40, device="cuda")
+    y = sv.linear(x[:, :, :0], w[:, :, :0], bias=bias, residual=res, activation="relu", out_dtype=torch.float32)
+    assert torch.equal(y, bias.unsqueeze(1).clamp(min=0) + res)
+    assert sv.linear(x[:, :0], w).shape == (2, 0, 40)
+    assert sv.linear(x, w[:, :0]).shape == (2, 5, 0)
+    assert sv.linear(x[:0], w[:0]).shape == (0, 5, 40)
+
+
+def test_linear_keeps_infinities_and_nan_where_they_are(sv):
+    x, w, g = _operands(5, 1, 40, 300, 128)
+    x, w = x[0].clone(), w[0].clone()
+    x[3, 7] = float("inf")
+    x[9, 100] = float("nan")
+    w[17, 5] = float("-inf")
+    w[:, 7] = w[:, 7].abs() + 0.5
+    y = sv.linear(x, w, out_dtype=torch.float32)
+    want = x.double() @ w.double().T
+    assert bool((torch.isnan(y) == torch.isnan(want)).all())
+    at = torch.isinf(want)
+    assert bool((y.double()[at] == want[at]).all()) and bool((torch.isinf(y) == at).all())
+
+
+def test_linear_is_deterministic_and_replays(sv):
+    x, w, g = _operands(8, 4, 3, 1024, 2048, shared=True)
+    first = sv.linear(x, w, out_dtype=torch.float32)
+    assert all(torch.equal(first, sv.linear(x, w, out_dtype=torch.float32)) for _ in range(5))
+    out = torch.empty_like(first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sv.linear(x, w, out=out)
+    for i in range(2):
+        x.normal_(generator=g)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, sv.linear(x, w, out_dtype=torch.float32))
+
+
+def test_linear_large_offsets(sv):
+    # the last rows of w and y start past 2^31 elements
+    n_far, K = 40, 128
+    w = torch.empty((1 << 31) + 4096 * K, dtype=torch.bfloat16, device="cuda")
+    stride = ((1 << 31) // (n_far - 1) // 8 + 1) * 8
+    view = torch.as_strided(w, (n_far, K), (stride, 1))
+    x, wv, g = _operands(4, 1, 20, n_far, K)
+    view.copy_(wv[0])
+    y = torch.as_strided(torch.empty((1 << 31) + 4096, device="cuda"), (20, n_far), ((1 << 31) // 19, 1))
+    sv.linear(x[0], view, out=y)
+    ref.assert_linear(y, x[0], wv[0], None, None, "none", 0.0)
+
+
+# ------------------------------------------------------------- softmax
+
+def _assert_softmax(got, logits, t):
+    """An exponent's argument a (in powers of two) is off by 4 half steps of itself, so exp2 by 4 ln 2 |a| of them;
+    exp2 by 4 and the division and product by 2 more; a sum of V terms in runs of at most V / 256 + 32 additions."""
+    V = logits.shape[1]
+    t = t if isinstance(t, float) else t.double().unsqueeze(1)
+    z = logits.double() / t
+    want = torch.softmax(z, 1)
+    a = (z - z.amax(1, keepdim=True)).abs() * 1.4427
+    mean_a = (want * a).sum(1, keepdim=True)  # the sum's own error from its terms' arguments
+    steps = 4 * 0.7 * (a + mean_a) + 16 + V / 256 + 32
+    bound = steps * 2.0 ** -24 * want + 2.0 ** -126
+    off = (got.double() - want).abs()
+    assert bool((off <= bound).all()), float((off / bound).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,V", [(1, 1), (3, 2), (5, 7), (2, 1023), (4, 1024), (1, 4097), (9, 32000), (2, 128256),
+                                    (1, 262143), (700, 2049), (3, 65537), (40, 50001)])
+def test_softmax_sizes(sv, dtype, rows, V):
+    g = _gen(rows + V)
+    x = (torch.randn(rows, V, generator=g, device="cuda") * 4).to(dtype)
+    _assert_softmax(sv.softmax(x, 0.7), x, 0.7)
+    t = torch.rand(rows, generator=g, device="cuda") + 0.3
+    _assert_softmax(sv.softmax(x, t), x, t)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad,offset", [(1, 0), (3, 1), (8, 0), (4, 2)])
+def test_softmax_strides_and_alignment(sv, dtype, pad, offset):
+    rows, V = 6, 3001
+    store = torch.full((offset + rows * (V + pad),), float("nan"), dtype=dtype, device="cuda")
+    x = store[offset:].view(rows, V + pad)[:, :V]
+    x.copy_(torch.randn(rows, V, generator=_gen(pad), device="cuda"))
+    out_store = torch.full((rows, V + 2 * pad), 9.0, device="cuda")
+    out = out_store[:, pad:pad + V]
+    sv.softmax(x, 1.3, out=out)
+    _assert_softmax(out, x, 1.3)
+    assert bool((out_store[:, :pad] == 9).all()) and bool((out_store[:, pad + V:] == 9).all())
+
+
+def test_softmax_temperature_zero_takes_the_first_largest(sv):
+    x = torch.randn(5, 40000, generator=_gen(1), device="cuda").to(torch.bfloat16)
+    x[1, 30000] = x[1, 5] = 50.0
+    x[2] = 1.0
+    x[3] = float("-inf")
+    x[3, 39999] = -3.0e38
+    x[4, 7:] = float("-inf")
+    y = sv.softmax(x, 0.0)
+    want = torch.zeros_like(y)
+    want[torch.arange(5), x.float().argmax(1)] = 1
+    want[1] = 0
+    want[1, 5] = 1
+    want[2] = 0
+    want[2, 0] = 1
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [10, 5000, 140000])
+def test_softmax_rows_without_a_distribution(sv, dtype, V):
+    x = torch.randn(9, V, generator=_gen(V), device="cuda").to(dtype)
+    x[1, V - 1] = float("nan")
+    x[2, V // 2] = float("inf")
+    x[3] = float("-inf")
+    x[4, : V - 1] = float("-inf")
+    x[5] = torch.finfo(dtype).min
+    t = torch.ones(9, device="cuda")
+    t[6], t[7], t[8] = -1.0, float("nan"), float("inf")
+    y = sv.softmax(x, t)
+    assert bool(torch.isnan(y[[1, 2, 3, 6, 7, 8]]).all())
+    assert torch.equal(y[4], torch.nn.functional.one_hot(torch.tensor(V - 1), V).float().cuda())
+    _assert_softmax(y[[0, 5]], x[[0, 5]], 1.0)
+
+
+def test_softmax_in_place_and_empty(sv):
+    x = torch.randn(7, 30000, generator=_gen(2), device="cuda")
+    before = x.clone()
+    sv.softmax(x, 0.9, out=x)
+    _assert_softmax(x, before, 0.9)
+    assert sv.softmax(x[:0], 1.0).shape == (0, 30000)
+
+
+# ------------------------------------------------------------- tree
+
+def _run_tree(sv, batch, max_nodes, max_depth, replacement=True, pad=0, offset=0, **kw):
+    t = ref.on_gpu(batch, pad, offset)
+    cnt = torch.zeros(8, dtype=torch.int64, device="cuda")
+    out = sv.verify_tree(t["p"], t["q"], t["tokens"], t["parent"], t["draft_row"], t["node_start"], t["u_accept"],
+                         t["u_pick"], max_nodes=max_nodes, max_depth=max_depth, replacement=replacement, counters=cnt,
+                         **kw)
+    torch.cuda.synchronize()
+    return {k: v.cpu().numpy() for k, v in out.items()}, cnt.cpu().numpy()
+
+
+def _assert_tree(got, want):
+    (g, gc), (w, wc) = got, want
+    for name in ("accepted_len", "tokens", "path", "flags"):
+        assert np.array_equal(g[name], w[name]), (name, np.argwhere(g[name] != w[name])[:5])
+    # one rounding to fp32 of a value good to 1e-12
+    np.testing.assert_allclose(g["accept_prob"], w["accept_prob"], rtol=2.0 ** -24 + 1e-9, atol=1e-30)
+    assert np.array_equal(gc, wc), (gc, wc)
+
+
+def _check_tree(sv, batch, max_nodes, max_depth, replacement=True, **kw):
+    want = ref.tree(batch["p"], batch["q"], batch["tokens"], batch["parent"], batch["draft_row"], batch["node_start"],
+                    batch["u_accept"], batch["u_pick"], max_nodes, max_depth, replacement)
+    _assert_tree(_run_tree(sv, batch, max_nodes, max_depth, replacement, **kw), want)
+    return want
+
+
+@pytest.mark.parametrize("replacement", [True, False])
+@pytest.mark.parametrize("kind", ["sampled", "mixed", "certain"])
+@pytest.mark.parametrize("V", [1, 2, 7, 67, 1000, 1024, 1025, 5000])
+def test_tree_random(sv, V, kind, replacement):
+    batch = ref.random_tree_batch(V + 17 * replacement + len(kind), 40, V, 12, 5, replacement, kind, noise=1.2)
+    w, cnt = _check_tree(sv, batch, 12, 5, replacement)
+    if V > 2 and (kind != "certain" or V < 100):  # certain proposals of a flat long row are hardly ever accepted
+        assert cnt[1] > 0 and cnt[3] > 0 and cnt[4] > 0
+
+
+@pytest.mark.parametrize("V,B", [(32000, 3), (128256, 2), (151936, 1), (262144, 1), (40001, 20), (9000, 170)])
+def test_tree_large_vocabularies(sv, V, B):
+    batch = ref.random_tree_batch(V, B, V, 5, 3, True, "mixed", sharp=3.0, noise=1.0)
+    _check_tree(sv, batch, 5, 3)
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 2), (4, 0), (8, 4)])
+def test_tree_strides_and_alignment(sv, pad, offset):
+    batch = ref.random_tree_batch(pad * 10 + offset, 12, 3003, 8, 4, False, "mixed", noise=1.2)
+    _check_tree(sv, batch, 8, 4, False, pad=pad, offset=offset)
+
+
+def test_tree_chains_stars_and_the_largest_tree(sv):
+    _check_tree(sv, ref.random_tree_batch(1, 6, 50, 256, 256, True, "sampled", noise=0.05, shape="chain"), 256, 256)
+    _check_tree(sv, ref.random_tree_batch(2, 6, 300, 256, 256, True, "sampled", noise=3.0, shape="star"), 256, 256)
+    _check_tree(sv, ref.random_tree_batch(3, 6, 300, 256, 256, False, "sampled", noise=3.0, shape="star"), 256, 1, False)
+    _check_tree(sv, ref.random_tree_batch(4, 6, 300, 256, 256, True, "certain", shape="star"), 256, 1)
+    _check_tree(sv, ref.random_tree_batch(5, 30, 300, 256, 9, True, "mixed", noise=1.0), 256, 9)
+
+
+def test_tree_without_nodes_samples_the_root(sv):
+    batch = ref.random_tree_batch(7, 33, 999, 0, 0, True)
+    w, cnt = _check_tree(sv, batch, 0, 0)
+    assert cnt[4] == 33
+    batch["q"] = np.zeros((0, 999), np.float32)
+    batch["draft_row"][:] = -1
+    _check_tree(sv, batch, 0, 0)
+
+
+def test_tree_ties_and_extreme_uniforms(sv):
+    # dyadic rows: every comparison is an equality somewhere, and exact in any order
+    rng = np.random.default_rng(3)
+    batch = ref.random_tree_batch(9, 200, 64, 6, 4, True, "mixed")
+    R = batch["p"].shape[0]
+    for name in ("p", "q"):
+        w = rng.multinomial(64, np.ones(64) / 64, R) / 64.0
+        batch[name] = w.astype(np.float32)
+    batch["u_accept"] = (rng.integers(0, 8, len(batch["u_accept"])) / 8).astype(np.float32)
+    batch["u_pick"] = (rng.integers(0, 16, 200) / 16).astype(np.float32)
+    batch["u_pick"][:20], batch["u_pick"][20:40] = 0.0, 1 - 2.0 ** -24
+    _check_tree(sv, batch, 6, 4)
+
+
+def test_tree_rows_with_zeros_and_no_mass(sv):
+    # rows that need not be normalised: rests without mass fall back to p, rows without mass are invalid
+    batch = ref.random_tree_batch(11, 64, 40, 4, 3, True, "mixed", shape="any")
+    rng = np.random.default_rng(4)
+    batch["p"] *= (rng.random(batch["p"].shape) < 0.3)
+    batch["q"] = np.where(rng.random(batch["q"].shape[0])[:, None] < 0.5, np.float32(1.0), batch["q"]).astype(np.float32)
+    batch["p"][batch["node_start"][5] + 5] = 0.0  # the root of sequence 5
+    w, cnt = _check_tree(sv, batch, 4, 3)
+    assert cnt[7] > 0 and cnt[6] > 0
+
+
+def test_tree_invalid_sequences_fail_closed(sv):
+    batch = ref.random_tree_batch(13, 20, 500, 6, 6, True, "sampled")
+    st = batch["node_start"]
+    has = [b for b in range(20) if st[b + 1] - st[b] >= 3]
+    assert len(has) >= 6
+    batch["tokens"][st[has[0]] + 1] = 500
+    batch["tokens"][st[has[1]] + 2] = -1
+    batch["parent"][st[has[2]] + 1] = 1
+    batch["parent"][st[has[3]]] = -2
+    batch["draft_row"][st[has[4]] + has[4]] = batch["q"].shape[0]
+    batch["draft_row"][st[has[5]] + has[5] + 1] = -7
+    w, cnt = _check_tree(sv, batch, 6, 6)
+    assert cnt[6] == 6
+    # too deep, too many nodes, ranges that leave the arrays
+    chain = ref.random_tree_batch(14, 8, 100, 6, 6, True, shape="chain")
+    w, cnt = _check_tree(sv, chain, 6, 3)
+    assert cnt[6] > 0
+    w, cnt = _check_tree(sv, chain, 4, 4)
+    assert cnt[6] > 0
+    for bad in (-1, 1 << 30, -(1 << 31)):
+        broken = dict(chain, node_start=chain["node_start"].copy())
+        broken["node_start"][3] = bad
+        got, gc = _run_tree(sv, broken, 6, 6)
+        assert got["accepted_len"][2] == -1 and got["accepted_len"][3] == -1
+        assert (got["tokens"][2:4] == -1).all() and (got["path"][2:4] == -1).all()
+        keep = [0, 1, 4, 5, 6, 7]
+        want = ref.tree(*(chain[k] for k in ("p", "q", "tokens", "parent", "draft_row", "node_start", "u_accept",
+                                             "u_pick")), 6, 6)[0]
+        assert np.array_equal(got["tokens"][keep], want["tokens"][keep])
+
+
+@pytest.mark.parametrize("what", ["nan_p", "inf_p", "nan_q", "nan_p_unread"])
+def test_tree_probabilities_that_are_none(sv, what):
+    batch = ref.random_tree_batch(15, 30, 3000, 3, 3, True, "sampled", shape="chain")
+    if what == "nan_p":
+        batch["p"][:, 2999] = np.nan
+    elif what == "inf_p":
+        batch["p"][:, 1500] = np.inf
+    elif what == "nan_q":
+        batch["q"][:, 17] = np.nan
+    else:
+        batch["p"][batch["node_start"][5] + 5 + 3 if batch["node_start"][6] - batch["node_start"][5] == 3 else 0] = np.nan
+    _check_tree(sv, batch, 3, 3)
+
+
+@pytest.mark.parametrize("kind,replacement", [("sampled", True), ("sampled", False), ("certain", True)])
+def test_tree_keeps_the_target_law(sv, kind, replacement):
+    # one place with three candidates over six tokens: the first emitted token is distributed as p
+    from scipy.stats import chi2
+    B, V, W = 60000, 6, 3
+    g = _gen(31 + replacement)
+    p1 = torch.tensor([0.32, 0.05, 0.2, 0.03, 0.3, 0.1])
+    q1 = torch.tensor([0.1, 0.3, 0.25, 0.15, 0.05, 0.15])
+    toks = torch.multinomial(q1.expand(B, V).cuda(), W, replacement=replacement, generator=g)
+    start = (torch.arange(B + 1, device="cuda") * W).int()
+    p = p1.expand(B * (W + 1), V).contiguous().cuda()
+    q = q1.unsqueeze(0).contiguous().cuda()
+    row = torch.full((B, W + 1), -1, dtype=torch.int32, device="cuda")
+    if kind == "sampled":
+        row[:, 0] = 0
+    out = sv.verify_tree(p, q, toks.reshape(-1).int(), torch.full((B * W,), -1, dtype=torch.int32, device="cuda"),
+                         row.reshape(-1), start, torch.rand(B * W, generator=g, device="cuda"),
+                         torch.rand(B, generator=g, device="cuda"), max_nodes=W, max_depth=1, replacement=replacement)
+    count = torch.bincount(out["tokens"][:, 0].long(), minlength=V).double().cpu()
+    stat = float(((count - B * p1.double()) ** 2 / (B * p1.double())).sum())
+    assert stat < chi2.ppf(1 - 1e-4, V - 1), stat
+    assert int(out["accepted_len"].sum()) > B // 4
+
+
+def test_tree_results_do_not_depend_on_the_batch(sv):
+    batch = ref.random_tree_batch(21, 100, 7000, 6, 4, True, "mixed", noise=1.0)
+    whole, _ = _run_tree(sv, batch, 6, 4)
+    st = batch["node_start"]
+    for b in (0, 17, 99):
+        lo, hi = st[b], st[b + 1]
+        one = dict(p=batch["p"][lo + b:hi + b + 1], q=batch["q"], tokens=batch["tokens"][lo:hi],
+                   parent=batch["parent"][lo:hi], draft_row=batch["draft_row"][lo + b:hi + b + 1],
+                   node_start=np.array([0, hi - lo], np.int32), u_accept=batch["u_accept"][lo:hi],
+                   u_pick=batch["u_pick"][b:b + 1])
+        got, _ = _run_tree(sv, one, 6, 4)
+        assert np.array_equal(got["tokens"][0], whole["tokens"][b])
+        assert np.array_equal(got["accept_prob"], whole["accept_prob"][lo:hi])
+
+
+def test_tree_leaves_what_belongs_to_no_sequence(sv):
+    batch = ref.random_tree_batch(22, 5, 300, 4, 4, True, "sampled")
+    n = len(batch["tokens"])
+    more = dict(batch, tokens=np.append(batch["tokens"], [5, 6]).astype(np.int32),
+                parent=np.append(batch["parent"], [-1, -1]).astype(np.int32),
+                u_accept=np.append(batch["u_accept"], [0.5, 0.5]).astype(np.float32),
+                p=np.concatenate([batch["p"], batch["p"][:2]]),
+                draft_row=np.append(batch["draft_row"], [-1, -1]).astype(np.int32))
+    out = dict(accepted_len=torch.full((5,), 77, dtype=torch.int32, device="cuda"),
+               tokens=torch.full((5, 5), 77, dtype=torch.int32, device="cuda"),
+               path=torch.full((5, 4), 77, dtype=torch.int32, device="cuda"),
+               accept_prob=torch.full((n + 2,), 77.0, device="cuda"),
+               flags=torch.full((n + 2,), 77, dtype=torch.int8, device="cuda"))
+    got, _ = _run_tree(sv, more, 4, 4, out=out)
+    assert (got["accept_prob"][n:] == 77).all() and (got["flags"][n:] == 77).all()
+    assert (got["accepted_len"] < 77).all()
+
+
+def test_tree_captured_on_another_stream(sv):
+    batch = ref.random_tree_batch(23, 16, 20000, 5, 5, True, "mixed", noise=1.0)
+    t = ref.on_gpu(batch)
+    args = [t[k] for k in ("p", "q", "tokens", "parent", "draft_row", "node_start", "u_accept", "u_pick")]
+    eager = sv.verify_tree(*args, max_nodes=5, max_depth=5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out = sv.verify_tree(*args, max_nodes=5, max_depth=5)
+        for v in out.values():
+            v.fill_(55)
+        graph.replay()
+        again = sv.verify_tree(*args, max_nodes=5, max_depth=5)  # eager beside the captured one
+    torch.cuda.synchronize()
+    for k in eager:
+        assert torch.equal(eager[k], out[k]) and torch.equal(eager[k], again[k])
+
+
+# ------------------------------------------------------------- together
+
+def test_chain_agrees_with_the_verifier(sv):
+    """Logits through softmax and the tree call give what spec_verify_run gives for the same uniforms."""
+    B, k, V = 50, 4, 257
+    g = _gen(41)
+    Lt = torch.randn(B, k + 1, V, generator=g, device="cuda") * 2
+    Ld = (Lt[:, :k] + torch.randn(B, k, V, generator=g, device="cuda")).contiguous()
+    D = torch.multinomial(torch.softmax(Ld.view(-1, V) / 0.8, 1), 1, generator=g).view(B, k).int()
+    u0, u1 = torch.rand(B, k, generator=g, device="cuda"), torch.rand(B, generator=g, device="cuda")
+    ver = sv.SpecVerifier(B, k, V)
+    a = ver.run(Lt, Ld, D, 0.8, u_accept=u0, u_residual=u1)
+    p, q = sv.softmax(Lt.view(-1, V), 0.8), sv.softmax(Ld.view(-1, V), 0.8)
+    i = torch.arange(B, device="cuda", dtype=torch.int32)
+    j = torch.arange(k + 1, device="cuda", dtype=torch.int32)
+    row = torch.where(j[None] < k, i[:, None] * k + j[None], -1).int().reshape(-1)
+    b = sv.verify_tree(p, q, D.reshape(-1), (j[:k] - 1).repeat(B), row, (torch.arange(B + 1, device="cuda") * k).int(),
+                       u0.reshape(-1), u1, max_nodes=k, max_depth=k)
+    r = O.verify(Lt.cpu().numpy(), Ld.cpu().numpy(), D.cpu().numpy(), 0.8, np.zeros(B, np.uint8), np.full(B, 0.5),
+                 u0=u0.cpu().numpy(), u1=u1.cpu().numpy())
+    clear = torch.as_tensor(r["margin"] >= 1e-6)
+    assert int(clear.sum()) > 40
+    assert torch.equal(a["accepted_len"].cpu()[clear], b["accepted_len"].cpu()[clear])
+    assert torch.equal(a["tokens"].cpu()[clear], b["tokens"].cpu()[clear])
+    f = b["flags"].view(B, k)
+    assert torch.equal(a["flags"].cpu()[clear], f.cpu()[clear])
+    tested = (f != 0) & clear.cuda()[:, None]
+    torch.testing.assert_close(a["accept_prob"][tested], b["accept_prob"].view(B, k)[tested], rtol=2e-5, atol=0)
+    ver.close()
+
+
+def test_hidden_states_to_accepted_tokens(sv):
+    """Draft blocks, output heads, probabilities and a tree, one after another, against 64 bits at each step."""
+    B, G, H, V = 6, 3, 256, 2000
+    g = _gen(51)
+    hidden = torch.randn(B, H, generator=g, device="cuda").to(torch.bfloat16)
+    w_block = (torch.randn(G, H, H, generator=g, device="cuda") / 16).to(torch.bfloat16)
+    head = (torch.randn(V, H, generator=g, device="cuda") / 5).to(torch.bfloat16)
+    blocks = torch.empty(B, G, H, dtype=torch.bfloat16, device="cuda")
+    sv.linear(hidden, w_block, residual=hidden.unsqueeze(0).expand(G, B, H), activation="silu",
+              out=blocks.transpose(0, 1))
+    ref.assert_linear(blocks.transpose(0, 1), hidden, w_block, None, hidden.unsqueeze(0).expand(G, B, H), "silu", 0)
+    draft_logits = sv.linear(blocks.view(B * G, H), head, activation="softcap", cap=20.0, out_dtype=torch.float32)
+    ref.assert_linear(draft_logits, blocks.view(B * G, H), head, None, None, "softcap", 20.0)
+    q = sv.softmax(draft_logits, 0.9)
+    _assert_softmax(q, draft_logits, 0.9)
+    # two candidates for the first place, chains of the further heads behind the first one
+    two = torch.multinomial(q.view(B, G, V)[:, 0], 2, replacement=True, generator=g)
+    more = torch.multinomial(q, 1, generator=g).view(B, G)[:, 1:]
+    tokens = torch.cat([two, more], 1).int()
+    parent = torch.tensor([-1, -1, 0, 2], dtype=torch.int32, device="cuda").repeat(B)
+    n = 4
+    target_hidden = torch.randn(B * (n + 1), H, generator=g, device="cuda") * 0.3
+    target_hidden = (target_hidden + hidden.repeat_interleave(n + 1, 0)).to(torch.bfloat16)
+    target_logits = sv.linear(target_hidden, head, activation="softcap", cap=20.0, out_dtype=torch.float32)
+    p = sv.softmax(target_logits, 0.9)
+    base = torch.arange(B, device="cuda", dtype=torch.int32)[:, None] * G
+    row = torch.cat([base, base + 1, torch.full_like(base, -1), base + 2, torch.full_like(base, -1)], 1).reshape(-1)
+    batch = dict(p=p, q=q, tokens=tokens.reshape(-1), parent=parent, draft_row=row.int(),
+                 node_start=(torch.arange(B + 1, device="cuda") * n).int(),
+                 u_accept=torch.rand(B * n, generator=g, device="cuda"), u_pick=torch.rand(B, generator=g, device="cuda"))
+    batch = {k: v.contiguous().cpu().numpy() for k, v in batch.items()}
+    _check_tree(sv, batch, n, 3)
+
+
+@pytest.mark.parametrize("per_position", [False, True])
+def test_run_hidden_is_the_heads_and_the_verifier(sv, per_position):
+    B, k, H, V = 9, 3, 128, 3000
+    g = _gen(61 + per_position)
+    th = torch.randn(B, k + 1, H, generator=g, device="cuda").to(torch.bfloat16)
+    dh = torch.randn(B, k, 64, generator=g, device="cuda").to(torch.bfloat16)
+    wt = (torch.randn(V, H, generator=g, device="cuda") / 4).to(torch.bfloat16)
+    shape = (k, V, 64) if per_position else (V, 64)
+    wd = (torch.randn(shape, generator=g, device="cuda") / 4).to(torch.bfloat16)
+    bias = torch.randn(shape[:-1], generator=g, device="cuda")
+    D = torch.randint(0, V, (B, k), generator=g, device="cuda").int()
+    ver = sv.SpecVerifier(B, k, V)
+    out = ver.run_hidden(th, wt, dh, wd, D, 0.9, draft_bias=bias, cap=15.0, seed=5, logits_dtype=torch.float32)
+    ref.assert_linear(out["target_logits"].view(-1, V), th.view(-1, H), wt, None, None, "softcap", 15.0)
+    if per_position:
+        ref.assert_linear(out["draft_logits"].transpose(0, 1), dh.transpose(0, 1), wd, bias, None, "softcap", 15.0)
+    else:
+        ref.assert_linear(out["draft_logits"].view(-1, V), dh.view(-1, 64), wd, bias, None, "softcap", 15.0)
+    same = ver.run(out["target_logits"], out["draft_logits"], D, 0.9, seed=5)
+    for name in ("accepted_len", "tokens", "accept_prob", "flags"):
+        assert torch.equal(out[name], same[name])
+    ver.close()
