@@ -1,9 +1,15 @@
 // Grouped matrix products with an epilogue: spec_verify_linear.
 //
 //   y[g, m, n] = act(sum_k x[g, m, k] w[g, n, k] + bias[g, n]) + residual[g, m, n]
+//
+// Rows of x and w that start at multiples of 16 bytes go through the tensor
+// cores (mma_kernel), others through plain_kernel.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -86,6 +92,378 @@ __global__ void __launch_bounds__(256) plain_kernel(LinearParams P) {
   }
 }
 
+// ------------------------------------------------------------ tensor cores
+//
+// Persistent CTAs, one per SM, each taking every gridDim-th tile of y.  Warp 0
+// fetches tiles of both operands by TMA into a ring of stages, 64 entries of
+// K at a time (rows of 128 bytes, 128-byte swizzle); warp 1 multiplies them
+// into tensor memory, 128 rows of one operand (A) by nt rows of the other (B);
+// warps 2 to 9 take the sums out and finish them while the next tile is
+// multiplied into the other half of the accumulators.
+//
+// Which operand is A:
+//  * M > 128: w.  A lane of tensor memory is one n, so a warp's 32 lanes write
+//    32 neighbours of y for each m, straight from registers.
+//  * M <= 128: x.  The call is bound by reading w, and the width of a tile of
+//    w is then free (any multiple of 16 up to 256), so that the tiles come out
+//    even over the SMs.  Lanes are tokens here; sums pass through shared memory
+//    so that neighbouring threads finish neighbouring n, however few tokens
+//    there are.  Only the rows of x that exist are fetched: a product row that
+//    belongs to no token multiplies whatever lies behind them in shared memory
+//    and is never read.
+
+constexpr int kMmaK = 64;        // entries of K a stage holds of each row: 128 bytes
+constexpr int kRowBytes = 128;
+constexpr int kMaxStages = 12;
+constexpr int kEpiWarps = 8;
+constexpr int kMmaThreads = 32 * (2 + kEpiWarps);
+constexpr int kStageCols = 64;   // columns of a tile that the epilogue passes through shared memory at a time
+constexpr int kMmaSmem = 225 * 1024;
+
+struct MmaParams {
+  LinearParams L;
+  int nt;                // rows of B in a tile
+  int ra;                // rows of A that are fetched
+  int stages, tmem_cols;
+  int tiles_a, tiles_b, kblocks;
+  int a_groups, b_groups;  // 0: the operand is shared by all groups
+  unsigned tiles;
+  unsigned idesc;
+  unsigned staging;      // where the epilogue's staging starts in dynamic shared memory
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void mbar_init(uint64_t* bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+// Waits for a phase; gives up after two seconds, or when another role has, and
+// then marks the CTA: its remaining results become NaN.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, volatile int* dead) {
+  if (mbar_try(bar, parity)) return true;
+  unsigned long long since = 0;
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(bar, parity)) return true;
+    const unsigned long long t = now_ns();
+    if (since == 0) since = t;
+    if (*dead || t - since > 2000000000ull) {
+      *dead = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void tma_load(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int k, int row, int g) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(map), "r"(smem_addr(bar)), "r"(k), "r"(row), "r"(g)
+      : "memory");
+}
+
+// rows of 128 bytes in groups of 8 (1024 bytes), 128-byte swizzle, K innermost
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, unsigned idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(add))
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+// 16 columns of this warp's 32 lanes
+__device__ __forceinline__ void tc_load16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "{\n tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+struct TileAt {
+  int ta, tb, g;
+};
+
+__device__ __forceinline__ TileAt tile_at(const MmaParams& P, unsigned t) {
+  const unsigned tb = t % P.tiles_b, rest = t / P.tiles_b;
+  return {static_cast<int>(rest % P.tiles_a), static_cast<int>(tb), static_cast<int>(rest / P.tiles_a)};
+}
+
+template <bool kWeightsA>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ CUtensorMap map_a,
+               const __grid_constant__ CUtensorMap map_b) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int dead;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
+  const uint32_t a_bytes = P.ra * kRowBytes, stage_bytes = a_bytes + P.nt * kRowBytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], kEpiWarps);
+    mbar_init(&drained, 1);
+    dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b));
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
+                 "r"(P.tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      unsigned fill = 0;
+      for (unsigned t = blockIdx.x; t < P.tiles && !dead; t += gridDim.x) {
+        const TileAt at = tile_at(P, t);
+        for (int kb = 0; kb < P.kblocks; ++kb, ++fill) {
+          const unsigned s = fill % P.stages, round = fill / P.stages;
+          if (!mbar_wait(&empty[s], (round & 1) ^ 1, &dead)) break;
+          mbar_expect(&full[s], stage_bytes);
+          const uint32_t dst = base + s * stage_bytes;
+          tma_load(&map_a, dst, &full[s], kb * kMmaK, kWeightsA ? at.ta * 128 : 0, P.a_groups ? at.g : 0);
+          tma_load(&map_b, dst + a_bytes, &full[s], kb * kMmaK, at.tb * P.nt, P.b_groups ? at.g : 0);
+        }
+      }
+      if (dead) {
+        // copies still in flight land before the CTA's memory goes
+        int gave_up = 0;
+        for (unsigned f = fill > static_cast<unsigned>(P.stages) ? fill - P.stages : 0; f < fill; ++f)
+          mbar_wait(&full[f % P.stages], (f / P.stages) & 1, &gave_up);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      unsigned use = 0, n = 0;
+      for (unsigned t = blockIdx.x; t < P.tiles && !dead; t += gridDim.x, ++n) {
+        const unsigned buf = n & 1;
+        if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, &dead)) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t d = tmem + buf * P.nt;
+        for (int kb = 0; kb < P.kblocks; ++kb, ++use) {
+          const unsigned s = use % P.stages, round = use / P.stages;
+          if (!mbar_wait(&full[s], round & 1, &dead)) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t da = smem_desc(base + s * stage_bytes), db = smem_desc(base + s * stage_bytes + a_bytes);
+          for (int k = 0; k < kMmaK / 16; ++k) tc_mma(d, da + 2 * k, db + 2 * k, P.idesc, kb > 0 || k > 0);
+          tc_commit(&empty[s]);
+        }
+        tc_commit(&acc_full[buf]);
+      }
+      if (dead) {
+        int gave_up = 0;
+        tc_commit(&drained);
+        mbar_wait(&drained, 0, &gave_up);
+      }
+    }
+  } else {
+    const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
+    const int et = threadIdx.x - 64;
+    float* staging = reinterpret_cast<float*>(smem + P.staging);
+    unsigned n = 0;
+    for (unsigned t = blockIdx.x; t < P.tiles; t += gridDim.x, ++n) {
+      const TileAt at = tile_at(P, t);
+      const unsigned buf = n & 1;
+      const bool ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t acc = tmem + buf * P.nt + (static_cast<uint32_t>(quad * 32) << 16);
+      if constexpr (kWeightsA) {
+        const int64_t col = static_cast<int64_t>(at.ta) * 128 + quad * 32 + lane;
+        for (int c = half * 16; c < P.nt; c += 32) {
+          float v[16];
+          __syncwarp();
+          tc_load16(acc + c, v);
+          const int64_t m0 = static_cast<int64_t>(at.tb) * P.nt + c;
+          if (col < P.L.N)
+            for (int i = 0; i < 16; ++i)
+              if (m0 + i < P.L.M) finish_value(P.L, at.g, m0 + i, col, ok ? v[i] : NAN);
+        }
+      } else {
+        const int cols = min(P.nt, static_cast<int>(P.L.N - static_cast<int64_t>(at.tb) * P.nt));
+        for (int c0 = 0; c0 < cols; c0 += kStageCols) {
+          if (quad * 32 < P.L.M)
+            for (int c = c0 + half * 32; c < min(c0 + half * 32 + 32, P.nt); c += 16) {
+              float v[16];
+              __syncwarp();
+              tc_load16(acc + c, v);
+              if (quad * 32 + lane < P.L.M)
+                for (int i = 0; i < 16; ++i)
+                  staging[(quad * 32 + lane) * (kStageCols + 1) + c - c0 + i] = ok ? v[i] : NAN;
+            }
+          asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+          const int width = min(kStageCols, cols - c0);
+          for (int i = et; i < P.L.M * kStageCols; i += kEpiWarps * 32) {
+            const int m = i / kStageCols, c = i % kStageCols;
+            if (c < width)
+              finish_value(P.L, at.g, m, static_cast<int64_t>(at.tb) * P.nt + c0 + c, staging[m * (kStageCols + 1) + c]);
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  __syncwarp();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols) : "memory");
+}
+
+// ------------------------------------------------------------ host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static std::atomic<EncodeTiled> found{nullptr};
+  EncodeTiled f = found.load();
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult r;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+      r != cudaDriverEntryPointSuccess) {
+    (void)cudaGetLastError();
+    return nullptr;
+  }
+  f = reinterpret_cast<EncodeTiled>(p);
+  found.store(f);
+  return f;
+}
+
+// A map of [groups, rows, K] bf16 entries in boxes of box_rows x kMmaK, where
+// TMA can address it: the base and the strides multiples of 16 bytes.  *grouped:
+// whether the groups are a dimension of it (a shared operand has one).
+bool make_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t groups, int64_t row_stride,
+              int64_t group_stride, int box_rows, int* grouped) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode || reinterpret_cast<uintptr_t>(base) % 16) return false;
+  const cuuint64_t any = static_cast<cuuint64_t>((K * 2 + 15) / 16 * 16);
+  if (rows > 1 && (row_stride == 0 || row_stride % 8)) return false;
+  *grouped = groups > 1 && group_stride > 0;
+  if (*grouped && group_stride % 8) return false;
+  if (row_stride >= (int64_t{1} << 38) || group_stride >= (int64_t{1} << 38)) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(*grouped ? groups : 1)};
+  const cuuint64_t strides[2] = {rows > 1 ? static_cast<cuuint64_t>(row_stride) * 2 : any,
+                                 *grouped ? static_cast<cuuint64_t>(group_stride) * 2 : any};
+  const cuuint32_t box[3] = {kMmaK, static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The width of a tile: the one with the least time by this estimate.  A stage
+// (64 entries of K) of 128 x nt products takes 2 nt cycles of the tensor core, and
+// its (rows of A + nt) rows of 128 bytes come in at about 40 bytes a cycle; the
+// SMs take their tiles in waves, and each wave pays for starting and ending.
+int choose_width(int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, int64_t kblocks, int sms) {
+  int best = 16;
+  double least = 1e300;
+  for (int nt = 16; nt <= 256; nt += 16) {
+    const int64_t tiles = (rows_b + nt - 1) / nt * tiles_a * groups;
+    const int64_t waves = (tiles + sms - 1) / sms;
+    const double stage = std::max(2.0 * nt, (rows_a + nt) * 128 / 40.0);
+    const double t = waves * (kblocks * stage + 1500.0);
+    if (t < least * 0.999) least = t, best = nt;
+  }
+  return best;
+}
+
+template <bool kWeightsA>
+cudaError_t launch_mma(const LinearParams& L, int sms, cudaStream_t st, bool* taken) {
+  *taken = false;
+  MmaParams P = {};
+  P.L = L;
+  P.kblocks = (L.K + kMmaK - 1) / kMmaK;
+  P.ra = kWeightsA ? 128 : (L.M + 7) / 8 * 8;
+  const int64_t rows_a = kWeightsA ? L.N : L.M, rows_b = kWeightsA ? L.M : L.N;
+  P.tiles_a = static_cast<int>((rows_a + 127) / 128);
+  P.nt = choose_width(rows_b, P.tiles_a, P.ra, L.groups, P.kblocks, sms);
+  P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
+  const int64_t tiles = static_cast<int64_t>(P.tiles_a) * P.tiles_b * L.groups;
+  if (tiles >= (int64_t{1} << 31)) return cudaSuccess;
+  P.tiles = static_cast<unsigned>(tiles);
+  CUtensorMap map_x, map_w;
+  int gx = 0, gw = 0;
+  if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? P.nt : P.ra, &gx) ||
+      !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : P.nt, &gw))
+    return cudaSuccess;
+  P.a_groups = kWeightsA ? gw : gx;
+  P.b_groups = kWeightsA ? gx : gw;
+  const int stage_bytes = (P.ra + P.nt) * kRowBytes;
+  const int staging = kWeightsA ? 0 : L.M * (kStageCols + 1) * 4;
+  // a product reads 128 rows of A from the last stage on: they stay inside the allocation
+  const int slack = std::max(0, 128 * kRowBytes - stage_bytes);
+  P.stages = std::min(kMaxStages, (kMmaSmem - 1024 - staging - slack) / stage_bytes);
+  P.staging = 1024 + P.stages * stage_bytes + slack;
+  const int smem = static_cast<int>(P.staging) + staging;
+  P.tmem_cols = 32;
+  while (P.tmem_cols < 2 * P.nt) P.tmem_cols *= 2;
+  // fp32 sums, bf16 operands, both K-major, N = nt, M = 128
+  P.idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(P.nt / 8) << 17) | ((128u / 16) << 24);
+  const cudaError_t e =
+      cudaFuncSetAttribute(mma_kernel<kWeightsA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, sms));
+  *taken = true;
+  mma_kernel<kWeightsA><<<grid, kMmaThreads, smem, st>>>(P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
+  return cudaGetLastError();
+}
+
 bool valid_dtype(int d) { return d == SV_F32 || d == SV_BF16; }
 bool aligned_to(const void* p, int d) { return reinterpret_cast<uintptr_t>(p) % (d == SV_BF16 ? 2 : 4) == 0; }
 
@@ -140,6 +518,15 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   P.act = act;
   P.cap = cap;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (K > 0) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
+    bool taken = false;
+    const cudaError_t e =
+        M > 128 ? sv::launch_mma<true>(P, sms, st, &taken) : sv::launch_mma<false>(P, sms, st, &taken);
+    if (e != cudaSuccess) return SV_ECUDA;
+    if (taken) return SV_OK;
+  }
   const int64_t tiles = (static_cast<int64_t>(N) + sv::kPlainTile - 1) / sv::kPlainTile *
                         ((static_cast<int64_t>(M) + sv::kPlainTile - 1) / sv::kPlainTile) * groups;
   const unsigned grid = static_cast<unsigned>(tiles < (1 << 20) ? tiles : (1 << 20));
