@@ -47,11 +47,20 @@ __device__ __forceinline__ float activate(float z, int act, float cap) {
   }
 }
 
+__device__ __forceinline__ float load_bias(const LinearParams& P, int g, int64_t n) {
+  return P.bias ? load_either(P.bias, g * P.b_group + n, P.bias_bf16) : 0.f;
+}
+
+__device__ __forceinline__ float load_residual(const LinearParams& P, int g, int64_t m, int64_t n) {
+  return P.res ? load_either(P.res, g * P.r_group + m * P.r_row + n, P.res_bf16) : 0.f;
+}
+
 // The sum's way out: the one rounding to bf16, where y is bf16, is the last step.
-__device__ __forceinline__ void finish_value(const LinearParams& P, int g, int64_t m, int64_t n, float z) {
-  if (P.bias) z += load_either(P.bias, g * P.b_group + n, P.bias_bf16);
+__device__ __forceinline__ void finish_value(const LinearParams& P, int g, int64_t m, int64_t n, float z, float bias,
+                                             float res) {
+  if (P.bias) z += bias;
   z = activate(z, P.act, P.cap);
-  if (P.res) z += load_either(P.res, g * P.r_group + m * P.r_row + n, P.res_bf16);
+  if (P.res) z += res;
   const int64_t at = g * P.y_group + m * P.y_row + n;
   if (P.y_bf16)
     static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16(z);
@@ -87,14 +96,16 @@ __global__ void __launch_bounds__(256) plain_kernel(LinearParams P) {
     }
     for (int i = 0; i < 4; ++i)
       for (int j = 0; j < 4; ++j)
-        if (m0 + ty + 16 * i < P.M && n0 + tx + 16 * j < P.N)
-          finish_value(P, g, m0 + ty + 16 * i, n0 + tx + 16 * j, acc[i][j]);
+        if (m0 + ty + 16 * i < P.M && n0 + tx + 16 * j < P.N) {
+          const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
+          finish_value(P, g, m, n, acc[i][j], load_bias(P, g, n), load_residual(P, g, m, n));
+        }
   }
 }
 
 // ------------------------------------------------------------ tensor cores
 //
-// Persistent CTAs, one per SM, each taking every gridDim-th tile of y.  Warp 0
+// Persistent CTAs, one per SM, each (or each pair) taking every n-th tile of y.  Warp 0
 // fetches tiles of both operands by TMA into a ring of stages, 64 entries of
 // K at a time (rows of 128 bytes, 128-byte swizzle); warp 1 multiplies them
 // into tensor memory, 128 rows of one operand (A) by nt rows of the other (B);
@@ -102,8 +113,11 @@ __global__ void __launch_bounds__(256) plain_kernel(LinearParams P) {
 // multiplied into the other half of the accumulators.
 //
 // Which operand is A:
-//  * M > 128: w.  A lane of tensor memory is one n, so a warp's 32 lanes write
-//    32 neighbours of y for each m, straight from registers.
+//  * M > 128: w, 256 rows of it by a pair of CTAs (a cluster of two, on one
+//    pair of SMs): each holds 128 rows of A and half the rows of B, and one
+//    product instruction of the first CTA works on both.  A lane of tensor
+//    memory is one n, so a warp's 32 lanes write 32 neighbours of y for each m,
+//    straight from registers.
 //  * M <= 128: x.  The call is bound by reading w, and the width of a tile of
 //    w is then free (any multiple of 16 up to 256), so that the tiles come out
 //    even over the SMs.  Lanes are tokens here; sums pass through shared memory
@@ -181,6 +195,36 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, volati
   }
 }
 
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// the address of the same place in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t in_cta(const void* p, unsigned rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ void mbar_arrive_in(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// into this CTA's memory, its bytes counted by the barrier of the pair's first CTA
+__device__ __forceinline__ void tma_load_pair(const CUtensorMap* map, uint32_t dst, uint32_t bar, int k, int row, int g) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(k), "r"(row), "r"(g)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int k, int row, int g) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -194,17 +238,34 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
+template <bool kPair>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, unsigned idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(add))
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(add))
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(add))
+        : "memory");
 }
 
+// an arrival at `bar` (of both CTAs of a pair) once the products issued so far are done
+template <bool kPair>
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
 
 // 16 columns of this warp's 32 lanes
@@ -229,20 +290,25 @@ __device__ __forceinline__ TileAt tile_at(const MmaParams& P, unsigned t) {
   return {static_cast<int>(rest % P.tiles_a), static_cast<int>(tb), static_cast<int>(rest / P.tiles_a)};
 }
 
+// kWeightsA: w is A, and the CTAs work in pairs
 template <bool kWeightsA>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
+  constexpr bool kPair = kWeightsA;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned rank = kPair ? cluster_rank() : 0;
+  const unsigned first = kPair ? blockIdx.x / 2 : blockIdx.x, step = kPair ? gridDim.x / 2 : gridDim.x;
+  const int b_rows = kPair ? P.nt / 2 : P.nt;  // of B in this CTA
   const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
-  const uint32_t a_bytes = P.ra * kRowBytes, stage_bytes = a_bytes + P.nt * kRowBytes;
+  const uint32_t a_bytes = P.ra * kRowBytes, stage_bytes = a_bytes + b_rows * kRowBytes;
   if (threadIdx.x == 0) {
     for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], kEpiWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], kPair ? 2 * kEpiWarps : kEpiWarps);
     mbar_init(&drained, 1);
     dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -250,31 +316,47 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b));
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
-                 "r"(P.tmem_cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
+                   "r"(P.tmem_cols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
+                   "r"(P.tmem_cols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if constexpr (kPair) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
 
   if (warp == 0) {
     if (lane == 0) {
       unsigned fill = 0;
-      for (unsigned t = blockIdx.x; t < P.tiles && !dead; t += gridDim.x) {
+      for (unsigned t = first; t < P.tiles && !dead; t += step) {
         const TileAt at = tile_at(P, t);
         for (int kb = 0; kb < P.kblocks; ++kb, ++fill) {
           const unsigned s = fill % P.stages, round = fill / P.stages;
           if (!mbar_wait(&empty[s], (round & 1) ^ 1, &dead)) break;
-          mbar_expect(&full[s], stage_bytes);
           const uint32_t dst = base + s * stage_bytes;
-          tma_load(&map_a, dst, &full[s], kb * kMmaK, kWeightsA ? at.ta * 128 : 0, P.a_groups ? at.g : 0);
-          tma_load(&map_b, dst + a_bytes, &full[s], kb * kMmaK, at.tb * P.nt, P.b_groups ? at.g : 0);
+          const int k = kb * kMmaK, ga = P.a_groups ? at.g : 0, gb = P.b_groups ? at.g : 0;
+          if constexpr (kPair) {
+            const uint32_t bar = in_cta(&full[s], 0);
+            if (rank == 0) mbar_expect(&full[s], 2 * stage_bytes);
+            tma_load_pair(&map_a, dst, bar, k, at.ta * 256 + static_cast<int>(rank) * 128, ga);
+            tma_load_pair(&map_b, dst + a_bytes, bar, k, at.tb * P.nt + static_cast<int>(rank) * b_rows, gb);
+          } else {
+            mbar_expect(&full[s], stage_bytes);
+            tma_load(&map_a, dst, &full[s], k, 0, ga);
+            tma_load(&map_b, dst + a_bytes, &full[s], k, at.tb * P.nt, gb);
+          }
         }
       }
-      if (dead) {
+      if (dead && rank == 0) {
         // copies still in flight land before the CTA's memory goes
         int gave_up = 0;
         for (unsigned f = fill > static_cast<unsigned>(P.stages) ? fill - P.stages : 0; f < fill; ++f)
@@ -282,9 +364,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       unsigned use = 0, n = 0;
-      for (unsigned t = blockIdx.x; t < P.tiles && !dead; t += gridDim.x, ++n) {
+      for (unsigned t = first; t < P.tiles && !dead; t += step, ++n) {
         const unsigned buf = n & 1;
         if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, &dead)) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -294,14 +376,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           if (!mbar_wait(&full[s], round & 1, &dead)) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint64_t da = smem_desc(base + s * stage_bytes), db = smem_desc(base + s * stage_bytes + a_bytes);
-          for (int k = 0; k < kMmaK / 16; ++k) tc_mma(d, da + 2 * k, db + 2 * k, P.idesc, kb > 0 || k > 0);
-          tc_commit(&empty[s]);
+          for (int k = 0; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, kb > 0 || k > 0);
+          tc_commit<kPair>(&empty[s]);
         }
-        tc_commit(&acc_full[buf]);
+        tc_commit<kPair>(&acc_full[buf]);
       }
       if (dead) {
         int gave_up = 0;
-        tc_commit(&drained);
+        tc_commit<kPair>(&drained);
         mbar_wait(&drained, 0, &gave_up);
       }
     }
@@ -310,56 +392,88 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const int et = threadIdx.x - 64;
     float* staging = reinterpret_cast<float*>(smem + P.staging);
     unsigned n = 0;
-    for (unsigned t = blockIdx.x; t < P.tiles; t += gridDim.x, ++n) {
+    for (unsigned t = first; t < P.tiles; t += step, ++n) {
       const TileAt at = tile_at(P, t);
       const unsigned buf = n & 1;
-      const bool ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t acc = tmem + buf * P.nt + (static_cast<uint32_t>(quad * 32) << 16);
       if constexpr (kWeightsA) {
-        const int64_t col = static_cast<int64_t>(at.ta) * 128 + quad * 32 + lane;
+        const int64_t col = static_cast<int64_t>(at.ta) * 256 + rank * 128 + quad * 32 + lane;
+        const bool in = col < P.L.N;
+        const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
+        const bool ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int c = half * 16; c < P.nt; c += 32) {
-          float v[16];
+          float v[16], r[16];
+          const int64_t m0 = static_cast<int64_t>(at.tb) * P.nt + c;
+          const int rows = in ? static_cast<int>(min(static_cast<int64_t>(16), P.L.M - m0)) : 0;
+          if (P.L.res)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = i < rows ? load_residual(P.L, at.g, m0 + i, col) : 0.f;
           __syncwarp();
           tc_load16(acc + c, v);
-          const int64_t m0 = static_cast<int64_t>(at.tb) * P.nt + c;
-          if (col < P.L.N)
-            for (int i = 0; i < 16; ++i)
-              if (m0 + i < P.L.M) finish_value(P.L, at.g, m0 + i, col, ok ? v[i] : NAN);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < rows) finish_value(P.L, at.g, m0 + i, col, ok ? v[i] : NAN, bias, P.L.res ? r[i] : 0.f);
         }
       } else {
         const int cols = min(P.nt, static_cast<int>(P.L.N - static_cast<int64_t>(at.tb) * P.nt));
+        // each thread finishes one column of every fourth token: its residuals come in before the sums do
+        const int c = et % kStageCols, row = et / kStageCols;
+        constexpr int kRows = kEpiWarps * 32 / kStageCols;
+        bool ok = true;
         for (int c0 = 0; c0 < cols; c0 += kStageCols) {
+          const int64_t col = static_cast<int64_t>(at.tb) * P.nt + c0 + c;
+          const bool in = c0 + c < cols;
+          const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
+          float r[128 / kRows];
+          if (P.L.res)
+#pragma unroll
+            for (int i = 0; i < 128 / kRows; ++i)
+              r[i] = in && row + i * kRows < P.L.M ? load_residual(P.L, at.g, row + i * kRows, col) : 0.f;
+          if (c0 == 0) {
+            ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          }
           if (quad * 32 < P.L.M)
-            for (int c = c0 + half * 32; c < min(c0 + half * 32 + 32, P.nt); c += 16) {
+            for (int cc = c0 + half * 32; cc < min(c0 + half * 32 + 32, P.nt); cc += 16) {
               float v[16];
               __syncwarp();
-              tc_load16(acc + c, v);
+              tc_load16(acc + cc, v);
               if (quad * 32 + lane < P.L.M)
                 for (int i = 0; i < 16; ++i)
-                  staging[(quad * 32 + lane) * (kStageCols + 1) + c - c0 + i] = ok ? v[i] : NAN;
+                  staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = ok ? v[i] : NAN;
             }
           asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
-          const int width = min(kStageCols, cols - c0);
-          for (int i = et; i < P.L.M * kStageCols; i += kEpiWarps * 32) {
-            const int m = i / kStageCols, c = i % kStageCols;
-            if (c < width)
-              finish_value(P.L, at.g, m, static_cast<int64_t>(at.tb) * P.nt + c0 + c, staging[m * (kStageCols + 1) + c]);
+#pragma unroll
+          for (int i = 0; i < 128 / kRows; ++i) {
+            const int m = row + i * kRows;
+            if (in && m < P.L.M)
+              finish_value(P.L, at.g, m, col, staging[m * (kStageCols + 1) + c], bias, P.L.res ? r[i] : 0.f);
           }
           asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (lane == 0) {
+        if constexpr (kPair)
+          mbar_arrive_in(in_cta(&acc_empty[buf], 0));
+        else
+          mbar_arrive(&acc_empty[buf]);
+      }
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if constexpr (kPair) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   __syncwarp();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols) : "memory");
+  if (warp == 1) {
+    if constexpr (kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols) : "memory");
+  }
 }
 
 // ------------------------------------------------------------ host
@@ -407,16 +521,18 @@ bool make_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64
 }
 
 // The width of a tile: the one with the least time by this estimate.  A stage
-// (64 entries of K) of 128 x nt products takes 2 nt cycles of the tensor core, and
-// its (rows of A + nt) rows of 128 bytes come in at about 40 bytes a cycle; the
-// SMs take their tiles in waves, and each wave pays for starting and ending.
-int choose_width(int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, int64_t kblocks, int sms) {
+// (64 entries of K) of 128 x nt products takes 2 nt cycles of an SM's tensor
+// core, and the rows of 128 bytes that the SM fetches for it come in at about 46
+// bytes a cycle; the SMs (or pairs of them) take their tiles in waves, and each
+// wave pays for starting and ending.
+int choose_width(bool pair, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, int64_t kblocks, int sms) {
   int best = 16;
   double least = 1e300;
+  const int workers = pair ? std::max(1, sms / 2) : sms;
   for (int nt = 16; nt <= 256; nt += 16) {
     const int64_t tiles = (rows_b + nt - 1) / nt * tiles_a * groups;
-    const int64_t waves = (tiles + sms - 1) / sms;
-    const double stage = std::max(2.0 * nt, (rows_a + nt) * 128 / 40.0);
+    const int64_t waves = (tiles + workers - 1) / workers;
+    const double stage = std::max(2.0 * nt, (rows_a + (pair ? nt / 2 : nt)) * 128 / 46.0);
     const double t = waves * (kblocks * stage + 1500.0);
     if (t < least * 0.999) least = t, best = nt;
   }
@@ -425,26 +541,28 @@ int choose_width(int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, in
 
 template <bool kWeightsA>
 cudaError_t launch_mma(const LinearParams& L, int sms, cudaStream_t st, bool* taken) {
+  constexpr bool kPair = kWeightsA;
   *taken = false;
   MmaParams P = {};
   P.L = L;
   P.kblocks = (L.K + kMmaK - 1) / kMmaK;
   P.ra = kWeightsA ? 128 : (L.M + 7) / 8 * 8;
   const int64_t rows_a = kWeightsA ? L.N : L.M, rows_b = kWeightsA ? L.M : L.N;
-  P.tiles_a = static_cast<int>((rows_a + 127) / 128);
-  P.nt = choose_width(rows_b, P.tiles_a, P.ra, L.groups, P.kblocks, sms);
+  P.tiles_a = static_cast<int>((rows_a + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
+  P.nt = choose_width(kPair, rows_b, P.tiles_a, P.ra, L.groups, P.kblocks, sms);
   P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
   const int64_t tiles = static_cast<int64_t>(P.tiles_a) * P.tiles_b * L.groups;
   if (tiles >= (int64_t{1} << 31)) return cudaSuccess;
   P.tiles = static_cast<unsigned>(tiles);
+  const int b_rows = kPair ? P.nt / 2 : P.nt;
   CUtensorMap map_x, map_w;
   int gx = 0, gw = 0;
-  if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? P.nt : P.ra, &gx) ||
-      !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : P.nt, &gw))
+  if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? b_rows : P.ra, &gx) ||
+      !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : b_rows, &gw))
     return cudaSuccess;
   P.a_groups = kWeightsA ? gw : gx;
   P.b_groups = kWeightsA ? gx : gw;
-  const int stage_bytes = (P.ra + P.nt) * kRowBytes;
+  const int stage_bytes = (P.ra + b_rows) * kRowBytes;
   const int staging = kWeightsA ? 0 : L.M * (kStageCols + 1) * 4;
   // a product reads 128 rows of A from the last stage on: they stay inside the allocation
   const int slack = std::max(0, 128 * kRowBytes - stage_bytes);
@@ -453,15 +571,25 @@ cudaError_t launch_mma(const LinearParams& L, int sms, cudaStream_t st, bool* ta
   const int smem = static_cast<int>(P.staging) + staging;
   P.tmem_cols = 32;
   while (P.tmem_cols < 2 * P.nt) P.tmem_cols *= 2;
-  // fp32 sums, bf16 operands, both K-major, N = nt, M = 128
-  P.idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(P.nt / 8) << 17) | ((128u / 16) << 24);
+  // fp32 sums, bf16 operands, both K-major, N = nt, M = 128 or 256
+  P.idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(P.nt / 8) << 17) | ((kPair ? 16u : 8u) << 24);
   const cudaError_t e =
       cudaFuncSetAttribute(mma_kernel<kWeightsA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, sms));
   *taken = true;
-  mma_kernel<kWeightsA><<<grid, kMmaThreads, smem, st>>>(P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * std::min<int64_t>(tiles, std::max(1, sms / 2))
+                                                 : std::min<int64_t>(tiles, sms)));
+  cfg.blockDim = dim3(kMmaThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, mma_kernel<kWeightsA>, P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
 }
 
 bool valid_dtype(int d) { return d == SV_F32 || d == SV_BF16; }
