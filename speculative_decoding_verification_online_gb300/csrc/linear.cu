@@ -13,6 +13,7 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <type_traits>
 
 #include "device_guard.cuh"
 #include "spec_verify.h"
@@ -36,14 +37,27 @@ __device__ __forceinline__ float load_either(const void* p, int64_t i, int bf16)
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-__device__ __forceinline__ float activate(float z, int act, float cap) {
+template <int kAct>
+__device__ __forceinline__ float activate(float z, float cap) {
+  if constexpr (kAct == SV_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+  if constexpr (kAct == SV_ACT_SILU) return z / (1.f + expf(-z));
+  if constexpr (kAct == SV_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+  if constexpr (kAct == SV_ACT_GELU_TANH) return z / (1.f + expf(-1.59576912f * (z + 0.044715f * z * z * z)));
+  if constexpr (kAct == SV_ACT_SOFTCAP) return cap * tanhf(z / cap);
+  return z;
+}
+
+// f with the activation as a constant: code that a call does not use is not fetched either
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
   switch (act) {
-    case SV_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-    case SV_ACT_SILU: return z / (1.f + expf(-z));
-    case SV_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    case SV_ACT_GELU_TANH: return 0.5f * z * (1.f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-    case SV_ACT_SOFTCAP: return cap * tanhf(z / cap);
-    default: return z;
+    case SV_ACT_RELU: f(std::integral_constant<int, SV_ACT_RELU>()); break;
+    case SV_ACT_SILU: f(std::integral_constant<int, SV_ACT_SILU>()); break;
+    case SV_ACT_GELU: f(std::integral_constant<int, SV_ACT_GELU>()); break;
+    case SV_ACT_GELU_TANH: f(std::integral_constant<int, SV_ACT_GELU_TANH>()); break;
+    case SV_ACT_SOFTCAP: f(std::integral_constant<int, SV_ACT_SOFTCAP>()); break;
+    default: f(std::integral_constant<int, SV_ACT_NONE>());
   }
 }
 
@@ -56,12 +70,9 @@ __device__ __forceinline__ float load_residual(const LinearParams& P, int g, int
 }
 
 // The sum's way out: the one rounding to bf16, where y is bf16, is the last step.
-__device__ __forceinline__ void finish_value(const LinearParams& P, int g, int64_t m, int64_t n, float z, float bias,
-                                             float res) {
-  if (P.bias) z += bias;
-  z = activate(z, P.act, P.cap);
-  if (P.res) z += res;
-  const int64_t at = g * P.y_group + m * P.y_row + n;
+template <int kAct>
+__device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, float z, float bias, float res) {
+  z = activate<kAct>(z + bias, P.cap) + res;
   if (P.y_bf16)
     static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16(z);
   else
@@ -94,12 +105,15 @@ __global__ void __launch_bounds__(256) plain_kernel(LinearParams P) {
           for (int j = 0; j < 4; ++j) acc[i][j] += sx[kk][ty + 16 * i] * sw[kk][tx + 16 * j];
       __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j)
-        if (m0 + ty + 16 * i < P.M && n0 + tx + 16 * j < P.N) {
-          const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-          finish_value(P, g, m, n, acc[i][j], load_bias(P, g, n), load_residual(P, g, m, n));
-        }
+    with_activation(P.act, [&](auto act) {
+      for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j)
+          if (m0 + ty + 16 * i < P.M && n0 + tx + 16 * j < P.N) {
+            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
+            finish_value<act.value>(P, g * P.y_group + m * P.y_row + n, acc[i][j], load_bias(P, g, n),
+                                    load_residual(P, g, m, n));
+          }
+    });
   }
 }
 
@@ -336,24 +350,30 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      unsigned fill = 0;
+      // stage and phase go round by counting: a division by the number of stages
+      // costs more than everything else that a stage needs
+      unsigned s = 0, phase = 1, fill = 0;
+      const uint32_t leader = kPair ? in_cta(full, 0) : 0;
       for (unsigned t = first; t < P.tiles && !dead; t += step) {
         const TileAt at = tile_at(P, t);
-        for (int kb = 0; kb < P.kblocks; ++kb, ++fill) {
-          const unsigned s = fill % P.stages, round = fill / P.stages;
-          if (!mbar_wait(&empty[s], (round & 1) ^ 1, &dead)) break;
+        const int ga = P.a_groups ? at.g : 0, gb = P.b_groups ? at.g : 0;
+        const int row_a = kPair ? at.ta * 256 + static_cast<int>(rank) * 128 : 0;
+        const int row_b = at.tb * P.nt + (kPair ? static_cast<int>(rank) * b_rows : 0);
+        for (int kb = 0, k = 0; kb < P.kblocks; ++kb, k += kMmaK) {
+          if (!mbar_wait(&empty[s], phase, &dead)) break;
           const uint32_t dst = base + s * stage_bytes;
-          const int k = kb * kMmaK, ga = P.a_groups ? at.g : 0, gb = P.b_groups ? at.g : 0;
           if constexpr (kPair) {
-            const uint32_t bar = in_cta(&full[s], 0);
+            const uint32_t bar = leader + s * 8;
             if (rank == 0) mbar_expect(&full[s], 2 * stage_bytes);
-            tma_load_pair(&map_a, dst, bar, k, at.ta * 256 + static_cast<int>(rank) * 128, ga);
-            tma_load_pair(&map_b, dst + a_bytes, bar, k, at.tb * P.nt + static_cast<int>(rank) * b_rows, gb);
+            tma_load_pair(&map_a, dst, bar, k, row_a, ga);
+            tma_load_pair(&map_b, dst + a_bytes, bar, k, row_b, gb);
           } else {
             mbar_expect(&full[s], stage_bytes);
             tma_load(&map_a, dst, &full[s], k, 0, ga);
-            tma_load(&map_b, dst + a_bytes, &full[s], k, at.tb * P.nt, gb);
+            tma_load(&map_b, dst + a_bytes, &full[s], k, row_b, gb);
           }
+          ++fill;
+          if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
         }
       }
       if (dead && rank == 0) {
@@ -365,19 +385,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      unsigned use = 0, n = 0;
+      unsigned s = 0, phase = 0, n = 0;
+      const uint64_t desc_a = smem_desc(base), desc_b = smem_desc(base + a_bytes);
+      const unsigned desc_step = stage_bytes / 16;
       for (unsigned t = first; t < P.tiles && !dead; t += step, ++n) {
         const unsigned buf = n & 1;
         if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, &dead)) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + buf * P.nt;
-        for (int kb = 0; kb < P.kblocks; ++kb, ++use) {
-          const unsigned s = use % P.stages, round = use / P.stages;
-          if (!mbar_wait(&full[s], round & 1, &dead)) break;
+        for (int kb = 0; kb < P.kblocks; ++kb) {
+          if (!mbar_wait(&full[s], phase, &dead)) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t da = smem_desc(base + s * stage_bytes), db = smem_desc(base + s * stage_bytes + a_bytes);
-          for (int k = 0; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, kb > 0 || k > 0);
+          const uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
+          tc_mma<kPair>(d, da, db, P.idesc, kb > 0);
+#pragma unroll
+          for (int k = 1; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, true);
           tc_commit<kPair>(&empty[s]);
+          if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
         }
         tc_commit<kPair>(&acc_full[buf]);
       }
@@ -402,56 +426,74 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
         const bool ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int c = half * 16; c < P.nt; c += 32) {
-          float v[16], r[16];
-          const int64_t m0 = static_cast<int64_t>(at.tb) * P.nt + c;
-          const int rows = in ? static_cast<int>(min(static_cast<int64_t>(16), P.L.M - m0)) : 0;
-          if (P.L.res)
+        with_activation(P.L.act, [&](auto act) {
+#pragma unroll 1
+          for (int c = half * 16; c < P.nt; c += 32) {
+            float v[16], r[16];
+            const int64_t m0 = static_cast<int64_t>(at.tb) * P.nt + c;
+            const int rows = in ? static_cast<int>(min(static_cast<int64_t>(16), P.L.M - m0)) : 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = i < rows ? load_residual(P.L, at.g, m0 + i, col) : 0.f;
-          __syncwarp();
-          tc_load16(acc + c, v);
+            for (int i = 0; i < 16; ++i)
+              r[i] = P.L.res && i < rows ? load_residual(P.L, at.g, m0 + i, col) : 0.f;
+            __syncwarp();
+            tc_load16(acc + c, v);
+            int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + col;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i < rows) finish_value(P.L, at.g, m0 + i, col, ok ? v[i] : NAN, bias, P.L.res ? r[i] : 0.f);
-        }
+            for (int i = 0; i < 16; ++i, to += P.L.y_row)
+              if (i < rows) finish_value<act.value>(P.L, to, ok ? v[i] : NAN, bias, r[i]);
+          }
+        });
       } else {
         const int cols = min(P.nt, static_cast<int>(P.L.N - static_cast<int64_t>(at.tb) * P.nt));
-        // each thread finishes one column of every fourth token: its residuals come in before the sums do
+        // each thread finishes one column of every fourth token, eight tokens at a time:
+        // the first ones' residuals come in before the sums do
         const int c = et % kStageCols, row = et / kStageCols;
         constexpr int kRows = kEpiWarps * 32 / kStageCols;
         bool ok = true;
-        for (int c0 = 0; c0 < cols; c0 += kStageCols) {
-          const int64_t col = static_cast<int64_t>(at.tb) * P.nt + c0 + c;
-          const bool in = c0 + c < cols;
-          const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
-          float r[128 / kRows];
-          if (P.L.res)
+        with_activation(P.L.act, [&](auto act) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < cols; c0 += kStageCols) {
+            const int64_t col = static_cast<int64_t>(at.tb) * P.nt + c0 + c;
+            const int rows = c0 + c < cols ? P.L.M : 0;
+            const float bias = rows ? load_bias(P.L, at.g, col) : 0.f;
+            float r[8];
+            auto residuals = [&](int m0) {
 #pragma unroll
-            for (int i = 0; i < 128 / kRows; ++i)
-              r[i] = in && row + i * kRows < P.L.M ? load_residual(P.L, at.g, row + i * kRows, col) : 0.f;
-          if (c0 == 0) {
-            ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          }
-          if (quad * 32 < P.L.M)
-            for (int cc = c0 + half * 32; cc < min(c0 + half * 32 + 32, P.nt); cc += 16) {
-              float v[16];
-              __syncwarp();
-              tc_load16(acc + cc, v);
-              if (quad * 32 + lane < P.L.M)
-                for (int i = 0; i < 16; ++i)
-                  staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = ok ? v[i] : NAN;
+              for (int i = 0; i < 8; ++i)
+                r[i] = P.L.res && m0 + i * kRows < rows ? load_residual(P.L, at.g, m0 + i * kRows, col) : 0.f;
+            };
+            residuals(row);
+            if (c0 == 0) {
+              ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
-          asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+            if (quad * 32 < P.L.M)
+#pragma unroll 1
+              for (int cc = c0 + half * 32; cc < min(c0 + half * 32 + 32, P.nt); cc += 16) {
+                float v[16];
+                __syncwarp();
+                tc_load16(acc + cc, v);
+                if (quad * 32 + lane < P.L.M)
 #pragma unroll
-          for (int i = 0; i < 128 / kRows; ++i) {
-            const int m = row + i * kRows;
-            if (in && m < P.L.M)
-              finish_value(P.L, at.g, m, col, staging[m * (kStageCols + 1) + c], bias, P.L.res ? r[i] : 0.f);
+                  for (int i = 0; i < 16; ++i)
+                    staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = ok ? v[i] : NAN;
+              }
+            asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+#pragma unroll 1
+            for (int m0 = row; m0 < P.L.M; m0 += 8 * kRows) {
+              if (m0 != row) residuals(m0);
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                v[i] = m0 + i * kRows < rows ? staging[(m0 + i * kRows) * (kStageCols + 1) + c] : 0.f;
+              int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + col;
+#pragma unroll
+              for (int i = 0; i < 8; ++i, to += kRows * P.L.y_row)
+                if (m0 + i * kRows < rows) finish_value<act.value>(P.L, to, v[i], bias, r[i]);
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
           }
-          asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
-        }
+        });
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
