@@ -209,6 +209,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, volati
   }
 }
 
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  unsigned e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
   asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
@@ -348,19 +355,22 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
 
+  // Warps 0 and 1 go through their loops as whole warps, and one lane that elect
+  // picks issues: with a branch on the lane instead the compiler takes the
+  // operands for different in every lane, and an issue costs several times as much.
   if (warp == 0) {
-    if (lane == 0) {
-      // stage and phase go round by counting: a division by the number of stages
-      // costs more than everything else that a stage needs
-      unsigned s = 0, phase = 1, fill = 0;
-      const uint32_t leader = kPair ? in_cta(full, 0) : 0;
-      for (unsigned t = first; t < P.tiles && !dead; t += step) {
-        const TileAt at = tile_at(P, t);
-        const int ga = P.a_groups ? at.g : 0, gb = P.b_groups ? at.g : 0;
-        const int row_a = kPair ? at.ta * 256 + static_cast<int>(rank) * 128 : 0;
-        const int row_b = at.tb * P.nt + (kPair ? static_cast<int>(rank) * b_rows : 0);
-        for (int kb = 0, k = 0; kb < P.kblocks; ++kb, k += kMmaK) {
-          if (!mbar_wait(&empty[s], phase, &dead)) break;
+    // stage and phase go round by counting: a division by the number of stages
+    // costs more than everything else that a stage needs
+    unsigned s = 0, phase = 1, fill = 0;
+    const uint32_t leader = kPair ? in_cta(full, 0) : 0;
+    for (unsigned t = first; t < P.tiles && !dead; t += step) {
+      const TileAt at = tile_at(P, t);
+      const int ga = P.a_groups ? at.g : 0, gb = P.b_groups ? at.g : 0;
+      const int row_a = kPair ? at.ta * 256 + static_cast<int>(rank) * 128 : 0;
+      const int row_b = at.tb * P.nt + (kPair ? static_cast<int>(rank) * b_rows : 0);
+      for (int kb = 0, k = 0; kb < P.kblocks; ++kb, k += kMmaK) {
+        if (!mbar_wait(&empty[s], phase, &dead)) break;
+        if (elect_one()) {
           const uint32_t dst = base + s * stage_bytes;
           if constexpr (kPair) {
             const uint32_t bar = leader + s * 8;
@@ -372,19 +382,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             tma_load(&map_a, dst, &full[s], k, 0, ga);
             tma_load(&map_b, dst + a_bytes, &full[s], k, row_b, gb);
           }
-          ++fill;
-          if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
         }
-      }
-      if (dead && rank == 0) {
-        // copies still in flight land before the CTA's memory goes
-        int gave_up = 0;
-        for (unsigned f = fill > static_cast<unsigned>(P.stages) ? fill - P.stages : 0; f < fill; ++f)
-          mbar_wait(&full[f % P.stages], (f / P.stages) & 1, &gave_up);
+        __syncwarp();
+        ++fill;
+        if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
       }
     }
+    if (dead && rank == 0) {
+      // copies still in flight land before the CTA's memory goes
+      int gave_up = 0;
+      for (unsigned f = fill > static_cast<unsigned>(P.stages) ? fill - P.stages : 0; f < fill; ++f)
+        mbar_wait(&full[f % P.stages], (f / P.stages) & 1, &gave_up);
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       unsigned s = 0, phase = 0, n = 0;
       const uint64_t desc_a = smem_desc(base), desc_b = smem_desc(base + a_bytes);
       const unsigned desc_step = stage_bytes / 16;
@@ -396,18 +407,22 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         for (int kb = 0; kb < P.kblocks; ++kb) {
           if (!mbar_wait(&full[s], phase, &dead)) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
-          tc_mma<kPair>(d, da, db, P.idesc, kb > 0);
+          if (elect_one()) {
+            const uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
+            tc_mma<kPair>(d, da, db, P.idesc, kb > 0);
 #pragma unroll
-          for (int k = 1; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, true);
-          tc_commit<kPair>(&empty[s]);
+            for (int k = 1; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, true);
+            tc_commit<kPair>(&empty[s]);
+            if (kb == P.kblocks - 1) tc_commit<kPair>(&acc_full[buf]);
+          }
+          __syncwarp();
           if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
         }
-        tc_commit<kPair>(&acc_full[buf]);
       }
       if (dead) {
         int gave_up = 0;
-        tc_commit<kPair>(&drained);
+        if (elect_one()) tc_commit<kPair>(&drained);
+        __syncwarp();
         mbar_wait(&drained, 0, &gave_up);
       }
     }
