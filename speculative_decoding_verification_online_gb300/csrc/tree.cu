@@ -12,10 +12,18 @@
 //
 // A pick among V tokens hangs on the last digits of its prefix sums: with
 // sums good to 1e-7 one pick in a hundred would land beside the token that
-// exact sums give.  Weights and sums are held in 64 bits.
+// exact sums give.  fp64 has two lanes an SM and clock here, so the row sums are
+// carried as pairs of floats (error-free sums and products, about 48 bits); one
+// warp does the few scalar steps in fp64.
+//
+// A sequence is a cluster of up to eight CTAs, each with a part of the row; every
+// CTA's first warp takes the same walk, and a sum over a row is one exchange of
+// partial sums through the cluster's shared memory.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstdlib>
 #include <initializer_list>
 
 #include "device_guard.cuh"
@@ -24,9 +32,12 @@
 namespace sv {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kTreeThreads = 512;
 constexpr int kTreeWarps = kTreeThreads / 32;
-constexpr int kTreeChunk = 1024;  // entries of a row whose weight is kept as one sum
+constexpr int kTreeCluster = 8;  // CTAs of a sequence at most
+constexpr int kTreeChunk = 512;  // entries of a row whose weight is kept as one sum: 16 a lane
 
 struct TreeParams {
   const float* p;
@@ -43,111 +54,203 @@ struct TreeParams {
 
 struct TreeShared {
   int32_t tok[SV_MAX_NODES], par[SV_MAX_NODES], drow[SV_MAX_NODES + 1];
-  float px[SV_MAX_NODES], qx[SV_MAX_NODES], u[SV_MAX_NODES];
-  int8_t flag[SV_MAX_NODES];
-  float alpha[SV_MAX_NODES];
-  double warp_sum[kTreeWarps];
-  double total;
-  int pick;
-};
-
-// the tokens refused at a node without a draft row
-struct Refused {
-  const TreeShared& s;
-  int n, cur;
-  __device__ bool holds(int v) const {
-    for (int i = 0; i < n; ++i)
-      if (s.par[i] == cur && s.tok[i] == v && s.flag[i] == SV_FLAG_REJECT) return true;
-    return false;
-  }
-};
-
-struct Rest {
-  const float* p;
-  const float* q;  // null: no draft row, or c is 0
+  int32_t first[SV_MAX_NODES + 1], next[SV_MAX_NODES];  // children of node i - 1; the sibling after node i
+  float px[SV_MAX_NODES], qx[SV_MAX_NODES], u[SV_MAX_NODES], alpha[SV_MAX_NODES];
+  int32_t refused[SV_MAX_NODES];  // distinct tokens refused at a node without a draft row
+  int8_t flag[SV_MAX_NODES], again[SV_MAX_NODES];
+  double slot[2][kTreeCluster];  // the CTAs' sums of a pass, by its parity
+  // what the first warp asks of the others
+  const float* row_p;
+  const float* row_q;  // null: c is 0
   double c;
-  __device__ double operator()(int v) const {
-    const double r = q ? static_cast<double>(p[v]) - c * static_cast<double>(q[v]) : static_cast<double>(p[v]);
-    return r < 0.0 ? 0.0 : r;  // a NaN stays
+  int n_refused, work;
+};
+
+enum { kTreeSum = 0, kTreePick = 1, kTreeEnd = 2 };
+
+// s + l, s the nearest float: sums of floats without losing what does not fit
+struct Pair {
+  float s, l;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, z = t - s;
+    l += (s - (t - z)) + (x - z);
+    s = t;
+  }
+  __device__ __forceinline__ void add(const Pair& o) {
+    add(o.s);
+    l += o.l;
   }
 };
 
-__device__ __forceinline__ double warp_total(double x) {
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+// (p - (c + cl) q)+ onto a sum; a NaN stays
+__device__ __forceinline__ void add_rest(Pair& sum, float p, float q, float c, float cl) {
+  const float h = __fmul_rn(c, q);  // not to be fused into the difference below
+  const float hl = fmaf(cl, q, fmaf(c, q, -h));
+  const float d = p - h, z = d - p;
+  const float dl = ((p - (d - z)) - (h + z)) - hl;
+  if (!(d + dl <= 0.f)) {
+    sum.add(d);
+    sum.l += dl;
+  }
+}
+
+__device__ __forceinline__ Pair warp_total(Pair x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x.add(Pair{__shfl_xor_sync(~0u, x.s, o), __shfl_xor_sync(~0u, x.l, o)});
   return x;
 }
 
-// the weight of every chunk into chunk_sum, their total returned to every thread
-__device__ double row_sums(TreeShared& s, double* chunk_sum, const Rest& rest, const Refused* refused, int V,
-                           int nchunk) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double mine = 0.0;
-  for (int ch = warp; ch < nchunk; ch += kTreeWarps) {
-    const int lo = ch * kTreeChunk, hi = min(lo + kTreeChunk, V);
-    double sum = 0.0;
-    for (int v = lo + lane; v < hi; v += 32) sum += refused && refused->holds(v) ? 0.0 : rest(v);
-    sum = warp_total(sum);
-    if (lane == 0) chunk_sum[ch] = sum;
-    mine += sum;
-  }
-  if (lane == 0) s.warp_sum[warp] = mine;
-  __syncthreads();
-  double t = 0.0;
-  for (int w = 0; w < kTreeWarps; ++w) t += s.warp_sum[w];
-  __syncthreads();
-  return t;
+__device__ __forceinline__ double rest_at(const TreeShared& s, int v) {
+  for (int i = 0; i < s.n_refused; ++i)
+    if (s.refused[i] == v) return 0.0;
+  const double p = s.row_p[v];
+  const double r = s.row_q ? fma(-s.c, static_cast<double>(s.row_q[v]), p) : p;
+  return r < 0.0 ? 0.0 : r;
 }
 
-// the smallest v whose inclusive prefix sum exceeds y (the last v with weight
-// when rounding leaves none): warp 0
-__device__ int pick(const double* chunk_sum, const Rest& rest, const Refused* refused, int V, int nchunk, double y) {
+// four neighbouring entries of a row; nothing beyond its end
+template <bool kVec>
+__device__ __forceinline__ float4 load4(const float* row, int v, int V) {
+  if constexpr (kVec) {
+    if (v + 4 <= V) return *reinterpret_cast<const float4*>(row + v);
+  } else if (v + 4 <= V) {
+    return make_float4(row[v], row[v + 1], row[v + 2], row[v + 3]);
+  }
+  return make_float4(v < V ? row[v] : 0.f, v + 1 < V ? row[v + 1] : 0.f, v + 2 < V ? row[v + 2] : 0.f, 0.f);
+}
+
+// the weight of each of this CTA's chunks into chunk_sum: every warp
+template <bool kVec>
+__device__ __forceinline__ void chunk_sums(const TreeShared& s, double* chunk_sum, int V, int first, int last) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float c = static_cast<float>(s.c), cl = static_cast<float>(s.c - static_cast<double>(c));
+  for (int ch = first + warp; ch < last; ch += kTreeWarps) {
+    Pair sum[4] = {};
+    const int v0 = ch * kTreeChunk + lane * 4;
+    float4 p[4], q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = load4<kVec>(s.row_p, v0 + j * 128, V);
+    if (s.row_q) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = load4<kVec>(s.row_q, v0 + j * 128, V);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        add_rest(sum[0], p[j].x, q[j].x, c, cl);
+        add_rest(sum[1], p[j].y, q[j].y, c, cl);
+        add_rest(sum[2], p[j].z, q[j].z, c, cl);
+        add_rest(sum[3], p[j].w, q[j].w, c, cl);
+      }
+    } else {
+      bool hit = false;
+      for (int i = 0; i < s.n_refused; ++i) hit |= s.refused[i] / kTreeChunk == ch;
+      if (hit)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          for (int i = 0; i < s.n_refused; ++i) {
+            const int at = s.refused[i] - (v0 + j * 128);
+            if (at == 0) p[j].x = 0.f;
+            if (at == 1) p[j].y = 0.f;
+            if (at == 2) p[j].z = 0.f;
+            if (at == 3) p[j].w = 0.f;
+          }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[0].add(fmaxf(p[j].x, 0.f) + (p[j].x - p[j].x));  // a NaN or an infinity stays
+        sum[1].add(fmaxf(p[j].y, 0.f) + (p[j].y - p[j].y));
+        sum[2].add(fmaxf(p[j].z, 0.f) + (p[j].z - p[j].z));
+        sum[3].add(fmaxf(p[j].w, 0.f) + (p[j].w - p[j].w));
+      }
+    }
+    sum[0].add(sum[1]);
+    sum[2].add(sum[3]);
+    sum[0].add(sum[2]);
+    const Pair t = warp_total(sum[0]);
+    if (lane == 0) chunk_sum[ch - first] = static_cast<double>(t.s) + static_cast<double>(t.l);
+  }
+}
+
+__device__ __forceinline__ double scan(double x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double up = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += up;
+  }
+  return x;
+}
+
+// The smallest v of this CTA's chunks whose inclusive prefix sum exceeds y, or the last v with weight when rounding
+// leaves none: the first warp.
+__device__ int pick(const TreeShared& s, const double* chunk_sum, int V, int first, int last, double y) {
   const int lane = threadIdx.x & 31;
   double before = 0.0;
-  int ch = -1, last = 0;
-  for (int i = 0; i < nchunk; ++i) {
-    const double sum = chunk_sum[i];
-    if (sum > 0.0) last = i;
-    if (before + sum > y) {
-      ch = i;
-      break;
+  int ch = -1, heavy = first;
+  for (int i0 = first; i0 < last && ch < 0; i0 += 32) {
+    const int i = i0 + lane;
+    const double w = i < last ? chunk_sum[i - first] : 0.0;
+    const double incl = before + scan(w);
+    const unsigned past = __ballot_sync(~0u, w > 0.0 && incl > y), some = __ballot_sync(~0u, w > 0.0);
+    if (some) heavy = i0 + 31 - __clz(some);
+    if (past) {
+      ch = i0 + __ffs(past) - 1;
+      before = __shfl_sync(~0u, incl - w, __ffs(past) - 1);
+    } else {
+      before = __shfl_sync(~0u, incl, 31);
     }
-    before += sum;
   }
   if (ch < 0) {
-    // every chunk's sum is at or below y: the last weight of the last chunk that has one
-    ch = last;
-    before = 0.0;
+    ch = heavy;
     y = INFINITY;
   }
-  const int lo = ch * kTreeChunk, hi = min(lo + kTreeChunk, V);
-  int found = -1, last_v = -1;
-  for (int v0 = lo; v0 < hi && found < 0; v0 += 32) {
-    const int v = v0 + lane;
-    const double w = v < hi && !(refused && refused->holds(v)) ? rest(v) : 0.0;
-    double incl = w;
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += up;
+  // 16 neighbours a lane
+  constexpr int kRun = kTreeChunk / 32;
+  const int v0 = ch * kTreeChunk + lane * kRun;
+  double w[kRun], mine = 0.0;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) w[i] = v0 + i < V ? rest_at(s, v0 + i) : 0.0;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) mine += w[i];
+  const double incl = before + scan(mine);
+  const unsigned past = __ballot_sync(~0u, mine > 0.0 && incl > y), some = __ballot_sync(~0u, mine > 0.0);
+  const int owner = past ? __ffs(past) - 1 : 31 - __clz(some);
+  int v = -1;
+  if (lane == owner) {
+    double sum = incl - mine;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      sum += w[i];
+      if (w[i] > 0.0 && (v < 0 || !past)) v = v0 + i;
+      if (past && w[i] > 0.0 && sum <= y) v = -1;
     }
-    const unsigned past = __ballot_sync(~0u, w > 0.0 && before + incl > y), some = __ballot_sync(~0u, w > 0.0);
-    if (past) found = v0 + __ffs(past) - 1;
-    if (some) last_v = v0 + 31 - __clz(some);
-    before += __shfl_sync(~0u, incl, 31);
+    if (v < 0)  // rounding: the lane's last weight
+#pragma unroll
+      for (int i = 0; i < kRun; ++i)
+        if (w[i] > 0.0) v = v0 + i;
   }
-  return found >= 0 ? found : last_v;
+  return __shfl_sync(~0u, v, owner);
 }
 
-__global__ void __launch_bounds__(kTreeThreads) tree_kernel(TreeParams P) {
+template <bool kVec>
+__global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_constant__ TreeParams P) {
   extern __shared__ double chunk_sum[];
   __shared__ TreeShared s;
-  const int b = blockIdx.x, tid = threadIdx.x;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
+  cluster.barrier_arrive();  // every CTA of the cluster runs before any writes into another
+  const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31;
+  const int first = static_cast<int>(static_cast<int64_t>(P.nchunk) * rank / ctas);
+  const int last = static_cast<int>(static_cast<int64_t>(P.nchunk) * (rank + 1) / ctas);
   const int start = P.node_start[b], end = P.node_start[b + 1];
   const bool inside = start >= 0 && end >= start && end <= P.total_nodes;
   const bool range = inside && end - start <= P.max_nodes;
   const int n = range ? end - start : 0;
   const int64_t root = static_cast<int64_t>(start) + b;
   int bad = !range;
-  for (int i = tid; i < n; i += kTreeThreads) {
+  for (int i = tid; range && i <= n; i += kTreeThreads) {
+    s.drow[i] = P.draft_row[root + i];
+    s.first[i] = SV_MAX_NODES;
+    bad |= s.drow[i] < -1 || s.drow[i] >= P.draft_rows;
+    if (i == n) break;
     s.tok[i] = P.tokens[start + i];
     s.par[i] = P.parent[start + i];
     s.u[i] = P.u_accept[start + i];
@@ -155,90 +258,183 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(TreeParams P) {
     s.alpha[i] = 0.f;
     bad |= s.tok[i] < 0 || s.tok[i] >= P.V || s.par[i] < -1 || s.par[i] >= i;
   }
-  for (int i = tid; range && i <= n; i += kTreeThreads) {
-    s.drow[i] = P.draft_row[root + i];
-    bad |= s.drow[i] < -1 || s.drow[i] >= P.draft_rows;
-  }
   bad = __syncthreads_or(bad);
   if (!bad) {
     for (int i = tid; i < n; i += kTreeThreads) {
-      int depth = 1;
-      for (int a = s.par[i]; a >= 0; a = s.par[a]) ++depth;
-      bad |= depth > P.max_depth;
-      const int d = s.drow[s.par[i] + 1];
-      s.px[i] = P.p[(root + 1 + s.par[i]) * P.p_stride + s.tok[i]];
-      s.qx[i] = d < 0 ? 1.f : P.q[d * P.q_stride + s.tok[i]];
+      const int par = s.par[i], tok = s.tok[i], d = s.drow[par + 1];
+      s.px[i] = P.p[(root + 1 + par) * P.p_stride + tok];
+      s.qx[i] = d < 0 ? 1.f : P.q[d * P.q_stride + tok];
+      atomicMin(&s.first[par + 1], i);
+      int next = SV_MAX_NODES, again = 0;
+      for (int j = 0; j < n; ++j)
+        if (s.par[j] == par) {
+          if (j > i) next = min(next, j);
+          if (j < i && s.tok[j] == tok) again = 1;
+        }
+      s.next[i] = next;
+      s.again[i] = static_cast<int8_t>(again);
+      if (n > P.max_depth) {
+        int depth = 1;
+        for (int a = par; a >= 0; a = s.par[a]) ++depth;
+        bad |= depth > P.max_depth;
+      }
     }
     bad = __syncthreads_or(bad);
   }
 
-  // the walk: every thread takes the same steps; thread 0 writes what they leave
-  int cur = -1, len = 0, refused = 0, tested = 0, offered = 0;  // offered: at cur
-  double c = 0.0, Z = 1.0, mass = 0.0;
-  for (int i = 0; i < n && !bad; ++i) {
-    if (s.par[i] != cur) continue;
-    const bool bare = s.drow[cur + 1] < 0;
-    const double qx = s.qx[i], px = s.px[i];
-    if (!(px >= 0.0 && px < INFINITY && qx >= 0.0 && qx < INFINITY)) {
-      bad = 1;
-      break;
-    }
-    double r = bare ? px : fma(-c, qx, px);
-    if (bare)
-      for (int j = 0; j < i; ++j)
-        if (s.par[j] == cur && s.tok[j] == s.tok[i]) r = 0.0;  // offered here before, so refused
-    if (r < 0.0) r = 0.0;
-    const double w = bare || P.replacement ? 1.0 : fmax(1.0 - mass, qx);
-    const double most = qx * Z;
-    const bool yes = r > 0.0 && s.u[i] * most <= r * w;
-    if (tid == 0) {
-      s.alpha[i] = most > 0.0 ? static_cast<float>(fmin(1.0, r * w / most)) : (r > 0.0 ? 1.f : 0.f);
-      s.flag[i] = yes ? SV_FLAG_ACCEPT : SV_FLAG_REJECT;
-    }
-    ++tested;
-    ++offered;
-    if (yes) {
-      if (tid == 0 && P.path) P.path[static_cast<int64_t>(b) * P.max_depth + len] = i;
-      if (tid == 0) P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + len] = s.tok[i];
-      ++len;
-      cur = i, c = 0.0, Z = 1.0, mass = 0.0, offered = 0;
-      continue;
-    }
-    ++refused;
-    mass += qx;
-    if (bare) {
-      Z -= r;
-    } else {
-      if (w > 0.0) c = fmin(c + Z / w, 1e30);
-      const Rest rest = {P.p + (root + 1 + cur) * P.p_stride, P.q + s.drow[cur + 1] * P.q_stride, c};
-      Z = row_sums(s, chunk_sum, rest, nullptr, P.V, P.nchunk);
-      if (!(Z < INFINITY)) bad = 1;
-    }
-  }
-  __syncthreads();
+  cluster.barrier_wait();
 
-  int degenerate = 0;
-  if (!bad) {
-    const float* p = P.p + (root + 1 + cur) * P.p_stride;
-    const bool bare = s.drow[cur + 1] < 0;
-    const Refused here = {s, n, cur};
-    const Refused* ref = bare ? &here : nullptr;
-    Rest rest = {p, bare || c == 0.0 ? nullptr : P.q + s.drow[cur + 1] * P.q_stride, c};
-    double total = row_sums(s, chunk_sum, rest, ref, P.V, P.nchunk);
-    if (total == 0.0) {
-      // nothing is left: the node's own row
-      degenerate = 1;
-      rest.q = nullptr;
-      ref = nullptr;
-      total = row_sums(s, chunk_sum, rest, ref, P.V, P.nchunk);
+  // The walk: the first warp of every CTA takes the same steps, and stops where a sum over a row is needed.
+  int cur = -1, child = bad ? SV_MAX_NODES : s.first[0];
+  int len = 0, refused = 0, tested = 0, offered = 0, degenerate = 0, pass = 0;  // offered: children of cur
+  double c = 0.0, Z = 1.0, mass = 0.0;
+  bool summed = false, closing = false;  // chunk_sum is that of cur and c; the sum for the pick is under way
+  if (n == 0) child = SV_MAX_NODES;
+  for (;;) {
+    if (tid < 32) {
+      int work = bad ? kTreeEnd : -1;
+      bool bare = bad || s.drow[cur + 1] < 0;
+      if (work < 0 && pass > 0) {
+        // what the last pass was for
+        double t = 0.0;
+        for (int r = 0; r < ctas; ++r) t += s.slot[(pass - 1) & 1][r];
+        Z = t;
+        if (!(t >= 0.0 && t < INFINITY)) bad = 1, work = kTreeEnd;
+        if (closing && work < 0) {
+          if (t > 0.0) {
+            work = kTreePick;
+          } else if (degenerate) {
+            bad = 1, work = kTreeEnd;  // the node's own row has no mass
+          } else {
+            degenerate = 1;
+            c = 0.0;
+            if (lane == 0) s.row_q = nullptr, s.c = 0.0, s.n_refused = 0;
+            work = kTreeSum;
+          }
+        }
+      }
+      while (work < 0) {
+        if (child >= SV_MAX_NODES) {
+          // no child is left: the token comes from what is left of this row
+          closing = true;
+          if (summed && Z > 0.0) {
+            work = kTreePick;
+          } else {
+            if (summed) degenerate = 1, c = 0.0;
+            if (lane == 0) {
+              s.row_p = P.p + (root + 1 + cur) * P.p_stride;
+              s.row_q = nullptr;
+              s.c = 0.0;
+              int k = 0;
+              if (bare)
+                for (int i = s.first[cur + 1]; i < SV_MAX_NODES && n > 0; i = s.next[i])
+                  if (!s.again[i]) s.refused[k++] = s.tok[i];
+              s.n_refused = k;
+            }
+            work = kTreeSum;
+          }
+          break;
+        }
+        const int i = child;
+        const double qx = s.qx[i], px = s.px[i];
+        if (!(px >= 0.0 && px < INFINITY && qx >= 0.0 && qx < INFINITY)) {
+          bad = 1, work = kTreeEnd;
+          break;
+        }
+        double r = bare ? (s.again[i] ? 0.0 : px) : fma(-c, qx, px);
+        if (r < 0.0) r = 0.0;
+        const double w = bare || P.replacement ? 1.0 : fmax(1.0 - mass, qx);
+        const double most = qx * Z;
+        const bool yes = r > 0.0 && s.u[i] * most <= r * w;
+        if (lane == 0 && rank == 0) {
+          s.alpha[i] = most > 0.0 ? static_cast<float>(fmin(1.0, r * w / most)) : (r > 0.0 ? 1.f : 0.f);
+          s.flag[i] = yes ? SV_FLAG_ACCEPT : SV_FLAG_REJECT;
+          if (yes) {
+            if (P.path) P.path[static_cast<int64_t>(b) * P.max_depth + len] = i;
+            P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + len] = s.tok[i];
+          }
+        }
+        ++tested;
+        ++offered;
+        if (yes) {
+          ++len;
+          cur = i, child = s.first[i + 1];
+          c = 0.0, Z = 1.0, mass = 0.0, offered = 0, summed = false;
+          bare = s.drow[cur + 1] < 0;
+          continue;
+        }
+        ++refused;
+        mass += qx;
+        child = s.next[i];
+        if (bare) {
+          Z -= r;
+        } else if (Z > 0.0 || !summed) {
+          if (w > 0.0) c = fmin(c + Z / w, 1e30);
+          summed = true;
+          if (lane == 0) {
+            s.row_p = P.p + (root + 1 + cur) * P.p_stride;
+            s.row_q = P.q + s.drow[cur + 1] * P.q_stride;
+            s.c = c;
+            s.n_refused = 0;
+          }
+          work = kTreeSum;
+        }
+      }
+      if (lane == 0) s.work = work;
     }
-    if (!(total > 0.0 && total < INFINITY)) bad = 1;
-    if (!bad && tid < 32) {
-      const int v = pick(chunk_sum, rest, ref, P.V, P.nchunk, static_cast<double>(P.u_pick[b]) * total);
-      if (tid == 0) P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + len] = v;
+    __syncthreads();
+    if (s.work != kTreeSum) break;
+    chunk_sums<kVec>(s, chunk_sum, P.V, first, last);
+    __syncthreads();
+    if (tid < 32) {
+      double t = 0.0;
+      for (int i = lane; i < last - first; i += 32) t += chunk_sum[i];
+      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+      if (lane < ctas) *cluster.map_shared_rank(&s.slot[pass & 1][rank], lane) = t;
+    }
+    ++pass;
+    cluster.sync();
+  }
+
+  if (tid < 32 && s.work == kTreePick) {
+    // the CTA whose part of the row holds u * Z
+    const double* sums = s.slot[(pass - 1) & 1];
+    const double y = static_cast<double>(P.u_pick[b]) * Z;
+    double before = 0.0, mine_before = 0.0;
+    int owner = -1, heavy = 0;
+    for (int r = 0; r < ctas; ++r) {
+      if (r == rank) mine_before = before;
+      if (sums[r] > 0.0) heavy = r;
+      if (owner < 0 && sums[r] > 0.0 && before + sums[r] > y) owner = r;
+      before += sums[r];
+    }
+    const bool none = owner < 0;
+    if (none) owner = heavy;
+    if (owner == rank) {
+      const int v = pick(s, chunk_sum, P.V, first, last, none ? INFINITY : y - mine_before);
+      if (lane == 0) P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + len] = v;
+    }
+  }
+  if (rank != 0) return;
+  // rank 0 leaves the rest; its first warp knows how the walk went
+  __shared__ int s_len, s_bad;
+  if (tid == 0) {
+    s_len = len, s_bad = bad;
+    P.accepted_len[b] = bad ? -1 : len;
+    if (P.counters) {
+      if (bad) {
+        atomicAdd(P.counters + SV_CNT_INVALID, 1ull);
+      } else {
+        if (tested) atomicAdd(P.counters + SV_CNT_TESTED, static_cast<unsigned long long>(tested));
+        if (len) atomicAdd(P.counters + SV_CNT_ACCEPTED, static_cast<unsigned long long>(len));
+        if (refused) atomicAdd(P.counters + SV_CNT_REJECTED, static_cast<unsigned long long>(refused));
+        if (degenerate) atomicAdd(P.counters + SV_CNT_DEGENERATE, 1ull);
+        if (offered == 0) atomicAdd(P.counters + SV_CNT_BONUS, 1ull);
+      }
     }
   }
   __syncthreads();
+  len = s_len, bad = s_bad;
   const int from = bad ? 0 : len;
   for (int i = tid; i <= P.max_depth; i += kTreeThreads) {
     if (i > len || bad) P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + i] = -1;
@@ -247,20 +443,6 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(TreeParams P) {
   for (int i = tid; i < (inside ? end - start : 0); i += kTreeThreads) {
     if (P.accept_prob) P.accept_prob[start + i] = bad ? 0.f : s.alpha[i];
     if (P.flags) P.flags[start + i] = bad ? static_cast<int8_t>(SV_FLAG_INVALID) : s.flag[i];
-  }
-  if (tid == 0) {
-    P.accepted_len[b] = bad ? -1 : len;
-    if (P.counters) {
-      if (bad) {
-        atomicAdd(P.counters + SV_CNT_INVALID, 1ull);
-      } else {
-        atomicAdd(P.counters + SV_CNT_TESTED, static_cast<unsigned long long>(tested));
-        atomicAdd(P.counters + SV_CNT_ACCEPTED, static_cast<unsigned long long>(len));
-        atomicAdd(P.counters + SV_CNT_REJECTED, static_cast<unsigned long long>(refused));
-        if (degenerate) atomicAdd(P.counters + SV_CNT_DEGENERATE, 1ull);
-        if (offered == 0) atomicAdd(P.counters + SV_CNT_BONUS, 1ull);
-      }
-    }
   }
 }
 
@@ -304,6 +486,32 @@ extern "C" sv_status spec_verify_tree(const float* target_probs, int64_t target_
   P.accepted_len = accepted_len, P.out_tokens = tokens, P.path = path;
   P.accept_prob = accept_prob, P.flags = flags;
   P.counters = reinterpret_cast<unsigned long long*>(counters);
-  sv::tree_kernel<<<B, sv::kTreeThreads, P.nchunk * sizeof(double), static_cast<cudaStream_t>(cuda_stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
+  // as many CTAs a sequence as two per SM allow, each with a chunk for every other warp at least
+  int ctas = 1;
+  while (ctas < sv::kTreeCluster && static_cast<int64_t>(B) * ctas * 2 <= 2ll * sms &&
+         ctas * sv::kTreeWarps < P.nchunk)
+    ctas *= 2;
+  if (getenv("TREEC")) ctas = atoi(getenv("TREEC"));
+  if (static_cast<int64_t>(B) * ctas > 0x7fffffff) return SV_EUNSUPPORTED;
+  const bool vec = reinterpret_cast<uintptr_t>(target_probs) % 16 == 0 && reinterpret_cast<uintptr_t>(draft_probs) % 16 == 0 &&
+                   target_stride % 4 == 0 && draft_stride % 4 == 0;
+  const size_t smem = (static_cast<size_t>(P.nchunk) + ctas - 1) / ctas * sizeof(double) + sizeof(double);
+  const auto kernel = vec ? sv::tree_kernel<true> : sv::tree_kernel<false>;
+  if (smem > (32u << 10) &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 << 10) != cudaSuccess)
+    return SV_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B * ctas));
+  cfg.blockDim = dim3(sv::kTreeThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(cuda_stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? SV_OK : SV_ECUDA;
 }

@@ -97,7 +97,7 @@ def _tree_one(p, q, tokens, parent, draft_row, u, u_pick, max_depth, replacement
                 Z -= rest[x]
                 rest[x] = 0.0
             else:
-                if not (np.all(np.isfinite(row)) and not np.any(np.isnan(prop))):
+                if not (np.all(np.isfinite(row)) and np.all(np.isfinite(prop))):
                     return None
                 if w > 0:
                     rest = np.maximum(rest - Z * (prop / w), 0.0)
