@@ -597,7 +597,7 @@ int choose_width(bool pair, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t
 }
 
 template <bool kWeightsA>
-cudaError_t launch_mma(const LinearParams& L, int sms, cudaStream_t st, bool* taken) {
+cudaError_t launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st, bool* taken) {
   constexpr bool kPair = kWeightsA;
   *taken = false;
   MmaParams P = {};
@@ -630,9 +630,14 @@ cudaError_t launch_mma(const LinearParams& L, int sms, cudaStream_t st, bool* ta
   while (P.tmem_cols < 2 * P.nt) P.tmem_cols *= 2;
   // fp32 sums, bf16 operands, both K-major, N = nt, M = 128 or 256
   P.idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(P.nt / 8) << 17) | ((kPair ? 16u : 8u) << 24);
-  const cudaError_t e =
-      cudaFuncSetAttribute(mma_kernel<kWeightsA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
-  if (e != cudaSuccess) return e;
+  // once a device
+  static std::atomic<bool> opted_in[64];
+  if (device >= 64 || !opted_in[device].load()) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(mma_kernel<kWeightsA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
+    if (e != cudaSuccess) return e;
+    if (device < 64) opted_in[device].store(true);
+  }
   *taken = true;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * std::min<int64_t>(tiles, std::max(1, sms / 2))
@@ -708,7 +713,7 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
     bool taken = false;
     const cudaError_t e =
-        M > 128 ? sv::launch_mma<true>(P, sms, st, &taken) : sv::launch_mma<false>(P, sms, st, &taken);
+        M > 128 ? sv::launch_mma<true>(P, device, sms, st, &taken) : sv::launch_mma<false>(P, device, sms, st, &taken);
     if (e != cudaSuccess) return SV_ECUDA;
     if (taken) return SV_OK;
   }

@@ -243,7 +243,8 @@ def _cuda_device(t: torch.Tensor, name: str):
 
 
 def _stream(dev: torch.device, stream):
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    # the handle of current_stream(dev) without its Python object: 0.1 us against 2 us
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream
 
 
 def linear(x, weight, bias=None, residual=None, activation="none", cap=0.0, out=None, out_dtype=None, stream=None):
