@@ -15,7 +15,7 @@
 #include <initializer_list>
 #include <type_traits>
 
-#include "device_guard.cuh"
+#include "entry.cuh"
 #include "spec_verify.h"
 
 namespace sv {
@@ -160,55 +160,6 @@ struct MmaParams {
   unsigned staging;      // where the epilogue's staging starts in dynamic shared memory
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* bar, int count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect(uint64_t* bar, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint64_t* bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-
-// Waits for a phase; gives up after two seconds, or when another role has, and
-// then marks the CTA: its remaining results become NaN.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, volatile int* dead) {
-  if (mbar_try(bar, parity)) return true;
-  unsigned long long since = 0;
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(bar, parity)) return true;
-    const unsigned long long t = now_ns();
-    if (since == 0) since = t;
-    if (*dead || t - since > 2000000000ull) {
-      *dead = 1;
-      return false;
-    }
-  }
-}
-
 // one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
   unsigned e;
@@ -224,13 +175,6 @@ __device__ __forceinline__ unsigned cluster_rank() {
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// the address of the same place in the shared memory of the cluster's CTA `rank`
-__device__ __forceinline__ uint32_t in_cta(const void* p, unsigned rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  return a;
 }
 
 __device__ __forceinline__ void mbar_arrive_in(uint32_t cluster_addr) {
@@ -354,6 +298,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   if constexpr (kPair) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
+  wait_for_stream();
 
   // Warps 0 and 1 go through their loops as whole warps, and one lane that elect
   // picks issues: with a branch on the lane instead the compiler takes the
@@ -639,19 +584,10 @@ cudaError_t launch_mma(const LinearParams& L, int device, int sms, cudaStream_t 
     if (device < 64) opted_in[device].store(true);
   }
   *taken = true;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * std::min<int64_t>(tiles, std::max(1, sms / 2))
-                                                 : std::min<int64_t>(tiles, sms)));
-  cfg.blockDim = dim3(kMmaThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, mma_kernel<kWeightsA>, P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
+  const unsigned grid = static_cast<unsigned>(kPair ? 2 * std::min<int64_t>(tiles, std::max(1, sms / 2))
+                                                    : std::min<int64_t>(tiles, sms));
+  return launch_waiting(mma_kernel<kWeightsA>, grid, kMmaThreads, smem, kPair ? 2 : 1, st, P,
+                        kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
 }
 
 bool valid_dtype(int d) { return d == SV_F32 || d == SV_BF16; }

@@ -6,7 +6,9 @@
 //
 // Bound by memory: every logit read once and every probability written once.  A
 // row is a cluster of up to sixteen CTAs, each holding its part of the row in
-// registers (32 entries a thread) from the one read to the write.  A thread takes
+// registers (32 entries a thread) from the one read to the write.  A cluster takes
+// every n-th row, and its next rows are on their way into shared memory (every
+// thread copies and reads back its own entries) while it works on one.  A thread takes
 // the exponentials of its own entries against its own largest, so that one
 // exchange of (largest, sum) through the cluster is all that the row needs; the
 // last factor exp((largest of the thread - largest of the row) / T) / sum is one
@@ -16,10 +18,12 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
-#include "device_guard.cuh"
+#include "entry.cuh"
 #include "spec_verify.h"
 
 namespace sv {
@@ -40,99 +44,167 @@ struct SoftParams {
   int64_t y_stride;
   const float* t_row;
   float t;
+  int64_t rows;
   int V, part;  // part: entries of a row for each CTA, a multiple of 4
 };
 
 struct SoftShared {
   float warp_m[kSoftThreads / 32], warp_s[kSoftThreads / 32];
   int warp_at[kSoftThreads / 32];
-  float m[kSoftCluster], s[kSoftCluster];
-  int at[kSoftCluster];
+  // the CTAs' parts of a row, by turns: a CTA writes a place again only after every other one has passed the
+  // exchange between
+  float2 part[2][kSoftCluster];  // (largest, sum)
+  float m[2][kSoftCluster];      // (largest, its place) where T = 0
+  int at[2][kSoftCluster];
+  uint64_t arrived[2];
+  int dead;
 };
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-__device__ __forceinline__ float4 load_logits4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load_logits4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
+// Two floats in a 64-bit register: one instruction for both, each rounded by itself.
+using Two = unsigned long long;
+
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two t) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(t));
+  return f;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x; results below 2^-126 become 0
+__device__ __forceinline__ float power(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// Entries lo + 4 (j threads + thread) .. + 3 of a row, or with kVec false lo + (4 j + i) threads + thread; -inf
-// beyond the part's end
-template <typename T, bool kVec, int kThreads>
-__device__ __forceinline__ void load_part(const T* x, int lo, int hi, float (&v)[kSoftHeld]) {
-#pragma unroll
-  for (int j = 0; j < kSoftHeld / 4; ++j) {
-    if constexpr (kVec) {
-      const int at = lo + 4 * (j * kThreads + threadIdx.x);
-      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (at + 4 <= hi) {
-        f = load_logits4(x + at);
-      } else {
-        if (at < hi) f.x = load_logit(x + at);
-        if (at + 1 < hi) f.y = load_logit(x + at + 1);
-        if (at + 2 < hi) f.z = load_logit(x + at + 2);
-      }
-      v[4 * j] = f.x, v[4 * j + 1] = f.y, v[4 * j + 2] = f.z, v[4 * j + 3] = f.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = lo + (4 * j + i) * kThreads + threadIdx.x;
-        v[4 * j + i] = at < hi ? load_logit(x + at) : -INFINITY;
-      }
-    }
+// four neighbouring logits, as they lie in memory
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+  float4 f;
+  __device__ __forceinline__ void set(float a, float b, float c, float d) { f = make_float4(a, b, c, d); }
+  __device__ __forceinline__ void load(const void* p) { f = *static_cast<const float4*>(p); }
+  __device__ __forceinline__ float max() const { return fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)); }
+  __device__ __forceinline__ Two first() const { return two(f.x, f.y); }
+  __device__ __forceinline__ Two second() const { return two(f.z, f.w); }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void set(float a, float b, float c, float d) {
+    u.x = __float_as_uint(a) >> 16 | __float_as_uint(b);  // bf16 values: the low halves are 0
+    u.y = __float_as_uint(c) >> 16 | __float_as_uint(d);
   }
+  __device__ __forceinline__ void load(const void* p) { u = *static_cast<const uint2*>(p); }
+  __device__ __forceinline__ float max() const {
+    uint32_t m;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(u.x), "r"(u.y));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  __device__ __forceinline__ Two first() const {
+    return two(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+  }
+  __device__ __forceinline__ Two second() const {
+    return two(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+  }
+};
+
+constexpr int kSoftFours = kSoftHeld / 4;
+
+// The j-th four of a thread are the entries lo + 4 (j threads + thread) .. + 3 of a row, or with kVec false the entries
+// lo + (4 j + i) threads + thread; -inf beyond hi.  from: where the four lies, x + its place or a copy.
+template <typename T, bool kVec, int kThreads>
+__device__ __forceinline__ void load_four(Four<T>& f, const T* x, const T* from, int lo, int hi, int j) {
+  if constexpr (kVec) {
+    const int at = lo + 4 * (j * kThreads + static_cast<int>(threadIdx.x));
+    if (at + 4 <= hi)
+      f.load(from + 4 * (j * kThreads + static_cast<int>(threadIdx.x)));
+    else
+      f.set(at < hi ? load_logit(x + at) : -INFINITY, at + 1 < hi ? load_logit(x + at + 1) : -INFINITY,
+            at + 2 < hi ? load_logit(x + at + 2) : -INFINITY, -INFINITY);
+  } else {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = lo + (4 * j + i) * kThreads + static_cast<int>(threadIdx.x);
+      v[i] = at < hi ? load_logit(x + at) : -INFINITY;
+    }
+    f.set(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// The exponentials exp((l - m) / T) of a part's entries against the thread's largest m, and their sum.  With nothing
+// but -inf (or NaN) m is -inf and the terms are 0 (or NaN).
+template <typename T, bool kVec, int kThreads>
+__device__ __forceinline__ void load_part(const T* x, const T* from, int lo, int hi, float c, Two (&e)[2 * kSoftFours],
+                                          float& m, float& sum) {
+  Four<T> f[kSoftFours];
+#pragma unroll
+  for (int j = 0; j < kSoftFours; ++j) load_four<T, kVec, kThreads>(f[j], x, from, lo, hi, j);
+  m = f[0].max();
+#pragma unroll
+  for (int j = 1; j < kSoftFours; ++j) m = fmaxf(m, f[j].max());
+  const float ref = m == -INFINITY ? 0.f : -m;
+  const Two ref2 = two(ref, ref), c2 = two(c, c);
+  Two s[2] = {};
+#pragma unroll
+  for (int j = 0; j < kSoftFours; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = both(mul2(add2(i ? f[j].second() : f[j].first(), ref2), c2));
+      e[2 * j + i] = two(power(a.x), power(a.y));
+      s[i] = add2(s[i], e[2 * j + i]);
+    }
+  const float2 t = both(add2(s[0], s[1]));
+  sum = t.x + t.y;
 }
 
 template <bool kVec, int kThreads>
-__device__ __forceinline__ void store_part(float* y, int lo, int hi, const float (&v)[kSoftHeld], float scale) {
+__device__ __forceinline__ void store_part(float* y, int lo, int hi, const Two (&e)[2 * kSoftFours], float scale) {
+  const Two scale2 = two(scale, scale);
 #pragma unroll
-  for (int j = 0; j < kSoftHeld / 4; ++j) {
+  for (int j = 0; j < kSoftFours; ++j) {
+    const float2 a = both(mul2(e[2 * j], scale2)), b = both(mul2(e[2 * j + 1], scale2));
     if constexpr (kVec) {
-      const int at = lo + 4 * (j * kThreads + threadIdx.x);
+      const int at = lo + 4 * (j * kThreads + static_cast<int>(threadIdx.x));
       if (at + 4 <= hi) {
-        *reinterpret_cast<float4*>(y + at) =
-            make_float4(v[4 * j] * scale, v[4 * j + 1] * scale, v[4 * j + 2] * scale, v[4 * j + 3] * scale);
+        *reinterpret_cast<float4*>(y + at) = make_float4(a.x, a.y, b.x, b.y);
       } else {
-        if (at < hi) y[at] = v[4 * j] * scale;
-        if (at + 1 < hi) y[at + 1] = v[4 * j + 1] * scale;
-        if (at + 2 < hi) y[at + 2] = v[4 * j + 2] * scale;
+        if (at < hi) y[at] = a.x;
+        if (at + 1 < hi) y[at + 1] = a.y;
+        if (at + 2 < hi) y[at + 2] = b.x;
       }
     } else {
+      const float v[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = lo + (4 * j + i) * kThreads + threadIdx.x;
-        if (at < hi) y[at] = v[4 * j + i] * scale;
+        const int at = lo + (4 * j + i) * kThreads + static_cast<int>(threadIdx.x);
+        if (at < hi) y[at] = v[i];
       }
     }
   }
-}
-
-__device__ __forceinline__ float largest(const float (&v)[kSoftHeld]) {
-  float m = v[0];
-#pragma unroll
-  for (int i = 1; i < kSoftHeld; ++i) m = fmaxf(m, v[i]);
-  return m;
 }
 
 // how much a sum against `from` counts in one against `to` >= from
 __device__ __forceinline__ float rescale(float from, float to, float c) {
-  return from == to ? 1.f : exp2f((from - to) * c);
-}
-
-// v becomes exp((v - m) / T), summed.  With m = -inf (nothing but -inf, or NaN) the terms are 0, or NaN.
-__device__ __forceinline__ float exponentials(float (&v)[kSoftHeld], float m, float c) {
-  const float ref = m == -INFINITY ? 0.f : m;
-  float s[4] = {};
-#pragma unroll
-  for (int i = 0; i < kSoftHeld; ++i) {
-    v[i] = exp2f((v[i] - ref) * c);
-    s[i % 4] += v[i];
-  }
-  return (s[0] + s[1]) + (s[2] + s[3]);
+  return from == to ? 1.f : power((from - to) * c);
 }
 
 // the larger logit, the smaller index among equal ones; a NaN wins over everything
@@ -146,7 +218,7 @@ __device__ __forceinline__ void take_larger(float& m, int& at, float om, int oat
 
 // T = 0
 template <typename T, int kThreads>
-__device__ __noinline__ void one_hot(SoftShared& s, const T* x, float* y, int lo, int hi) {
+__device__ __noinline__ void one_hot(SoftShared& s, const T* x, float* y, int lo, int hi, int turn) {
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -162,85 +234,140 @@ __device__ __noinline__ void one_hot(SoftShared& s, const T* x, float* y, int lo
     for (int o = 16; o; o >>= 1) take_larger(m, at, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, at, o));
     if (lane < ctas) {
       SoftShared* to = cluster.map_shared_rank(&s, lane);
-      to->m[rank] = m, to->at[rank] = at;
+      to->m[turn][rank] = m, to->at[turn][rank] = at;
     }
   }
   cluster.sync();
-  m = s.m[0], at = s.at[0];
-  for (int r = 1; r < ctas; ++r) take_larger(m, at, s.m[r], s.at[r]);
+  m = s.m[turn][0], at = s.at[turn][0];
+  for (int r = 1; r < ctas; ++r) take_larger(m, at, s.m[turn][r], s.at[turn][r]);
   const bool valid = fabsf(m) < INFINITY;
   for (int v = lo + threadIdx.x; v < hi; v += kThreads) y[v] = valid ? (v == at ? 1.f : 0.f) : NAN;
 }
 
+// a thread's entries of a part on their way into its places of a stage
+template <typename T, int kThreads>
+__device__ __forceinline__ void copy_part(const T* x, int lo, int hi, uint32_t stage) {
+#pragma unroll
+  for (int j = 0; j < kSoftHeld / 4; ++j) {
+    const int place = j * kThreads + threadIdx.x, at = lo + 4 * place;
+    if (at + 4 <= hi)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(stage + place * 4 * static_cast<int>(sizeof(T))),
+                   "l"(x + at), "n"(4 * sizeof(T))
+                   : "memory");
+  }
+}
+
+template <typename T>
+constexpr int kSoftStages = sizeof(T) == 2 ? 3 : 1;  // two CTAs of 512 threads fill an SM's shared memory
+
 template <typename T, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(const __grid_constant__ SoftParams P) {
+  extern __shared__ __align__(16) uint8_t stages[];
   __shared__ SoftShared s;
+  constexpr int kStages = kSoftStages<T>, kStageBytes = kThreads * kSoftHeld * sizeof(T);
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
-  cluster.barrier_arrive();  // every CTA of the cluster runs before any writes into another
-  const int64_t r = blockIdx.x / ctas;
-  const T* x = static_cast<const T*>(P.x) + r * P.x_stride;
-  float* y = P.y + r * P.y_stride;
+  const int clusters = gridDim.x / ctas;
+  if (threadIdx.x == 0) {
+    mbar_init(&s.arrived[0], 1);
+    mbar_init(&s.arrived[1], 1);
+    s.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster.sync();  // every CTA of the cluster runs before any writes into another
+  wait_for_stream();
+  unsigned phases = 0;  // of the two barriers
+  const T* x0 = static_cast<const T*>(P.x);
   const int lo = min(rank * P.part, P.V), hi = min(lo + P.part, P.V);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float t = P.t_row ? P.t_row[r] : P.t;
-  if (t == 0.f) {
-    cluster.barrier_wait();
-    one_hot<T, kThreads>(s, x, y, lo, hi);
-    return;
+  const bool held = P.part <= kThreads * kSoftHeld, staged = kVec && held;
+  int64_t r = blockIdx.x / ctas;
+  uint32_t stage = 0;  // of row r
+  if constexpr (kVec) {
+    if (staged)
+      for (int i = 0; i < kStages; ++i) {
+        if (r + i * clusters < P.rows)
+          copy_part<T, kThreads>(x0 + (r + i * clusters) * P.x_stride, lo, hi,
+                                 static_cast<uint32_t>(__cvta_generic_to_shared(stages)) + i * kStageBytes);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
   }
-  // 1.44.. / t overflows below 1e-38, where every logit but the largest has no probability
-  const float c = fminf(1.4426950408889634f / t, 3.0e38f);
-  const bool held = P.part <= kThreads * kSoftHeld;
-  float v[kSoftHeld];
-  float m, sum;
-  if (held) {
-    load_part<T, kVec, kThreads>(x, lo, hi, v);
-    m = largest(v);
-    sum = exponentials(v, m, c);
-  } else {
-    m = -INFINITY, sum = 0.f;
+  for (int turn = 0; r < P.rows; r += clusters, turn ^= 1) {
+    const T* x = x0 + r * P.x_stride;
+    float* y = P.y + r * P.y_stride;
+    const float t = P.t_row ? P.t_row[r] : P.t;
+    // 1.44.. / t overflows below 1e-38, where every logit but the largest has no probability
+    const float c = t > 0.f ? fminf(1.4426950408889634f / t, 3.0e38f) : 1.f;
+    Two e[2 * kSoftFours];
+    float m, sum;
+    if (staged) {
+      if constexpr (kVec) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        load_part<T, kVec, kThreads>(x, reinterpret_cast<const T*>(stages + stage * kStageBytes), lo, hi, c, e, m, sum);
+        const int64_t ahead = r + static_cast<int64_t>(kStages) * clusters;
+        if (ahead < P.rows)
+          copy_part<T, kThreads>(x0 + ahead * P.x_stride, lo, hi,
+                                 static_cast<uint32_t>(__cvta_generic_to_shared(stages)) + stage * kStageBytes);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++stage == kStages) stage = 0;
+      }
+    } else if (held) {
+      load_part<T, kVec, kThreads>(x, x + lo, lo, hi, c, e, m, sum);
+    } else {
+      m = -INFINITY, sum = 0.f;
 #pragma unroll 1
-    for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
-      load_part<T, kVec, kThreads>(x, at, hi, v);
-      const float mv = largest(v), to = fmaxf(m, mv), sv = exponentials(v, mv, c);
-      sum = sum * rescale(m, to, c) + sv * rescale(mv, to, c);
-      m = to;
+      for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
+        float mv, sv;
+        load_part<T, kVec, kThreads>(x, x + at, at, hi, c, e, mv, sv);
+        const float to = fmaxf(m, mv);
+        sum = sum * rescale(m, to, c) + sv * rescale(mv, to, c);
+        m = to;
+      }
     }
-  }
-  const float mine = m;
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  sum *= rescale(mine, m, c);
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (lane == 0) s.warp_m[warp] = m, s.warp_s[warp] = sum;
-  __syncthreads();
-  cluster.barrier_wait();
-  if (warp == 0) {
-    const float wm = lane < kThreads / 32 ? s.warp_m[lane] : -INFINITY;
-    float bm = wm, bs = lane < kThreads / 32 ? s.warp_s[lane] : 0.f;
-    for (int o = 16; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, o));
-    bs *= rescale(wm, bm, c);
-    for (int o = 16; o; o >>= 1) bs += __shfl_xor_sync(~0u, bs, o);
-    if (lane < ctas) {
-      SoftShared* to = cluster.map_shared_rank(&s, lane);
-      to->m[rank] = bm, to->s[rank] = bs;
+    if (t == 0.f) {
+      one_hot<T, kThreads>(s, x, y, lo, hi, turn);
+      continue;
     }
-  }
-  cluster.sync();
-  m = s.m[0];
-  for (int i = 1; i < ctas; ++i) m = fmaxf(m, s.m[i]);
-  sum = 0.f;
-  for (int i = 0; i < ctas; ++i) sum += s.s[i] * rescale(s.m[i], m, c);
-  // a NaN, a +inf and a row of nothing but -inf have made the sum NaN or 0, and the row NaN
-  const float inv = t > 0.f && t < INFINITY ? 1.f / sum : NAN;
-  if (held) {
-    store_part<kVec, kThreads>(y, lo, hi, v, rescale(mine, m, c) * inv);
-  } else {
+    const float mine = m;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    sum *= rescale(mine, m, c);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) s.warp_m[warp] = m, s.warp_s[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const float wm = lane < kThreads / 32 ? s.warp_m[lane] : -INFINITY;
+      float bm = wm, bs = lane < kThreads / 32 ? s.warp_s[lane] : 0.f;
+      for (int o = 16; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, o));
+      bs *= rescale(wm, bm, c);
+      for (int o = 16; o; o >>= 1) bs += __shfl_xor_sync(~0u, bs, o);
+      // Every CTA writes its part into every other's memory, and the write itself counts there.  A cluster barrier
+      // would first wait for the stores of the row before.
+      if (lane == 0) mbar_expect(&s.arrived[turn], ctas * sizeof(float2));
+      if (lane < ctas)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                         in_cta(&s.part[turn][rank], lane)),
+                     "l"(two(bm, bs)), "r"(in_cta(&s.arrived[turn], lane))
+                     : "memory");
+    }
+    const bool ok = mbar_wait(&s.arrived[turn], phases >> turn & 1, &s.dead);
+    phases ^= 1u << turn;
+    const float2 part = lane < ctas ? s.part[turn][lane] : make_float2(-INFINITY, 0.f);
+    m = part.x;
+    for (int o = kSoftCluster / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o, kSoftCluster));
+    sum = lane < ctas ? part.y * rescale(part.x, m, c) : 0.f;
+    for (int o = kSoftCluster / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o, kSoftCluster);
+    m = __shfl_sync(~0u, m, 0), sum = __shfl_sync(~0u, sum, 0);
+    // a NaN, a +inf and a row of nothing but -inf have made the sum NaN or 0, and the row NaN
+    const float inv = ok && t > 0.f && t < INFINITY ? 1.f / sum : NAN;
+    if (held) {
+      store_part<kVec, kThreads>(y, lo, hi, e, rescale(mine, m, c) * inv);
+    } else {
 #pragma unroll 1
-    for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
-      load_part<T, kVec, kThreads>(x, at, hi, v);
-      exponentials(v, m, c);
-      store_part<kVec, kThreads>(y, at, hi, v, inv);
+      for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
+        float mv, sv;
+        load_part<T, kVec, kThreads>(x, x + at, at, hi, c, e, mv, sv);
+        store_part<kVec, kThreads>(y, at, hi, e, rescale(mv, m, c) * inv);
+      }
     }
   }
 }
@@ -278,25 +405,30 @@ extern "C" sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_
   while (ctas < sv::kSoftCluster && (V > ctas * sv::kSoftPart || (static_cast<int64_t>(rows) * ctas * 2 <= 2ll * sms &&
                                                                   V > ctas * sv::kSoftThreads * 4)))
     ctas *= 2;
-  if (static_cast<int64_t>(rows) * ctas > 0x7fffffff) return SV_EUNSUPPORTED;
   const int part = ((V + ctas - 1) / ctas + 3) / 4 * 4;
-  const sv::SoftParams P = {logits, logits_stride, probs, probs_stride, temperature_per_row, temperature, V, part};
+  const sv::SoftParams P = {logits, logits_stride, probs, probs_stride, temperature_per_row, temperature, rows, V, part};
   const bool vec = reinterpret_cast<uintptr_t>(logits) % (4 * es) == 0 && reinterpret_cast<uintptr_t>(probs) % 16 == 0 &&
                    (rows == 1 || (logits_stride % 4 == 0 && probs_stride % 4 == 0));
-  const auto kernel = ctas == 1 && V <= sv::kSoftShort ? sv::softmax_variant<sv::kSoftFew>(dt, vec)
-                                                       : sv::softmax_variant<sv::kSoftThreads>(dt, vec);
-  // sixteen CTAs are more than the portable eight
-  if (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return SV_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
-  cfg.blockDim = dim3(ctas == 1 && V <= sv::kSoftShort ? sv::kSoftFew : sv::kSoftThreads);
-  cfg.stream = static_cast<cudaStream_t>(cuda_stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? SV_OK : SV_ECUDA;
+  const bool few = ctas == 1 && V <= sv::kSoftShort;
+  const int threads = few ? sv::kSoftFew : sv::kSoftThreads;
+  const auto kernel = few ? sv::softmax_variant<sv::kSoftFew>(dt, vec) : sv::softmax_variant<sv::kSoftThreads>(dt, vec);
+  const bool staged = vec && part <= threads * sv::kSoftHeld;
+  const size_t smem = !staged ? 0
+                      : dt == SV_BF16 ? sv::kSoftStages<__nv_bfloat16> * threads * sv::kSoftHeld * 2
+                                      : sv::kSoftStages<float> * threads * sv::kSoftHeld * 4;
+  // how many clusters of this variant run at once: asked once a device
+  static std::atomic<int> known[64][2][2][2][2][5];
+  int log = 0;
+  while (1 << log < ctas) ++log;
+  std::atomic<int>* at = device < 64 ? &known[device][dt == SV_BF16][vec][few][staged][log] : nullptr;
+  int resident = at ? at->load() : 0;
+  if (resident == 0) {
+    if (sv::prepare_waiting(kernel, threads, smem, ctas, &resident) != cudaSuccess || resident < 1) return SV_ECUDA;
+    if (at) at->store(resident);
+  }
+  const int64_t clusters = std::min<int64_t>(rows, resident);
+  return sv::launch_waiting(kernel, static_cast<unsigned>(clusters * ctas), threads, smem, ctas,
+                            static_cast<cudaStream_t>(cuda_stream), P) == cudaSuccess
+             ? SV_OK
+             : SV_ECUDA;
 }

@@ -12,7 +12,7 @@
 #include <mutex>
 #include <new>
 
-#include "device_guard.cuh"
+#include "entry.cuh"
 #include "handle.h"
 
 

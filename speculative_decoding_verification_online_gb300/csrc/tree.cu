@@ -26,7 +26,7 @@
 #include <cstdlib>
 #include <initializer_list>
 
-#include "device_guard.cuh"
+#include "entry.cuh"
 #include "spec_verify.h"
 
 namespace sv {
@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
   cluster.barrier_arrive();  // every CTA of the cluster runs before any writes into another
+  wait_for_stream();
   const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31;
   const int first = static_cast<int>(static_cast<int64_t>(P.nchunk) * rank / ctas);
   const int last = static_cast<int>(static_cast<int64_t>(P.nchunk) * (rank + 1) / ctas);
@@ -502,16 +503,8 @@ extern "C" sv_status spec_verify_tree(const float* target_probs, int64_t target_
   if (smem > (32u << 10) &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 << 10) != cudaSuccess)
     return SV_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(B * ctas));
-  cfg.blockDim = dim3(sv::kTreeThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(cuda_stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? SV_OK : SV_ECUDA;
+  return sv::launch_waiting(kernel, static_cast<unsigned>(B * ctas), sv::kTreeThreads, smem, ctas,
+                            static_cast<cudaStream_t>(cuda_stream), P) == cudaSuccess
+             ? SV_OK
+             : SV_ECUDA;
 }
