@@ -12,9 +12,10 @@
 //
 // A pick among V tokens hangs on the last digits of its prefix sums: with
 // sums good to 1e-7 one pick in a hundred would land beside the token that
-// exact sums give.  fp64 has two lanes an SM and clock here, so the row sums are
-// carried as pairs of floats (error-free sums and products, about 48 bits); one
-// warp does the few scalar steps in fp64.
+// exact sums give.  fp64 has two lanes an SM and clock here (a warp's instruction
+// takes its partition 64 clocks, and a walk and a pick in fp64 took 4 and 8 us), so
+// everything is carried as pairs of floats: error-free sums and products, about 48
+// bits.
 //
 // A sequence is a cluster of up to eight CTAs, each with a part of the row; every
 // CTA's first warp takes the same walk, and a sum over a row is one exchange of
@@ -58,17 +59,17 @@ struct TreeShared {
   float px[SV_MAX_NODES], qx[SV_MAX_NODES], u[SV_MAX_NODES], alpha[SV_MAX_NODES];
   int32_t refused[SV_MAX_NODES];  // distinct tokens refused at a node without a draft row
   int8_t flag[SV_MAX_NODES], again[SV_MAX_NODES];
-  double slot[2][kTreeCluster];  // the CTAs' sums of a pass, by its parity
+  float2 slot[2][kTreeCluster];  // the CTAs' sums of a pass, by its parity
   // what the first warp asks of the others
   const float* row_p;
   const float* row_q;  // null: c is 0
-  double c;
+  float c, cl;
   int n_refused, work;
 };
 
 enum { kTreeSum = 0, kTreePick = 1, kTreeEnd = 2 };
 
-// s + l, s the nearest float: sums of floats without losing what does not fit
+// s + l, l what s does not hold
 struct Pair {
   float s, l;
   __device__ __forceinline__ void add(float x) {
@@ -80,18 +81,36 @@ struct Pair {
     add(o.s);
     l += o.l;
   }
+  __device__ __forceinline__ float value() const { return s + l; }
+  // s the float nearest to s + l
+  __device__ __forceinline__ Pair settled() const {
+    const float t = s + l;
+    return {t, l - (t - s)};
+  }
 };
 
-// (p - (c + cl) q)+ onto a sum; a NaN stays
-__device__ __forceinline__ void add_rest(Pair& sum, float p, float q, float c, float cl) {
-  const float h = __fmul_rn(c, q);  // not to be fused into the difference below
-  const float hl = fmaf(cl, q, fmaf(c, q, -h));
+__device__ __forceinline__ Pair times(const Pair& a, const Pair& b) {
+  const float h = __fmul_rn(a.s, b.s);
+  return Pair{h, fmaf(a.s, b.s, -h) + fmaf(a.s, b.l, a.l * b.s)}.settled();
+}
+
+__device__ __forceinline__ bool above(const Pair& a, const Pair& b) { return (a.s - b.s) + (a.l - b.l) > 0.f; }
+
+// a / b, b not 0
+__device__ __forceinline__ Pair over(const Pair& a, const Pair& b) {
+  const float x = a.s / b.s;
+  const Pair back = times(Pair{x, 0.f}, b);
+  return Pair{x, ((a.s - back.s) + (a.l - back.l)) / b.s}.settled();
+}
+
+// (p - (c + cl) q)+; a NaN stays.  kOne: c + cl is 1, as after a first refusal
+template <bool kOne>
+__device__ __forceinline__ Pair rest_of(float p, float q, float c, float cl) {
+  const float h = kOne ? q : __fmul_rn(c, q);  // not to be fused into the difference below
+  const float hl = kOne ? 0.f : fmaf(cl, q, fmaf(c, q, -h));
   const float d = p - h, z = d - p;
   const float dl = ((p - (d - z)) - (h + z)) - hl;
-  if (!(d + dl <= 0.f)) {
-    sum.add(d);
-    sum.l += dl;
-  }
+  return d + dl <= 0.f ? Pair{0.f, 0.f} : Pair{d, dl};
 }
 
 __device__ __forceinline__ Pair warp_total(Pair x) {
@@ -100,12 +119,26 @@ __device__ __forceinline__ Pair warp_total(Pair x) {
   return x;
 }
 
-__device__ __forceinline__ double rest_at(const TreeShared& s, int v) {
+// inclusive sums over the lanes
+__device__ __forceinline__ Pair scan(Pair x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair up = {__shfl_up_sync(~0u, x.s, o), __shfl_up_sync(~0u, x.l, o)};
+    if (lane >= o) x.add(up);
+  }
+  return x.settled();
+}
+
+__device__ __forceinline__ Pair from_lane(const Pair& x, int lane) {
+  return {__shfl_sync(~0u, x.s, lane), __shfl_sync(~0u, x.l, lane)};
+}
+
+__device__ __forceinline__ Pair rest_at(const TreeShared& s, int v) {
   for (int i = 0; i < s.n_refused; ++i)
-    if (s.refused[i] == v) return 0.0;
-  const double p = s.row_p[v];
-  const double r = s.row_q ? fma(-s.c, static_cast<double>(s.row_q[v]), p) : p;
-  return r < 0.0 ? 0.0 : r;
+    if (s.refused[i] == v) return {0.f, 0.f};
+  const float p = s.row_p[v];
+  return s.row_q ? rest_of<false>(p, s.row_q[v], s.c, s.cl) : Pair{fmaxf(p, 0.f), 0.f};
 }
 
 // four neighbouring entries of a row; nothing beyond its end
@@ -119,11 +152,19 @@ __device__ __forceinline__ float4 load4(const float* row, int v, int V) {
   return make_float4(v < V ? row[v] : 0.f, v + 1 < V ? row[v + 1] : 0.f, v + 2 < V ? row[v + 2] : 0.f, 0.f);
 }
 
+template <bool kOne>
+__device__ __forceinline__ void add_rests(Pair (&sum)[4], const float4& p, const float4& q, float c, float cl) {
+  sum[0].add(rest_of<kOne>(p.x, q.x, c, cl));
+  sum[1].add(rest_of<kOne>(p.y, q.y, c, cl));
+  sum[2].add(rest_of<kOne>(p.z, q.z, c, cl));
+  sum[3].add(rest_of<kOne>(p.w, q.w, c, cl));
+}
+
 // the weight of each of this CTA's chunks into chunk_sum: every warp
 template <bool kVec>
-__device__ __forceinline__ void chunk_sums(const TreeShared& s, double* chunk_sum, int V, int first, int last) {
+__device__ __forceinline__ void chunk_sums(const TreeShared& s, float2* chunk_sum, int V, int first, int last) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float c = static_cast<float>(s.c), cl = static_cast<float>(s.c - static_cast<double>(c));
+  const float c = s.c, cl = s.cl;
   for (int ch = first + warp; ch < last; ch += kTreeWarps) {
     Pair sum[4] = {};
     const int v0 = ch * kTreeChunk + lane * 4;
@@ -133,12 +174,12 @@ __device__ __forceinline__ void chunk_sums(const TreeShared& s, double* chunk_su
     if (s.row_q) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) q[j] = load4<kVec>(s.row_q, v0 + j * 128, V);
+      if (c == 1.f && cl == 0.f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        add_rest(sum[0], p[j].x, q[j].x, c, cl);
-        add_rest(sum[1], p[j].y, q[j].y, c, cl);
-        add_rest(sum[2], p[j].z, q[j].z, c, cl);
-        add_rest(sum[3], p[j].w, q[j].w, c, cl);
+        for (int j = 0; j < 4; ++j) add_rests<true>(sum, p[j], q[j], c, cl);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) add_rests<false>(sum, p[j], q[j], c, cl);
       }
     } else {
       bool hit = false;
@@ -164,75 +205,58 @@ __device__ __forceinline__ void chunk_sums(const TreeShared& s, double* chunk_su
     sum[0].add(sum[1]);
     sum[2].add(sum[3]);
     sum[0].add(sum[2]);
-    const Pair t = warp_total(sum[0]);
-    if (lane == 0) chunk_sum[ch - first] = static_cast<double>(t.s) + static_cast<double>(t.l);
+    const Pair t = warp_total(sum[0]).settled();
+    if (lane == 0) chunk_sum[ch - first] = make_float2(t.s, t.l);
   }
 }
 
-__device__ __forceinline__ double scan(double x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double up = __shfl_up_sync(~0u, x, o);
-    if (lane >= o) x += up;
-  }
-  return x;
+// The first lane whose weight carries the sums past y; the last lane with weight where `any` and none does; else -1.
+// *before becomes the sum in front of that lane.
+__device__ __forceinline__ int lane_past(const Pair& w, const Pair& y, bool any, Pair* before) {
+  Pair incl = scan(w);
+  incl.add(*before);
+  incl = incl.settled();
+  const bool some = w.value() > 0.f;
+  const unsigned past = __ballot_sync(~0u, some && above(incl, y)), heavy = __ballot_sync(~0u, some);
+  const int at = past ? __ffs(past) - 1 : any && heavy ? 31 - __clz(heavy) : -1;
+  const Pair up = from_lane(incl, at < 0 ? 31 : at ? at - 1 : 0);
+  if (at != 0) *before = up;
+  return at;
 }
 
 // The smallest v of this CTA's chunks whose inclusive prefix sum exceeds y, or the last v with weight when rounding
-// leaves none: the first warp.
-__device__ int pick(const TreeShared& s, const double* chunk_sum, int V, int first, int last, double y) {
+// leaves none (or y is infinite): the first warp.
+__device__ int pick(const TreeShared& s, const float2* chunk_sum, int V, int first, int last, Pair y) {
   const int lane = threadIdx.x & 31;
-  double before = 0.0;
+  Pair before = {0.f, 0.f};
   int ch = -1, heavy = first;
   for (int i0 = first; i0 < last && ch < 0; i0 += 32) {
-    const int i = i0 + lane;
-    const double w = i < last ? chunk_sum[i - first] : 0.0;
-    const double incl = before + scan(w);
-    const unsigned past = __ballot_sync(~0u, w > 0.0 && incl > y), some = __ballot_sync(~0u, w > 0.0);
+    const float2 f = i0 + lane < last ? chunk_sum[i0 + lane - first] : make_float2(0.f, 0.f);
+    const unsigned some = __ballot_sync(~0u, f.x + f.y > 0.f);
     if (some) heavy = i0 + 31 - __clz(some);
-    if (past) {
-      ch = i0 + __ffs(past) - 1;
-      before = __shfl_sync(~0u, incl - w, __ffs(past) - 1);
-    } else {
-      before = __shfl_sync(~0u, incl, 31);
-    }
+    const int at = lane_past(Pair{f.x, f.y}, y, false, &before);
+    if (at >= 0) ch = i0 + at;
   }
   if (ch < 0) {
     ch = heavy;
-    y = INFINITY;
+    y = Pair{INFINITY, 0.f};
   }
-  // 16 neighbours a lane
+  // runs of 16 neighbours a lane, then the 16 of one run
   constexpr int kRun = kTreeChunk / 32;
   const int v0 = ch * kTreeChunk + lane * kRun;
-  double w[kRun], mine = 0.0;
-#pragma unroll
-  for (int i = 0; i < kRun; ++i) w[i] = v0 + i < V ? rest_at(s, v0 + i) : 0.0;
-#pragma unroll
-  for (int i = 0; i < kRun; ++i) mine += w[i];
-  const double incl = before + scan(mine);
-  const unsigned past = __ballot_sync(~0u, mine > 0.0 && incl > y), some = __ballot_sync(~0u, mine > 0.0);
-  const int owner = past ? __ffs(past) - 1 : 31 - __clz(some);
-  int v = -1;
-  if (lane == owner) {
-    double sum = incl - mine;
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      sum += w[i];
-      if (w[i] > 0.0 && (v < 0 || !past)) v = v0 + i;
-      if (past && w[i] > 0.0 && sum <= y) v = -1;
-    }
-    if (v < 0)  // rounding: the lane's last weight
-#pragma unroll
-      for (int i = 0; i < kRun; ++i)
-        if (w[i] > 0.0) v = v0 + i;
-  }
-  return __shfl_sync(~0u, v, owner);
+  Pair mine = {0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < kRun; ++i)
+    if (v0 + i < V) mine.add(rest_at(s, v0 + i));
+  const int run = lane_past(mine.settled(), y, true, &before);
+  const int at = ch * kTreeChunk + run * kRun + lane;
+  const Pair w = lane < kRun && at < V ? rest_at(s, at) : Pair{0.f, 0.f};
+  return ch * kTreeChunk + run * kRun + lane_past(w, y, true, &before);
 }
 
 template <bool kVec>
 __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_constant__ TreeParams P) {
-  extern __shared__ double chunk_sum[];
+  extern __shared__ float2 chunk_sum[];
   __shared__ TreeShared s;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
@@ -288,7 +312,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
   // The walk: the first warp of every CTA takes the same steps, and stops where a sum over a row is needed.
   int cur = -1, child = bad ? SV_MAX_NODES : s.first[0];
   int len = 0, refused = 0, tested = 0, offered = 0, degenerate = 0, pass = 0;  // offered: children of cur
-  double c = 0.0, Z = 1.0, mass = 0.0;
+  const Pair zero = {0.f, 0.f}, one = {1.f, 0.f};
+  Pair c = zero, Z = one, mass = zero;
   bool summed = false, closing = false;  // chunk_sum is that of cur and c; the sum for the pick is under way
   if (n == 0) child = SV_MAX_NODES;
   for (;;) {
@@ -297,19 +322,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
       bool bare = bad || s.drow[cur + 1] < 0;
       if (work < 0 && pass > 0) {
         // what the last pass was for
-        double t = 0.0;
-        for (int r = 0; r < ctas; ++r) t += s.slot[(pass - 1) & 1][r];
-        Z = t;
-        if (!(t >= 0.0 && t < INFINITY)) bad = 1, work = kTreeEnd;
+        Z = zero;
+        for (int r = 0; r < ctas; ++r) Z.add(Pair{s.slot[(pass - 1) & 1][r].x, s.slot[(pass - 1) & 1][r].y});
+        Z = Z.settled();
+        if (!(Z.value() >= 0.f && Z.value() < INFINITY)) bad = 1, work = kTreeEnd;
         if (closing && work < 0) {
-          if (t > 0.0) {
+          if (Z.value() > 0.f) {
             work = kTreePick;
           } else if (degenerate) {
             bad = 1, work = kTreeEnd;  // the node's own row has no mass
           } else {
             degenerate = 1;
-            c = 0.0;
-            if (lane == 0) s.row_q = nullptr, s.c = 0.0, s.n_refused = 0;
+            if (lane == 0) s.row_q = nullptr, s.n_refused = 0;
             work = kTreeSum;
           }
         }
@@ -318,14 +342,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
         if (child >= SV_MAX_NODES) {
           // no child is left: the token comes from what is left of this row
           closing = true;
-          if (summed && Z > 0.0) {
+          if (summed && Z.value() > 0.f) {
             work = kTreePick;
           } else {
-            if (summed) degenerate = 1, c = 0.0;
+            if (summed) degenerate = 1;
             if (lane == 0) {
               s.row_p = P.p + (root + 1 + cur) * P.p_stride;
               s.row_q = nullptr;
-              s.c = 0.0;
               int k = 0;
               if (bare)
                 for (int i = s.first[cur + 1]; i < SV_MAX_NODES && n > 0; i = s.next[i])
@@ -337,18 +360,32 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
           break;
         }
         const int i = child;
-        const double qx = s.qx[i], px = s.px[i];
-        if (!(px >= 0.0 && px < INFINITY && qx >= 0.0 && qx < INFINITY)) {
+        const float qx = s.qx[i], px = s.px[i], u = s.u[i];
+        if (!(px >= 0.f && px < INFINITY && qx >= 0.f && qx < INFINITY)) {
           bad = 1, work = kTreeEnd;
           break;
         }
-        double r = bare ? (s.again[i] ? 0.0 : px) : fma(-c, qx, px);
-        if (r < 0.0) r = 0.0;
-        const double w = bare || P.replacement ? 1.0 : fmax(1.0 - mass, qx);
-        const double most = qx * Z;
-        const bool yes = r > 0.0 && s.u[i] * most <= r * w;
+        bool yes;
+        float alpha;
+        Pair r, w = one;
+        if (offered == 0 && (bare || P.replacement || qx <= 1.f) && px >= 1e-30f) {
+          // a first child: rest is p and Z is 1, and the sign of u q - p is exact in one fused step
+          r = Pair{px, 0.f};
+          yes = fmaf(u, qx, -px) <= 0.f;
+          alpha = qx > px ? px / qx : 1.f;
+        } else {
+          r = bare ? Pair{s.again[i] ? 0.f : px, 0.f} : rest_of<false>(px, qx, c.s, c.l);
+          if (!bare && !P.replacement) {
+            w.add(-mass.s);
+            w.l -= mass.l;
+            w = w.value() > qx ? w.settled() : Pair{qx, 0.f};
+          }
+          const Pair most = times(Z, Pair{qx, 0.f}), rw = times(r, w);
+          yes = r.value() > 0.f && !above(times(most, Pair{u, 0.f}), rw);
+          alpha = most.value() > 0.f ? (above(most, rw) ? over(rw, most).value() : 1.f) : (r.value() > 0.f ? 1.f : 0.f);
+        }
         if (lane == 0 && rank == 0) {
-          s.alpha[i] = most > 0.0 ? static_cast<float>(fmin(1.0, r * w / most)) : (r > 0.0 ? 1.f : 0.f);
+          s.alpha[i] = alpha;
           s.flag[i] = yes ? SV_FLAG_ACCEPT : SV_FLAG_REJECT;
           if (yes) {
             if (P.path) P.path[static_cast<int64_t>(b) * P.max_depth + len] = i;
@@ -360,22 +397,28 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
         if (yes) {
           ++len;
           cur = i, child = s.first[i + 1];
-          c = 0.0, Z = 1.0, mass = 0.0, offered = 0, summed = false;
+          c = zero, Z = one, mass = zero, offered = 0, summed = false;
           bare = s.drow[cur + 1] < 0;
           continue;
         }
         ++refused;
-        mass += qx;
+        mass.add(qx);
         child = s.next[i];
         if (bare) {
-          Z -= r;
-        } else if (Z > 0.0 || !summed) {
-          if (w > 0.0) c = fmin(c + Z / w, 1e30);
+          Z.add(-r.s);
+          Z = Z.settled();
+        } else if (Z.value() > 0.f || !summed) {
+          if (w.s == 1.f && w.l == 0.f) {
+            c.add(Z);
+          } else if (w.value() > 0.f) {
+            c.add(over(Z, w));
+          }
+          c = c.s < 1e30f ? c.settled() : Pair{1e30f, 0.f};
           summed = true;
           if (lane == 0) {
             s.row_p = P.p + (root + 1 + cur) * P.p_stride;
             s.row_q = P.q + s.drow[cur + 1] * P.q_stride;
-            s.c = c;
+            s.c = c.s, s.cl = c.l;
             s.n_refused = 0;
           }
           work = kTreeSum;
@@ -388,10 +431,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
     chunk_sums<kVec>(s, chunk_sum, P.V, first, last);
     __syncthreads();
     if (tid < 32) {
-      double t = 0.0;
-      for (int i = lane; i < last - first; i += 32) t += chunk_sum[i];
-      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
-      if (lane < ctas) *cluster.map_shared_rank(&s.slot[pass & 1][rank], lane) = t;
+      Pair t = zero;
+      for (int i = lane; i < last - first; i += 32) t.add(Pair{chunk_sum[i].x, chunk_sum[i].y});
+      t = warp_total(t).settled();
+      if (lane < ctas) *cluster.map_shared_rank(&s.slot[pass & 1][rank], lane) = make_float2(t.s, t.l);
     }
     ++pass;
     cluster.sync();
@@ -399,20 +442,20 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
 
   if (tid < 32 && s.work == kTreePick) {
     // the CTA whose part of the row holds u * Z
-    const double* sums = s.slot[(pass - 1) & 1];
-    const double y = static_cast<double>(P.u_pick[b]) * Z;
-    double before = 0.0, mine_before = 0.0;
-    int owner = -1, heavy = 0;
-    for (int r = 0; r < ctas; ++r) {
-      if (r == rank) mine_before = before;
-      if (sums[r] > 0.0) heavy = r;
-      if (owner < 0 && sums[r] > 0.0 && before + sums[r] > y) owner = r;
-      before += sums[r];
+    const float2 f = lane < ctas ? s.slot[(pass - 1) & 1][lane] : make_float2(0.f, 0.f);
+    Pair y = times(Z, Pair{P.u_pick[b], 0.f}), before = zero;
+    const unsigned some = __ballot_sync(~0u, f.x + f.y > 0.f);
+    int owner = lane_past(Pair{f.x, f.y}, y, false, &before);
+    if (owner < 0) {
+      owner = 31 - __clz(some);
+      y = Pair{INFINITY, 0.f};
+    } else {
+      y.add(-before.s);
+      y.l -= before.l;
+      y = y.settled();
     }
-    const bool none = owner < 0;
-    if (none) owner = heavy;
     if (owner == rank) {
-      const int v = pick(s, chunk_sum, P.V, first, last, none ? INFINITY : y - mine_before);
+      const int v = pick(s, chunk_sum, P.V, first, last, y);
       if (lane == 0) P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + len] = v;
     }
   }
@@ -498,7 +541,7 @@ extern "C" sv_status spec_verify_tree(const float* target_probs, int64_t target_
   if (static_cast<int64_t>(B) * ctas > 0x7fffffff) return SV_EUNSUPPORTED;
   const bool vec = reinterpret_cast<uintptr_t>(target_probs) % 16 == 0 && reinterpret_cast<uintptr_t>(draft_probs) % 16 == 0 &&
                    target_stride % 4 == 0 && draft_stride % 4 == 0;
-  const size_t smem = (static_cast<size_t>(P.nchunk) + ctas - 1) / ctas * sizeof(double) + sizeof(double);
+  const size_t smem = (static_cast<size_t>(P.nchunk) + ctas - 1) / ctas * sizeof(float2) + sizeof(float2);
   const auto kernel = vec ? sv::tree_kernel<true> : sv::tree_kernel<false>;
   if (smem > (32u << 10) &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 << 10) != cudaSuccess)
