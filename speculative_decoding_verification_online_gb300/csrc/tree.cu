@@ -226,6 +226,7 @@ __device__ __forceinline__ int lane_past(const Pair& w, const Pair& y, bool any,
 
 // The smallest v of this CTA's chunks whose inclusive prefix sum exceeds y, or the last v with weight when rounding
 // leaves none (or y is infinite): the first warp.
+template <bool kVec>
 __device__ int pick(const TreeShared& s, const float2* chunk_sum, int V, int first, int last, Pair y) {
   const int lane = threadIdx.x & 31;
   Pair before = {0.f, 0.f};
@@ -245,9 +246,31 @@ __device__ int pick(const TreeShared& s, const float2* chunk_sum, int V, int fir
   constexpr int kRun = kTreeChunk / 32;
   const int v0 = ch * kTreeChunk + lane * kRun;
   Pair mine = {0.f, 0.f};
-#pragma unroll 4
-  for (int i = 0; i < kRun; ++i)
-    if (v0 + i < V) mine.add(rest_at(s, v0 + i));
+  float4 p[kRun / 4], q[kRun / 4];
+#pragma unroll
+  for (int j = 0; j < kRun / 4; ++j) p[j] = load4<kVec>(s.row_p, v0 + 4 * j, V);
+  if (s.row_q) {
+#pragma unroll
+    for (int j = 0; j < kRun / 4; ++j) q[j] = load4<kVec>(s.row_q, v0 + 4 * j, V);
+    Pair sum[4] = {};
+#pragma unroll
+    for (int j = 0; j < kRun / 4; ++j) add_rests<false>(sum, p[j], q[j], s.c, s.cl);
+    sum[0].add(sum[1]);
+    sum[2].add(sum[3]);
+    sum[0].add(sum[2]);
+    mine = sum[0];
+  } else if (s.n_refused == 0) {
+#pragma unroll
+    for (int j = 0; j < kRun / 4; ++j) {
+      mine.add(fmaxf(p[j].x, 0.f));
+      mine.add(fmaxf(p[j].y, 0.f));
+      mine.add(fmaxf(p[j].z, 0.f));
+      mine.add(fmaxf(p[j].w, 0.f));
+    }
+  } else {
+    for (int i = 0; i < kRun; ++i)
+      if (v0 + i < V) mine.add(rest_at(s, v0 + i));
+  }
   const int run = lane_past(mine.settled(), y, true, &before);
   const int at = ch * kTreeChunk + run * kRun + lane;
   const Pair w = lane < kRun && at < V ? rest_at(s, at) : Pair{0.f, 0.f};
@@ -455,7 +478,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
       y = y.settled();
     }
     if (owner == rank) {
-      const int v = pick(s, chunk_sum, P.V, first, last, y);
+      const int v = pick<kVec>(s, chunk_sum, P.V, first, last, y);
       if (lane == 0) P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + len] = v;
     }
   }
