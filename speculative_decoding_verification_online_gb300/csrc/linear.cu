@@ -2,8 +2,9 @@
 //
 //   y[g, m, n] = act(sum_k x[g, m, k] w[g, n, k] + bias[g, n]) + residual[g, m, n]
 //
-// Rows of x and w that start at multiples of 16 bytes go through the tensor
-// cores (mma_kernel), others through plain_kernel.
+// The products run on the tensor cores (tcgen05).  Rows of x and w that start at
+// multiples of 16 bytes come in by TMA; where one of the two does not, eight warps
+// of each CTA load both instead.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -79,49 +80,11 @@ __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, 
     static_cast<float*>(P.y)[at] = z;
 }
 
-constexpr int kPlainTile = 64, kPlainK = 32;
-
-// Any sizes, strides and alignment: 64 x 64 tiles of y by 256 threads, each
-// 4 x 4 sums in fp32, elements loaded one by one.
-__global__ void __launch_bounds__(256) plain_kernel(LinearParams P) {
-  __shared__ float sx[kPlainK][kPlainTile + 1], sw[kPlainK][kPlainTile + 1];
-  const int64_t tn = (P.N + kPlainTile - 1) / kPlainTile, tm = (P.M + kPlainTile - 1) / kPlainTile;
-  for (int64_t tile = blockIdx.x; tile < tn * tm * P.groups; tile += gridDim.x) {
-    const int g = static_cast<int>(tile / (tn * tm));
-    const int64_t m0 = tile / tn % tm * kPlainTile, n0 = tile % tn * kPlainTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < P.K; k0 += kPlainK) {
-      for (int i = threadIdx.x; i < kPlainK * kPlainTile; i += 256) {
-        const int kk = i % kPlainK, r = i / kPlainK;
-        const bool in = k0 + kk < P.K;
-        sx[kk][r] = in && m0 + r < P.M ? __bfloat162float(P.x[g * P.x_group + (m0 + r) * P.x_row + k0 + kk]) : 0.f;
-        sw[kk][r] = in && n0 + r < P.N ? __bfloat162float(P.w[g * P.w_group + (n0 + r) * P.w_row + k0 + kk]) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll 8
-      for (int kk = 0; kk < kPlainK; ++kk)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) acc[i][j] += sx[kk][ty + 16 * i] * sw[kk][tx + 16 * j];
-      __syncthreads();
-    }
-    with_activation(P.act, [&](auto act) {
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-          if (m0 + ty + 16 * i < P.M && n0 + tx + 16 * j < P.N) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            finish_value<act.value>(P, g * P.y_group + m * P.y_row + n, acc[i][j], load_bias(P, g, n),
-                                    load_residual(P, g, m, n));
-          }
-    });
-  }
-}
-
 // ------------------------------------------------------------ tensor cores
 //
 // Persistent CTAs, one per SM, each (or each pair) taking every n-th tile of y.  Warp 0
 // fetches tiles of both operands by TMA into a ring of stages, 64 entries of
-// K at a time (rows of 128 bytes, 128-byte swizzle); warp 1 multiplies them
+// K at a time (rows of 128 bytes, 128-byte swizzle), or warps 10 to 17 load them; warp 1 multiplies them
 // into tensor memory, 128 rows of one operand (A) by nt rows of the other (B);
 // warps 2 to 9 take the sums out and finish them while the next tile is
 // multiplied into the other half of the accumulators.
@@ -131,7 +94,7 @@ __global__ void __launch_bounds__(256) plain_kernel(LinearParams P) {
 //    pair of SMs): each holds 128 rows of A and half the rows of B, and one
 //    product instruction of the first CTA works on both.  A lane of tensor
 //    memory is one n, so a warp's 32 lanes write 32 neighbours of y for each m,
-//    straight from registers.
+//    straight from registers.  (Stages that warps load are not shared by pairs.)
 //  * M <= 128: x.  The call is bound by reading w, and the width of a tile of
 //    w is then free (any multiple of 16 up to 256), so that the tiles come out
 //    even over the SMs.  Lanes are tokens here; sums pass through shared memory
@@ -144,6 +107,7 @@ constexpr int kMmaK = 64;        // entries of K a stage holds of each row: 128 
 constexpr int kRowBytes = 128;
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
+constexpr int kLoadWarps = 8;
 constexpr int kMmaThreads = 32 * (2 + kEpiWarps);
 constexpr int kStageCols = 64;   // columns of a tile that the epilogue passes through shared memory at a time
 constexpr int kMmaSmem = 225 * 1024;
@@ -255,12 +219,70 @@ __device__ __forceinline__ TileAt tile_at(const MmaParams& P, unsigned t) {
   return {static_cast<int>(rest % P.tiles_a), static_cast<int>(tb), static_cast<int>(rest / P.tiles_a)};
 }
 
-// kWeightsA: w is A, and the CTAs work in pairs
-template <bool kWeightsA>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+// Eight entries of a row from any address that bf16 entries have, in the one or two aligned blocks of 16 bytes that hold
+// them.  Only blocks with an entry of the row are read: an allocation has all of such a block.
+struct Run {
+  uint4 a, b;
+  int shift;  // bytes in front of the first entry
+
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int valid) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint4* block = reinterpret_cast<const uint4*>(at & ~uintptr_t{15});
+    shift = static_cast<int>(at & 15);
+    a = valid > 0 ? block[0] : make_uint4(0, 0, 0, 0);
+    b = shift + 2 * valid > 16 ? block[1] : make_uint4(0, 0, 0, 0);
+  }
+
+  // the entries, zeros behind the valid ones
+  __device__ __forceinline__ uint4 entries(int valid) const {
+    const bool two = shift & 8, one = shift & 4;
+    const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w,
+                   w4 = two ? b.z : b.x, w5 = two ? b.w : b.y;
+    const uint32_t v0 = one ? w1 : w0, v1 = one ? w2 : w1, v2 = one ? w3 : w2, v3 = one ? w4 : w3, v4 = one ? w5 : w4;
+    const int bits = (shift & 2) * 8;
+    uint4 r = make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits), __funnelshift_r(v2, v3, bits),
+                         __funnelshift_r(v3, v4, bits));
+    if (valid < 8) {
+      r.x &= valid > 1 ? ~0u : valid > 0 ? 0xffffu : 0u;
+      r.y &= valid > 3 ? ~0u : valid > 2 ? 0xffffu : 0u;
+      r.z &= valid > 5 ? ~0u : valid > 4 ? 0xffffu : 0u;
+      r.w &= valid > 7 ? ~0u : valid > 6 ? 0xffffu : 0u;
+    }
+    return r;
+  }
+};
+
+// A warp's share (warp `mine` of the loading ones) of `rows` rows of 64 entries from k on, zeros beyond row `there` and
+// entry `K`, as TMA would lay them down: 16 bytes a lane, eight lanes a row.
+__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* p, int64_t stride, int rows, int64_t there,
+                                          int k, int K, int mine) {
+  const int lane = threadIdx.x & 31, c = lane % 8;
+  const int valid = max(0, min(8, K - k - 8 * c));
+  constexpr int kBatch = 4, kStep = 4 * kLoadWarps;
+  int r0 = 4 * mine + lane / 8;
+  p += r0 * stride + k + 8 * c;
+  for (; r0 < rows; r0 += kBatch * kStep, p += kBatch * kStep * stride) {
+    Run v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) v[i].load(p + i * kStep * stride, r0 + i * kStep < there ? valid : 0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = r0 + i * kStep;
+      const uint4 e = v[i].entries(valid);
+      if (r < rows)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * kRowBytes + ((c ^ (r & 7)) << 4)),
+                     "r"(e.x), "r"(e.y), "r"(e.z), "r"(e.w)
+                     : "memory");
+    }
+  }
+}
+
+// kWeightsA: w is A.  kLoad: warps load the stages; otherwise TMA does, and where w is A the CTAs work in pairs.
+template <bool kWeightsA, bool kLoad>
+__global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1)
     mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
-  constexpr bool kPair = kWeightsA;
+  constexpr bool kPair = kWeightsA && !kLoad;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
@@ -272,13 +294,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
   const uint32_t a_bytes = P.ra * kRowBytes, stage_bytes = a_bytes + b_rows * kRowBytes;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], kLoad ? kLoadWarps : 1), mbar_init(&empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], kPair ? 2 * kEpiWarps : kEpiWarps);
     mbar_init(&drained, 1);
     dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a));
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b));
+    if constexpr (!kLoad) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a));
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b));
+    }
   }
   if (warp == 1) {
     if constexpr (kPair) {
@@ -303,7 +327,34 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   // Warps 0 and 1 go through their loops as whole warps, and one lane that elect
   // picks issues: with a branch on the lane instead the compiler takes the
   // operands for different in every lane, and an issue costs several times as much.
-  if (warp == 0) {
+  if (kLoad && warp >= 2 + kEpiWarps) {
+    // Every warp takes part in every stage.  (Warps that took whole stages in turn could come to a stage two phases
+    // early where there were more of them than stages, and a parity does not tell two phases from none.)
+    const int mine = warp - 2 - kEpiWarps;
+    unsigned s = 0, phase = 1;
+    for (unsigned t = first; t < P.tiles && !dead; t += step) {
+      const TileAt at = tile_at(P, t);
+      const int64_t m0 = kWeightsA ? static_cast<int64_t>(at.tb) * P.nt : 0;
+      const int64_t n0 = kWeightsA ? static_cast<int64_t>(at.ta) * 128 : static_cast<int64_t>(at.tb) * P.nt;
+      const __nv_bfloat16* x = P.L.x + at.g * P.L.x_group + m0 * P.L.x_row;
+      const __nv_bfloat16* w = P.L.w + at.g * P.L.w_group + n0 * P.L.w_row;
+      for (int kb = 0; kb < P.kblocks; ++kb) {
+        if (!mbar_wait(&empty[s], phase, &dead)) break;
+        const uint32_t dst = base + s * stage_bytes;
+        load_rows(kWeightsA ? dst : dst + a_bytes, w, P.L.w_row, kWeightsA ? P.ra : P.nt, P.L.N - n0, kb * kMmaK, P.L.K,
+                  mine);
+        load_rows(kWeightsA ? dst + a_bytes : dst, x, P.L.x_row, kWeightsA ? P.nt : P.ra, P.L.M - m0, kb * kMmaK, P.L.K,
+                  mine);
+        // the tensor core reads what these stores wrote
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
+      }
+    }
+  } else if (kLoad && warp == 0) {
+    // nothing to fetch
+  } else if (warp == 0) {
     // stage and phase go round by counting: a division by the number of stages
     // costs more than everything else that a stage needs
     unsigned s = 0, phase = 1, fill = 0;
@@ -340,7 +391,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         mbar_wait(&full[f % P.stages], (f / P.stages) & 1, &gave_up);
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && P.kblocks > 0) {
       unsigned s = 0, phase = 0, n = 0;
       const uint64_t desc_a = smem_desc(base), desc_b = smem_desc(base + a_bytes);
       const unsigned desc_step = stage_bytes / 16;
@@ -376,15 +427,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const int et = threadIdx.x - 64;
     float* staging = reinterpret_cast<float*>(smem + P.staging);
     unsigned n = 0;
+    auto sum = [&](bool ok, float v) { return !ok ? NAN : P.kblocks == 0 ? 0.f : v; };  // no entries: no product ran
     for (unsigned t = first; t < P.tiles; t += step, ++n) {
       const TileAt at = tile_at(P, t);
       const unsigned buf = n & 1;
       const uint32_t acc = tmem + buf * P.nt + (static_cast<uint32_t>(quad * 32) << 16);
       if constexpr (kWeightsA) {
-        const int64_t col = static_cast<int64_t>(at.ta) * 256 + rank * 128 + quad * 32 + lane;
+        const int64_t col = static_cast<int64_t>(at.ta) * (kPair ? 256 : 128) + rank * 128 + quad * 32 + lane;
         const bool in = col < P.L.N;
         const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
-        const bool ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
+        const bool ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         with_activation(P.L.act, [&](auto act) {
 #pragma unroll 1
@@ -400,15 +452,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + col;
 #pragma unroll
             for (int i = 0; i < 16; ++i, to += P.L.y_row)
-              if (i < rows) finish_value<act.value>(P.L, to, ok ? v[i] : NAN, bias, r[i]);
+              if (i < rows) finish_value<act.value>(P.L, to, sum(ok, v[i]), bias, r[i]);
           }
         });
       } else {
         const int cols = min(P.nt, static_cast<int>(P.L.N - static_cast<int64_t>(at.tb) * P.nt));
-        // each thread finishes one column of every fourth token, eight tokens at a time:
-        // the first ones' residuals come in before the sums do
+        // each thread finishes one column of every fourth token, sixteen tokens at a time.  Residuals are asked into
+        // L2 while the products run, and the first ones are in registers before the sums come.
         const int c = et % kStageCols, row = et / kStageCols;
-        constexpr int kRows = kEpiWarps * 32 / kStageCols;
+        constexpr int kRows = kEpiWarps * 32 / kStageCols, kBatch = 16;
+        if (P.L.res && c % 16 == 0)
+          for (int c0 = c; c0 < cols; c0 += kStageCols)
+            for (int m = row; m < P.L.M; m += kRows) {
+              const int64_t i = at.g * P.L.r_group + m * P.L.r_row + static_cast<int64_t>(at.tb) * P.nt + c0;
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(P.L.res) + i * (P.L.res_bf16 ? 2 : 4)));
+            }
         bool ok = true;
         with_activation(P.L.act, [&](auto act) {
 #pragma unroll 1
@@ -416,15 +474,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int64_t col = static_cast<int64_t>(at.tb) * P.nt + c0 + c;
             const int rows = c0 + c < cols ? P.L.M : 0;
             const float bias = rows ? load_bias(P.L, at.g, col) : 0.f;
-            float r[8];
+            float r[kBatch];
             auto residuals = [&](int m0) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < kBatch; ++i)
                 r[i] = P.L.res && m0 + i * kRows < rows ? load_residual(P.L, at.g, m0 + i * kRows, col) : 0.f;
             };
             residuals(row);
             if (c0 == 0) {
-              ok = !dead && mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead);
+              ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead));
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
             if (quad * 32 < P.L.M)
@@ -436,19 +494,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (quad * 32 + lane < P.L.M)
 #pragma unroll
                   for (int i = 0; i < 16; ++i)
-                    staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = ok ? v[i] : NAN;
+                    staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = sum(ok, v[i]);
               }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
 #pragma unroll 1
-            for (int m0 = row; m0 < P.L.M; m0 += 8 * kRows) {
+            for (int m0 = row; m0 < P.L.M; m0 += kBatch * kRows) {
               if (m0 != row) residuals(m0);
-              float v[8];
+              float v[kBatch];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < kBatch; ++i)
                 v[i] = m0 + i * kRows < rows ? staging[(m0 + i * kRows) * (kStageCols + 1) + c] : 0.f;
               int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + col;
 #pragma unroll
-              for (int i = 0; i < 8; ++i, to += kRows * P.L.y_row)
+              for (int i = 0; i < kBatch; ++i, to += kRows * P.L.y_row)
                 if (m0 + i * kRows < rows) finish_value<act.value>(P.L, to, v[i], bias, r[i]);
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
@@ -527,10 +585,9 @@ bool make_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64
 // core, and the rows of 128 bytes that the SM fetches for it come in at about 46
 // bytes a cycle; the SMs (or pairs of them) take their tiles in waves, and each
 // wave pays for starting and ending.
-int choose_width(bool pair, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, int64_t kblocks, int sms) {
+int choose_width(bool pair, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, int64_t kblocks, int workers) {
   int best = 16;
   double least = 1e300;
-  const int workers = pair ? std::max(1, sms / 2) : sms;
   for (int nt = 16; nt <= 256; nt += 16) {
     const int64_t tiles = (rows_b + nt - 1) / nt * tiles_a * groups;
     const int64_t waves = (tiles + workers - 1) / workers;
@@ -541,29 +598,31 @@ int choose_width(bool pair, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t
   return best;
 }
 
-template <bool kWeightsA>
-cudaError_t launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st, bool* taken) {
-  constexpr bool kPair = kWeightsA;
-  *taken = false;
+template <bool kWeightsA, bool kLoad>
+sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st) {
+  constexpr bool kPair = kWeightsA && !kLoad;
   MmaParams P = {};
   P.L = L;
-  P.kblocks = (L.K + kMmaK - 1) / kMmaK;
+  P.kblocks = static_cast<int>((static_cast<int64_t>(L.K) + kMmaK - 1) / kMmaK);
   P.ra = kWeightsA ? 128 : (L.M + 7) / 8 * 8;
   const int64_t rows_a = kWeightsA ? L.N : L.M, rows_b = kWeightsA ? L.M : L.N;
+  const int workers = kPair ? std::max(1, sms / 2) : sms;
   P.tiles_a = static_cast<int>((rows_a + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
-  P.nt = choose_width(kPair, rows_b, P.tiles_a, P.ra, L.groups, P.kblocks, sms);
+  P.nt = choose_width(kPair, rows_b, P.tiles_a, P.ra, L.groups, P.kblocks, workers);
   P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
   const int64_t tiles = static_cast<int64_t>(P.tiles_a) * P.tiles_b * L.groups;
-  if (tiles >= (int64_t{1} << 31)) return cudaSuccess;
+  if (tiles >= (int64_t{1} << 31)) return SV_EUNSUPPORTED;
   P.tiles = static_cast<unsigned>(tiles);
   const int b_rows = kPair ? P.nt / 2 : P.nt;
-  CUtensorMap map_x, map_w;
-  int gx = 0, gw = 0;
-  if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? b_rows : P.ra, &gx) ||
-      !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : b_rows, &gw))
-    return cudaSuccess;
-  P.a_groups = kWeightsA ? gw : gx;
-  P.b_groups = kWeightsA ? gx : gw;
+  CUtensorMap map_x = {}, map_w = {};
+  if constexpr (!kLoad) {
+    int gx = 0, gw = 0;
+    if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? b_rows : P.ra, &gx) ||
+        !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : b_rows, &gw))
+      return launch_mma<kWeightsA, true>(L, device, sms, st);
+    P.a_groups = kWeightsA ? gw : gx;
+    P.b_groups = kWeightsA ? gx : gw;
+  }
   const int stage_bytes = (P.ra + b_rows) * kRowBytes;
   const int staging = kWeightsA ? 0 : L.M * (kStageCols + 1) * 4;
   // a product reads 128 rows of A from the last stage on: they stay inside the allocation
@@ -578,16 +637,15 @@ cudaError_t launch_mma(const LinearParams& L, int device, int sms, cudaStream_t 
   // once a device
   static std::atomic<bool> opted_in[64];
   if (device >= 64 || !opted_in[device].load()) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(mma_kernel<kWeightsA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
-    if (e != cudaSuccess) return e;
+    if (cudaFuncSetAttribute(mma_kernel<kWeightsA, kLoad>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem) !=
+        cudaSuccess)
+      return SV_ECUDA;
     if (device < 64) opted_in[device].store(true);
   }
-  *taken = true;
-  const unsigned grid = static_cast<unsigned>(kPair ? 2 * std::min<int64_t>(tiles, std::max(1, sms / 2))
-                                                    : std::min<int64_t>(tiles, sms));
-  return launch_waiting(mma_kernel<kWeightsA>, grid, kMmaThreads, smem, kPair ? 2 : 1, st, P,
-                        kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, workers)) * (kPair ? 2 : 1);
+  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad>, grid, kMmaThreads + (kLoad ? 32 * kLoadWarps : 0),
+                                       smem, kPair ? 2 : 1, st, P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
+  return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
 bool valid_dtype(int d) { return d == SV_F32 || d == SV_BF16; }
@@ -644,18 +702,8 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   P.act = act;
   P.cap = cap;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (K > 0) {
-    int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
-    bool taken = false;
-    const cudaError_t e =
-        M > 128 ? sv::launch_mma<true>(P, device, sms, st, &taken) : sv::launch_mma<false>(P, device, sms, st, &taken);
-    if (e != cudaSuccess) return SV_ECUDA;
-    if (taken) return SV_OK;
-  }
-  const int64_t tiles = (static_cast<int64_t>(N) + sv::kPlainTile - 1) / sv::kPlainTile *
-                        ((static_cast<int64_t>(M) + sv::kPlainTile - 1) / sv::kPlainTile) * groups;
-  const unsigned grid = static_cast<unsigned>(tiles < (1 << 20) ? tiles : (1 << 20));
-  sv::plain_kernel<<<grid, 256, 0, st>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
+  if (K == 0) return M > 128 ? sv::launch_mma<true, true>(P, device, sms, st) : sv::launch_mma<false, true>(P, device, sms, st);
+  return M > 128 ? sv::launch_mma<true, false>(P, device, sms, st) : sv::launch_mma<false, false>(P, device, sms, st);
 }
