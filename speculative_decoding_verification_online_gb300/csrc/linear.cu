@@ -221,6 +221,17 @@ __device__ __forceinline__ TileAt tile_at(const MmaParams& P, unsigned t) {
 
 // Eight entries of a row from any address that bf16 entries have, in the one or two aligned blocks of 16 bytes that hold
 // them.  Only blocks with an entry of the row are read: an allocation has all of such a block.
+__device__ __forceinline__ uint4 load_if(const uint4* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
+      " mov.u32 %3, 0;\n @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<unsigned>(there))
+      : "memory");
+  return v;
+}
+
 struct Run {
   uint4 a, b;
   int shift;  // bytes in front of the first entry
@@ -229,8 +240,8 @@ struct Run {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
     const uint4* block = reinterpret_cast<const uint4*>(at & ~uintptr_t{15});
     shift = static_cast<int>(at & 15);
-    a = valid > 0 ? block[0] : make_uint4(0, 0, 0, 0);
-    b = shift + 2 * valid > 16 ? block[1] : make_uint4(0, 0, 0, 0);
+    a = load_if(block, valid > 0);
+    b = load_if(block + 1, shift + 2 * valid > 16);
   }
 
   // the entries, zeros behind the valid ones
@@ -345,8 +356,6 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
                   mine);
         load_rows(kWeightsA ? dst + a_bytes : dst, x, P.L.x_row, kWeightsA ? P.nt : P.ra, P.L.M - m0, kb * kMmaK, P.L.K,
                   mine);
-        // the tensor core reads what these stores wrote
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
         if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
@@ -402,6 +411,9 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
         const uint32_t d = tmem + buf * P.nt;
         for (int kb = 0; kb < P.kblocks; ++kb) {
           if (!mbar_wait(&full[s], phase, &dead)) break;
+          // What warps stored is now seen here; the tensor core reads it by another way.  The fence stands here because in
+          // a loading warp it would wait for the loads on their way.
+          if constexpr (kLoad) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
             const uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
