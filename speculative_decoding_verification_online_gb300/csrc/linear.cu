@@ -41,10 +41,10 @@ __device__ __forceinline__ float load_either(const void* p, int64_t i, int bf16)
 template <int kAct>
 __device__ __forceinline__ float activate(float z, float cap) {
   if constexpr (kAct == SV_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-  if constexpr (kAct == SV_ACT_SILU) return z / (1.f + expf(-z));
+  if constexpr (kAct == SV_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
   if constexpr (kAct == SV_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
   // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
-  if constexpr (kAct == SV_ACT_GELU_TANH) return z / (1.f + expf(-1.59576912f * (z + 0.044715f * z * z * z)));
+  if constexpr (kAct == SV_ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-1.59576912f * (z + 0.044715f * z * z * z)));
   if constexpr (kAct == SV_ACT_SOFTCAP) return cap * tanhf(z / cap);
   return z;
 }
@@ -68,6 +68,10 @@ __device__ __forceinline__ float load_bias(const LinearParams& P, int g, int64_t
 
 __device__ __forceinline__ float load_residual(const LinearParams& P, int g, int64_t m, int64_t n) {
   return P.res ? load_either(P.res, g * P.r_group + m * P.r_row + n, P.res_bf16) : 0.f;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p, int64_t i, int bf16) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + i * (bf16 ? 2 : 4)));
 }
 
 // The sum's way out: the one rounding to bf16, where y is bf16, is the last step.
@@ -469,30 +473,35 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
         });
       } else {
         const int cols = min(P.nt, static_cast<int>(P.L.N - static_cast<int64_t>(at.tb) * P.nt));
-        // each thread finishes one column of every fourth token, sixteen tokens at a time.  Residuals are asked into
-        // L2 while the products run, and the first ones are in registers before the sums come.
+        // Each thread finishes one column of every fourth token, sixteen tokens at a time.  Biases and residuals are
+        // asked into L2 while the products run; the first ones are in registers before the sums come, and each chunk's
+        // before the chunk in front of it is finished.
         const int c = et % kStageCols, row = et / kStageCols;
         constexpr int kRows = kEpiWarps * 32 / kStageCols, kBatch = 16;
-        if (P.L.res && c % 16 == 0)
-          for (int c0 = c; c0 < cols; c0 += kStageCols)
-            for (int m = row; m < P.L.M; m += kRows) {
-              const int64_t i = at.g * P.L.r_group + m * P.L.r_row + static_cast<int64_t>(at.tb) * P.nt + c0;
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(P.L.res) + i * (P.L.res_bf16 ? 2 : 4)));
-            }
+        const int64_t n0 = static_cast<int64_t>(at.tb) * P.nt;
+        if (c % 16 == 0)
+          for (int c0 = c; c0 < cols; c0 += kStageCols) {
+            if (P.L.bias && row == 0)
+              prefetch_l2(P.L.bias, at.g * P.L.b_group + n0 + c0, P.L.bias_bf16);
+            for (int m = row; P.L.res && m < P.L.M; m += kRows)
+              prefetch_l2(P.L.res, at.g * P.L.r_group + m * P.L.r_row + n0 + c0, P.L.res_bf16);
+          }
         bool ok = true;
         with_activation(P.L.act, [&](auto act) {
+          float r[kBatch], r_next[kBatch], bias, bias_next = 0.f;
+          auto residuals = [&](float (&to)[kBatch], int c0, int m0) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int m = m0 + i * kRows;
+              to[i] = P.L.res && c0 + c < cols && m < P.L.M ? load_residual(P.L, at.g, m, n0 + c0 + c) : 0.f;
+            }
+          };
+          auto biases = [&](int c0) { return c0 + c < cols ? load_bias(P.L, at.g, n0 + c0 + c) : 0.f; };
+          residuals(r_next, 0, row);
+          bias_next = biases(0);
 #pragma unroll 1
           for (int c0 = 0; c0 < cols; c0 += kStageCols) {
-            const int64_t col = static_cast<int64_t>(at.tb) * P.nt + c0 + c;
             const int rows = c0 + c < cols ? P.L.M : 0;
-            const float bias = rows ? load_bias(P.L, at.g, col) : 0.f;
-            float r[kBatch];
-            auto residuals = [&](int m0) {
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i)
-                r[i] = P.L.res && m0 + i * kRows < rows ? load_residual(P.L, at.g, m0 + i * kRows, col) : 0.f;
-            };
-            residuals(row);
             if (c0 == 0) {
               ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead));
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -509,14 +518,21 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
                     staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = sum(ok, v[i]);
               }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+            bias = bias_next;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) r[i] = r_next[i];
+            if (c0 + kStageCols < cols) {
+              residuals(r_next, c0 + kStageCols, row);
+              bias_next = biases(c0 + kStageCols);
+            }
 #pragma unroll 1
             for (int m0 = row; m0 < P.L.M; m0 += kBatch * kRows) {
-              if (m0 != row) residuals(m0);
+              if (m0 != row) residuals(r, c0, m0);
               float v[kBatch];
 #pragma unroll
               for (int i = 0; i < kBatch; ++i)
                 v[i] = m0 + i * kRows < rows ? staging[(m0 + i * kRows) * (kStageCols + 1) + c] : 0.f;
-              int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + col;
+              int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + n0 + c0 + c;
 #pragma unroll
               for (int i = 0; i < kBatch; ++i, to += kRows * P.L.y_row)
                 if (m0 + i * kRows < rows) finish_value<act.value>(P.L, to, v[i], bias, r[i]);
