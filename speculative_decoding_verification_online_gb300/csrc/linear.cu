@@ -121,7 +121,9 @@ struct MmaParams {
   int nt;                // rows of B in a tile
   int ra;                // rows of A that are fetched
   int stages, tmem_cols;
-  int tiles_a, tiles_b, kblocks;
+  int tiles_a, tiles_b;
+  int sub;               // blocks of 64 entries of K in a stage
+  int kblocks;           // stages that K takes
   int a_groups, b_groups;  // 0: the operand is shared by all groups
   unsigned tiles;
   unsigned idesc;
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
   const unsigned first = kPair ? blockIdx.x / 2 : blockIdx.x, step = kPair ? gridDim.x / 2 : gridDim.x;
   const int b_rows = kPair ? P.nt / 2 : P.nt;  // of B in this CTA
   const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
-  const uint32_t a_bytes = P.ra * kRowBytes, stage_bytes = a_bytes + b_rows * kRowBytes;
+  const uint32_t a_bytes = P.ra * kRowBytes, sub_bytes = a_bytes + b_rows * kRowBytes, stage_bytes = P.sub * sub_bytes;
   if (threadIdx.x == 0) {
     for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], kLoad ? kLoadWarps : 1), mbar_init(&empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], kPair ? 2 * kEpiWarps : kEpiWarps);
@@ -377,19 +379,23 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
       const int ga = P.a_groups ? at.g : 0, gb = P.b_groups ? at.g : 0;
       const int row_a = kPair ? at.ta * 256 + static_cast<int>(rank) * 128 : 0;
       const int row_b = at.tb * P.nt + (kPair ? static_cast<int>(rank) * b_rows : 0);
-      for (int kb = 0, k = 0; kb < P.kblocks; ++kb, k += kMmaK) {
+      for (int kb = 0, k = 0; kb < P.kblocks; ++kb, k += P.sub * kMmaK) {
         if (!mbar_wait(&empty[s], phase, &dead)) break;
         if (elect_one()) {
-          const uint32_t dst = base + s * stage_bytes;
+          uint32_t dst = base + s * stage_bytes;
           if constexpr (kPair) {
             const uint32_t bar = leader + s * 8;
             if (rank == 0) mbar_expect(&full[s], 2 * stage_bytes);
-            tma_load_pair(&map_a, dst, bar, k, row_a, ga);
-            tma_load_pair(&map_b, dst + a_bytes, bar, k, row_b, gb);
+            for (int u = 0; u < P.sub; ++u, dst += sub_bytes) {
+              tma_load_pair(&map_a, dst, bar, k + u * kMmaK, row_a, ga);
+              tma_load_pair(&map_b, dst + a_bytes, bar, k + u * kMmaK, row_b, gb);
+            }
           } else {
             mbar_expect(&full[s], stage_bytes);
-            tma_load(&map_a, dst, &full[s], k, 0, ga);
-            tma_load(&map_b, dst + a_bytes, &full[s], k, row_b, gb);
+            for (int u = 0; u < P.sub; ++u, dst += sub_bytes) {
+              tma_load(&map_a, dst, &full[s], k + u * kMmaK, 0, ga);
+              tma_load(&map_b, dst + a_bytes, &full[s], k + u * kMmaK, row_b, gb);
+            }
           }
         }
         __syncwarp();
@@ -420,10 +426,12 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
           if constexpr (kLoad) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
-            const uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
-            tc_mma<kPair>(d, da, db, P.idesc, kb > 0);
+            uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
+            for (int u = 0; u < P.sub; ++u, da += sub_bytes / 16, db += sub_bytes / 16) {
+              tc_mma<kPair>(d, da, db, P.idesc, kb > 0 || u > 0);
 #pragma unroll
-            for (int k = 1; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, true);
+              for (int k = 1; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, true);
+            }
             tc_commit<kPair>(&empty[s]);
             if (kb == P.kblocks - 1) tc_commit<kPair>(&acc_full[buf]);
           }
@@ -631,12 +639,12 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   constexpr bool kPair = kWeightsA && !kLoad;
   MmaParams P = {};
   P.L = L;
-  P.kblocks = static_cast<int>((static_cast<int64_t>(L.K) + kMmaK - 1) / kMmaK);
+  const int64_t blocks = (static_cast<int64_t>(L.K) + kMmaK - 1) / kMmaK;
   P.ra = kWeightsA ? 128 : (L.M + 7) / 8 * 8;
   const int64_t rows_a = kWeightsA ? L.N : L.M, rows_b = kWeightsA ? L.M : L.N;
   const int workers = kPair ? std::max(1, sms / 2) : sms;
   P.tiles_a = static_cast<int>((rows_a + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
-  P.nt = choose_width(kPair, rows_b, P.tiles_a, P.ra, L.groups, P.kblocks, workers);
+  P.nt = choose_width(kPair, rows_b, P.tiles_a, P.ra, L.groups, blocks, workers);
   P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
   const int64_t tiles = static_cast<int64_t>(P.tiles_a) * P.tiles_b * L.groups;
   if (tiles >= (int64_t{1} << 31)) return SV_EUNSUPPORTED;
@@ -651,11 +659,20 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
     P.a_groups = kWeightsA ? gw : gx;
     P.b_groups = kWeightsA ? gx : gw;
   }
-  const int stage_bytes = (P.ra + b_rows) * kRowBytes;
+  const int sub_bytes = (P.ra + b_rows) * kRowBytes;
   const int staging = kWeightsA ? 0 : L.M * (kStageCols + 1) * 4;
-  // a product reads 128 rows of A from the last stage on: they stay inside the allocation
-  const int slack = std::max(0, 128 * kRowBytes - stage_bytes);
-  P.stages = std::min(kMaxStages, (kMmaSmem - 1024 - staging - slack) / stage_bytes);
+  // a product reads 128 rows of A from a stage's last block on: they stay inside the allocation
+  const int slack = std::max(0, 128 * kRowBytes - sub_bytes);
+  const int room = kMmaSmem - 1024 - staging - slack;
+  // Two or four blocks of K to a stage, as far as four stages fit: waiting for a stage and releasing it costs the issuing
+  // warp as much as the products of a block (N = 2048 in 4 groups, K = 2048, M = 1: 12.5 us with one, 9.1 us with four;
+  // M = 384, N = 128256, K = 4096: 253 us with one, 241 us with two; three stages are too few: M = 256, N = 32000, K =
+  // 4096 53.2 us with one block, 56.8 us with two).
+  P.sub = 1;
+  while (!kLoad && P.sub < 4 && P.sub < blocks && 2 * P.sub * sub_bytes * 4 <= room) P.sub *= 2;
+  P.kblocks = static_cast<int>((blocks + P.sub - 1) / P.sub);
+  const int stage_bytes = P.sub * sub_bytes;
+  P.stages = std::min(kMaxStages, room / stage_bytes);
   P.staging = 1024 + P.stages * stage_bytes + slack;
   const int smem = static_cast<int>(P.staging) + staging;
   P.tmem_cols = 32;
