@@ -34,8 +34,26 @@ struct LinearParams {
   float cap, inv_cap;
 };
 
+// An fp32 or bf16 entry as its bits; shifted up by wide(bf16) they are the fp32 value.  Several entries are loaded under
+// one branch on the type: a branch for each would wait for each.
+__device__ __forceinline__ uint32_t bits_f32(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
+__device__ __forceinline__ uint32_t bits_bf16(const void* p, int64_t i) { return static_cast<const uint16_t*>(p)[i]; }
+__device__ __forceinline__ int wide(int bf16) { return bf16 ? 16 : 0; }
+
 __device__ __forceinline__ float load_either(const void* p, int64_t i, int bf16) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+  return __uint_as_float((bf16 ? bits_bf16(p, i) : bits_f32(p, i)) << wide(bf16));
+}
+
+// entries i, i + step, .. of the first n of kCount, 0 behind them
+template <int kCount>
+__device__ __forceinline__ void load_entries(uint32_t (&r)[kCount], const void* p, int64_t i, int64_t step, int n, int bf16) {
+  if (bf16) {
+#pragma unroll
+    for (int k = 0; k < kCount; ++k, i += step) r[k] = k < n ? bits_bf16(p, i) : 0u;
+  } else {
+#pragma unroll
+    for (int k = 0; k < kCount; ++k, i += step) r[k] = k < n ? bits_f32(p, i) : 0u;
+  }
 }
 
 // tanh to about 8 half steps: its series below 1/4, 1 - 2 / (1 + exp 2x) above
@@ -57,16 +75,24 @@ __device__ __forceinline__ float activate(float z, float cap, float inv_cap) {
   return z;
 }
 
-// f with the activation as a constant: code that a call does not use is not fetched either
+// f with the activation and y's type as constants: code that a call does not use is not fetched either
+template <int kAct, typename F>
+__device__ __forceinline__ void with_type(int y_bf16, F&& f) {
+  if (y_bf16)
+    f(std::integral_constant<int, kAct>(), std::true_type());
+  else
+    f(std::integral_constant<int, kAct>(), std::false_type());
+}
+
 template <typename F>
-__device__ __forceinline__ void with_activation(int act, F&& f) {
+__device__ __forceinline__ void with_epilogue(int act, int y_bf16, F&& f) {
   switch (act) {
-    case SV_ACT_RELU: f(std::integral_constant<int, SV_ACT_RELU>()); break;
-    case SV_ACT_SILU: f(std::integral_constant<int, SV_ACT_SILU>()); break;
-    case SV_ACT_GELU: f(std::integral_constant<int, SV_ACT_GELU>()); break;
-    case SV_ACT_GELU_TANH: f(std::integral_constant<int, SV_ACT_GELU_TANH>()); break;
-    case SV_ACT_SOFTCAP: f(std::integral_constant<int, SV_ACT_SOFTCAP>()); break;
-    default: f(std::integral_constant<int, SV_ACT_NONE>());
+    case SV_ACT_RELU: with_type<SV_ACT_RELU>(y_bf16, f); break;
+    case SV_ACT_SILU: with_type<SV_ACT_SILU>(y_bf16, f); break;
+    case SV_ACT_GELU: with_type<SV_ACT_GELU>(y_bf16, f); break;
+    case SV_ACT_GELU_TANH: with_type<SV_ACT_GELU_TANH>(y_bf16, f); break;
+    case SV_ACT_SOFTCAP: with_type<SV_ACT_SOFTCAP>(y_bf16, f); break;
+    default: with_type<SV_ACT_NONE>(y_bf16, f);
   }
 }
 
@@ -74,19 +100,15 @@ __device__ __forceinline__ float load_bias(const LinearParams& P, int g, int64_t
   return P.bias ? load_either(P.bias, g * P.b_group + n, P.bias_bf16) : 0.f;
 }
 
-__device__ __forceinline__ float load_residual(const LinearParams& P, int g, int64_t m, int64_t n) {
-  return P.res ? load_either(P.res, g * P.r_group + m * P.r_row + n, P.res_bf16) : 0.f;
-}
-
 __device__ __forceinline__ void prefetch_l2(const void* p, int64_t i, int bf16) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + i * (bf16 ? 2 : 4)));
 }
 
 // The sum's way out: the one rounding to bf16, where y is bf16, is the last step.
-template <int kAct>
+template <int kAct, bool kBf16>
 __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, float z, float bias, float res) {
   z = activate<kAct>(z + bias, P.cap, P.inv_cap) + res;
-  if (P.y_bf16)
+  if constexpr (kBf16)
     static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16(z);
   else
     static_cast<float*>(P.y)[at] = z;
@@ -468,23 +490,32 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
         const int64_t col = static_cast<int64_t>(at.ta) * (kPair ? 256 : 128) + rank * 128 + quad * 32 + lane;
         const bool in = col < P.L.N;
         const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
+        // 16 tokens at a time, the next ones' residuals on their way meanwhile
+        const int64_t m_tile = static_cast<int64_t>(at.tb) * P.nt;
+        const int rows_here = in ? static_cast<int>(min(static_cast<int64_t>(P.nt), P.L.M - m_tile)) : 0;
+        uint32_t r_next[16] = {};
+        const int shift = wide(P.L.res_bf16);
+        auto residuals = [&](int c) {
+          if (P.L.res)
+            load_entries(r_next, P.L.res, at.g * P.L.r_group + (m_tile + c) * P.L.r_row + col, P.L.r_row, rows_here - c,
+                         P.L.res_bf16);
+        };
+        residuals(half * 16);
         const bool ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        with_activation(P.L.act, [&](auto act) {
+        with_epilogue(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
 #pragma unroll 1
           for (int c = half * 16; c < P.nt; c += 32) {
             float v[16], r[16];
-            const int64_t m0 = static_cast<int64_t>(at.tb) * P.nt + c;
-            const int rows = in ? static_cast<int>(min(static_cast<int64_t>(16), P.L.M - m0)) : 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              r[i] = P.L.res && i < rows ? load_residual(P.L, at.g, m0 + i, col) : 0.f;
             __syncwarp();
             tc_load16(acc + c, v);
-            int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + col;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(r_next[i] << shift);
+            residuals(c + 32);
+            int64_t to = at.g * P.L.y_group + (m_tile + c) * P.L.y_row + col;
 #pragma unroll
             for (int i = 0; i < 16; ++i, to += P.L.y_row)
-              if (i < rows) finish_value<act.value>(P.L, to, sum(ok, v[i]), bias, r[i]);
+              if (c + i < rows_here) finish_value<act.value, y_bf16.value>(P.L, to, sum(ok, v[i]), bias, r[i]);
           }
         });
       } else {
@@ -503,14 +534,14 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
               prefetch_l2(P.L.res, at.g * P.L.r_group + m * P.L.r_row + n0 + c0, P.L.res_bf16);
           }
         bool ok = true;
-        with_activation(P.L.act, [&](auto act) {
-          float r[kBatch], r_next[kBatch], bias, bias_next = 0.f;
-          auto residuals = [&](float (&to)[kBatch], int c0, int m0) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int m = m0 + i * kRows;
-              to[i] = P.L.res && c0 + c < cols && m < P.L.M ? load_residual(P.L, at.g, m, n0 + c0 + c) : 0.f;
-            }
+        with_epilogue(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+          uint32_t r[kBatch] = {}, r_next[kBatch] = {};
+          float bias, bias_next = 0.f;
+          const int shift = wide(P.L.res_bf16);
+          auto residuals = [&](uint32_t (&to)[kBatch], int c0, int m0) {
+            if (P.L.res)
+              load_entries(to, P.L.res, at.g * P.L.r_group + m0 * P.L.r_row + n0 + c0 + c, kRows * P.L.r_row,
+                           c0 + c < cols ? (P.L.M - m0 + kRows - 1) / kRows : 0, P.L.res_bf16);
           };
           auto biases = [&](int c0) { return c0 + c < cols ? load_bias(P.L, at.g, n0 + c0 + c) : 0.f; };
           residuals(r_next, 0, row);
@@ -551,7 +582,8 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
               int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + n0 + c0 + c;
 #pragma unroll
               for (int i = 0; i < kBatch; ++i, to += kRows * P.L.y_row)
-                if (m0 + i * kRows < rows) finish_value<act.value>(P.L, to, v[i], bias, r[i]);
+                if (m0 + i * kRows < rows)
+                  finish_value<act.value, y_bf16.value>(P.L, to, v[i], bias, __uint_as_float(r[i] << shift));
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
           }
