@@ -233,17 +233,28 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                  : "memory");
 }
 
-// 16 columns of this warp's 32 lanes
-__device__ __forceinline__ void tc_load16(uint32_t addr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "{\n tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+// kCols (16 or 32) columns of this warp's 32 lanes
+template <int kCols>
+__device__ __forceinline__ void tc_load(uint32_t addr, uint32_t (&r)[kCols]) {
+#pragma unroll
+  for (int c = 0; c < kCols; c += 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[c]), "=r"(r[c + 1]), "=r"(r[c + 2]), "=r"(r[c + 3]), "=r"(r[c + 4]), "=r"(r[c + 5]), "=r"(r[c + 6]),
+          "=r"(r[c + 7]), "=r"(r[c + 8]), "=r"(r[c + 9]), "=r"(r[c + 10]), "=r"(r[c + 11]), "=r"(r[c + 12]),
+          "=r"(r[c + 13]), "=r"(r[c + 14]), "=r"(r[c + 15])
+        : "r"(addr + c)
+        : "memory");
+  // the registers pass through the wait, so that nothing reads them in front of it
+#pragma unroll
+  for (int c = 0; c < kCols; c += 16)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[c]), "+r"(r[c + 1]), "+r"(r[c + 2]), "+r"(r[c + 3]), "+r"(r[c + 4]), "+r"(r[c + 5]),
+                   "+r"(r[c + 6]), "+r"(r[c + 7]), "+r"(r[c + 8]), "+r"(r[c + 9]), "+r"(r[c + 10]), "+r"(r[c + 11]),
+                   "+r"(r[c + 12]), "+r"(r[c + 13]), "+r"(r[c + 14]), "+r"(r[c + 15])
+                 :
+                 : "memory");
 }
 
 struct TileAt {
@@ -490,32 +501,44 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
         const int64_t col = static_cast<int64_t>(at.ta) * (kPair ? 256 : 128) + rank * 128 + quad * 32 + lane;
         const bool in = col < P.L.N;
         const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
-        // 16 tokens at a time, the next ones' residuals on their way meanwhile
+        // 32 tokens at a time (16 where the loading warps leave fewer registers), the next ones' residuals on their way
+        // meanwhile.  nt is a multiple of 16: where a last 16 of 32 columns is not the tile's, it is read (the allocation
+        // has it) and not used.
+        constexpr int kCols = kLoad ? 16 : 32;
         const int64_t m_tile = static_cast<int64_t>(at.tb) * P.nt;
         const int rows_here = in ? static_cast<int>(min(static_cast<int64_t>(P.nt), P.L.M - m_tile)) : 0;
-        uint32_t r_next[16] = {};
+        uint32_t r_next[kCols] = {};
         const int shift = wide(P.L.res_bf16);
         auto residuals = [&](int c) {
           if (P.L.res)
             load_entries(r_next, P.L.res, at.g * P.L.r_group + (m_tile + c) * P.L.r_row + col, P.L.r_row, rows_here - c,
                          P.L.res_bf16);
         };
-        residuals(half * 16);
+        residuals(half * kCols);
         const bool ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         with_epilogue(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
 #pragma unroll 1
-          for (int c = half * 16; c < P.nt; c += 32) {
-            float v[16], r[16];
+          for (int c = half * kCols; c < P.nt; c += 2 * kCols) {
+            uint32_t v[kCols], r[kCols];
             __syncwarp();
-            tc_load16(acc + c, v);
+            tc_load<kCols>(acc + c, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(r_next[i] << shift);
-            residuals(c + 32);
+            for (int i = 0; i < kCols; ++i) r[i] = r_next[i];
+            residuals(c + 2 * kCols);
             int64_t to = at.g * P.L.y_group + (m_tile + c) * P.L.y_row + col;
+            auto finish = [&](int i) {
+              finish_value<act.value, y_bf16.value>(P.L, to, sum(ok, __uint_as_float(v[i])), bias,
+                                                    __uint_as_float(r[i] << shift));
+            };
+            if (__all_sync(~0u, c + kCols <= rows_here)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i, to += P.L.y_row)
-              if (c + i < rows_here) finish_value<act.value, y_bf16.value>(P.L, to, sum(ok, v[i]), bias, r[i]);
+              for (int i = 0; i < kCols; ++i, to += P.L.y_row) finish(i);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kCols; ++i, to += P.L.y_row)
+                if (c + i < rows_here) finish(i);
+            }
           }
         });
       } else {
@@ -556,13 +579,13 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
             if (quad * 32 < P.L.M)
 #pragma unroll 1
               for (int cc = c0 + half * 32; cc < min(c0 + half * 32 + 32, P.nt); cc += 16) {
-                float v[16];
+                uint32_t v[16];
                 __syncwarp();
-                tc_load16(acc + cc, v);
+                tc_load<16>(acc + cc, v);
                 if (quad * 32 + lane < P.L.M)
 #pragma unroll
                   for (int i = 0; i < 16; ++i)
-                    staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = sum(ok, v[i]);
+                    staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = sum(ok, __uint_as_float(v[i]));
               }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
             bias = bias_next;
@@ -716,7 +739,7 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   P.staging = 1024 + P.stages * stage_bytes + slack;
   const int smem = static_cast<int>(P.staging) + staging;
   P.tmem_cols = 32;
-  while (P.tmem_cols < 2 * P.nt) P.tmem_cols *= 2;
+  while (P.tmem_cols < P.nt + (P.nt + 31) / 32 * 32) P.tmem_cols *= 2;  // two accumulators, read 32 columns at a time
   // fp32 sums, bf16 operands, both K-major, N = nt, M = 128 or 256
   P.idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(P.nt / 8) << 17) | ((kPair ? 16u : 8u) << 24);
   // once a device
