@@ -76,23 +76,23 @@ __device__ __forceinline__ float activate(float z, float cap, float inv_cap) {
 }
 
 // f with the activation and y's type as constants: code that a call does not use is not fetched either
-template <int kAct, typename F>
+template <int kAct, bool kOnlyF32, typename F>
 __device__ __forceinline__ void with_type(int y_bf16, F&& f) {
-  if (y_bf16)
-    f(std::integral_constant<int, kAct>(), std::true_type());
+  if (!kOnlyF32 && y_bf16)
+    f(std::integral_constant<int, kAct>(), std::bool_constant<!kOnlyF32>());
   else
     f(std::integral_constant<int, kAct>(), std::false_type());
 }
 
-template <typename F>
+template <bool kOnlyF32, typename F>
 __device__ __forceinline__ void with_epilogue(int act, int y_bf16, F&& f) {
   switch (act) {
-    case SV_ACT_RELU: with_type<SV_ACT_RELU>(y_bf16, f); break;
-    case SV_ACT_SILU: with_type<SV_ACT_SILU>(y_bf16, f); break;
-    case SV_ACT_GELU: with_type<SV_ACT_GELU>(y_bf16, f); break;
-    case SV_ACT_GELU_TANH: with_type<SV_ACT_GELU_TANH>(y_bf16, f); break;
-    case SV_ACT_SOFTCAP: with_type<SV_ACT_SOFTCAP>(y_bf16, f); break;
-    default: with_type<SV_ACT_NONE>(y_bf16, f);
+    case SV_ACT_RELU: with_type<SV_ACT_RELU, kOnlyF32>(y_bf16, f); break;
+    case SV_ACT_SILU: with_type<SV_ACT_SILU, kOnlyF32>(y_bf16, f); break;
+    case SV_ACT_GELU: with_type<SV_ACT_GELU, kOnlyF32>(y_bf16, f); break;
+    case SV_ACT_GELU_TANH: with_type<SV_ACT_GELU_TANH, kOnlyF32>(y_bf16, f); break;
+    case SV_ACT_SOFTCAP: with_type<SV_ACT_SOFTCAP, kOnlyF32>(y_bf16, f); break;
+    default: with_type<SV_ACT_NONE, kOnlyF32>(y_bf16, f);
   }
 }
 
@@ -137,6 +137,15 @@ __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, 
 //    belongs to no token multiplies whatever lies behind them in shared memory
 //    and is never read.
 
+//
+// The tensor core cuts its sums off after each step of 16 entries of K, towards
+// zero: after K = 2048 a sum is 2.1e-6 short, about in proportion to K.  bf16
+// results do not show that.  For fp32 results of K > 768 (kSegments) a sum is
+// carried through the tensor core for at most 768 entries: two segments in the two
+// accumulators where that is enough, added when a tile is finished; else segments
+// of 512, which the epilogue's warps add up in tensor memory beside the two
+// accumulators (for which a tile is then 160 wide at most).
+
 constexpr int kMmaK = 64;        // entries of K a stage holds of each row: 128 bytes
 constexpr int kRowBytes = 128;
 constexpr int kMaxStages = 12;
@@ -154,6 +163,8 @@ struct MmaParams {
   int tiles_a, tiles_b;
   int sub;               // blocks of 64 entries of K in a stage
   int kblocks;           // stages that K takes
+  int seg_blocks, segs;  // stages of a segment, segments
+  int halves;            // two segments, which stay in their accumulators until the tile is finished
   int a_groups, b_groups;  // 0: the operand is shared by all groups
   unsigned tiles;
   unsigned idesc;
@@ -257,6 +268,16 @@ __device__ __forceinline__ void tc_load(uint32_t addr, uint32_t (&r)[kCols]) {
                  : "memory");
 }
 
+// 16 columns back into tensor memory
+__device__ __forceinline__ void tc_store(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
 struct TileAt {
   int ta, tb, g;
 };
@@ -335,8 +356,8 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* p, 
   }
 }
 
-// kWeightsA: w is A.  kLoad: warps load the stages; otherwise TMA does, and where w is A the CTAs work in pairs.
-template <bool kWeightsA, bool kLoad>
+// kWeightsA: w is A.  kSegments: see above.  kLoad: warps load the stages; otherwise TMA does, and where w is A the CTAs work in pairs.
+template <bool kWeightsA, bool kLoad, bool kSegments>
 __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1)
     mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
@@ -455,29 +476,32 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
       unsigned s = 0, phase = 0, n = 0;
       const uint64_t desc_a = smem_desc(base), desc_b = smem_desc(base + a_bytes);
       const unsigned desc_step = stage_bytes / 16;
-      for (unsigned t = first; t < P.tiles && !dead; t += step, ++n) {
-        const unsigned buf = n & 1;
-        if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, &dead)) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + buf * P.nt;
-        for (int kb = 0; kb < P.kblocks; ++kb) {
-          if (!mbar_wait(&full[s], phase, &dead)) break;
-          // What warps stored is now seen here; the tensor core reads it by another way.  The fence stands here because in
-          // a loading warp it would wait for the loads on their way.
-          if constexpr (kLoad) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (unsigned t = first; t < P.tiles && !dead; t += step) {
+        for (int kb0 = 0; kb0 < P.kblocks && !dead; kb0 += P.seg_blocks, ++n) {
+          const unsigned buf = n & 1;
+          if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, &dead)) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (elect_one()) {
-            uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
-            for (int u = 0; u < P.sub; ++u, da += sub_bytes / 16, db += sub_bytes / 16) {
-              tc_mma<kPair>(d, da, db, P.idesc, kb > 0 || u > 0);
+          const uint32_t d = tmem + buf * P.nt;
+          const int end = kSegments ? min(P.kblocks, kb0 + P.seg_blocks) : P.kblocks;
+          for (int kb = kb0; kb < end; ++kb) {
+            if (!mbar_wait(&full[s], phase, &dead)) break;
+            // What warps stored is now seen here; the tensor core reads it by another way.  The fence stands here because
+            // in a loading warp it would wait for the loads on their way.
+            if constexpr (kLoad) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (elect_one()) {
+              uint64_t da = desc_a + s * desc_step, db = desc_b + s * desc_step;
+              for (int u = 0; u < P.sub; ++u, da += sub_bytes / 16, db += sub_bytes / 16) {
+                tc_mma<kPair>(d, da, db, P.idesc, kb > kb0 || u > 0);
 #pragma unroll
-              for (int k = 1; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, true);
+                for (int k = 1; k < kMmaK / 16; ++k) tc_mma<kPair>(d, da + 2 * k, db + 2 * k, P.idesc, true);
+              }
+              tc_commit<kPair>(&empty[s]);
+              if (kb == end - 1) tc_commit<kPair>(&acc_full[buf]);
             }
-            tc_commit<kPair>(&empty[s]);
-            if (kb == P.kblocks - 1) tc_commit<kPair>(&acc_full[buf]);
+            __syncwarp();
+            if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
           }
-          __syncwarp();
-          if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
         }
       }
       if (dead) {
@@ -493,18 +517,60 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
     float* staging = reinterpret_cast<float*>(smem + P.staging);
     unsigned n = 0;
     auto sum = [&](bool ok, float v) { return !ok ? NAN : P.kblocks == 0 ? 0.f : v; };  // no entries: no product ran
-    for (unsigned t = first; t < P.tiles; t += step, ++n) {
+    // columns of a tile that go together to one of the two warps of 32 lanes
+    constexpr int kCols = kWeightsA && (kLoad || kSegments) ? 16 : 32;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16), carried = lanes + 2 * P.nt;
+    const bool idle = !kWeightsA && quad * 32 >= P.L.M;  // no token in these lanes
+    auto wait_sums = [&]() {
+      const bool ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[n & 1], (n >> 1) & 1, &dead));
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      return ok;
+    };
+    auto release = [&](unsigned buf) {
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair)
+          mbar_arrive_in(in_cta(&acc_empty[buf], 0));
+        else
+          mbar_arrive(&acc_empty[buf]);
+      }
+    };
+    // 16 columns' sums: the last segment's and what the others have carried
+    auto sums16 = [&](int c, uint32_t (&v)[16], bool add) {
+      tc_load<16>(lanes + (n & 1) * P.nt + c, v);
+      if (!add) return;
+      uint32_t w[16];
+      tc_load<16>((kSegments && P.halves ? lanes + (~n & 1) * P.nt : carried) + c, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+    };
+    auto carry = [&]() {
+      for (int seg = 0; seg + 1 < P.segs; ++seg, ++n) {
+        if (wait_sums() && !idle && !P.halves) {
+          __syncwarp();
+#pragma unroll 1
+          for (int c0 = half * kCols; c0 < P.nt; c0 += 2 * kCols)
+#pragma unroll 1
+            for (int c = c0; c < min(c0 + kCols, P.nt); c += 16) {
+              uint32_t v[16];
+              sums16(c, v, seg > 0);
+              tc_store(carried + c, v);
+            }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        if (!P.halves) release(n & 1);
+      }
+    };
+    for (unsigned t = first; t < P.tiles; t += step) {
       const TileAt at = tile_at(P, t);
-      const unsigned buf = n & 1;
-      const uint32_t acc = tmem + buf * P.nt + (static_cast<uint32_t>(quad * 32) << 16);
       if constexpr (kWeightsA) {
         const int64_t col = static_cast<int64_t>(at.ta) * (kPair ? 256 : 128) + rank * 128 + quad * 32 + lane;
         const bool in = col < P.L.N;
         const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
-        // 32 tokens at a time (16 where the loading warps leave fewer registers), the next ones' residuals on their way
-        // meanwhile.  nt is a multiple of 16: where a last 16 of 32 columns is not the tile's, it is read (the allocation
-        // has it) and not used.
-        constexpr int kCols = kLoad ? 16 : 32;
+        // 32 tokens at a time (16 where registers are few), the next ones' residuals on their way meanwhile.  nt is a
+        // multiple of 16: where a last 16 of 32 columns is not the tile's, it is read (the allocation has it) and not
+        // used.
         const int64_t m_tile = static_cast<int64_t>(at.tb) * P.nt;
         const int rows_here = in ? static_cast<int>(min(static_cast<int64_t>(P.nt), P.L.M - m_tile)) : 0;
         uint32_t r_next[kCols] = {};
@@ -514,15 +580,18 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
             load_entries(r_next, P.L.res, at.g * P.L.r_group + (m_tile + c) * P.L.r_row + col, P.L.r_row, rows_here - c,
                          P.L.res_bf16);
         };
+        if constexpr (kSegments) carry();
         residuals(half * kCols);
-        const bool ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead));
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        with_epilogue(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+        const bool ok = wait_sums();
+        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
 #pragma unroll 1
           for (int c = half * kCols; c < P.nt; c += 2 * kCols) {
             uint32_t v[kCols], r[kCols];
             __syncwarp();
-            tc_load<kCols>(acc + c, v);
+            if constexpr (kSegments)
+              sums16(c, v, P.segs > 1);
+            else
+              tc_load<kCols>(lanes + (n & 1) * P.nt + c, v);
 #pragma unroll
             for (int i = 0; i < kCols; ++i) r[i] = r_next[i];
             residuals(c + 2 * kCols);
@@ -556,8 +625,9 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
             for (int m = row; P.L.res && m < P.L.M; m += kRows)
               prefetch_l2(P.L.res, at.g * P.L.r_group + m * P.L.r_row + n0 + c0, P.L.res_bf16);
           }
+        if constexpr (kSegments) carry();
         bool ok = true;
-        with_epilogue(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
           uint32_t r[kBatch] = {}, r_next[kBatch] = {};
           float bias, bias_next = 0.f;
           const int shift = wide(P.L.res_bf16);
@@ -572,16 +642,13 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
 #pragma unroll 1
           for (int c0 = 0; c0 < cols; c0 += kStageCols) {
             const int rows = c0 + c < cols ? P.L.M : 0;
-            if (c0 == 0) {
-              ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[buf], (n >> 1) & 1, &dead));
-              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            }
-            if (quad * 32 < P.L.M)
+            if (c0 == 0) ok = wait_sums();
+            if (!idle)
 #pragma unroll 1
               for (int cc = c0 + half * 32; cc < min(c0 + half * 32 + 32, P.nt); cc += 16) {
                 uint32_t v[16];
                 __syncwarp();
-                tc_load<16>(acc + cc, v);
+                sums16(cc, v, kSegments && P.segs > 1);
                 if (quad * 32 + lane < P.L.M)
 #pragma unroll
                   for (int i = 0; i < 16; ++i)
@@ -612,14 +679,9 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
           }
         });
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair)
-          mbar_arrive_in(in_cta(&acc_empty[buf], 0));
-        else
-          mbar_arrive(&acc_empty[buf]);
-      }
+      if (kSegments && P.halves) release(~n & 1);
+      release(n & 1);
+      ++n;
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -684,10 +746,11 @@ bool make_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64
 // core, and the rows of 128 bytes that the SM fetches for it come in at about 46
 // bytes a cycle; the SMs (or pairs of them) take their tiles in waves, and each
 // wave pays for starting and ending.
-int choose_width(bool pair, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, int64_t kblocks, int workers) {
+int choose_width(bool pair, int most, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t groups, int64_t kblocks,
+                 int workers) {
   int best = 16;
   double least = 1e300;
-  for (int nt = 16; nt <= 256; nt += 16) {
+  for (int nt = 16; nt <= most; nt += 16) {
     const int64_t tiles = (rows_b + nt - 1) / nt * tiles_a * groups;
     const int64_t waves = (tiles + workers - 1) / workers;
     const double stage = std::max(2.0 * nt, (rows_a + (pair ? nt / 2 : nt)) * 128 / 46.0);
@@ -697,7 +760,7 @@ int choose_width(bool pair, int64_t rows_b, int64_t tiles_a, int rows_a, int64_t
   return best;
 }
 
-template <bool kWeightsA, bool kLoad>
+template <bool kWeightsA, bool kLoad, bool kSegments>
 sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st) {
   constexpr bool kPair = kWeightsA && !kLoad;
   MmaParams P = {};
@@ -707,7 +770,8 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   const int64_t rows_a = kWeightsA ? L.N : L.M, rows_b = kWeightsA ? L.M : L.N;
   const int workers = kPair ? std::max(1, sms / 2) : sms;
   P.tiles_a = static_cast<int>((rows_a + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
-  P.nt = choose_width(kPair, rows_b, P.tiles_a, P.ra, L.groups, blocks, workers);
+  P.halves = kSegments && L.K <= 2 * 768;
+  P.nt = choose_width(kPair, kSegments && !P.halves ? 160 : 256, rows_b, P.tiles_a, P.ra, L.groups, blocks, workers);
   P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
   const int64_t tiles = static_cast<int64_t>(P.tiles_a) * P.tiles_b * L.groups;
   if (tiles >= (int64_t{1} << 31)) return SV_EUNSUPPORTED;
@@ -718,7 +782,7 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
     int gx = 0, gw = 0;
     if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? b_rows : P.ra, &gx) ||
         !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : b_rows, &gw))
-      return launch_mma<kWeightsA, true>(L, device, sms, st);
+      return launch_mma<kWeightsA, true, kSegments>(L, device, sms, st);
     P.a_groups = kWeightsA ? gw : gx;
     P.b_groups = kWeightsA ? gx : gw;
   }
@@ -734,24 +798,27 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   P.sub = 1;
   while (!kLoad && P.sub < 4 && P.sub < blocks && 2 * P.sub * sub_bytes * 4 <= room) P.sub *= 2;
   P.kblocks = static_cast<int>((blocks + P.sub - 1) / P.sub);
+  P.seg_blocks = P.halves ? (P.kblocks + 1) / 2 : kSegments ? 8 / P.sub : std::max(1, P.kblocks);
+  P.segs = std::max(1, (P.kblocks + P.seg_blocks - 1) / P.seg_blocks);
   const int stage_bytes = P.sub * sub_bytes;
   P.stages = std::min(kMaxStages, room / stage_bytes);
   P.staging = 1024 + P.stages * stage_bytes + slack;
   const int smem = static_cast<int>(P.staging) + staging;
   P.tmem_cols = 32;
-  while (P.tmem_cols < P.nt + (P.nt + 31) / 32 * 32) P.tmem_cols *= 2;  // two accumulators, read 32 columns at a time
+  // two accumulators, read 32 columns at a time, or three regions of sums, read 16 at a time
+  while (P.tmem_cols < (kSegments && !P.halves ? 3 * P.nt : P.nt + (P.nt + 31) / 32 * 32)) P.tmem_cols *= 2;
   // fp32 sums, bf16 operands, both K-major, N = nt, M = 128 or 256
   P.idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<unsigned>(P.nt / 8) << 17) | ((kPair ? 16u : 8u) << 24);
   // once a device
   static std::atomic<bool> opted_in[64];
   if (device >= 64 || !opted_in[device].load()) {
-    if (cudaFuncSetAttribute(mma_kernel<kWeightsA, kLoad>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem) !=
+    if (cudaFuncSetAttribute(mma_kernel<kWeightsA, kLoad, kSegments>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem) !=
         cudaSuccess)
       return SV_ECUDA;
     if (device < 64) opted_in[device].store(true);
   }
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, workers)) * (kPair ? 2 : 1);
-  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad>, grid, kMmaThreads + (kLoad ? 32 * kLoadWarps : 0),
+  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad, kSegments>, grid, kMmaThreads + (kLoad ? 32 * kLoadWarps : 0),
                                        smem, kPair ? 2 : 1, st, P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
   return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
@@ -813,6 +880,12 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
-  if (K == 0) return M > 128 ? sv::launch_mma<true, true>(P, device, sms, st) : sv::launch_mma<false, true>(P, device, sms, st);
-  return M > 128 ? sv::launch_mma<true, false>(P, device, sms, st) : sv::launch_mma<false, false>(P, device, sms, st);
+  if (K == 0)
+    return M > 128 ? sv::launch_mma<true, true, false>(P, device, sms, st)
+                   : sv::launch_mma<false, true, false>(P, device, sms, st);
+  if (y_dt == SV_F32 && K > 768)
+    return M > 128 ? sv::launch_mma<true, false, true>(P, device, sms, st)
+                   : sv::launch_mma<false, false, true>(P, device, sms, st);
+  return M > 128 ? sv::launch_mma<true, false, false>(P, device, sms, st)
+                 : sv::launch_mma<false, false, false>(P, device, sms, st);
 }

@@ -59,6 +59,23 @@ def test_linear_sizes(sv, M, N, K, out):
     ref.assert_linear(y, x[0], w[0], None, None, "none", 0.0, f"{M}x{N}x{K}")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 500, 8192), (6, 2000, 4100), (100, 300, 3001), (128, 160, 2048), (200, 700, 8192),
+                                   (384, 512, 1030), (150, 300, 2049), (7, 500, 1536), (130, 600, 1537), (77, 900, 1001), (300, 500, 1280), (40, 64, 769), (300, 64, 768)])
+def test_linear_long_sums_in_fp32(sv, M, N, K):
+    # Whatever K, at most 48 steps of 16 products go into one sum of the tensor core, and 48 + 16 where halves of K are
+    # rounded up to whole stages: K <= 768 in one, up to 1536 in two, longer ones in segments of 512, added in fp32.  A step is off by less than 2^-23 of the sums of |x w| for each of
+    # its 16 products and itself.
+    x, w, g = _operands(M + K, 1, M, N, K)
+    x, w = x[0], w[0]
+    y = sv.linear(x, w, out_dtype=torch.float32)
+    want, mag = x.double() @ w.double().T, x.double().abs() @ w.double().abs().T
+    off = (y.double() - want).abs()
+    assert bool((off <= (64 * 2.0 ** -23 + K / 512 * 2.0 ** -24) * mag).all())
+    # a sum of n steps that each cut off half a step on the average: n / 2 * 2^-23 in the 2-norm at most
+    assert float(off.norm() / want.norm()) <= 32 * 2.0 ** -23
+    ref.assert_linear(y, x, w, None, None, "none", 0.0)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh", "softcap"])
 @pytest.mark.parametrize("M,N,K", [(3, 200, 64), (70, 333, 257), (300, 512, 128)])
 def test_linear_epilogues(sv, act, M, N, K):
