@@ -45,7 +45,7 @@ struct SoftParams {
   const float* t_row;
   float t;
   int64_t rows;
-  int V, part;  // part: entries of a row for each CTA, a multiple of 4
+  int V, staged, part;  // staged: rows start at multiples of 16 bytes; part: entries of a row for each CTA, a multiple of 8
 };
 
 struct SoftShared {
@@ -56,8 +56,8 @@ struct SoftShared {
   float2 part[2][kSoftCluster];  // (largest, sum)
   float m[2][kSoftCluster];      // (largest, its place) where T = 0
   int at[2][kSoftCluster];
-  uint64_t arrived[2];
-  int dead;
+  uint64_t arrived[2], copied[3];
+  int dead, copy_dead;  // two marks: a row whose exchange failed still waits for its copy
 };
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -131,14 +131,14 @@ constexpr int kSoftFours = kSoftHeld / 4;
 // The j-th four of a thread are the entries lo + 4 (j threads + thread) .. + 3 of a row, or with kVec false the entries
 // lo + (4 j + i) threads + thread; -inf beyond hi.  from: where the four lies, x + its place or a copy.
 template <typename T, bool kVec, int kThreads>
-__device__ __forceinline__ void load_four(Four<T>& f, const T* x, const T* from, int lo, int hi, int j) {
+__device__ __forceinline__ void load_four(Four<T>& f, const T* x, const T* from, int lo, int hi, int whole, int j) {
   if constexpr (kVec) {
     const int at = lo + 4 * (j * kThreads + static_cast<int>(threadIdx.x));
-    if (at + 4 <= hi)
+    if (4 * (j + 1) * kThreads <= whole || at + 4 <= lo + whole)
       f.load(from + 4 * (j * kThreads + static_cast<int>(threadIdx.x)));
     else
       f.set(at < hi ? load_logit(x + at) : -INFINITY, at + 1 < hi ? load_logit(x + at + 1) : -INFINITY,
-            at + 2 < hi ? load_logit(x + at + 2) : -INFINITY, -INFINITY);
+            at + 2 < hi ? load_logit(x + at + 2) : -INFINITY, at + 3 < hi ? load_logit(x + at + 3) : -INFINITY);
   } else {
     float v[4];
 #pragma unroll
@@ -153,11 +153,11 @@ __device__ __forceinline__ void load_four(Four<T>& f, const T* x, const T* from,
 // The exponentials exp((l - m) / T) of a part's entries against the thread's largest m, and their sum.  With nothing
 // but -inf (or NaN) m is -inf and the terms are 0 (or NaN).
 template <typename T, bool kVec, int kThreads>
-__device__ __forceinline__ void load_part(const T* x, const T* from, int lo, int hi, float c, Two (&e)[2 * kSoftFours],
+__device__ __forceinline__ void load_part(const T* x, const T* from, int lo, int hi, int whole, float c, Two (&e)[2 * kSoftFours],
                                           float& m, float& sum) {
   Four<T> f[kSoftFours];
 #pragma unroll
-  for (int j = 0; j < kSoftFours; ++j) load_four<T, kVec, kThreads>(f[j], x, from, lo, hi, j);
+  for (int j = 0; j < kSoftFours; ++j) load_four<T, kVec, kThreads>(f[j], x, from, lo, hi, whole, j);
   m = f[0].max();
 #pragma unroll
   for (int j = 1; j < kSoftFours; ++j) m = fmaxf(m, f[j].max());
@@ -184,7 +184,7 @@ __device__ __forceinline__ void store_part(float* y, int lo, int hi, const Two (
     const float2 a = both(mul2(e[2 * j], scale2)), b = both(mul2(e[2 * j + 1], scale2));
     if constexpr (kVec) {
       const int at = lo + 4 * (j * kThreads + static_cast<int>(threadIdx.x));
-      if (at + 4 <= hi) {
+      if (4 * (j + 1) * kThreads <= hi - lo || at + 4 <= hi) {
         *reinterpret_cast<float4*>(y + at) = make_float4(a.x, a.y, b.x, b.y);
       } else {
         if (at < hi) y[at] = a.x;
@@ -244,17 +244,16 @@ __device__ __noinline__ void one_hot(SoftShared& s, const T* x, float* y, int lo
   for (int v = lo + threadIdx.x; v < hi; v += kThreads) y[v] = valid ? (v == at ? 1.f : 0.f) : NAN;
 }
 
-// a thread's entries of a part on their way into its places of a stage
-template <typename T, int kThreads>
-__device__ __forceinline__ void copy_part(const T* x, int lo, int hi, uint32_t stage) {
-#pragma unroll
-  for (int j = 0; j < kSoftHeld / 4; ++j) {
-    const int place = j * kThreads + threadIdx.x, at = lo + 4 * place;
-    if (at + 4 <= hi)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(stage + place * 4 * static_cast<int>(sizeof(T))),
-                   "l"(x + at), "n"(4 * sizeof(T))
-                   : "memory");
-  }
+// a part's entries on their way into a stage, as far as they fill vectors of 16 bytes: one thread
+template <typename T>
+__device__ __forceinline__ void copy_part(const T* x, int lo, int hi, uint8_t* stage, uint64_t* bar) {
+  const unsigned bytes = static_cast<unsigned>(hi - lo) * sizeof(T) / 16 * 16;
+  mbar_expect(bar, bytes);
+  if (bytes > 0)
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(stage)),
+                 "l"(x + lo), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
 }
 
 template <typename T>
@@ -271,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
   if (threadIdx.x == 0) {
     mbar_init(&s.arrived[0], 1);
     mbar_init(&s.arrived[1], 1);
-    s.dead = 0;
+    for (int i = 0; i < 3; ++i) mbar_init(&s.copied[i], 1);
+    s.dead = s.copy_dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   cluster.sync();  // every CTA of the cluster runs before any writes into another
@@ -280,18 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
   const T* x0 = static_cast<const T*>(P.x);
   const int lo = min(rank * P.part, P.V), hi = min(lo + P.part, P.V);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool held = P.part <= kThreads * kSoftHeld, staged = kVec && held;
+  const bool held = P.part <= kThreads * kSoftHeld, staged = kVec && held && P.staged;
   int64_t r = blockIdx.x / ctas;
-  uint32_t stage = 0;  // of row r
-  if constexpr (kVec) {
-    if (staged)
-      for (int i = 0; i < kStages; ++i) {
-        if (r + i * clusters < P.rows)
-          copy_part<T, kThreads>(x0 + (r + i * clusters) * P.x_stride, lo, hi,
-                                 static_cast<uint32_t>(__cvta_generic_to_shared(stages)) + i * kStageBytes);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-  }
+  const int whole = (hi - lo) * static_cast<int>(sizeof(T)) / 16 * (16 / static_cast<int>(sizeof(T)));
+  uint32_t stage = 0, stage_phase = 0;  // of row r
+  if (staged && threadIdx.x == 0)
+    for (int i = 0; i < kStages; ++i)
+      if (r + i * clusters < P.rows)
+        copy_part<T>(x0 + (r + i * clusters) * P.x_stride, lo, hi, stages + i * kStageBytes, &s.copied[i]);
   for (int turn = 0; r < P.rows; r += clusters, turn ^= 1) {
     const T* x = x0 + r * P.x_stride;
     float* y = P.y + r * P.y_stride;
@@ -300,32 +296,34 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
     const float c = t > 0.f ? fminf(1.4426950408889634f / t, 3.0e38f) : 1.f;
     Two e[2 * kSoftFours];
     float m, sum;
+    bool ok = true;
     if (staged) {
-      if constexpr (kVec) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        load_part<T, kVec, kThreads>(x, reinterpret_cast<const T*>(stages + stage * kStageBytes), lo, hi, c, e, m, sum);
-        const int64_t ahead = r + static_cast<int64_t>(kStages) * clusters;
-        if (ahead < P.rows)
-          copy_part<T, kThreads>(x0 + ahead * P.x_stride, lo, hi,
-                                 static_cast<uint32_t>(__cvta_generic_to_shared(stages)) + stage * kStageBytes);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (++stage == kStages) stage = 0;
-      }
+      ok = mbar_wait(&s.copied[stage], stage_phase, &s.copy_dead);
+      load_part<T, kVec, kThreads>(x, reinterpret_cast<const T*>(stages + stage * kStageBytes), lo, hi, whole, c, e, m, sum);
     } else if (held) {
-      load_part<T, kVec, kThreads>(x, x + lo, lo, hi, c, e, m, sum);
+      load_part<T, kVec, kThreads>(x, x + lo, lo, hi, hi - lo, c, e, m, sum);
     } else {
       m = -INFINITY, sum = 0.f;
 #pragma unroll 1
       for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
         float mv, sv;
-        load_part<T, kVec, kThreads>(x, x + at, at, hi, c, e, mv, sv);
+        load_part<T, kVec, kThreads>(x, x + at, at, hi, hi - at, c, e, mv, sv);
         const float to = fmaxf(m, mv);
         sum = sum * rescale(m, to, c) + sv * rescale(mv, to, c);
         m = to;
       }
     }
+    // once every thread has read its stage, the row that is to follow there
+    auto ahead = [&]() {
+      if (!staged) return;
+      const int64_t next = r + static_cast<int64_t>(kStages) * clusters;
+      if (threadIdx.x == 0 && next < P.rows)
+        copy_part<T>(x0 + next * P.x_stride, lo, hi, stages + stage * kStageBytes, &s.copied[stage]);
+      if (++stage == kStages) stage = 0, stage_phase ^= 1;
+    };
     if (t == 0.f) {
       one_hot<T, kThreads>(s, x, y, lo, hi, turn);
+      ahead();
       continue;
     }
     const float mine = m;
@@ -334,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     if (lane == 0) s.warp_m[warp] = m, s.warp_s[warp] = sum;
     __syncthreads();
+    ahead();
     if (warp == 0) {
       const float wm = lane < kThreads / 32 ? s.warp_m[lane] : -INFINITY;
       float bm = wm, bs = lane < kThreads / 32 ? s.warp_s[lane] : 0.f;
@@ -349,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
                      "l"(two(bm, bs)), "r"(in_cta(&s.arrived[turn], lane))
                      : "memory");
     }
-    const bool ok = mbar_wait(&s.arrived[turn], phases >> turn & 1, &s.dead);
+    ok = mbar_wait(&s.arrived[turn], phases >> turn & 1, &s.dead) && ok;
     phases ^= 1u << turn;
     const float2 part = lane < ctas ? s.part[turn][lane] : make_float2(-INFINITY, 0.f);
     m = part.x;
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
 #pragma unroll 1
       for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
         float mv, sv;
-        load_part<T, kVec, kThreads>(x, x + at, at, hi, c, e, mv, sv);
+        load_part<T, kVec, kThreads>(x, x + at, at, hi, hi - at, c, e, mv, sv);
         store_part<kVec, kThreads>(y, at, hi, e, rescale(mv, m, c) * inv);
       }
     }
@@ -405,14 +404,16 @@ extern "C" sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_
   while (ctas < sv::kSoftCluster && (V > ctas * sv::kSoftPart || (static_cast<int64_t>(rows) * ctas * 2 <= 2ll * sms &&
                                                                   V > ctas * sv::kSoftThreads * 4)))
     ctas *= 2;
-  const int part = ((V + ctas - 1) / ctas + 3) / 4 * 4;
-  const sv::SoftParams P = {logits, logits_stride, probs, probs_stride, temperature_per_row, temperature, rows, V, part};
+  const int part = ((V + ctas - 1) / ctas + 7) / 8 * 8;
   const bool vec = reinterpret_cast<uintptr_t>(logits) % (4 * es) == 0 && reinterpret_cast<uintptr_t>(probs) % 16 == 0 &&
                    (rows == 1 || (logits_stride % 4 == 0 && probs_stride % 4 == 0));
   const bool few = ctas == 1 && V <= sv::kSoftShort;
   const int threads = few ? sv::kSoftFew : sv::kSoftThreads;
   const auto kernel = few ? sv::softmax_variant<sv::kSoftFew>(dt, vec) : sv::softmax_variant<sv::kSoftThreads>(dt, vec);
-  const bool staged = vec && part <= threads * sv::kSoftHeld;
+  const bool staged = vec && part <= threads * sv::kSoftHeld && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
+                      (rows == 1 || logits_stride * es % 16 == 0);
+  const sv::SoftParams P = {logits, logits_stride, probs, probs_stride, temperature_per_row, temperature, rows, V,
+                            staged, part};
   const size_t smem = !staged ? 0
                       : dt == SV_BF16 ? sv::kSoftStages<__nv_bfloat16> * threads * sv::kSoftHeld * 2
                                       : sv::kSoftStages<float> * threads * sv::kSoftHeld * 4;
