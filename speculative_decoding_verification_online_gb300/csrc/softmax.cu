@@ -36,6 +36,7 @@ constexpr int kSoftFew = 128;
 constexpr int kSoftHeld = 32;  // entries of a row that a thread keeps
 constexpr int kSoftPart = kSoftThreads * kSoftHeld, kSoftShort = kSoftFew * kSoftHeld;
 constexpr int kSoftCluster = 16;
+constexpr int kSoftSpare = 32;  // bytes of a stage for what lies around a part in its first and last block
 
 struct SoftParams {
   const void* x;
@@ -45,7 +46,7 @@ struct SoftParams {
   const float* t_row;
   float t;
   int64_t rows;
-  int V, staged, part;  // staged: rows start at multiples of 16 bytes; part: entries of a row for each CTA, a multiple of 8
+  int V, part;  // part: entries of a row for each CTA, a multiple of 8
 };
 
 struct SoftShared {
@@ -128,23 +129,23 @@ struct Four<__nv_bfloat16> {
 
 constexpr int kSoftFours = kSoftHeld / 4;
 
-// The j-th four of a thread are the entries lo + 4 (j threads + thread) .. + 3 of a row, or with kVec false the entries
-// lo + (4 j + i) threads + thread; -inf beyond hi.  from: where the four lies, x + its place or a copy.
+// The j-th four of a thread are the entries 4 (j threads + thread) .. + 3 of a part of n, or with kVec false the entries
+// (4 j + i) threads + thread; -inf behind the part.
 template <typename T, bool kVec, int kThreads>
-__device__ __forceinline__ void load_four(Four<T>& f, const T* x, const T* from, int lo, int hi, int whole, int j) {
+__device__ __forceinline__ void load_four(Four<T>& f, const T* part, int n, int j) {
   if constexpr (kVec) {
-    const int at = lo + 4 * (j * kThreads + static_cast<int>(threadIdx.x));
-    if (4 * (j + 1) * kThreads <= whole || at + 4 <= lo + whole)
-      f.load(from + 4 * (j * kThreads + static_cast<int>(threadIdx.x)));
+    const int at = 4 * (j * kThreads + static_cast<int>(threadIdx.x));
+    if (4 * (j + 1) * kThreads <= n || at + 4 <= n)
+      f.load(part + at);
     else
-      f.set(at < hi ? load_logit(x + at) : -INFINITY, at + 1 < hi ? load_logit(x + at + 1) : -INFINITY,
-            at + 2 < hi ? load_logit(x + at + 2) : -INFINITY, at + 3 < hi ? load_logit(x + at + 3) : -INFINITY);
+      f.set(at < n ? load_logit(part + at) : -INFINITY, at + 1 < n ? load_logit(part + at + 1) : -INFINITY,
+            at + 2 < n ? load_logit(part + at + 2) : -INFINITY, -INFINITY);
   } else {
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int at = lo + (4 * j + i) * kThreads + static_cast<int>(threadIdx.x);
-      v[i] = at < hi ? load_logit(x + at) : -INFINITY;
+      const int at = (4 * j + i) * kThreads + static_cast<int>(threadIdx.x);
+      v[i] = (4 * j + i + 1) * kThreads <= n || at < n ? load_logit(part + at) : -INFINITY;
     }
     f.set(v[0], v[1], v[2], v[3]);
   }
@@ -153,11 +154,10 @@ __device__ __forceinline__ void load_four(Four<T>& f, const T* x, const T* from,
 // The exponentials exp((l - m) / T) of a part's entries against the thread's largest m, and their sum.  With nothing
 // but -inf (or NaN) m is -inf and the terms are 0 (or NaN).
 template <typename T, bool kVec, int kThreads>
-__device__ __forceinline__ void load_part(const T* x, const T* from, int lo, int hi, int whole, float c, Two (&e)[2 * kSoftFours],
-                                          float& m, float& sum) {
+__device__ __forceinline__ void load_part(const T* part, int n, float c, Two (&e)[2 * kSoftFours], float& m, float& sum) {
   Four<T> f[kSoftFours];
 #pragma unroll
-  for (int j = 0; j < kSoftFours; ++j) load_four<T, kVec, kThreads>(f[j], x, from, lo, hi, whole, j);
+  for (int j = 0; j < kSoftFours; ++j) load_four<T, kVec, kThreads>(f[j], part, n, j);
   m = f[0].max();
 #pragma unroll
   for (int j = 1; j < kSoftFours; ++j) m = fmaxf(m, f[j].max());
@@ -244,15 +244,21 @@ __device__ __noinline__ void one_hot(SoftShared& s, const T* x, float* y, int lo
   for (int v = lo + threadIdx.x; v < hi; v += kThreads) y[v] = valid ? (v == at ? 1.f : 0.f) : NAN;
 }
 
-// a part's entries on their way into a stage, as far as they fill vectors of 16 bytes: one thread
+// A part's entries on their way into a stage: one thread.  The copy takes the aligned blocks of 16 bytes that hold an
+// entry of the part (an allocation has all of such a block); the first entry lies `shift_of` bytes into the stage.
+__device__ __forceinline__ unsigned shift_of(const void* first) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>(first) & 15);
+}
+
 template <typename T>
 __device__ __forceinline__ void copy_part(const T* x, int lo, int hi, uint8_t* stage, uint64_t* bar) {
-  const unsigned bytes = static_cast<unsigned>(hi - lo) * sizeof(T) / 16 * 16;
+  const unsigned shift = shift_of(x + lo);
+  const unsigned bytes = hi > lo ? (shift + static_cast<unsigned>(hi - lo) * static_cast<unsigned>(sizeof(T)) + 15) / 16 * 16 : 0;
   mbar_expect(bar, bytes);
   if (bytes > 0)
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_addr(stage)),
-                 "l"(x + lo), "r"(bytes), "r"(smem_addr(bar))
+                 "l"(reinterpret_cast<const uint8_t*>(x + lo) - shift), "r"(bytes), "r"(smem_addr(bar))
                  : "memory");
 }
 
@@ -263,7 +269,7 @@ template <typename T, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(const __grid_constant__ SoftParams P) {
   extern __shared__ __align__(16) uint8_t stages[];
   __shared__ SoftShared s;
-  constexpr int kStages = kSoftStages<T>, kStageBytes = kThreads * kSoftHeld * sizeof(T);
+  constexpr int kStages = kSoftStages<T>, kStageBytes = kThreads * kSoftHeld * sizeof(T) + kSoftSpare;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int clusters = gridDim.x / ctas;
@@ -280,11 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
   const T* x0 = static_cast<const T*>(P.x);
   const int lo = min(rank * P.part, P.V), hi = min(lo + P.part, P.V);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool held = P.part <= kThreads * kSoftHeld, staged = kVec && held && P.staged;
+  const bool held = P.part <= kThreads * kSoftHeld;
   int64_t r = blockIdx.x / ctas;
-  const int whole = (hi - lo) * static_cast<int>(sizeof(T)) / 16 * (16 / static_cast<int>(sizeof(T)));
   uint32_t stage = 0, stage_phase = 0;  // of row r
-  if (staged && threadIdx.x == 0)
+  if (held && threadIdx.x == 0)
     for (int i = 0; i < kStages; ++i)
       if (r + i * clusters < P.rows)
         copy_part<T>(x0 + (r + i * clusters) * P.x_stride, lo, hi, stages + i * kStageBytes, &s.copied[i]);
@@ -297,17 +302,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
     Two e[2 * kSoftFours];
     float m, sum;
     bool ok = true;
-    if (staged) {
+    if (held) {
       ok = mbar_wait(&s.copied[stage], stage_phase, &s.copy_dead);
-      load_part<T, kVec, kThreads>(x, reinterpret_cast<const T*>(stages + stage * kStageBytes), lo, hi, whole, c, e, m, sum);
-    } else if (held) {
-      load_part<T, kVec, kThreads>(x, x + lo, lo, hi, hi - lo, c, e, m, sum);
+      load_part<T, kVec, kThreads>(reinterpret_cast<const T*>(stages + stage * kStageBytes + shift_of(x + lo)), hi - lo, c, e,
+                                   m, sum);
     } else {
       m = -INFINITY, sum = 0.f;
 #pragma unroll 1
       for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
         float mv, sv;
-        load_part<T, kVec, kThreads>(x, x + at, at, hi, hi - at, c, e, mv, sv);
+        load_part<T, kVec, kThreads>(x + at, hi - at, c, e, mv, sv);
         const float to = fmaxf(m, mv);
         sum = sum * rescale(m, to, c) + sv * rescale(mv, to, c);
         m = to;
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
     }
     // once every thread has read its stage, the row that is to follow there
     auto ahead = [&]() {
-      if (!staged) return;
+      if (!held) return;
       const int64_t next = r + static_cast<int64_t>(kStages) * clusters;
       if (threadIdx.x == 0 && next < P.rows)
         copy_part<T>(x0 + next * P.x_stride, lo, hi, stages + stage * kStageBytes, &s.copied[stage]);
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
 #pragma unroll 1
       for (int at = lo; at < hi; at += kThreads * kSoftHeld) {
         float mv, sv;
-        load_part<T, kVec, kThreads>(x, x + at, at, hi, hi - at, c, e, mv, sv);
+        load_part<T, kVec, kThreads>(x + at, hi - at, c, e, mv, sv);
         store_part<kVec, kThreads>(y, at, hi, e, rescale(mv, m, c) * inv);
       }
     }
@@ -410,18 +414,15 @@ extern "C" sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_
   const bool few = ctas == 1 && V <= sv::kSoftShort;
   const int threads = few ? sv::kSoftFew : sv::kSoftThreads;
   const auto kernel = few ? sv::softmax_variant<sv::kSoftFew>(dt, vec) : sv::softmax_variant<sv::kSoftThreads>(dt, vec);
-  const bool staged = vec && part <= threads * sv::kSoftHeld && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
-                      (rows == 1 || logits_stride * es % 16 == 0);
-  const sv::SoftParams P = {logits, logits_stride, probs, probs_stride, temperature_per_row, temperature, rows, V,
-                            staged, part};
-  const size_t smem = !staged ? 0
-                      : dt == SV_BF16 ? sv::kSoftStages<__nv_bfloat16> * threads * sv::kSoftHeld * 2
-                                      : sv::kSoftStages<float> * threads * sv::kSoftHeld * 4;
+  const bool held = part <= threads * sv::kSoftHeld;
+  const sv::SoftParams P = {logits, logits_stride, probs, probs_stride, temperature_per_row, temperature, rows, V, part};
+  const int stages = dt == SV_BF16 ? sv::kSoftStages<__nv_bfloat16> : sv::kSoftStages<float>;
+  const size_t smem = held ? stages * (threads * sv::kSoftHeld * es + sv::kSoftSpare) : 0;
   // how many clusters of this variant run at once: asked once a device
   static std::atomic<int> known[64][2][2][2][2][5];
   int log = 0;
   while (1 << log < ctas) ++log;
-  std::atomic<int>* at = device < 64 ? &known[device][dt == SV_BF16][vec][few][staged][log] : nullptr;
+  std::atomic<int>* at = device < 64 ? &known[device][dt == SV_BF16][vec][few][held][log] : nullptr;
   int resident = at ? at->load() : 0;
   if (resident == 0) {
     if (sv::prepare_waiting(kernel, threads, smem, ctas, &resident) != cudaSuccess || resident < 1) return SV_ECUDA;
