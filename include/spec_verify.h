@@ -375,12 +375,14 @@ sv_status spec_verify_run_noalloc(const void* target_logits, sv_dtype tdt,
  *     (SV_EINVAL); it may be the residual itself, with the same strides and
  *     type, and must not overlap any other input.
  *   bias_dt, residual_dt, y_dt: SV_F32 or SV_BF16 each.
- *   Products are summed in fp32, the epilogue is fp32, and y is rounded once.
+ *   Products are summed in fp32 (on the tensor cores, at most 768 entries of K
+ *   in one sum where y is fp32), the epilogue is fp32, and y is rounded once.
  *   cap: the bound of SV_ACT_SOFTCAP (cap * tanh(z / cap)), finite and > 0;
  *     otherwise not used.
  * groups, M or N = 0 is a no-op; K = 0 sums nothing.  Any size, stride and
  * alignment of the element is taken; rows of x and w that start at multiples
- * of 16 bytes take the fast path.  SV_EUNSUPPORTED: a stride of 2^40 or more. */
+ * of 16 bytes take the fast path.  SV_EUNSUPPORTED: a stride of 2^40 or more, or
+ * groups, M, N or K above 2^30. */
 typedef enum {
   SV_ACT_NONE = 0,
   SV_ACT_RELU = 1,
@@ -461,7 +463,8 @@ sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_t logits_st
  * is NaN, infinite or (at a node offered) negative, fails closed as invalid
  * input: accepted_len, tokens and path -1, and for nodes of a valid range
  * accept_prob 0 and SV_FLAG_INVALID.  Of a row only what the walk needs is read: single entries, and
- * whole rows where a sum over them is.  Uniforms are expected in [0, 1).
+ * whole rows where a sum over them is.  Uniforms are expected in [0, 1) (a child
+ * whose uniform is NaN is refused).
  * SV_EUNSUPPORTED beyond SV_MAX_V or SV_MAX_NODES; B = 0 is a no-op. */
 #define SV_MAX_NODES 256
 

@@ -853,6 +853,7 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
     return SV_EINVAL;
   for (const int64_t stride : {x_row, x_group, w_row, w_group, bias_group, residual_row, residual_group, y_row, y_group})
     if (stride >= (int64_t{1} << 40)) return SV_EUNSUPPORTED;
+  if (std::max({groups, M, N, K}) > (1 << 30)) return SV_EUNSUPPORTED;
   if (groups == 0 || M == 0 || N == 0) return SV_OK;
   if (!y || (K > 0 && (!x || !w))) return SV_EINVAL;
   if (!sv::aligned_to(x, SV_BF16) || !sv::aligned_to(w, SV_BF16) || !sv::aligned_to(y, y_dt) ||

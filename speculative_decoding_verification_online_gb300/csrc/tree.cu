@@ -24,7 +24,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <cstdlib>
 #include <initializer_list>
 
 #include "entry.cuh"
@@ -95,6 +94,7 @@ __device__ __forceinline__ Pair times(const Pair& a, const Pair& b) {
 }
 
 __device__ __forceinline__ bool above(const Pair& a, const Pair& b) { return (a.s - b.s) + (a.l - b.l) > 0.f; }
+__device__ __forceinline__ bool at_most(const Pair& a, const Pair& b) { return (a.s - b.s) + (a.l - b.l) <= 0.f; }
 
 // a / b, b not 0
 __device__ __forceinline__ Pair over(const Pair& a, const Pair& b) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
             w = w.value() > qx ? w.settled() : Pair{qx, 0.f};
           }
           const Pair most = times(Z, Pair{qx, 0.f}), rw = times(r, w);
-          yes = r.value() > 0.f && !above(times(most, Pair{u, 0.f}), rw);
+          yes = r.value() > 0.f && at_most(times(most, Pair{u, 0.f}), rw);
           alpha = most.value() > 0.f ? (above(most, rw) ? over(rw, most).value() : 1.f) : (r.value() > 0.f ? 1.f : 0.f);
         }
         if (lane == 0 && rank == 0) {
@@ -560,7 +560,6 @@ extern "C" sv_status spec_verify_tree(const float* target_probs, int64_t target_
   while (ctas < sv::kTreeCluster && static_cast<int64_t>(B) * ctas * 2 <= 2ll * sms &&
          ctas * sv::kTreeWarps < P.nchunk)
     ctas *= 2;
-  if (getenv("TREEC")) ctas = atoi(getenv("TREEC"));
   if (static_cast<int64_t>(B) * ctas > 0x7fffffff) return SV_EUNSUPPORTED;
   const bool vec = reinterpret_cast<uintptr_t>(target_probs) % 16 == 0 && reinterpret_cast<uintptr_t>(draft_probs) % 16 == 0 &&
                    target_stride % 4 == 0 && draft_stride % 4 == 0;

@@ -167,6 +167,59 @@ def test_linear_large_offsets(sv):
     ref.assert_linear(y, x[0], wv[0], None, None, "none", 0.0)
 
 
+def test_linear_rows_that_share_their_place(sv):
+    # operands whose rows or groups are one (strides of 0), as expand leaves them
+    g = _gen(12)
+    row = torch.randn(1, 192, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(3, 300, 192, generator=g, device="cuda").to(torch.bfloat16)
+    res = torch.randn(1, 300, generator=g, device="cuda").to(torch.bfloat16)
+    for M in (5, 150):
+        x = row.expand(M, 192)
+        y = sv.linear(x, w, residual=res.expand(3, M, 300), bias=res[0].expand(3, 300), out_dtype=torch.float32)
+        ref.assert_linear(y, x, w, res[0].expand(3, 300), res.expand(3, M, 300), "none", 0.0)
+        same = sv.linear(x.expand(3, M, 192), w[:1].expand(3, 300, 192), out_dtype=torch.float32)
+        ref.assert_linear(same, x, w[:1].expand(3, 300, 192), None, None, "none", 0.0)
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_linear_without_entries_of_k_over_many_tiles(sv, M):
+    bias = torch.randn(4, 20000, generator=_gen(M), device="cuda")
+    empty = torch.empty(4, 20000, 0, dtype=torch.bfloat16, device="cuda")
+    y = sv.linear(empty[0, :M], empty, bias=bias, activation="relu", out_dtype=torch.float32)
+    assert torch.equal(y, bias.clamp(min=0).unsqueeze(1).expand(4, M, 20000))
+
+
+def test_calls_at_once_on_two_streams(sv):
+    # eager calls of every operator and a replayed capture of them, side by side
+    x, w, g = _operands(14, 2, 200, 1000, 512)
+    xs, ws, _ = _operands(15, 4, 2, 700, 1032, shared=True, pad=3)
+    logits = torch.randn(60, 50000, generator=g, device="cuda").to(torch.bfloat16)
+    t = ref.on_gpu(ref.random_tree_batch(24, 16, 20000, 5, 5, True, "mixed", noise=1.0))
+    tree = [t[k] for k in ("p", "q", "tokens", "parent", "draft_row", "node_start", "u_accept", "u_pick")]
+
+    def all_of_them():
+        out = sv.verify_tree(*tree, max_nodes=5, max_depth=5)
+        return [sv.linear(x, w, out_dtype=torch.float32), sv.linear(xs, ws), sv.softmax(logits, 0.8)] + \
+            [out[k] for k in sorted(out)]
+
+    want = all_of_them()
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=one):
+        captured = all_of_them()
+    got = []
+    for _ in range(8):
+        with torch.cuda.stream(one):
+            graph.replay()
+        with torch.cuda.stream(two):
+            got.append(all_of_them())
+    torch.cuda.synchronize()
+    for result in got + [captured]:
+        for a, b in zip(result, want):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------- softmax
 
 def _assert_softmax(got, logits, t):
@@ -239,6 +292,12 @@ def test_softmax_rows_without_a_distribution(sv, dtype, V):
     t[6], t[7], t[8] = -1.0, float("nan"), float("inf")
     y = sv.softmax(x, t)
     assert bool(torch.isnan(y[[1, 2, 3, 6, 7, 8]]).all())
+    cold = sv.softmax(x, torch.where(t > 0, 0.0, t))
+    assert bool(torch.isnan(cold[[1, 2, 3, 6, 7]]).all())
+    assert torch.equal(cold[[0, 4, 5]].argmax(1), x[[0, 4, 5]].float().argmax(1))
+    assert bool((cold[[0, 4, 5]].sum(1) == 1).all())
+    mixed = sv.softmax(x, torch.tensor([0.0, 1, 0, 1, 1, 1, 0, 0, 1], device="cuda"))  # warm and cold rows in turn
+    assert torch.equal(mixed[[0, 4]], torch.cat([cold[:1], y[4:5]]))
     assert torch.equal(y[4], torch.nn.functional.one_hot(torch.tensor(V - 1), V).float().cuda())
     _assert_softmax(y[[0, 5]], x[[0, 5]], 1.0)
 
@@ -386,6 +445,13 @@ def test_tree_probabilities_that_are_none(sv, what):
     else:
         batch["p"][batch["node_start"][5] + 5 + 3 if batch["node_start"][6] - batch["node_start"][5] == 3 else 0] = np.nan
     _check_tree(sv, batch, 3, 3)
+
+
+def test_tree_uniforms_that_are_none_refuse(sv):
+    batch = ref.random_tree_batch(16, 30, 300, 5, 3, True, "mixed", noise=0.3)
+    batch["u_accept"][:] = np.nan
+    w, cnt = _check_tree(sv, batch, 5, 3)
+    assert cnt[1] == 0 and cnt[3] > 0
 
 
 @pytest.mark.parametrize("kind,replacement", [("sampled", True), ("sampled", False), ("certain", True)])

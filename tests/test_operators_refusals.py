@@ -42,6 +42,7 @@ def _call(fn, base, change):
     (dict(bias=A + 1, bias_dt=1), m.SV_EINVAL), (dict(residual=A + 2, residual_dt=0), m.SV_EINVAL),
     (dict(y_row=31), m.SV_EINVAL), (dict(y_group=96), m.SV_EINVAL), (dict(y_row=64, y_group=33), m.SV_EINVAL),
     (dict(y_row=0), m.SV_EINVAL), (dict(y_group=0), m.SV_EINVAL),
+    (dict(K=(1 << 30) + 1), m.SV_EUNSUPPORTED), (dict(N=(1 << 31) - 1, y_row=1 << 33, y_group=1 << 31), m.SV_EUNSUPPORTED),
 ])
 def test_linear_refuses(change, status):
     assert _call(sv.spec_verify_linear, LINEAR, change) == status
