@@ -150,7 +150,7 @@ constexpr int kMmaK = 64;        // entries of K a stage holds of each row: 128 
 constexpr int kRowBytes = 128;
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
-constexpr int kLoadWarps = 8;
+constexpr int kLoadWarps = 8, kLoadGroups = 2;  // warps that load a stage together; groups of them, by turns
 constexpr int kMmaThreads = 32 * (2 + kEpiWarps);
 constexpr int kStageCols = 64;   // columns of a tile that the epilogue passes through shared memory at a time
 constexpr int kMmaSmem = 225 * 1024;
@@ -358,7 +358,7 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* p, 
 
 // kWeightsA: w is A.  kSegments: see above.  kLoad: warps load the stages; otherwise TMA does, and where w is A the CTAs work in pairs.
 template <bool kWeightsA, bool kLoad, bool kSegments>
-__global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1)
+__global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoadWarps : 0), 1)
     mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
   constexpr bool kPair = kWeightsA && !kLoad;
@@ -407,9 +407,11 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
   // picks issues: with a branch on the lane instead the compiler takes the
   // operands for different in every lane, and an issue costs several times as much.
   if (kLoad && warp >= 2 + kEpiWarps) {
-    // Every warp takes part in every stage.  (Warps that took whole stages in turn could come to a stage two phases
-    // early where there were more of them than stages, and a parity does not tell two phases from none.)
-    const int mine = warp - 2 - kEpiWarps;
+    // Two groups of warps fill the stages by turns, so that the loads of one are on their way while the other stores.
+    // (More groups than stages could come to a stage two phases early, and a parity does not tell two phases from none;
+    // there are three stages at least.)
+    const int mine = (warp - 2 - kEpiWarps) % kLoadWarps, group = (warp - 2 - kEpiWarps) / kLoadWarps;
+    int turn = 0;
     unsigned s = 0, phase = 1;
     for (unsigned t = first; t < P.tiles && !dead; t += step) {
       const TileAt at = tile_at(P, t);
@@ -418,14 +420,17 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadWarps : 0), 1
       const __nv_bfloat16* x = P.L.x + at.g * P.L.x_group + m0 * P.L.x_row;
       const __nv_bfloat16* w = P.L.w + at.g * P.L.w_group + n0 * P.L.w_row;
       for (int kb = 0; kb < P.kblocks; ++kb) {
-        if (!mbar_wait(&empty[s], phase, &dead)) break;
-        const uint32_t dst = base + s * stage_bytes;
-        load_rows(kWeightsA ? dst : dst + a_bytes, w, P.L.w_row, kWeightsA ? P.ra : P.nt, P.L.N - n0, kb * kMmaK, P.L.K,
-                  mine);
-        load_rows(kWeightsA ? dst + a_bytes : dst, x, P.L.x_row, kWeightsA ? P.nt : P.ra, P.L.M - m0, kb * kMmaK, P.L.K,
-                  mine);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+        if (turn == group) {
+          if (!mbar_wait(&empty[s], phase, &dead)) break;
+          const uint32_t dst = base + s * stage_bytes;
+          load_rows(kWeightsA ? dst : dst + a_bytes, w, P.L.w_row, kWeightsA ? P.ra : P.nt, P.L.N - n0, kb * kMmaK, P.L.K,
+                    mine);
+          load_rows(kWeightsA ? dst + a_bytes : dst, x, P.L.x_row, kWeightsA ? P.nt : P.ra, P.L.M - m0, kb * kMmaK, P.L.K,
+                    mine);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
+        if (++turn == kLoadGroups) turn = 0;
         if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
       }
     }
@@ -802,6 +807,7 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   P.segs = std::max(1, (P.kblocks + P.seg_blocks - 1) / P.seg_blocks);
   const int stage_bytes = P.sub * sub_bytes;
   P.stages = std::min(kMaxStages, room / stage_bytes);
+  if (kLoad && P.stages < kLoadGroups) return SV_EUNSUPPORTED;  // never: see the loading warps
   P.staging = 1024 + P.stages * stage_bytes + slack;
   const int smem = static_cast<int>(P.staging) + staging;
   P.tmem_cols = 32;
@@ -818,7 +824,7 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
     if (device < 64) opted_in[device].store(true);
   }
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, workers)) * (kPair ? 2 : 1);
-  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad, kSegments>, grid, kMmaThreads + (kLoad ? 32 * kLoadWarps : 0),
+  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad, kSegments>, grid, kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoadWarps : 0),
                                        smem, kPair ? 2 : 1, st, P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
   return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
