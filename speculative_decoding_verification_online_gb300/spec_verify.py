@@ -214,7 +214,7 @@ def _ptr(t):
 
 
 def _check(t: torch.Tensor, name: str, shape, dtype=None, device=None):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
@@ -225,15 +225,17 @@ def _check(t: torch.Tensor, name: str, shape, dtype=None, device=None):
 
 
 def _check_rows(t: torch.Tensor, name: str, dim: int, dtype=None, device=None):
-    """A tensor of ``dim`` dimensions whose rows are contiguous, the other strides being free."""
-    if t.dim() != dim:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dim}")
+    """A tensor of ``dim`` dimensions whose rows are contiguous, the other strides being free; returns its strides."""
+    strides = t.stride()
+    if len(strides) != dim:
+        raise ValueError(f"{name}: {len(strides)} dimensions, expected {dim}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype} != {dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and 0 not in t.shape:
+    if strides[-1] != 1 and t.shape[-1] > 1 and 0 not in t.shape:
         raise ValueError(f"{name}: rows must be contiguous")
+    return strides
 
 
 def _cuda_device(t: torch.Tensor, name: str):
@@ -261,40 +263,47 @@ def linear(x, weight, bias=None, residual=None, activation="none", cap=0.0, out=
     is recorded."""
     dev = _cuda_device(x, "x")
     bf16 = torch.bfloat16
-    if weight.dim() not in (2, 3):
-        raise ValueError(f"weight: {weight.dim()} dimensions, expected 2 or 3")
-    grouped = weight.dim() == 3
-    _check_rows(weight, "weight", weight.dim(), bf16, dev)
-    G = weight.shape[0] if grouped else 1
-    N, K = weight.shape[-2:]
-    shared = x.dim() == 2
-    _check_rows(x, "x", 2 if shared else 3, bf16, dev)
-    if not shared and (not grouped or x.shape[0] != G):
-        raise ValueError(f"x: shape {tuple(x.shape)} does not go with weight {tuple(weight.shape)}")
-    M = x.shape[-2]
-    if x.shape[-1] != K:
-        raise ValueError(f"x: rows of {x.shape[-1]}, weight has rows of {K}")
+    wshape, xshape = weight.shape, x.shape
+    dim = len(wshape)
+    if dim not in (2, 3):
+        raise ValueError(f"weight: {dim} dimensions, expected 2 or 3")
+    ws = _check_rows(weight, "weight", dim, bf16, dev)
+    grouped = dim == 3
+    shared = len(xshape) == 2
+    xs = _check_rows(x, "x", 2 if shared else 3, bf16, dev)
+    G = wshape[0] if grouped else 1
+    if not shared and (not grouped or xshape[0] != G):
+        raise ValueError(f"x: shape {tuple(xshape)} does not go with weight {tuple(wshape)}")
+    M, N, K = xshape[-2], wshape[-2], wshape[-1]
+    if xshape[-1] != K:
+        raise ValueError(f"x: rows of {xshape[-1]}, weight has rows of {K}")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
     shape = (G, M, N) if grouped else (M, N)
-    dim = len(shape)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or bf16, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: dtype {out.dtype} != {out_dtype}")
-    for t, name, shp in ((out, "out", shape), (residual, "residual", shape), (bias, "bias", (G, N) if grouped else (N,))):
-        if t is not None:
-            _check_rows(t, name, len(shp), None, dev)
-            if t.shape != shp:
-                raise ValueError(f"{name}: shape {tuple(t.shape)} != {shp}")
-    r = residual
+    ys = _check_rows(out, "out", dim, None, dev)
+    if out.shape != shape:
+        raise ValueError(f"out: shape {tuple(out.shape)} != {shape}")
+    rp, rdt, rrow, rgroup = None, 0, 0, 0
+    if residual is not None:
+        rs = _check_rows(residual, "residual", dim, None, dev)
+        if residual.shape != shape:
+            raise ValueError(f"residual: shape {tuple(residual.shape)} != {shape}")
+        rp, rdt, rrow, rgroup = residual.data_ptr(), _dt(residual), rs[-2], rs[0] if grouped else 0
+    bp, bdt, bgroup = None, 0, 0
+    if bias is not None:
+        bs = _check_rows(bias, "bias", dim - 1, None, dev)
+        if bias.shape != ((G, N) if grouped else (N,)):
+            raise ValueError(f"bias: shape {tuple(bias.shape)} != {(G, N) if grouped else (N,)}")
+        bp, bdt, bgroup = bias.data_ptr(), _dt(bias), bs[0] if grouped else 0
     rc = spec_verify_linear(
-        x.data_ptr(), x.stride(-2), 0 if shared else x.stride(0), weight.data_ptr(), weight.stride(-2),
-        weight.stride(0) if grouped else 0, _ptr(bias), 0 if bias is None else _dt(bias),
-        bias.stride(0) if grouped and bias is not None else 0, _ptr(r), 0 if r is None else _dt(r),
-        0 if r is None else r.stride(-2), r.stride(0) if grouped and r is not None else 0, out.data_ptr(), _dt(out),
-        out.stride(-2), out.stride(0) if dim == 3 else 0, G, M, N, K, act, float(cap), dev.index, _stream(dev, stream))
+        x.data_ptr(), xs[-2], 0 if shared else xs[0], weight.data_ptr(), ws[-2], ws[0] if grouped else 0, bp, bdt, bgroup,
+        rp, rdt, rrow, rgroup, out.data_ptr(), _dt(out), ys[-2], ys[0] if grouped else 0, G, M, N, K, act, float(cap),
+        dev.index, _stream(dev, stream))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_linear")
     return out
@@ -342,21 +351,24 @@ def verify_tree(target_probs, draft_probs, tokens, parent, draft_row, node_start
     path [B, max_depth], accept_prob and flags [nodes]."""
     dev = _cuda_device(target_probs, "target_probs")
     f32, i32 = torch.float32, torch.int32
-    _check_rows(target_probs, "target_probs", 2, f32, dev)
-    V = target_probs.shape[1]
+    p_stride = _check_rows(target_probs, "target_probs", 2, f32, dev)[0]
+    rows_p, V = target_probs.shape
     B, total = u_pick.shape[0], tokens.shape[0]
-    if target_probs.shape[0] != total + B:
-        raise ValueError(f"target_probs: {target_probs.shape[0]} rows, expected {total + B}")
-    rows_q, q_stride = 0, 0
+    if rows_p != total + B:
+        raise ValueError(f"target_probs: {rows_p} rows, expected {total + B}")
+    q, rows_q, q_stride = None, 0, 0
     if draft_probs is not None:
-        _check_rows(draft_probs, "draft_probs", 2, f32, dev)
-        if draft_probs.shape[1] != V:
-            raise ValueError(f"draft_probs: rows of {draft_probs.shape[1]}, expected {V}")
-        rows_q, q_stride = draft_probs.shape[0], draft_probs.stride(0)
-    for t, name, n, dtype in ((tokens, "tokens", total, i32), (parent, "parent", total, i32),
-                              (draft_row, "draft_row", total + B, i32), (node_start, "node_start", B + 1, i32),
-                              (u_accept, "u_accept", total, f32), (u_pick, "u_pick", B, f32)):
-        _check(t, name, (n,), dtype, dev)
+        q_stride = _check_rows(draft_probs, "draft_probs", 2, f32, dev)[0]
+        q, (rows_q, V_q) = draft_probs.data_ptr(), draft_probs.shape
+        if V_q != V:
+            raise ValueError(f"draft_probs: rows of {V_q}, expected {V}")
+    nodes = (total,)
+    _check(tokens, "tokens", nodes, i32, dev)
+    _check(parent, "parent", nodes, i32, dev)
+    _check(draft_row, "draft_row", (total + B,), i32, dev)
+    _check(node_start, "node_start", (B + 1,), i32, dev)
+    _check(u_accept, "u_accept", nodes, f32, dev)
+    _check(u_pick, "u_pick", (B,), f32, dev)
     if counters is not None:
         _check(counters, "counters", (8,), torch.int64, dev)
     if max_nodes is None:
@@ -376,7 +388,7 @@ def verify_tree(target_probs, draft_probs, tokens, parent, draft_row, node_start
             if name in out:
                 _check(out[name], name, shp, dtype, dev)
     rc = spec_verify_tree(
-        target_probs.data_ptr(), target_probs.stride(0), _ptr(draft_probs), q_stride, rows_q, node_start.data_ptr(),
+        target_probs.data_ptr(), p_stride, q, q_stride, rows_q, node_start.data_ptr(),
         tokens.data_ptr(), parent.data_ptr(), draft_row.data_ptr(), u_accept.data_ptr(), u_pick.data_ptr(), B, total,
         max_nodes, max_depth, V, SV_WITH_REPLACEMENT if replacement else SV_WITHOUT_REPLACEMENT,
         out["accepted_len"].data_ptr(), out["tokens"].data_ptr(), _ptr(out.get("path")), _ptr(out.get("accept_prob")),
