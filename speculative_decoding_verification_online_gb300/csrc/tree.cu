@@ -58,7 +58,11 @@ struct TreeShared {
   float px[SV_MAX_NODES], qx[SV_MAX_NODES], u[SV_MAX_NODES], alpha[SV_MAX_NODES];
   int32_t refused[SV_MAX_NODES];  // distinct tokens refused at a node without a draft row
   int8_t flag[SV_MAX_NODES], again[SV_MAX_NODES];
-  float2 slot[2][kTreeCluster];  // the CTAs' sums of a pass, by its parity
+  // the CTAs' sums of a pass, by its parity: a CTA writes a place again only after every other one has passed the
+  // exchange between
+  float2 slot[2][kTreeCluster];
+  uint64_t arrived[2];
+  int dead;
   // what the first warp asks of the others
   const float* row_p;
   const float* row_q;  // null: c is 0
@@ -103,14 +107,73 @@ __device__ __forceinline__ Pair over(const Pair& a, const Pair& b) {
   return Pair{x, ((a.s - back.s) + (a.l - back.l)) / b.s}.settled();
 }
 
-// (p - (c + cl) q)+; a NaN stays.  kOne: c + cl is 1, as after a first refusal
-template <bool kOne>
+// (p - (c + cl) q)+; a NaN stays
 __device__ __forceinline__ Pair rest_of(float p, float q, float c, float cl) {
-  const float h = kOne ? q : __fmul_rn(c, q);  // not to be fused into the difference below
-  const float hl = kOne ? 0.f : fmaf(cl, q, fmaf(c, q, -h));
+  const float h = __fmul_rn(c, q);  // not to be fused into the difference below
+  const float hl = fmaf(cl, q, fmaf(c, q, -h));
   const float d = p - h, z = d - p;
   const float dl = ((p - (d - z)) - (h + z)) - hl;
   return d + dl <= 0.f ? Pair{0.f, 0.f} : Pair{d, dl};
+}
+
+// Two floats in a 64-bit register: one instruction for both, each rounded by itself.
+using Two = unsigned long long;
+
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two t) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(t));
+  return f;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// b - a: a product with -1 is exact
+__device__ __forceinline__ Two minus2(Two b, Two a) { return fma2(a, two(-1.f, -1.f), b); }
+
+// two running sums
+struct Pairs {
+  Two s, l;
+  __device__ __forceinline__ void add(Two x) {
+    const Two t = add2(s, x), z = minus2(t, s);
+    l = add2(l, add2(minus2(s, minus2(t, z)), minus2(x, z)));
+    s = t;
+  }
+  __device__ __forceinline__ Pair total() const {
+    const float2 a = both(s), b = both(l);
+    Pair p = {a.x, b.x};
+    p.add(Pair{a.y, b.y});
+    return p;
+  }
+};
+
+// rest_of for two entries, onto the sums.  kOne: c + cl is 1
+template <bool kOne>
+__device__ __forceinline__ void add_rests(Pairs& sum, Two p, Two q, Two c, Two minus_c, Two cl) {
+  const Two nh = kOne ? minus2(two(0.f, 0.f), q) : mul2(minus_c, q);  // - c q, rounded
+  const Two d = add2(p, nh), z = minus2(d, p);
+  Two dl = minus2(minus2(p, minus2(d, z)), minus2(z, nh));
+  if (!kOne) dl = minus2(dl, fma2(cl, q, fma2(c, q, nh)));
+  const float2 r = both(add2(d, dl)), a = both(d), b = both(dl);
+  const bool x = r.x <= 0.f, y = r.y <= 0.f;  // not so for a NaN, which stays
+  sum.add(two(x ? 0.f : a.x, y ? 0.f : a.y));
+  sum.l = add2(sum.l, two(x ? 0.f : b.x, y ? 0.f : b.y));
 }
 
 __device__ __forceinline__ Pair warp_total(Pair x) {
@@ -138,7 +201,7 @@ __device__ __forceinline__ Pair rest_at(const TreeShared& s, int v) {
   for (int i = 0; i < s.n_refused; ++i)
     if (s.refused[i] == v) return {0.f, 0.f};
   const float p = s.row_p[v];
-  return s.row_q ? rest_of<false>(p, s.row_q[v], s.c, s.cl) : Pair{fmaxf(p, 0.f), 0.f};
+  return s.row_q ? rest_of(p, s.row_q[v], s.c, s.cl) : Pair{fmaxf(p, 0.f), 0.f};
 }
 
 // four neighbouring entries of a row; nothing beyond its end
@@ -152,21 +215,13 @@ __device__ __forceinline__ float4 load4(const float* row, int v, int V) {
   return make_float4(v < V ? row[v] : 0.f, v + 1 < V ? row[v + 1] : 0.f, v + 2 < V ? row[v + 2] : 0.f, 0.f);
 }
 
-template <bool kOne>
-__device__ __forceinline__ void add_rests(Pair (&sum)[4], const float4& p, const float4& q, float c, float cl) {
-  sum[0].add(rest_of<kOne>(p.x, q.x, c, cl));
-  sum[1].add(rest_of<kOne>(p.y, q.y, c, cl));
-  sum[2].add(rest_of<kOne>(p.z, q.z, c, cl));
-  sum[3].add(rest_of<kOne>(p.w, q.w, c, cl));
-}
-
 // the weight of each of this CTA's chunks into chunk_sum: every warp
 template <bool kVec>
 __device__ __forceinline__ void chunk_sums(const TreeShared& s, float2* chunk_sum, int V, int first, int last) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float c = s.c, cl = s.cl;
   for (int ch = first + warp; ch < last; ch += kTreeWarps) {
-    Pair sum[4] = {};
+    Pairs sum[2] = {};
     const int v0 = ch * kTreeChunk + lane * 4;
     float4 p[4], q[4];
 #pragma unroll
@@ -174,12 +229,19 @@ __device__ __forceinline__ void chunk_sums(const TreeShared& s, float2* chunk_su
     if (s.row_q) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) q[j] = load4<kVec>(s.row_q, v0 + j * 128, V);
+      const Two c2 = two(c, c), minus_c2 = two(-c, -c), cl2 = two(cl, cl);
       if (c == 1.f && cl == 0.f) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) add_rests<true>(sum, p[j], q[j], c, cl);
+        for (int j = 0; j < 4; ++j) {
+          add_rests<true>(sum[0], two(p[j].x, p[j].y), two(q[j].x, q[j].y), c2, minus_c2, cl2);
+          add_rests<true>(sum[1], two(p[j].z, p[j].w), two(q[j].z, q[j].w), c2, minus_c2, cl2);
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) add_rests<false>(sum, p[j], q[j], c, cl);
+        for (int j = 0; j < 4; ++j) {
+          add_rests<false>(sum[0], two(p[j].x, p[j].y), two(q[j].x, q[j].y), c2, minus_c2, cl2);
+          add_rests<false>(sum[1], two(p[j].z, p[j].w), two(q[j].z, q[j].w), c2, minus_c2, cl2);
+        }
       }
     } else {
       bool hit = false;
@@ -194,18 +256,17 @@ __device__ __forceinline__ void chunk_sums(const TreeShared& s, float2* chunk_su
             if (at == 2) p[j].z = 0.f;
             if (at == 3) p[j].w = 0.f;
           }
+      // a NaN or an infinity stays: p - p is 0 for every other p
+      auto weight = [](float x) { return fmaxf(x, 0.f) + (x - x); };
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sum[0].add(fmaxf(p[j].x, 0.f) + (p[j].x - p[j].x));  // a NaN or an infinity stays
-        sum[1].add(fmaxf(p[j].y, 0.f) + (p[j].y - p[j].y));
-        sum[2].add(fmaxf(p[j].z, 0.f) + (p[j].z - p[j].z));
-        sum[3].add(fmaxf(p[j].w, 0.f) + (p[j].w - p[j].w));
+        sum[0].add(two(weight(p[j].x), weight(p[j].y)));
+        sum[1].add(two(weight(p[j].z), weight(p[j].w)));
       }
     }
-    sum[0].add(sum[1]);
-    sum[2].add(sum[3]);
-    sum[0].add(sum[2]);
-    const Pair t = warp_total(sum[0]).settled();
+    Pair mine = sum[0].total();
+    mine.add(sum[1].total());
+    const Pair t = warp_total(mine).settled();
     if (lane == 0) chunk_sum[ch - first] = make_float2(t.s, t.l);
   }
 }
@@ -252,13 +313,15 @@ __device__ int pick(const TreeShared& s, const float2* chunk_sum, int V, int fir
   if (s.row_q) {
 #pragma unroll
     for (int j = 0; j < kRun / 4; ++j) q[j] = load4<kVec>(s.row_q, v0 + 4 * j, V);
-    Pair sum[4] = {};
+    Pairs sum[2] = {};
+    const Two c2 = two(s.c, s.c), minus_c2 = two(-s.c, -s.c), cl2 = two(s.cl, s.cl);
 #pragma unroll
-    for (int j = 0; j < kRun / 4; ++j) add_rests<false>(sum, p[j], q[j], s.c, s.cl);
-    sum[0].add(sum[1]);
-    sum[2].add(sum[3]);
-    sum[0].add(sum[2]);
-    mine = sum[0];
+    for (int j = 0; j < kRun / 4; ++j) {
+      add_rests<false>(sum[0], two(p[j].x, p[j].y), two(q[j].x, q[j].y), c2, minus_c2, cl2);
+      add_rests<false>(sum[1], two(p[j].z, p[j].w), two(q[j].z, q[j].w), c2, minus_c2, cl2);
+    }
+    mine = sum[0].total();
+    mine.add(sum[1].total());
   } else if (s.n_refused == 0) {
 #pragma unroll
     for (int j = 0; j < kRun / 4; ++j) {
@@ -283,6 +346,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
   __shared__ TreeShared s;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
+  if (threadIdx.x == 0) {
+    mbar_init(&s.arrived[0], 1);
+    mbar_init(&s.arrived[1], 1);
+    s.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   cluster.barrier_arrive();  // every CTA of the cluster runs before any writes into another
   wait_for_stream();
   const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31;
@@ -397,7 +466,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
           yes = fmaf(u, qx, -px) <= 0.f;
           alpha = qx > px ? px / qx : 1.f;
         } else {
-          r = bare ? Pair{s.again[i] ? 0.f : px, 0.f} : rest_of<false>(px, qx, c.s, c.l);
+          r = bare ? Pair{s.again[i] ? 0.f : px, 0.f} : rest_of(px, qx, c.s, c.l);
           if (!bare && !P.replacement) {
             w.add(-mass.s);
             w.l -= mass.l;
@@ -457,10 +526,17 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
       Pair t = zero;
       for (int i = lane; i < last - first; i += 32) t.add(Pair{chunk_sum[i].x, chunk_sum[i].y});
       t = warp_total(t).settled();
-      if (lane < ctas) *cluster.map_shared_rank(&s.slot[pass & 1][rank], lane) = make_float2(t.s, t.l);
+      // The sum goes into every CTA's memory, and the write itself counts there: a cluster barrier would hold up all
+      // threads, and first wait for their stores.
+      if (lane == 0) mbar_expect(&s.arrived[pass & 1], ctas * sizeof(float2));
+      if (lane < ctas)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                         in_cta(&s.slot[pass & 1][rank], lane)),
+                     "f"(t.s), "f"(t.l), "r"(in_cta(&s.arrived[pass & 1], lane))
+                     : "memory");
+      if (!mbar_wait(&s.arrived[pass & 1], pass >> 1 & 1, &s.dead)) bad = 1;
     }
     ++pass;
-    cluster.sync();
   }
 
   if (tid < 32 && s.work == kTreePick) {
