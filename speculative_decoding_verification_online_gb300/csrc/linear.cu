@@ -153,7 +153,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kLoadWarps = 8, kLoadGroups = 2;  // warps that load a stage together; groups of them, by turns
 constexpr int kMmaThreads = 32 * (2 + kEpiWarps);
 constexpr int kStageCols = 64;   // columns of a tile that the epilogue passes through shared memory at a time
-constexpr int kMmaSmem = 225 * 1024;
+constexpr int kMmaSmem = 226 * 1024;
 
 struct MmaParams {
   LinearParams L;
