@@ -2,7 +2,9 @@
 
 Modified rejection sampling in plain and mu/NULL-gated modes: a streaming
 kernel and a per-sequence finishing kernel behind the C ABI of
-``include/spec_verify.h``.  This package holds the CUDA sources (``csrc/``),
+``include/spec_verify.h``.  Around that call: grouped matrix products with an
+epilogue (``linear``), probabilities of logits rows (``softmax``) and the
+verification of drafted trees from probabilities (``verify_tree``).  This package holds the CUDA sources (``csrc/``),
 the build step, the ctypes binding, the sequence-sharding helper and the
 acceptance summary over the batch counters (``metrics``).
 """

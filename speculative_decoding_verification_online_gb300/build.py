@@ -2,7 +2,8 @@
 
 ``python -m speculative_decoding_verification_online_gb300.build`` (or
 ``build()``) compiles the translation units of ``csrc/`` (one nvcc process
-each, in parallel: the C ABI, and the kernels of each pair of logits types)
+each, in parallel: the C ABI, the kernels of each pair of logits types, and the
+operators around a verifying call)
 and links them into ``libspec_verify.so`` next to this file.  The build is in-tree and skipped when the library is newer
 than every source.
 """

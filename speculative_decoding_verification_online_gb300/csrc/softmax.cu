@@ -14,6 +14,11 @@
 // last factor exp((largest of the thread - largest of the row) / T) / sum is one
 // multiplication an entry.  Parts longer than the registers hold are read twice,
 // the second time from L2.
+//
+// Measured on a GB300: 384 rows of 128256 bf16 logits 57 to 61 us, 4.9 to 5.2 TB/s of
+// 6.78 (36 clusters of eight CTAs fit; a row's turn is its arithmetic, 17 warp
+// instructions for 32 entries, then an exchange that the other CTA of the SM has
+// to cover); 746 x 62236 49 us, 5.7 TB/s; seven rows of 262143 fp32 logits 5 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
