@@ -3,8 +3,9 @@
 //   y[g, m, n] = act(sum_k x[g, m, k] w[g, n, k] + bias[g, n]) + residual[g, m, n]
 //
 // The products run on the tensor cores (tcgen05).  Rows of x and w that start at
-// multiples of 16 bytes come in by TMA; where one of the two does not, sixteen warps
-// of each CTA load both instead.
+// multiples of 16 bytes come in by TMA.  Where one of the two does not, w still comes
+// by TMA, in classes of rows that start at the same place in 16 bytes, and warps load
+// x, shifted to match.
 //
 // What bounds it, measured on a GB300 (6.78 TB/s, 1.95 PFLOP/s bf16 measured with a
 // copy and a library product):
@@ -15,8 +16,10 @@
 //    4096: 298 us, 2.03 PFLOP/s alone, 1.79 under load; M = 384, N = 128256, K =
 //    4096: 248 us, 1.62 PFLOP/s (75 % of the cycles in products: 200 KB of stages in
 //    flight a SM do not cover what w takes to come from HBM).
-//  * rows at odd addresses: the loading warps' instructions.  M = 77, N = 32001, K =
-//    1001: 42 us, 1.7 TB/s.
+//  * rows at odd addresses: what the loading warps wait for and execute.  M = 77, N =
+//    32001, K = 1001: 30 us, 2.3 TB/s (42 us where warps load both operands); M = 8,
+//    K = 2001: 33 us (66); M = 300, K = 1001: 66 us (137); M = 2304, N = 32000,
+//    K = 4097: 775 us, 0.78 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -130,7 +133,7 @@ __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, 
 //
 // Persistent CTAs, one per SM, each (or each pair) taking every n-th tile of y.  Warp 0
 // fetches tiles of both operands by TMA into a ring of stages, 64 entries of
-// K at a time (rows of 128 bytes, 128-byte swizzle), or warps 10 to 25 load them;
+// K at a time (rows of 128 bytes, 128-byte swizzle), or warps 10 to 25 load x's;
 // warp 1 multiplies them into tensor memory, 128 rows of one operand (A) by nt rows
 // of the other (B); warps 2 to 9 take the sums out and finish them while the next
 // tile is multiplied into the other half of the accumulators.
@@ -140,8 +143,8 @@ __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, 
 //    pair of SMs): each holds 128 rows of A and half the rows of B, and one
 //    product instruction of the first CTA works on both.  A lane of tensor
 //    memory is one n, so a warp's 32 lanes write 32 neighbours of y for each m,
-//    straight from registers.  (Stages that warps load are not shared by pairs.)
-//  * M <= 128: x.  The call is bound by reading w, and the width of a tile of
+//    straight from registers.
+//  * M <= 128, or rows at odd addresses (128 tokens at a time): x.  The call is bound by reading w, and the width of a tile of
 //    w is then free (any multiple of 16 up to 256), so that the tiles come out
 //    even over the SMs.  Lanes are tokens here; sums pass through shared memory
 //    so that neighbouring threads finish neighbouring n, however few tokens
@@ -161,7 +164,10 @@ constexpr int kMmaK = 64;        // entries of K a stage holds of each row: 128 
 constexpr int kRowBytes = 128;
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
-constexpr int kLoadWarps = 8, kLoadGroups = 2;  // warps that load a stage together; groups of them, by turns
+// Warps that load a stage of x together; groups of them, by turns.  Four groups of four against two of eight and two of
+// four: M = 77, N = 32001, K = 2001 56, 59 and 69 us; M = 1000, N = 8001, K = 4097 178, 187 and 207 us; M = 8, N = 32001,
+// K = 2001 33, 32 and 31 us.
+constexpr int kLoadWarps = 4, kLoadGroups = 4;
 constexpr int kMmaThreads = 32 * (2 + kEpiWarps);
 constexpr int kStageCols = 64;   // columns of a tile that the epilogue passes through shared memory at a time
 constexpr int kMmaSmem = 226 * 1024;
@@ -180,7 +186,17 @@ struct MmaParams {
   unsigned tiles;
   unsigned idesc;
   unsigned staging;      // where the epilogue's staging starts in dynamic shared memory
+  // where warps load x (see below)
+  int w_mapped;          // 1: w comes by TMA, 0: the warps load it too
+  int every, classes;    // so many rows of w are between two of a class; classes that have rows
+  int group_classes;     // the same of groups
 };
+
+template <int kMaps>
+struct Maps {
+  CUtensorMap m[kMaps];
+};
+constexpr int kMostMaps = 64;  // eight classes of rows times eight of groups
 
 // one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
@@ -290,14 +306,34 @@ __device__ __forceinline__ void tc_store(uint32_t addr, const uint32_t (&r)[16])
 }
 
 struct TileAt {
-  int ta, tb, g;
+  int ta, tb, g, cls;
 };
 
+// Where warps load x, the tokens' tiles follow one another (they share w's), then the classes (they share y's sectors).
+template <bool kLoad>
 __device__ __forceinline__ TileAt tile_at(const MmaParams& P, unsigned t) {
+  if constexpr (kLoad) {
+    const unsigned ta = t % P.tiles_a, u = t / P.tiles_a, cls = u % P.classes, v = u / P.classes;
+    return {static_cast<int>(ta), static_cast<int>(v % P.tiles_b), static_cast<int>(v / P.tiles_b), static_cast<int>(cls)};
+  }
   const unsigned tb = t % P.tiles_b, rest = t / P.tiles_b;
-  return {static_cast<int>(rest % P.tiles_a), static_cast<int>(tb), static_cast<int>(rest / P.tiles_a)};
+  return {static_cast<int>(rest % P.tiles_a), static_cast<int>(tb), static_cast<int>(rest / P.tiles_a), 0};
 }
 
+// ---- rows at odd addresses
+//
+// TMA wants rows that start at multiples of 16 bytes.  If rows of w are s entries
+// apart, every 8 / gcd(8, s)-th row starts at the same place in 16 bytes: those rows
+// are a class, a matrix of its own, which has a map that begins at the multiple of 16
+// bytes in front of its first row.  In the map a row stands `behind` (0 to 7) entries
+// from its start; a sum over K does not mind if x's rows are moved behind by as much.
+// A tile of y takes columns of one class; the classes of the same columns follow one
+// another, so that the parts of a sector of y meet in L2.  What a map shows in front
+// of a row belongs to another row, or to nobody (and may be a NaN, which a zero of x
+// would not take out of a sum): the first 64 entries of K are loaded by the warps for
+// w too, with zeros there.  Behind a row's end the map has zeros.
+// Groups of w that are not multiples of 16 bytes apart are classes in the same way.
+//
 // Eight entries of a row from any address that bf16 entries have, in the one or two aligned blocks of 16 bytes that hold
 // them.  Only blocks with an entry of the row are read: an allocation has all of such a block.
 __device__ __forceinline__ uint4 load_if(const uint4* p, bool there) {
@@ -315,16 +351,17 @@ struct Run {
   uint4 a, b;
   int shift;  // bytes in front of the first entry
 
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int valid) {
+  // those from `front` on, in front of `valid`
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int front, int valid) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
     const uint4* block = reinterpret_cast<const uint4*>(at & ~uintptr_t{15});
     shift = static_cast<int>(at & 15);
-    a = load_if(block, valid > 0);
-    b = load_if(block + 1, shift + 2 * valid > 16);
+    a = load_if(block, valid > front && shift + 2 * front < 16);
+    b = load_if(block + 1, valid > front && shift + 2 * valid > 16);
   }
 
-  // the entries, zeros behind the valid ones
-  __device__ __forceinline__ uint4 entries(int valid) const {
+  // the entries, zeros in place of the others
+  __device__ __forceinline__ uint4 entries(int front, int valid) const {
     const bool two = shift & 8, one = shift & 4;
     const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w,
                    w4 = two ? b.z : b.x, w5 = two ? b.w : b.y;
@@ -338,27 +375,34 @@ struct Run {
       r.z &= valid > 5 ? ~0u : valid > 4 ? 0xffffu : 0u;
       r.w &= valid > 7 ? ~0u : valid > 6 ? 0xffffu : 0u;
     }
+    if (front > 0) {
+      r.x &= front > 1 ? 0u : 0xffff0000u;
+      r.y &= front > 3 ? 0u : front > 2 ? 0xffff0000u : ~0u;
+      r.z &= front > 5 ? 0u : front > 4 ? 0xffff0000u : ~0u;
+      r.w &= front > 6 ? 0xffff0000u : ~0u;
+    }
     return r;
   }
 };
 
-// A warp's share (warp `mine` of the loading ones) of `rows` rows of 64 entries from k on, zeros beyond row `there` and
-// entry `K`, as TMA would lay them down: 16 bytes a lane, eight lanes a row.
+// A warp's share (warp `mine` of the loading ones) of `rows` rows of 64 entries from k on, as TMA would lay them down: 16
+// bytes a lane, eight lanes a row.  p is where an entry 0 of the first row would be; entries in front of `lo` and from `hi`
+// on are zeros, and so are rows from `there` on.
 __device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* p, int64_t stride, int rows, int64_t there,
-                                          int k, int K, int mine) {
+                                          int k, int lo, int hi, int mine) {
   const int lane = threadIdx.x & 31, c = lane % 8;
-  const int valid = max(0, min(8, K - k - 8 * c));
+  const int front = max(0, lo - k - 8 * c), valid = max(0, min(8, hi - k - 8 * c));
   constexpr int kBatch = 4, kStep = 4 * kLoadWarps;
   int r0 = 4 * mine + lane / 8;
   p += r0 * stride + k + 8 * c;
   for (; r0 < rows; r0 += kBatch * kStep, p += kBatch * kStep * stride) {
     Run v[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) v[i].load(p + i * kStep * stride, r0 + i * kStep < there ? valid : 0);
+    for (int i = 0; i < kBatch; ++i) v[i].load(p + i * kStep * stride, front, r0 + i * kStep < there ? valid : 0);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = r0 + i * kStep;
-      const uint4 e = v[i].entries(valid);
+      const uint4 e = v[i].entries(front, valid);
       if (r < rows)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * kRowBytes + ((c ^ (r & 7)) << 4)),
                      "r"(e.x), "r"(e.y), "r"(e.z), "r"(e.w)
@@ -367,12 +411,20 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* p, 
   }
 }
 
-// kWeightsA: w is A.  kSegments: see above.  kLoad: warps load the stages; otherwise TMA does, and where w is A the CTAs work in pairs.
+// the first row of w of a tile, and how many entries it starts behind a multiple of 16 bytes
+__device__ __forceinline__ const __nv_bfloat16* first_row(const MmaParams& P, const TileAt& at, int* behind) {
+  const int64_t n = at.cls + static_cast<int64_t>(at.tb) * P.nt * P.every;
+  const __nv_bfloat16* p = P.L.w + at.g * P.L.w_group + n * P.L.w_row;
+  *behind = P.w_mapped ? static_cast<int>(reinterpret_cast<uintptr_t>(p) / 2 % 8) : 0;
+  return p;
+}
+
+// kWeightsA: w is A, and the CTAs work in pairs.  kSegments: see above.  kLoad: rows at odd addresses.
 template <bool kWeightsA, bool kLoad, bool kSegments>
 __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoadWarps : 0), 1)
-    mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ CUtensorMap map_a,
-               const __grid_constant__ CUtensorMap map_b) {
-  constexpr bool kPair = kWeightsA && !kLoad;
+    mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ Maps<kLoad ? kMostMaps : 2> maps) {
+  static_assert(!(kWeightsA && kLoad));
+  constexpr bool kPair = kWeightsA;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
@@ -384,14 +436,14 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
   const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
   const uint32_t a_bytes = P.ra * kRowBytes, sub_bytes = a_bytes + b_rows * kRowBytes, stage_bytes = P.sub * sub_bytes;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], kLoad ? kLoadWarps : 1), mbar_init(&empty[s], 1);
+    for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], kLoad ? kLoadWarps + P.w_mapped : 1), mbar_init(&empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], kPair ? 2 * kEpiWarps : kEpiWarps);
     mbar_init(&drained, 1);
     dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if constexpr (!kLoad) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a));
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b));
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.m[0]));
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.m[1]));
     }
   }
   if (warp == 1) {
@@ -418,26 +470,25 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
   // picks issues: with a branch on the lane instead the compiler takes the
   // operands for different in every lane, and an issue costs several times as much.
   if (kLoad && warp >= 2 + kEpiWarps) {
-    // Two groups of warps fill the stages by turns, so that the loads of one are on their way while the other stores.
-    // (More groups than stages could come to a stage two phases early, and a parity does not tell two phases from none;
-    // there are three stages at least.)
+    // Groups of warps fill the stages by turns, so that the loads of one are on their way while others store.  (More
+    // groups than stages could come to a stage two phases early, and a parity does not tell two phases from none.)
     const int mine = (warp - 2 - kEpiWarps) % kLoadWarps, group = (warp - 2 - kEpiWarps) / kLoadWarps;
     int turn = 0;
     unsigned s = 0, phase = 1;
     for (unsigned t = first; t < P.tiles && !dead; t += step) {
-      const TileAt at = tile_at(P, t);
-      const int64_t m0 = kWeightsA ? static_cast<int64_t>(at.tb) * P.nt : 0;
-      const int64_t n0 = kWeightsA ? static_cast<int64_t>(at.ta) * 128 : static_cast<int64_t>(at.tb) * P.nt;
-      const __nv_bfloat16* x = P.L.x + at.g * P.L.x_group + m0 * P.L.x_row;
-      const __nv_bfloat16* w = P.L.w + at.g * P.L.w_group + n0 * P.L.w_row;
+      const TileAt at = tile_at<kLoad>(P, t);
+      int behind;
+      const __nv_bfloat16* w = first_row(P, at, &behind) - behind;
+      const int64_t m0 = static_cast<int64_t>(at.ta) * 128;
+      const __nv_bfloat16* x = P.L.x + at.g * P.L.x_group + m0 * P.L.x_row - behind;
+      const int64_t w_rows = (P.L.N - at.cls + P.every - 1) / P.every - static_cast<int64_t>(at.tb) * P.nt;
       for (int kb = 0; kb < P.kblocks; ++kb) {
         if (turn == group) {
           if (!mbar_wait(&empty[s], phase, &dead)) break;
           const uint32_t dst = base + s * stage_bytes;
-          load_rows(kWeightsA ? dst : dst + a_bytes, w, P.L.w_row, kWeightsA ? P.ra : P.nt, P.L.N - n0, kb * kMmaK, P.L.K,
-                    mine);
-          load_rows(kWeightsA ? dst + a_bytes : dst, x, P.L.x_row, kWeightsA ? P.nt : P.ra, P.L.M - m0, kb * kMmaK, P.L.K,
-                    mine);
+          load_rows(dst, x, P.L.x_row, P.ra, P.L.M - m0, kb * kMmaK, behind, behind + P.L.K, mine);
+          if (!P.w_mapped || (kb == 0 && behind > 0))
+            load_rows(dst + a_bytes, w, P.every * P.L.w_row, P.nt, w_rows, kb * kMmaK, behind, behind + P.L.K, mine);
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[s]);
         }
@@ -446,14 +497,41 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
       }
     }
   } else if (kLoad && warp == 0) {
-    // nothing to fetch
+    // w's share of the stages, but for those that begin in front of its rows
+    unsigned s = 0, phase = 1, fill = 0;
+    for (unsigned t = P.w_mapped ? first : P.tiles; t < P.tiles && !dead; t += step) {
+      const TileAt at = tile_at<kLoad>(P, t);
+      int behind;
+      first_row(P, at, &behind);
+      const CUtensorMap* map = &maps.m[at.g % P.group_classes * P.classes + at.cls];
+      const int row = at.tb * P.nt, g = P.b_groups ? at.g / P.group_classes : 0;
+      for (int kb = 0; kb < P.kblocks; ++kb) {
+        if (!mbar_wait(&empty[s], phase, &dead)) break;
+        if (elect_one()) {
+          if (kb == 0 && behind > 0) {
+            mbar_arrive(&full[s]);
+          } else {
+            mbar_expect(&full[s], stage_bytes - a_bytes);
+            tma_load(map, base + s * stage_bytes + a_bytes, &full[s], kb * kMmaK, row, g);
+          }
+        }
+        __syncwarp();
+        ++fill;
+        if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
+      }
+    }
+    if (dead) {
+      int gave_up = 0;
+      for (unsigned f = fill > static_cast<unsigned>(P.stages) ? fill - P.stages : 0; f < fill; ++f)
+        mbar_wait(&full[f % P.stages], (f / P.stages) & 1, &gave_up);
+    }
   } else if (warp == 0) {
     // stage and phase go round by counting: a division by the number of stages
     // costs more than everything else that a stage needs
     unsigned s = 0, phase = 1, fill = 0;
     const uint32_t leader = kPair ? in_cta(full, 0) : 0;
     for (unsigned t = first; t < P.tiles && !dead; t += step) {
-      const TileAt at = tile_at(P, t);
+      const TileAt at = tile_at<kLoad>(P, t);
       const int ga = P.a_groups ? at.g : 0, gb = P.b_groups ? at.g : 0;
       const int row_a = kPair ? at.ta * 256 + static_cast<int>(rank) * 128 : 0;
       const int row_b = at.tb * P.nt + (kPair ? static_cast<int>(rank) * b_rows : 0);
@@ -465,14 +543,14 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
             const uint32_t bar = leader + s * 8;
             if (rank == 0) mbar_expect(&full[s], 2 * stage_bytes);
             for (int u = 0; u < P.sub; ++u, dst += sub_bytes) {
-              tma_load_pair(&map_a, dst, bar, k + u * kMmaK, row_a, ga);
-              tma_load_pair(&map_b, dst + a_bytes, bar, k + u * kMmaK, row_b, gb);
+              tma_load_pair(&maps.m[0], dst, bar, k + u * kMmaK, row_a, ga);
+              tma_load_pair(&maps.m[1], dst + a_bytes, bar, k + u * kMmaK, row_b, gb);
             }
           } else {
             mbar_expect(&full[s], stage_bytes);
             for (int u = 0; u < P.sub; ++u, dst += sub_bytes) {
-              tma_load(&map_a, dst, &full[s], k + u * kMmaK, 0, ga);
-              tma_load(&map_b, dst + a_bytes, &full[s], k + u * kMmaK, row_b, gb);
+              tma_load(&maps.m[0], dst, &full[s], k + u * kMmaK, 0, ga);
+              tma_load(&maps.m[1], dst + a_bytes, &full[s], k + u * kMmaK, row_b, gb);
             }
           }
         }
@@ -534,9 +612,9 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
     unsigned n = 0;
     auto sum = [&](bool ok, float v) { return !ok ? NAN : P.kblocks == 0 ? 0.f : v; };  // no entries: no product ran
     // columns of a tile that go together to one of the two warps of 32 lanes
-    constexpr int kCols = kWeightsA && (kLoad || kSegments) ? 16 : 32;
+    constexpr int kCols = kWeightsA && kSegments ? 16 : 32;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16), carried = lanes + 2 * P.nt;
-    const bool idle = !kWeightsA && quad * 32 >= P.L.M;  // no token in these lanes
+    const bool idle = !kWeightsA && !kLoad && quad * 32 >= P.L.M;  // no token in these lanes
     auto wait_sums = [&]() {
       const bool ok = !dead && (P.kblocks == 0 || mbar_wait(&acc_full[n & 1], (n >> 1) & 1, &dead));
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -579,9 +657,9 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
       }
     };
     for (unsigned t = first; t < P.tiles; t += step) {
-      const TileAt at = tile_at(P, t);
+      const TileAt at = tile_at<kLoad>(P, t);
       if constexpr (kWeightsA) {
-        const int64_t col = static_cast<int64_t>(at.ta) * (kPair ? 256 : 128) + rank * 128 + quad * 32 + lane;
+        const int64_t col = static_cast<int64_t>(at.ta) * 256 + rank * 128 + quad * 32 + lane;
         const bool in = col < P.L.N;
         const float bias = in ? load_bias(P.L, at.g, col) : 0.f;
         // 32 tokens at a time (16 where registers are few), the next ones' residuals on their way meanwhile.  nt is a
@@ -627,37 +705,44 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
           }
         });
       } else {
-        const int cols = min(P.nt, static_cast<int>(P.L.N - static_cast<int64_t>(at.tb) * P.nt));
-        // Each thread finishes one column of every fourth token, sixteen tokens at a time.  Biases and residuals are
+        const int every = kLoad ? P.every : 1;
+        const int64_t j0 = static_cast<int64_t>(at.tb) * P.nt, n0 = at.cls + j0 * every;
+        const int64_t m_tile = kLoad ? at.ta * int64_t{128} : 0;
+        const int cols = static_cast<int>(min(static_cast<int64_t>(P.nt), (P.L.N - at.cls + every - 1) / every - j0));
+        const int tokens = kLoad ? static_cast<int>(min(int64_t{128}, P.L.M - m_tile)) : P.L.M;
+        const int64_t y0 = at.g * P.L.y_group + m_tile * P.L.y_row + n0;
+        const int64_t r_from = at.g * P.L.r_group + m_tile * P.L.r_row + n0;
+        // Each thread finishes one column of every fourth token, sixteen tokens at a time (eight where sixteen would not
+        // stay in registers: 2 groups of M = 77, N = 32001, K = 1001 in fp32, 70 -> 63 us).  Biases and residuals are
         // asked into L2 while the products run; the first ones are in registers before the sums come, and each chunk's
         // before the chunk in front of it is finished.
         const int c = et % kStageCols, row = et / kStageCols;
-        constexpr int kRows = kEpiWarps * 32 / kStageCols, kBatch = 16;
-        const int64_t n0 = static_cast<int64_t>(at.tb) * P.nt;
-        if (c % 16 == 0)
+        constexpr int kRows = kEpiWarps * 32 / kStageCols, kBatch = kLoad && kSegments ? 8 : 16;
+        if (c * every % 16 == 0)
           for (int c0 = c; c0 < cols; c0 += kStageCols) {
             if (P.L.bias && row == 0)
-              prefetch_l2(P.L.bias, at.g * P.L.b_group + n0 + c0, P.L.bias_bf16);
-            for (int m = row; P.L.res && m < P.L.M; m += kRows)
-              prefetch_l2(P.L.res, at.g * P.L.r_group + m * P.L.r_row + n0 + c0, P.L.res_bf16);
+              prefetch_l2(P.L.bias, at.g * P.L.b_group + n0 + c0 * every, P.L.bias_bf16);
+            for (int m = row; P.L.res && m < tokens; m += kRows)
+              prefetch_l2(P.L.res, r_from + m * P.L.r_row + c0 * every, P.L.res_bf16);
           }
         if constexpr (kSegments) carry();
         bool ok = true;
+        if (kLoad && cols <= 0) wait_sums();  // the last tile of a class with a row less
         with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
           uint32_t r[kBatch] = {}, r_next[kBatch] = {};
           float bias, bias_next = 0.f;
           const int shift = wide(P.L.res_bf16);
           auto residuals = [&](uint32_t (&to)[kBatch], int c0, int m0) {
             if (P.L.res)
-              load_entries(to, P.L.res, at.g * P.L.r_group + m0 * P.L.r_row + n0 + c0 + c, kRows * P.L.r_row,
-                           c0 + c < cols ? (P.L.M - m0 + kRows - 1) / kRows : 0, P.L.res_bf16);
+              load_entries(to, P.L.res, r_from + m0 * P.L.r_row + (c0 + c) * every, kRows * P.L.r_row,
+                           c0 + c < cols ? (tokens - m0 + kRows - 1) / kRows : 0, P.L.res_bf16);
           };
-          auto biases = [&](int c0) { return c0 + c < cols ? load_bias(P.L, at.g, n0 + c0 + c) : 0.f; };
+          auto biases = [&](int c0) { return c0 + c < cols ? load_bias(P.L, at.g, n0 + (c0 + c) * every) : 0.f; };
           residuals(r_next, 0, row);
           bias_next = biases(0);
 #pragma unroll 1
           for (int c0 = 0; c0 < cols; c0 += kStageCols) {
-            const int rows = c0 + c < cols ? P.L.M : 0;
+            const int rows = c0 + c < cols ? tokens : 0;
             if (c0 == 0) ok = wait_sums();
             if (!idle)
 #pragma unroll 1
@@ -665,7 +750,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
                 uint32_t v[16];
                 __syncwarp();
                 sums16(cc, v, kSegments && P.segs > 1);
-                if (quad * 32 + lane < P.L.M)
+                if (quad * 32 + lane < tokens)
 #pragma unroll
                   for (int i = 0; i < 16; ++i)
                     staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = sum(ok, __uint_as_float(v[i]));
@@ -679,13 +764,13 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
               bias_next = biases(c0 + kStageCols);
             }
 #pragma unroll 1
-            for (int m0 = row; m0 < P.L.M; m0 += kBatch * kRows) {
+            for (int m0 = row; m0 < tokens; m0 += kBatch * kRows) {
               if (m0 != row) residuals(r, c0, m0);
               float v[kBatch];
 #pragma unroll
               for (int i = 0; i < kBatch; ++i)
                 v[i] = m0 + i * kRows < rows ? staging[(m0 + i * kRows) * (kStageCols + 1) + c] : 0.f;
-              int64_t to = at.g * P.L.y_group + m0 * P.L.y_row + n0 + c0 + c;
+              int64_t to = y0 + m0 * P.L.y_row + (c0 + c) * every;
 #pragma unroll
               for (int i = 0; i < kBatch; ++i, to += kRows * P.L.y_row)
                 if (m0 + i * kRows < rows)
@@ -776,34 +861,71 @@ int choose_width(bool pair, int most, int64_t rows_b, int64_t tiles_a, int rows_
   return best;
 }
 
+// Maps of w's classes of rows for a tile of P.nt of them; false where its rows cannot be had so.
+bool map_classes(MmaParams* P, Maps<kMostMaps>* maps) {
+  const LinearParams& L = P->L;
+  for (int gc = 0; gc < P->group_classes; ++gc)
+    for (int c = 0; c < P->classes; ++c) {
+      const __nv_bfloat16* p = L.w + gc * L.w_group + c * L.w_row;
+      const int behind = static_cast<int>(reinterpret_cast<uintptr_t>(p) / 2 % 8);
+      int grouped;
+      if (!make_map(&maps->m[gc * P->classes + c], p - behind, L.K + behind, (L.N - c + P->every - 1) / P->every,
+                    L.w_group > 0 ? (L.groups - gc + P->group_classes - 1) / P->group_classes : 1, P->every * L.w_row,
+                    P->group_classes * L.w_group, P->nt, &grouped))
+        return false;
+    }
+  return true;
+}
+
+// how many steps of `stride` entries come back to the same place in 16 bytes
+int period(int64_t stride) { return stride % 8 == 0 ? 1 : stride % 4 == 0 ? 2 : stride % 2 == 0 ? 4 : 8; }
+
 template <bool kWeightsA, bool kLoad, bool kSegments>
-sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st) {
-  constexpr bool kPair = kWeightsA && !kLoad;
+sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st, bool map_w = true) {
+  constexpr bool kPair = kWeightsA;
   MmaParams P = {};
   P.L = L;
-  const int64_t blocks = (static_cast<int64_t>(L.K) + kMmaK - 1) / kMmaK;
-  P.ra = kWeightsA ? 128 : (L.M + 7) / 8 * 8;
-  const int64_t rows_a = kWeightsA ? L.N : L.M, rows_b = kWeightsA ? L.M : L.N;
+  P.every = P.classes = P.group_classes = 1;
+  int64_t blocks = (static_cast<int64_t>(L.K) + kMmaK - 1) / kMmaK;
+  if (kLoad && map_w && L.K > 0) {
+    P.w_mapped = 1;
+    P.every = L.N > 1 ? period(L.w_row) : 1;
+    P.classes = std::min(P.every, L.N);
+    P.group_classes = L.groups > 1 ? std::min(period(L.w_group), L.groups) : 1;
+    if (P.classes * P.group_classes > 1 || reinterpret_cast<uintptr_t>(L.w) % 16)
+      blocks = (static_cast<int64_t>(L.K) + 7 + kMmaK - 1) / kMmaK;
+  }
+  const int tokens = kWeightsA ? L.M : std::min(L.M, 128);  // of a tile of x
+  P.ra = kWeightsA ? 128 : (tokens + 7) / 8 * 8;
+  const int64_t rows_a = kWeightsA ? L.N : L.M;
+  const int64_t rows_b = kWeightsA ? L.M : (static_cast<int64_t>(L.N) + P.every - 1) / P.every;
   const int workers = kPair ? std::max(1, sms / 2) : sms;
   P.tiles_a = static_cast<int>((rows_a + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
-  P.halves = kSegments && L.K <= 2 * 768;
-  P.nt = choose_width(kPair, kSegments && !P.halves ? 160 : 256, rows_b, P.tiles_a, P.ra, L.groups, blocks, workers);
+  P.halves = kSegments && blocks <= 2 * 768 / kMmaK;
+  const int64_t others = static_cast<int64_t>(P.tiles_a) * P.classes;
+  P.nt = choose_width(kPair, kSegments && !P.halves ? 160 : 256, rows_b, others, P.ra, L.groups, blocks, workers);
   P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
-  const int64_t tiles = static_cast<int64_t>(P.tiles_a) * P.tiles_b * L.groups;
-  if (tiles >= (int64_t{1} << 31)) return SV_EUNSUPPORTED;
+  const int64_t most_tiles = (int64_t{1} << 31) - 1;
+  if (others * P.tiles_b > most_tiles / L.groups) return SV_EUNSUPPORTED;
+  const int64_t tiles = others * P.tiles_b * L.groups;
   P.tiles = static_cast<unsigned>(tiles);
   const int b_rows = kPair ? P.nt / 2 : P.nt;
-  CUtensorMap map_x = {}, map_w = {};
-  if constexpr (!kLoad) {
+  Maps<kLoad ? kMostMaps : 2> maps;
+  if constexpr (kLoad) {
+    P.b_groups = L.w_group > 0;
+    if (P.w_mapped && !map_classes(&P, &maps)) return launch_mma<false, true, kSegments>(L, device, sms, st, false);
+  } else {
+    CUtensorMap& map_x = maps.m[kWeightsA ? 1 : 0];
+    CUtensorMap& map_w = maps.m[kWeightsA ? 0 : 1];
     int gx = 0, gw = 0;
     if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? b_rows : P.ra, &gx) ||
         !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : b_rows, &gw))
-      return launch_mma<kWeightsA, true, kSegments>(L, device, sms, st);
+      return launch_mma<false, true, kSegments>(L, device, sms, st);
     P.a_groups = kWeightsA ? gw : gx;
     P.b_groups = kWeightsA ? gx : gw;
   }
   const int sub_bytes = (P.ra + b_rows) * kRowBytes;
-  const int staging = kWeightsA ? 0 : L.M * (kStageCols + 1) * 4;
+  const int staging = kWeightsA ? 0 : tokens * (kStageCols + 1) * 4;
   // a product reads 128 rows of A from a stage's last block on: they stay inside the allocation
   const int slack = std::max(0, 128 * kRowBytes - sub_bytes);
   const int room = kMmaSmem - 1024 - staging - slack;
@@ -818,7 +940,7 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   P.segs = std::max(1, (P.kblocks + P.seg_blocks - 1) / P.seg_blocks);
   const int stage_bytes = P.sub * sub_bytes;
   P.stages = std::min(kMaxStages, room / stage_bytes);
-  if (kLoad && P.stages < kLoadGroups) return SV_EUNSUPPORTED;  // never: see the loading warps
+  if (kLoad && P.stages < kLoadGroups) return SV_EUNSUPPORTED;  // never: four stages of 128 + 256 rows fit
   P.staging = 1024 + P.stages * stage_bytes + slack;
   const int smem = static_cast<int>(P.staging) + staging;
   P.tmem_cols = 32;
@@ -835,8 +957,8 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
     if (device < 64) opted_in[device].store(true);
   }
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, workers)) * (kPair ? 2 : 1);
-  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad, kSegments>, grid, kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoadWarps : 0),
-                                       smem, kPair ? 2 : 1, st, P, kWeightsA ? map_w : map_x, kWeightsA ? map_x : map_w);
+  const unsigned threads = kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoadWarps : 0);
+  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad, kSegments>, grid, threads, smem, kPair ? 2 : 1, st, P, maps);
   return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
@@ -899,9 +1021,7 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
-  if (K == 0)
-    return M > 128 ? sv::launch_mma<true, true, false>(P, device, sms, st)
-                   : sv::launch_mma<false, true, false>(P, device, sms, st);
+  if (K == 0) return sv::launch_mma<false, true, false>(P, device, sms, st);
   if (y_dt == SV_F32 && K > 768)
     return M > 128 ? sv::launch_mma<true, false, true>(P, device, sms, st)
                    : sv::launch_mma<false, false, true>(P, device, sms, st);

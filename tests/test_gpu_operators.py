@@ -106,6 +106,38 @@ def test_linear_groups_strides_and_layouts(sv, G, M, N, K, shared, pad, offset):
     assert bool((store[:, :, 0] == 7).all()) and bool((store[:, :, -1] == 7).all())  # nothing beside the rows
 
 
+# rows, groups and the first entry at every place in 16 bytes; classes of rows that are empty, one row, one row more than a
+# tile; more groups than places; rows that overlap; several tiles of tokens
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("G,M,N,K,row,group,offset", [
+    (1, 5, 1, 70, 75, 0, 3), (1, 9, 3, 1, 5, 0, 1), (2, 4, 9, 64, 65, 593, 7), (3, 33, 17, 57, 61, 1041, 6),
+    (1, 20, 2049, 130, 133, 0, 5), (1, 130, 129, 200, 203, 0, 2), (17, 3, 40, 90, 91, 3645, 1), (9, 6, 50, 128, 132, 6603, 4),
+    (5, 2, 30, 65, 66, 1981, 0), (1, 300, 520, 1000, 1002, 0, 1), (2, 257, 100, 1100, 1101, 110107, 3),
+    (1, 129, 1030, 1601, 1603, 0, 7), (1, 40, 60, 100, 7, 0, 1), (4, 8, 24, 320, 320, 7681, 0), (3, 260, 80, 96, 96, 0, 1),
+    (2, 1, 4100, 2001, 2001, 8204100, 0), (3, 64, 1025, 63, 63, 64577, 5)])
+def test_linear_reads_nothing_beside_its_rows(sv, G, M, N, K, row, group, offset, out):
+    g = _gen(M * N + K)
+
+    def operand(groups, rows, row, group, offset):
+        store = torch.full((offset + (groups - 1) * group + (rows - 1) * row + K + 16,), float("nan"), dtype=torch.bfloat16,
+                           device="cuda")
+        view = torch.as_strided(store, (groups, rows, K), (group, row, 1), offset)
+        for i in range(groups):
+            for r in range(rows) if row < K else (slice(None),):  # rows that overlap: one after the other
+                part = view[i, r]
+                part.copy_(torch.randn(part.shape, generator=g, device="cuda") / K ** 0.5)
+        return view
+
+    w = operand(G, N, row, group, offset)
+    for x in (operand(1, M, K + 3, 0, 1)[0], operand(1, M, (K + 7) // 8 * 8, 0, 0)[0],
+              operand(G, M, K + 1, M * (K + 1) + 5, 6)):
+        res = torch.randn(M, N, generator=g, device="cuda").to(torch.bfloat16).expand(G, M, N)
+        bias = torch.randn(G, N, generator=g, device="cuda")
+        y = sv.linear(x, w, bias=bias, residual=res, activation="gelu",
+                      out_dtype=torch.bfloat16 if out == "bf16" else torch.float32)
+        ref.assert_linear(y, x, w, bias, res, "gelu", 0.0)
+
+
 def test_linear_into_its_own_residual(sv):
     x, w, g = _operands(3, 1, 70, 260, 192)
     res = torch.randn(70, 260, generator=g, device="cuda").to(torch.bfloat16)
