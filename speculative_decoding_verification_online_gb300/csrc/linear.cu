@@ -16,10 +16,11 @@
 //    4096: 298 us, 2.03 PFLOP/s alone, 1.79 under load; M = 384, N = 128256, K =
 //    4096: 248 us, 1.62 PFLOP/s (75 % of the cycles in products: 200 KB of stages in
 //    flight a SM do not cover what w takes to come from HBM).
-//  * rows at odd addresses: what the loading warps wait for and execute.  M = 77, N =
-//    32001, K = 1001: 30 us, 2.3 TB/s (42 us where warps load both operands); M = 8,
-//    K = 2001: 33 us (66); M = 300, K = 1001: 66 us (137); M = 2304, N = 32000,
-//    K = 4097: 775 us, 0.78 PFLOP/s.
+//  * rows at odd addresses: w's bytes where K is long (M = 77, N = 32001, K = 8001:
+//    103 us, 5.0 TB/s; 83 us for K = 8000), the start and the end of a tile where it is
+//    short (K = 1001: 29 us; 21 us for K = 1000; 42 us where warps load both operands).
+//    M = 8, K = 2001: 32 us (66); M = 300, K = 1001: 63 us (137); M = 2304, N = 32000,
+//    K = 4097: 763 us (1398), 0.79 PFLOP/s: there the loading warps' latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -330,13 +331,23 @@ __device__ __forceinline__ TileAt tile_at(const MmaParams& P, unsigned t) {
 // A tile of y takes columns of one class; the classes of the same columns follow one
 // another, so that the parts of a sector of y meet in L2.  What a map shows in front
 // of a row belongs to another row, or to nobody (and may be a NaN, which a zero of x
-// would not take out of a sum): the first 64 entries of K are loaded by the warps for
-// w too, with zeros there.  Behind a row's end the map has zeros.
+// would not take out of a sum): the loading warps put zeros there, in the first stage
+// of a tile (M = 77, N = 32001, K = 1001 29 us; 30 us with that stage of w loaded by
+// the warps).  Behind a row's end the map has zeros.
 // Groups of w that are not multiples of 16 bytes apart are classes in the same way.
 //
-// Eight entries of a row from any address that bf16 entries have, in the one or two aligned blocks of 16 bytes that hold
-// them.  Only blocks with an entry of the row are read: an allocation has all of such a block.
-__device__ __forceinline__ uint4 load_if(const uint4* p, bool there) {
+// eight entries, zeros in place of the first 1 to 7
+__device__ __forceinline__ uint4 without_front(uint4 e, int n) {
+  e.x &= n > 1 ? 0u : 0xffff0000u;
+  e.y &= n > 3 ? 0u : n > 2 ? 0xffff0000u : ~0u;
+  e.z &= n > 5 ? 0u : n > 4 ? 0xffff0000u : ~0u;
+  e.w &= n > 6 ? 0xffff0000u : ~0u;
+  return e;
+}
+
+// Eight entries of a row from any address that bf16 entries have lie in one or two aligned blocks of 16 bytes.  Only blocks
+// with an entry of the row are read: an allocation has all of such a block.
+__device__ __forceinline__ uint4 load_if(const char* p, bool there) {
   uint4 v;
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
@@ -347,68 +358,70 @@ __device__ __forceinline__ uint4 load_if(const uint4* p, bool there) {
   return v;
 }
 
-struct Run {
-  uint4 a, b;
-  int shift;  // bytes in front of the first entry
-
-  // those from `front` on, in front of `valid`
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int front, int valid) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint4* block = reinterpret_cast<const uint4*>(at & ~uintptr_t{15});
-    shift = static_cast<int>(at & 15);
-    a = load_if(block, valid > front && shift + 2 * front < 16);
-    b = load_if(block + 1, valid > front && shift + 2 * valid > 16);
+// The entries from `shift` bytes into the blocks a and b on; zeros in place of those in front of `front` and from `valid` on.
+__device__ __forceinline__ uint4 entries_of(const uint4& a, const uint4& b, int shift, int front, int valid) {
+  const bool two = shift & 8, one = shift & 4;
+  const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w,
+                 w4 = two ? b.z : b.x, w5 = two ? b.w : b.y;
+  const uint32_t v0 = one ? w1 : w0, v1 = one ? w2 : w1, v2 = one ? w3 : w2, v3 = one ? w4 : w3, v4 = one ? w5 : w4;
+  const int bits = (shift & 2) * 8;
+  uint4 r = make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits), __funnelshift_r(v2, v3, bits),
+                       __funnelshift_r(v3, v4, bits));
+  if (valid < 8) {
+    r.x &= valid > 1 ? ~0u : valid > 0 ? 0xffffu : 0u;
+    r.y &= valid > 3 ? ~0u : valid > 2 ? 0xffffu : 0u;
+    r.z &= valid > 5 ? ~0u : valid > 4 ? 0xffffu : 0u;
+    r.w &= valid > 7 ? ~0u : valid > 6 ? 0xffffu : 0u;
   }
-
-  // the entries, zeros in place of the others
-  __device__ __forceinline__ uint4 entries(int front, int valid) const {
-    const bool two = shift & 8, one = shift & 4;
-    const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w,
-                   w4 = two ? b.z : b.x, w5 = two ? b.w : b.y;
-    const uint32_t v0 = one ? w1 : w0, v1 = one ? w2 : w1, v2 = one ? w3 : w2, v3 = one ? w4 : w3, v4 = one ? w5 : w4;
-    const int bits = (shift & 2) * 8;
-    uint4 r = make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits), __funnelshift_r(v2, v3, bits),
-                         __funnelshift_r(v3, v4, bits));
-    if (valid < 8) {
-      r.x &= valid > 1 ? ~0u : valid > 0 ? 0xffffu : 0u;
-      r.y &= valid > 3 ? ~0u : valid > 2 ? 0xffffu : 0u;
-      r.z &= valid > 5 ? ~0u : valid > 4 ? 0xffffu : 0u;
-      r.w &= valid > 7 ? ~0u : valid > 6 ? 0xffffu : 0u;
-    }
-    if (front > 0) {
-      r.x &= front > 1 ? 0u : 0xffff0000u;
-      r.y &= front > 3 ? 0u : front > 2 ? 0xffff0000u : ~0u;
-      r.z &= front > 5 ? 0u : front > 4 ? 0xffff0000u : ~0u;
-      r.w &= front > 6 ? 0xffff0000u : ~0u;
-    }
-    return r;
-  }
-};
+  return front > 0 ? without_front(r, front) : r;
+}
 
 // A warp's share (warp `mine` of the loading ones) of `rows` rows of 64 entries from k on, as TMA would lay them down: 16
 // bytes a lane, eight lanes a row.  p is where an entry 0 of the first row would be; entries in front of `lo` and from `hi`
-// on are zeros, and so are rows from `there` on.
+// on are zeros, and so are rows from `there` on.  A lane's rows are kStep apart, a multiple of 8: they all start at the
+// same place in 16 bytes.
 __device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* p, int64_t stride, int rows, int64_t there,
                                           int k, int lo, int hi, int mine) {
+  constexpr int kBatch = 4, kStep = 4 * kLoadWarps;
+  static_assert(kStep % 8 == 0);
   const int lane = threadIdx.x & 31, c = lane % 8;
   const int front = max(0, lo - k - 8 * c), valid = max(0, min(8, hi - k - 8 * c));
-  constexpr int kBatch = 4, kStep = 4 * kLoadWarps;
-  int r0 = 4 * mine + lane / 8;
-  p += r0 * stride + k + 8 * c;
-  for (; r0 < rows; r0 += kBatch * kStep, p += kBatch * kStep * stride) {
-    Run v[kBatch];
+  int r = 4 * mine + lane / 8;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p + r * stride + k + 8 * c);
+  const int shift = static_cast<int>(at & 15);
+  const char* block = reinterpret_cast<const char*>(at & ~uintptr_t{15});
+  const int64_t step = kStep * 2 * stride;
+  const bool in_a = valid > front && shift + 2 * front < 16, in_b = valid > front && shift + 2 * valid > 16;
+  const int last = static_cast<int>(min(static_cast<int64_t>(rows), there));
+  dst += r * kRowBytes + ((c ^ (r & 7)) << 4);
+  for (; r < rows; r += kBatch * kStep, dst += kBatch * kStep * kRowBytes) {
+    uint4 a[kBatch], b[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) v[i].load(p + i * kStep * stride, front, r0 + i * kStep < there ? valid : 0);
+    for (int i = 0; i < kBatch; ++i, block += step) {
+      a[i] = load_if(block, in_a && r + i * kStep < last);
+      b[i] = load_if(block + 16, in_b && r + i * kStep < last);
+    }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + i * kStep;
-      const uint4 e = v[i].entries(front, valid);
-      if (r < rows)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * kRowBytes + ((c ^ (r & 7)) << 4)),
-                     "r"(e.x), "r"(e.y), "r"(e.z), "r"(e.w)
+      const uint4 e = entries_of(a[i], b[i], shift, front, valid);
+      if (r + i * kStep < rows)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * kStep * kRowBytes), "r"(e.x), "r"(e.y),
+                     "r"(e.z), "r"(e.w)
                      : "memory");
     }
   }
+}
+
+// zeros in place of the first `n` (below 8) entries of row r
+__device__ __forceinline__ void clear_front(uint32_t rows, int r, int n) {
+  const uint32_t at = rows + r * kRowBytes + ((r & 7) << 4);
+  uint4 e;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(e.x), "=r"(e.y), "=r"(e.z), "=r"(e.w)
+               : "r"(at)
+               : "memory");
+  e = without_front(e, n);
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(e.x), "r"(e.y), "r"(e.z), "r"(e.w) : "memory");
 }
 
 // the first row of w of a tile, and how many entries it starts behind a multiple of 16 bytes
@@ -427,6 +440,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
   constexpr bool kPair = kWeightsA;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+  __shared__ uint64_t fronts[kLoad ? kMaxStages : 1];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -437,6 +451,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
   const uint32_t a_bytes = P.ra * kRowBytes, sub_bytes = a_bytes + b_rows * kRowBytes, stage_bytes = P.sub * sub_bytes;
   if (threadIdx.x == 0) {
     for (int s = 0; s < P.stages; ++s) mbar_init(&full[s], kLoad ? kLoadWarps + P.w_mapped : 1), mbar_init(&empty[s], 1);
+    for (int s = 0; kLoad && s < P.stages; ++s) mbar_init(&fronts[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], kPair ? 2 * kEpiWarps : kEpiWarps);
     mbar_init(&drained, 1);
     dead = 0;
@@ -474,7 +489,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
     // groups than stages could come to a stage two phases early, and a parity does not tell two phases from none.)
     const int mine = (warp - 2 - kEpiWarps) % kLoadWarps, group = (warp - 2 - kEpiWarps) / kLoadWarps;
     int turn = 0;
-    unsigned s = 0, phase = 1;
+    unsigned s = 0, phase = 1, fronts_phase = 0;  // of each stage a bit
     for (unsigned t = first; t < P.tiles && !dead; t += step) {
       const TileAt at = tile_at<kLoad>(P, t);
       int behind;
@@ -487,17 +502,22 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
           if (!mbar_wait(&empty[s], phase, &dead)) break;
           const uint32_t dst = base + s * stage_bytes;
           load_rows(dst, x, P.L.x_row, P.ra, P.L.M - m0, kb * kMmaK, behind, behind + P.L.K, mine);
-          if (!P.w_mapped || (kb == 0 && behind > 0))
-            load_rows(dst + a_bytes, w, P.every * P.L.w_row, P.nt, w_rows, kb * kMmaK, behind, behind + P.L.K, mine);
+          if (!P.w_mapped) {
+            load_rows(dst + a_bytes, w, P.every * P.L.w_row, P.nt, w_rows, kb * kMmaK, 0, P.L.K, mine);
+          } else if (kb == 0 && behind > 0) {
+            if (!mbar_wait(&fronts[s], fronts_phase >> s & 1, &dead)) break;
+            for (int r = 32 * mine + lane; r < P.nt; r += 32 * kLoadWarps) clear_front(dst + a_bytes, r, behind);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[s]);
         }
+        if (kb == 0 && behind > 0) fronts_phase ^= 1u << s;
         if (++turn == kLoadGroups) turn = 0;
         if (++s == static_cast<unsigned>(P.stages)) s = 0, phase ^= 1;
       }
     }
   } else if (kLoad && warp == 0) {
-    // w's share of the stages, but for those that begin in front of its rows
+    // w's share of the stages; where it shows entries in front of w's rows, the loading warps wait for it
     unsigned s = 0, phase = 1, fill = 0;
     for (unsigned t = P.w_mapped ? first : P.tiles; t < P.tiles && !dead; t += step) {
       const TileAt at = tile_at<kLoad>(P, t);
@@ -508,12 +528,10 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
       for (int kb = 0; kb < P.kblocks; ++kb) {
         if (!mbar_wait(&empty[s], phase, &dead)) break;
         if (elect_one()) {
-          if (kb == 0 && behind > 0) {
-            mbar_arrive(&full[s]);
-          } else {
-            mbar_expect(&full[s], stage_bytes - a_bytes);
-            tma_load(map, base + s * stage_bytes + a_bytes, &full[s], kb * kMmaK, row, g);
-          }
+          uint64_t* bar = kb == 0 && behind > 0 ? &fronts[s] : &full[s];
+          if (bar != &full[s]) mbar_arrive(&full[s]);
+          mbar_expect(bar, stage_bytes - a_bytes);
+          tma_load(map, base + s * stage_bytes + a_bytes, bar, kb * kMmaK, row, g);
         }
         __syncwarp();
         ++fill;
