@@ -199,6 +199,19 @@ def test_linear_large_offsets(sv):
     ref.assert_linear(y, x[0], wv[0], None, None, "none", 0.0)
 
 
+@pytest.mark.parametrize("M", [20, 140])
+def test_linear_large_offsets_at_odd_addresses(sv, M):
+    # rows of both operands past 2^31 elements, at every place in 16 bytes
+    n_far, K = 40, 201
+    stride = (1 << 31) // (n_far - 1) // 8 * 8 + 9
+    w = torch.as_strided(torch.empty(stride * n_far, dtype=torch.bfloat16, device="cuda"), (n_far, K), (stride, 1), 3)
+    xs = (1 << 31) // (M - 1) // 8 * 8 + 13
+    x = torch.as_strided(torch.empty(xs * M, dtype=torch.bfloat16, device="cuda"), (M, K), (xs, 1), 1)
+    xv, wv, g = _operands(4, 1, M, n_far, K)
+    x.copy_(xv[0]), w.copy_(wv[0])
+    ref.assert_linear(sv.linear(x, w, out_dtype=torch.float32), xv[0], wv[0], None, None, "none", 0.0)
+
+
 def test_linear_rows_that_share_their_place(sv):
     # operands whose rows or groups are one (strides of 0), as expand leaves them
     g = _gen(12)
