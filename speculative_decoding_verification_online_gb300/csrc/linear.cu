@@ -18,8 +18,8 @@
 //    flight a SM do not cover what w takes to come from HBM).
 //  * rows at odd addresses: w's bytes where K is long (M = 77, N = 32001, K = 8001:
 //    103 us, 5.0 TB/s; 83 us for K = 8000), the start and the end of a tile where it is
-//    short (K = 1001: 29 us; 21 us for K = 1000; 42 us where warps load both operands).
-//    M = 8, K = 2001: 32 us (66); M = 300, K = 1001: 63 us (137); M = 2304, N = 32000,
+//    short (K = 1001: 27 us; 21 us for K = 1000; 42 us where warps load both operands).
+//    M = 8, K = 2001: 28 us (66); M = 300, K = 1001: 63 us (137); M = 2304, N = 32000,
 //    K = 4097: 763 us (1398), 0.79 PFLOP/s: there the loading warps' latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -80,15 +80,32 @@ __device__ __forceinline__ float tanh_of(float x) {
   return copysignf(a < 0.25f ? low : high, x);
 }
 
+// (1 + erf(z / sqrt 2)) / 2.  The part beyond |z| is t p(t) exp(-z^2 / 2) with t = 1 / (1 + 0.3275911 |z| / sqrt 2) and a p
+// of degree 4, off by 7.5e-8 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, halved), and by as much
+// again with fp32's roundings.  GELU of 357 x 37248 bf16 results with bias and residual, K = 128: 33.7 us, 35.4 with erff.
+__device__ __forceinline__ float normal_below(float z) {
+  const float a = fabsf(z), t = __fdividef(1.f, fmaf(0.231641888f, a, 1.f));
+  const float p = fmaf(fmaf(fmaf(fmaf(0.5307027145f, t, -0.7265760135f), t, 0.7107068705f), t, -0.142248368f), t, 0.127414796f);
+  const float beyond = t * p * __expf(-0.5f * a * a);
+  return z > 0.f ? 1.f - beyond : beyond;
+}
+
 template <int kAct>
 __device__ __forceinline__ float activate(float z, float cap, float inv_cap) {
   if constexpr (kAct == SV_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
   if constexpr (kAct == SV_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-  if constexpr (kAct == SV_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+  if constexpr (kAct == SV_ACT_GELU) return z * normal_below(z);
   // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
   if constexpr (kAct == SV_ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-1.59576912f * (z + 0.044715f * z * z * z)));
   if constexpr (kAct == SV_ACT_SOFTCAP) return cap * tanh_of(z * inv_cap);
   return z;
+}
+
+// Runs of tokens are finished in straight code; with these activations runs of 32 are slower than runs of 16 (357 x 37248
+// bf16 results, K = 128: GELU with bias and residual 39.2 -> 35.4 us, the soft cap 25.0 -> 23.4 us), the others are not
+// (a residual alone: 24.6 -> 30.5 us with 16).
+__host__ __device__ constexpr bool long_code(int act) {
+  return act == SV_ACT_GELU || act == SV_ACT_GELU_TANH || act == SV_ACT_SOFTCAP;
 }
 
 // f with the activation and y's type as constants: code that a call does not use is not fetched either
@@ -170,7 +187,7 @@ constexpr int kEpiWarps = 8;
 // K = 2001 33, 32 and 31 us.
 constexpr int kLoadWarps = 4, kLoadGroups = 4;
 constexpr int kMmaThreads = 32 * (2 + kEpiWarps);
-constexpr int kStageCols = 64;   // columns of a tile that the epilogue passes through shared memory at a time
+constexpr int kStageCols = 64;   // columns of a tile that pass through shared memory at a time where x is A
 constexpr int kMmaSmem = 226 * 1024;
 
 struct MmaParams {
@@ -186,6 +203,7 @@ struct MmaParams {
   int a_groups, b_groups;  // 0: the operand is shared by all groups
   unsigned tiles;
   unsigned idesc;
+  int at_once;           // a tile's columns pass through shared memory at once, not kStageCols at a time
   unsigned staging;      // where the epilogue's staging starts in dynamic shared memory
   // where warps load x (see below)
   int w_mapped;          // 1: w comes by TMA, 0: the warps load it too
@@ -685,39 +703,40 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
         // used.
         const int64_t m_tile = static_cast<int64_t>(at.tb) * P.nt;
         const int rows_here = in ? static_cast<int>(min(static_cast<int64_t>(P.nt), P.L.M - m_tile)) : 0;
-        uint32_t r_next[kCols] = {};
         const int shift = wide(P.L.res_bf16);
-        auto residuals = [&](int c) {
-          if (P.L.res)
-            load_entries(r_next, P.L.res, at.g * P.L.r_group + (m_tile + c) * P.L.r_row + col, P.L.r_row, rows_here - c,
-                         P.L.res_bf16);
-        };
         if constexpr (kSegments) carry();
-        residuals(half * kCols);
-        const bool ok = wait_sums();
         with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+          constexpr int kRun = long_code(act.value) ? 16 : kCols;
+          uint32_t r_next[kRun] = {};
+          auto residuals = [&](int c) {
+            if (P.L.res)
+              load_entries(r_next, P.L.res, at.g * P.L.r_group + (m_tile + c) * P.L.r_row + col, P.L.r_row, rows_here - c,
+                           P.L.res_bf16);
+          };
+          residuals(half * kRun);
+          const bool ok = wait_sums();
 #pragma unroll 1
-          for (int c = half * kCols; c < P.nt; c += 2 * kCols) {
-            uint32_t v[kCols], r[kCols];
+          for (int c = half * kRun; c < P.nt; c += 2 * kRun) {
+            uint32_t v[kRun], r[kRun];
             __syncwarp();
             if constexpr (kSegments)
               sums16(c, v, P.segs > 1);
             else
-              tc_load<kCols>(lanes + (n & 1) * P.nt + c, v);
+              tc_load<kRun>(lanes + (n & 1) * P.nt + c, v);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) r[i] = r_next[i];
-            residuals(c + 2 * kCols);
+            for (int i = 0; i < kRun; ++i) r[i] = r_next[i];
+            residuals(c + 2 * kRun);
             int64_t to = at.g * P.L.y_group + (m_tile + c) * P.L.y_row + col;
             auto finish = [&](int i) {
               finish_value<act.value, y_bf16.value>(P.L, to, sum(ok, __uint_as_float(v[i])), bias,
                                                     __uint_as_float(r[i] << shift));
             };
-            if (__all_sync(~0u, c + kCols <= rows_here)) {
+            if (__all_sync(~0u, c + kRun <= rows_here)) {
 #pragma unroll
-              for (int i = 0; i < kCols; ++i, to += P.L.y_row) finish(i);
+              for (int i = 0; i < kRun; ++i, to += P.L.y_row) finish(i);
             } else {
 #pragma unroll
-              for (int i = 0; i < kCols; ++i, to += P.L.y_row)
+              for (int i = 0; i < kRun; ++i, to += P.L.y_row)
                 if (c + i < rows_here) finish(i);
             }
           }
@@ -730,23 +749,28 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
         const int tokens = kLoad ? static_cast<int>(min(int64_t{128}, P.L.M - m_tile)) : P.L.M;
         const int64_t y0 = at.g * P.L.y_group + m_tile * P.L.y_row + n0;
         const int64_t r_from = at.g * P.L.r_group + m_tile * P.L.r_row + n0;
-        // Each thread finishes one column of every fourth token, sixteen tokens at a time (eight where sixteen would not
-        // stay in registers: 2 groups of M = 77, N = 32001, K = 1001 in fp32, 70 -> 63 us).  Biases and residuals are
-        // asked into L2 while the products run; the first ones are in registers before the sums come, and each chunk's
-        // before the chunk in front of it is finished.
-        const int c = et % kStageCols, row = et / kStageCols;
-        constexpr int kRows = kEpiWarps * 32 / kStageCols, kBatch = kLoad && kSegments ? 8 : 16;
-        if (c * every % 16 == 0)
-          for (int c0 = c; c0 < cols; c0 += kStageCols) {
-            if (P.L.bias && row == 0)
+        // Sums come kWidth columns at a time, and each thread finishes one column of every kRows-th token, kBatch of them at
+        // a time.  Biases and residuals are asked into L2 while the products run; the first ones are in registers before the
+        // sums come, and each chunk's before the chunk in front of it is finished.
+        //  * Few tokens and tiles wide enough for all threads: a whole tile at once, without the barriers between chunks (M =
+        //    5, N = 232072, K = 184 26.8 -> 22 us; M = 32, K = 192 with bias, GELU and residual 65 -> 49 us).
+        //  * Residuals: sixteen at a time, to have them on their way (eight where sixteen would not stay in registers: 2
+        //    groups of M = 77, N = 32001, K = 1001 in fp32, 70 -> 63 us).
+        //  * Else four at a time where that is faster, in a quarter of the code (M = 5, N = 232072, K = 184 33.3 -> 26.8 us;
+        //    with M = 128 52.6 us by sixteen, 56.2 by four).
+        if (et % kStageCols * every % 16 == 0)
+          for (int c0 = et % kStageCols; c0 < cols; c0 += kStageCols) {
+            if (P.L.bias && et < kStageCols)
               prefetch_l2(P.L.bias, at.g * P.L.b_group + n0 + c0 * every, P.L.bias_bf16);
-            for (int m = row; P.L.res && m < tokens; m += kRows)
+            for (int m = et / kStageCols; P.L.res && m < tokens; m += kEpiWarps * 32 / kStageCols)
               prefetch_l2(P.L.res, r_from + m * P.L.r_row + c0 * every, P.L.res_bf16);
           }
         if constexpr (kSegments) carry();
         bool ok = true;
         if (kLoad && cols <= 0) wait_sums();  // the last tile of a class with a row less
-        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+        auto finish_tile = [&](auto act, auto y_bf16, auto width, auto batch) {
+          constexpr int kWidth = width.value, kRows = kEpiWarps * 32 / kWidth, kBatch = batch.value;
+          const int c = et % kWidth, row = et / kWidth;
           uint32_t r[kBatch] = {}, r_next[kBatch] = {};
           float bias, bias_next = 0.f;
           const int shift = wide(P.L.res_bf16);
@@ -759,27 +783,27 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
           residuals(r_next, 0, row);
           bias_next = biases(0);
 #pragma unroll 1
-          for (int c0 = 0; c0 < cols; c0 += kStageCols) {
+          for (int c0 = 0; c0 < cols; c0 += kWidth) {
             const int rows = c0 + c < cols ? tokens : 0;
             if (c0 == 0) ok = wait_sums();
             if (!idle)
 #pragma unroll 1
-              for (int cc = c0 + half * 32; cc < min(c0 + half * 32 + 32, P.nt); cc += 16) {
+              for (int cc = c0 + half * (kWidth / 2); cc < min(c0 + (half + 1) * (kWidth / 2), P.nt); cc += 16) {
                 uint32_t v[16];
                 __syncwarp();
                 sums16(cc, v, kSegments && P.segs > 1);
                 if (quad * 32 + lane < tokens)
 #pragma unroll
                   for (int i = 0; i < 16; ++i)
-                    staging[(quad * 32 + lane) * (kStageCols + 1) + cc - c0 + i] = sum(ok, __uint_as_float(v[i]));
+                    staging[(quad * 32 + lane) * (kWidth + 1) + cc - c0 + i] = sum(ok, __uint_as_float(v[i]));
               }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
             bias = bias_next;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) r[i] = r_next[i];
-            if (c0 + kStageCols < cols) {
-              residuals(r_next, c0 + kStageCols, row);
-              bias_next = biases(c0 + kStageCols);
+            if (c0 + kWidth < cols) {
+              residuals(r_next, c0 + kWidth, row);
+              bias_next = biases(c0 + kWidth);
             }
 #pragma unroll 1
             for (int m0 = row; m0 < tokens; m0 += kBatch * kRows) {
@@ -787,7 +811,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
               float v[kBatch];
 #pragma unroll
               for (int i = 0; i < kBatch; ++i)
-                v[i] = m0 + i * kRows < rows ? staging[(m0 + i * kRows) * (kStageCols + 1) + c] : 0.f;
+                v[i] = m0 + i * kRows < rows ? staging[(m0 + i * kRows) * (kWidth + 1) + c] : 0.f;
               int64_t to = y0 + m0 * P.L.y_row + (c0 + c) * every;
 #pragma unroll
               for (int i = 0; i < kBatch; ++i, to += kRows * P.L.y_row)
@@ -796,6 +820,21 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
           }
+        };
+        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+          using Chunk = std::integral_constant<int, kStageCols>;
+          using Tile = std::integral_constant<int, kEpiWarps * 32>;
+          using Four = std::integral_constant<int, 4>;
+          using Eight = std::integral_constant<int, 8>;
+          using Most = std::integral_constant<int, kLoad && kSegments ? 8 : 16>;
+          if (P.at_once && (tokens <= 4 || !P.L.res))
+            finish_tile(act, y_bf16, Tile(), Four());
+          else if (P.at_once)
+            finish_tile(act, y_bf16, Tile(), Eight());
+          else if (tokens <= 16 || (!P.L.res && (kLoad || tokens <= 32)))
+            finish_tile(act, y_bf16, Chunk(), Four());
+          else
+            finish_tile(act, y_bf16, Chunk(), Most());
         });
       }
       if (kSegments && P.halves) release(~n & 1);
@@ -943,7 +982,8 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
     P.b_groups = kWeightsA ? gx : gw;
   }
   const int sub_bytes = (P.ra + b_rows) * kRowBytes;
-  const int staging = kWeightsA ? 0 : tokens * (kStageCols + 1) * 4;
+  P.at_once = tokens <= 32 && P.nt > 128;
+  const int staging = kWeightsA ? 0 : tokens * ((P.at_once ? kEpiWarps * 32 : kStageCols) + 1) * 4;
   // a product reads 128 rows of A from a stage's last block on: they stay inside the allocation
   const int slack = std::max(0, 128 * kRowBytes - sub_bytes);
   const int room = kMmaSmem - 1024 - staging - slack;

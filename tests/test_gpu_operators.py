@@ -138,6 +138,22 @@ def test_linear_reads_nothing_beside_its_rows(sv, G, M, N, K, row, group, offset
         ref.assert_linear(y, x, w, bias, res, "gelu", 0.0)
 
 
+# tiles wider than half of the finishing threads, few tokens and one more than few
+@pytest.mark.parametrize("M", [1, 4, 5, 20, 32, 33])
+@pytest.mark.parametrize("N,K", [(40001, 72), (40001, 75), (40000, 800), (30007, 1601)])
+def test_linear_few_tokens_wide_tiles(sv, M, N, K):
+    x, w, g = _operands(M + K, 1, M, N, K)
+    x, w = x[0], w[0]
+    res = torch.randn(M, N, generator=g, device="cuda").to(torch.bfloat16)
+    bias = torch.randn(N, generator=g, device="cuda")
+    for b, r, act, ydt in ((None, None, "none", torch.bfloat16), (bias, res, "gelu", torch.float32),
+                           (bias, None, "softcap", torch.float32), (None, res, "silu", torch.bfloat16)):
+        store = torch.full((M, N + 2), 7.0, device="cuda").to(ydt)
+        sv.linear(x, w, bias=b, residual=r, activation=act, cap=5.0, out=store[:, 1:N + 1])
+        ref.assert_linear(store[:, 1:N + 1], x, w, b, r, act, 5.0, act)
+        assert bool((store[:, 0] == 7).all()) and bool((store[:, -1] == 7).all())
+
+
 def test_linear_into_its_own_residual(sv):
     x, w, g = _operands(3, 1, 70, 260, 192)
     res = torch.randn(70, 260, generator=g, device="cuda").to(torch.bfloat16)
