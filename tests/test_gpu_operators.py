@@ -90,6 +90,24 @@ def test_linear_epilogues(sv, act, M, N, K):
         ref.assert_linear(y, x, w, bias, res, act, 5.0, f"{act} {bdt} {rdt} {ydt}")
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh", "softcap"])
+@pytest.mark.parametrize("M", [1, 200])
+def test_linear_activations_over_their_range(sv, act, M):
+    # without entries of K an activation's argument is the bias itself
+    z = torch.cat([torch.linspace(-40, 40, 20001), torch.logspace(-30, 30, 5000), -torch.logspace(-30, 30, 5000),
+                   torch.tensor([0.0, -0.0, float("inf"), float("-inf"), float("nan")])]).cuda()
+    empty = torch.empty(M, 0, dtype=torch.bfloat16, device="cuda")
+    y = sv.linear(empty, torch.empty(len(z), 0, dtype=torch.bfloat16, device="cuda"), bias=z, activation=act, cap=5.0,
+                  out_dtype=torch.float32)
+    finite = z.isfinite()
+    assert torch.equal(y[:, finite], y[:1, finite].expand(M, -1))
+    ref.assert_linear(y[:, finite], empty, torch.empty(int(finite.sum()), 0, device="cuda"), z[finite], None, act, 5.0, act)
+    want = ref.ACT[act](z[~finite].double(), 5.0)
+    assert torch.equal(torch.isnan(y[:, ~finite]), torch.isnan(want).expand(M, -1))
+    there = ~torch.isnan(want)
+    assert torch.equal(y[:, ~finite][:, there].double(), want[there].expand(M, -1))
+
+
 @pytest.mark.parametrize("G,M,N,K,shared,pad,offset", [
     (4, 1, 512, 256, True, 0, 0), (5, 6, 384, 512, True, 8, 0), (3, 17, 200, 100, False, 0, 0),
     (2, 77, 321, 129, False, 3, 1), (5, 64, 256, 320, False, 8, 8), (2, 130, 140, 72, True, 1, 0),
