@@ -3,8 +3,11 @@
 Argument marshalling only: every step of the verification runs in the CUDA
 kernels behind the C ABI of ``include/spec_verify.h``.  Functions keep the C
 names; ``SpecVerifier`` bundles a handle with torch-tensor marshalling
-(``data_ptr()`` and the current CUDA stream).  There is no CPU fallback: if
-the shared library is missing, loading raises.
+(``data_ptr()`` and the current CUDA stream).  ``stream=`` runs a call on
+another stream (a raw handle or a ``torch.cuda.Stream``); the results that it
+makes are then memory of that stream, and the caller orders the streams around
+the inputs and the results.  There is no CPU fallback: if the shared library is
+missing, loading raises.
 """
 from __future__ import annotations
 
@@ -249,6 +252,21 @@ def _stream(dev: torch.device, stream):
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream
 
 
+def _new(dev: torch.device, stream, make):
+    """The results that ``make`` allocates, as memory of the stream that the call runs on: torch gives a tensor's memory
+    on in the order of the stream it was allocated under, and a call on another one stands outside of that order."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = getattr(stream, "value", stream) or 0
+        if handle == torch._C._cuda_getCurrentRawStream(dev.index):
+            return make()
+        # (an ExternalStream of handle 0 would be a new stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def linear(x, weight, bias=None, residual=None, activation="none", cap=0.0, out=None, out_dtype=None, stream=None):
     """act(x @ weight.T + bias) + residual, with the sums and the epilogue in fp32 and one rounding.
 
@@ -282,7 +300,7 @@ def linear(x, weight, bias=None, residual=None, activation="none", cap=0.0, out=
         raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
     shape = (G, M, N) if grouped else (M, N)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or bf16, device=dev)
+        out = _new(dev, stream, lambda: torch.empty(shape, dtype=out_dtype or bf16, device=dev))
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: dtype {out.dtype} != {out_dtype}")
     ys = _check_rows(out, "out", dim, None, dev)
@@ -323,7 +341,7 @@ def softmax(logits, temperature, out=None, stream=None):
         _check(temperature, "temperature", (rows,), torch.float32, dev)
         per_row, temperature = temperature.data_ptr(), 1.0
     if out is None:
-        out = torch.empty(rows, V, dtype=torch.float32, device=dev)
+        out = _new(dev, stream, lambda: torch.empty(rows, V, dtype=torch.float32, device=dev))
     else:
         _check_rows(out, "out", 2, torch.float32, dev)
         if out.shape != logits.shape:
@@ -376,11 +394,12 @@ def verify_tree(target_probs, draft_probs, tokens, parent, draft_row, node_start
     if max_depth is None:
         max_depth = max_nodes
     if out is None:
-        out = dict(accepted_len=torch.empty(B, dtype=i32, device=dev),
-                   tokens=torch.empty(B, max_depth + 1, dtype=i32, device=dev),
-                   path=torch.empty(B, max_depth, dtype=i32, device=dev),
-                   accept_prob=torch.empty(total, dtype=f32, device=dev),
-                   flags=torch.empty(total, dtype=torch.int8, device=dev))
+        out = _new(dev, stream, lambda: dict(
+            accepted_len=torch.empty(B, dtype=i32, device=dev),
+            tokens=torch.empty(B, max_depth + 1, dtype=i32, device=dev),
+            path=torch.empty(B, max_depth, dtype=i32, device=dev),
+            accept_prob=torch.empty(total, dtype=f32, device=dev),
+            flags=torch.empty(total, dtype=torch.int8, device=dev)))
     else:
         for name, shp, dtype in (("accepted_len", (B,), i32), ("tokens", (B, max_depth + 1), i32),
                                  ("path", (B, max_depth), i32), ("accept_prob", (total,), f32),
@@ -476,8 +495,8 @@ class SpecVerifier:
             _check(u_residual, "u_residual", (B,), torch.float32, dev)
         if counters is not None:
             _check(counters, "counters", (8,), torch.int64, dev)
-        o = self.outputs(B) if out is None else out
-        rs = torch.empty(B, 2 * k + 1, 2, dtype=torch.float32, device=dev) if row_stats else None
+        o = _new(dev, stream, lambda: self.outputs(B)) if out is None else out
+        rs = _new(dev, stream, lambda: torch.empty(B, 2 * k + 1, 2, dtype=torch.float32, device=dev)) if row_stats else None
         st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
         rc = spec_verify_run_ex(self.handle, Lt.data_ptr(), _dt(Lt), Ld.data_ptr(), _dt(Ld),
                                 D.data_ptr(), B, float(temperature), int(gate_mode),
@@ -504,9 +523,9 @@ class SpecVerifier:
         B, k, V, dev = target_hidden.shape[0], self.k, self.V, self.device
         _check(target_hidden, "target_hidden", (B, k + 1, target_hidden.shape[-1]), torch.bfloat16, dev)
         _check(draft_hidden, "draft_hidden", (B, k, draft_hidden.shape[-1]), torch.bfloat16, dev)
-        Lt = torch.empty(B, k + 1, V, dtype=logits_dtype, device=dev)
-        Ld = torch.empty(B, k, V, dtype=logits_dtype, device=dev)
-        act = dict(activation="none" if cap is None else "softcap", cap=cap or 0.0, stream=kw.get("stream"))
+        stream = kw.get("stream")
+        Lt, Ld = _new(dev, stream, lambda: [torch.empty(B, n, V, dtype=logits_dtype, device=dev) for n in (k + 1, k)])
+        act = dict(activation="none" if cap is None else "softcap", cap=cap or 0.0, stream=stream)
         linear(target_hidden.view(B * (k + 1), target_hidden.shape[-1]), target_head, bias=target_bias,
                out=Lt.view(B * (k + 1), V), **act)
         if draft_head.dim() == 3:
@@ -533,8 +552,8 @@ class SpecVerifier:
         if threshold_per_seq is not None:
             _check(threshold_per_seq, "threshold_per_seq", (B,), torch.float32, dev)
         if out is None:
-            out = {key: torch.empty(B, k, dtype=torch.float32, device=dev)
-                   for key in ("min_sum", "pq_sum", "argmax_q")}
+            out = _new(dev, stream, lambda: {key: torch.empty(B, k, dtype=torch.float32, device=dev)
+                                             for key in ("min_sum", "pq_sum", "argmax_q")})
         st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
         rc = spec_verify_diagnostics(self.handle, Lt.data_ptr(), _dt(Lt), Ld.data_ptr(), _dt(Ld),
                                      D.data_ptr(), B, float(temperature), int(gate_mode),
@@ -585,10 +604,11 @@ def run_noalloc(Lt, Ld, D, temperature, gate_mode=SV_PLAIN, threshold=0.5, gate_
     _check(Ld, "draft_logits", (B, k, V), device=dev)
     _check(D, "draft_tokens", (B, k), torch.int32, dev)
     if out is None:
-        out = dict(accepted_len=torch.empty(B, dtype=torch.int32, device=dev),
-                   tokens=torch.empty(B, k + 1, dtype=torch.int32, device=dev),
-                   accept_prob=torch.empty(B, k, dtype=torch.float32, device=dev),
-                   flags=torch.empty(B, k, dtype=torch.int8, device=dev))
+        out = _new(dev, stream, lambda: dict(
+            accepted_len=torch.empty(B, dtype=torch.int32, device=dev),
+            tokens=torch.empty(B, k + 1, dtype=torch.int32, device=dev),
+            accept_prob=torch.empty(B, k, dtype=torch.float32, device=dev),
+            flags=torch.empty(B, k, dtype=torch.int8, device=dev)))
     with torch.cuda.device(dev):
         st = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
         rc = spec_verify_run_noalloc(Lt.data_ptr(), _dt(Lt), Ld.data_ptr(), _dt(Ld), D.data_ptr(), B,

@@ -697,3 +697,64 @@ def test_run_hidden_is_the_heads_and_the_verifier(sv, per_position):
     for name in ("accepted_len", "tokens", "accept_prob", "flags"):
         assert torch.equal(out[name], same[name])
     ver.close()
+
+
+# ------------------------------------------------------------- results on a stream of their own
+
+def test_results_belong_to_the_stream_of_the_call(sv):
+    """With ``stream=`` a new result is never memory that the current stream may still use, nor is a dropped one given
+    to the current stream, in whose order the call does not stand."""
+    g = _gen(71)
+    B, k, H, V = 5, 2, 64, 300000
+    x = torch.randn(B, H, generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(V, H, generator=g, device="cuda") / 8).to(torch.bfloat16)
+    th, dh = x.unsqueeze(1).repeat(1, k + 1, 1), x.unsqueeze(1).repeat(1, k, 1)
+    D = torch.randint(0, V, (B, k), generator=g, device="cuda").int()
+    logits = sv.linear(x, w, out_dtype=torch.float32)
+    probs = sv.softmax(logits, 0.9)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    nodes = 4
+    tree = (probs[:nodes + 1], probs[:1], torch.tensor([1, 2, 3, 4], **i32), torch.full((nodes,), -1, **i32),
+            torch.tensor([0, -1, -1, -1, -1], **i32), torch.tensor([0, nodes], **i32), torch.rand(nodes, generator=g, device="cuda"),
+            torch.rand(1, generator=g, device="cuda"))
+    Lt, Ld = logits.unsqueeze(1).repeat(1, k + 1, 1), logits.unsqueeze(1).repeat(1, k, 1)
+    ver = sv.SpecVerifier(B, k, V)
+
+    def places(tensors):
+        return [(t.data_ptr(), t.data_ptr() + t.nbytes) for t in tensors]
+
+    def meet(a, b):
+        return any(x[0] < y[1] and y[0] < x[1] for x in a for y in b)
+
+    calls = [lambda s: dict(y=sv.linear(x, w, out_dtype=torch.float32, stream=s)),
+             lambda s: dict(y=sv.softmax(logits, 0.9, stream=s)),
+             lambda s: sv.verify_tree(*tree, max_nodes=nodes, max_depth=nodes, stream=s),
+             lambda s: ver.run_hidden(th, w, dh, w, D, 0.9, seed=3, logits_dtype=torch.float32, stream=s),
+             lambda s: ver.run(Lt, Ld, D, 0.9, seed=3, row_stats=True, stream=s)]
+    for call in calls:
+        want = {n: v.clone() for n, v in call(None).items()}
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        for handle in (side.cuda_stream, side):
+            # blocks of every result's size that the current stream has used and given back
+            freed = [torch.empty_like(v) for v in want.values() for _ in range(3)]
+            ours = places(freed)
+            del freed
+            got = call(handle)
+            theirs = places(got.values())
+            assert not meet(ours, theirs)
+            side.synchronize()
+            for n in want:
+                assert torch.equal(got[n], want[n]), n
+            del got
+            again = [torch.empty_like(v) for v in want.values() for _ in range(3)]
+            assert not meet(theirs, places(again))
+            del again
+        # the current stream by its handle, the default stream among them
+        got = call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(side):
+            far = call(torch.cuda.default_stream().cuda_stream)
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(got[n], want[n]) and torch.equal(far[n], want[n]), n
+    ver.close()
