@@ -108,24 +108,30 @@ __host__ __device__ constexpr bool long_code(int act) {
   return act == SV_ACT_GELU || act == SV_ACT_GELU_TANH || act == SV_ACT_SOFTCAP;
 }
 
-// f with the activation and y's type as constants: code that a call does not use is not fetched either
-template <int kAct, bool kOnlyF32, typename F>
+// y's type: fp32, bf16, or looked up for each entry
+enum YType { kYF32 = 0, kYBf16 = 1, kYEither = 2 };
+
+// f with the activation and y's type as constants: code that a call does not use is not fetched either.  Where sums come in
+// segments (kEither) one code serves both types: those kernels are for fp32 results, and bf16 ones of very long K.
+template <int kAct, bool kEither, typename F>
 __device__ __forceinline__ void with_type(int y_bf16, F&& f) {
-  if (!kOnlyF32 && y_bf16)
-    f(std::integral_constant<int, kAct>(), std::bool_constant<!kOnlyF32>());
+  if constexpr (kEither)
+    f(std::integral_constant<int, kAct>(), std::integral_constant<int, kYEither>());
+  else if (y_bf16)
+    f(std::integral_constant<int, kAct>(), std::integral_constant<int, kYBf16>());
   else
-    f(std::integral_constant<int, kAct>(), std::false_type());
+    f(std::integral_constant<int, kAct>(), std::integral_constant<int, kYF32>());
 }
 
-template <bool kOnlyF32, typename F>
+template <bool kEither, typename F>
 __device__ __forceinline__ void with_epilogue(int act, int y_bf16, F&& f) {
   switch (act) {
-    case SV_ACT_RELU: with_type<SV_ACT_RELU, kOnlyF32>(y_bf16, f); break;
-    case SV_ACT_SILU: with_type<SV_ACT_SILU, kOnlyF32>(y_bf16, f); break;
-    case SV_ACT_GELU: with_type<SV_ACT_GELU, kOnlyF32>(y_bf16, f); break;
-    case SV_ACT_GELU_TANH: with_type<SV_ACT_GELU_TANH, kOnlyF32>(y_bf16, f); break;
-    case SV_ACT_SOFTCAP: with_type<SV_ACT_SOFTCAP, kOnlyF32>(y_bf16, f); break;
-    default: with_type<SV_ACT_NONE, kOnlyF32>(y_bf16, f);
+    case SV_ACT_RELU: with_type<SV_ACT_RELU, kEither>(y_bf16, f); break;
+    case SV_ACT_SILU: with_type<SV_ACT_SILU, kEither>(y_bf16, f); break;
+    case SV_ACT_GELU: with_type<SV_ACT_GELU, kEither>(y_bf16, f); break;
+    case SV_ACT_GELU_TANH: with_type<SV_ACT_GELU_TANH, kEither>(y_bf16, f); break;
+    case SV_ACT_SOFTCAP: with_type<SV_ACT_SOFTCAP, kEither>(y_bf16, f); break;
+    default: with_type<SV_ACT_NONE, kEither>(y_bf16, f);
   }
 }
 
@@ -138,10 +144,10 @@ __device__ __forceinline__ void prefetch_l2(const void* p, int64_t i, int bf16) 
 }
 
 // The sum's way out: the one rounding to bf16, where y is bf16, is the last step.
-template <int kAct, bool kBf16>
+template <int kAct, int kType>
 __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, float z, float bias, float res) {
   z = activate<kAct>(z + bias, P.cap, P.inv_cap) + res;
-  if constexpr (kBf16)
+  if (kType == kYBf16 || (kType == kYEither && P.y_bf16))
     static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16(z);
   else
     static_cast<float*>(P.y)[at] = z;
@@ -171,12 +177,17 @@ __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, 
 //    and is never read.
 //
 // The tensor core cuts its sums off after each step of 16 entries of K, towards
-// zero: after K = 2048 a sum is 2.1e-6 short, about in proportion to K.  bf16
-// results do not show that.  For fp32 results of K > 768 (kSegments) a sum is
-// carried through the tensor core for at most 768 entries: two segments in the two
-// accumulators where that is enough, added when a tile is finished; else segments
-// of 512, which the epilogue's warps add up in tensor memory beside the two
-// accumulators (for which a tile is then 160 wide at most).
+// zero: after K = 2048 a sum is 2.1e-6 short, about in proportion to K.  (Sums of
+// one sign: 1e-7 for each step, 6.3e-3 after K = 2^20.)  For fp32 results of K > 768
+// and bf16 results of K > 32768 (kSegments) a sum is carried through the tensor core
+// for at most 768 entries: two segments in the two accumulators where that is
+// enough, added when a tile is finished; else segments of 512, which the epilogue's
+// warps add up in tensor memory beside the two accumulators (for which a tile is
+// then 160 wide at most).  bf16 results of shorter K are at most 2e-4 short, a
+// twentieth of their own rounding, and few of them land on another bf16 value than
+// an exact sum's (at K = 4096 1.4e-4 in the 2-norm; either kind is 1.66e-3 from the
+// exact results).  So no wait for a sum is longer than 512 blocks of K, far below
+// the limit at which waits give up.
 
 constexpr int kMmaK = 64;        // entries of K a stage holds of each row: 128 bytes
 constexpr int kRowBytes = 128;
@@ -189,6 +200,7 @@ constexpr int kLoadWarps = 4, kLoadGroups = 4;
 constexpr int kMmaThreads = 32 * (2 + kEpiWarps);
 constexpr int kStageCols = 64;   // columns of a tile that pass through shared memory at a time where x is A
 constexpr int kMmaSmem = 226 * 1024;
+constexpr int kLongF32 = 768, kLongBf16 = 32768;  // the longest K without segments
 
 struct MmaParams {
   LinearParams L;
@@ -705,7 +717,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
         const int rows_here = in ? static_cast<int>(min(static_cast<int64_t>(P.nt), P.L.M - m_tile)) : 0;
         const int shift = wide(P.L.res_bf16);
         if constexpr (kSegments) carry();
-        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto type) {
           constexpr int kRun = long_code(act.value) ? 16 : kCols;
           uint32_t r_next[kRun] = {};
           auto residuals = [&](int c) {
@@ -728,7 +740,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
             residuals(c + 2 * kRun);
             int64_t to = at.g * P.L.y_group + (m_tile + c) * P.L.y_row + col;
             auto finish = [&](int i) {
-              finish_value<act.value, y_bf16.value>(P.L, to, sum(ok, __uint_as_float(v[i])), bias,
+              finish_value<act.value, type.value>(P.L, to, sum(ok, __uint_as_float(v[i])), bias,
                                                     __uint_as_float(r[i] << shift));
             };
             if (__all_sync(~0u, c + kRun <= rows_here)) {
@@ -768,7 +780,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
         if constexpr (kSegments) carry();
         bool ok = true;
         if (kLoad && cols <= 0) wait_sums();  // the last tile of a class with a row less
-        auto finish_tile = [&](auto act, auto y_bf16, auto width, auto batch) {
+        auto finish_tile = [&](auto act, auto type, auto width, auto batch) {
           constexpr int kWidth = width.value, kRows = kEpiWarps * 32 / kWidth, kBatch = batch.value;
           const int c = et % kWidth, row = et / kWidth;
           uint32_t r[kBatch] = {}, r_next[kBatch] = {};
@@ -816,25 +828,25 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
 #pragma unroll
               for (int i = 0; i < kBatch; ++i, to += kRows * P.L.y_row)
                 if (m0 + i * kRows < rows)
-                  finish_value<act.value, y_bf16.value>(P.L, to, v[i], bias, __uint_as_float(r[i] << shift));
+                  finish_value<act.value, type.value>(P.L, to, v[i], bias, __uint_as_float(r[i] << shift));
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
           }
         };
-        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
+        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto type) {
           using Chunk = std::integral_constant<int, kStageCols>;
           using Tile = std::integral_constant<int, kEpiWarps * 32>;
           using Four = std::integral_constant<int, 4>;
           using Eight = std::integral_constant<int, 8>;
           using Most = std::integral_constant<int, kLoad && kSegments ? 8 : 16>;
           if (P.at_once && (tokens <= 4 || !P.L.res))
-            finish_tile(act, y_bf16, Tile(), Four());
+            finish_tile(act, type, Tile(), Four());
           else if (P.at_once)
-            finish_tile(act, y_bf16, Tile(), Eight());
+            finish_tile(act, type, Tile(), Eight());
           else if (tokens <= 16 || (!P.L.res && (kLoad || tokens <= 32)))
-            finish_tile(act, y_bf16, Chunk(), Four());
+            finish_tile(act, type, Chunk(), Four());
           else
-            finish_tile(act, y_bf16, Chunk(), Most());
+            finish_tile(act, type, Chunk(), Most());
         });
       }
       if (kSegments && P.halves) release(~n & 1);
@@ -958,7 +970,7 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   const int64_t rows_b = kWeightsA ? L.M : (static_cast<int64_t>(L.N) + P.every - 1) / P.every;
   const int workers = kPair ? std::max(1, sms / 2) : sms;
   P.tiles_a = static_cast<int>((rows_a + (kPair ? 255 : 127)) / (kPair ? 256 : 128));
-  P.halves = kSegments && blocks <= 2 * 768 / kMmaK;
+  P.halves = kSegments && blocks <= 2 * kLongF32 / kMmaK;
   const int64_t others = static_cast<int64_t>(P.tiles_a) * P.classes;
   P.nt = choose_width(kPair, kSegments && !P.halves ? 160 : 256, rows_b, others, P.ra, L.groups, blocks, workers);
   P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
@@ -1080,7 +1092,7 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
   if (K == 0) return sv::launch_mma<false, true, false>(P, device, sms, st);
-  if (y_dt == SV_F32 && K > 768)
+  if (K > (y_dt == SV_F32 ? sv::kLongF32 : sv::kLongBf16))
     return M > 128 ? sv::launch_mma<true, false, true>(P, device, sms, st)
                    : sv::launch_mma<false, false, true>(P, device, sms, st);
   return M > 128 ? sv::launch_mma<true, false, false>(P, device, sms, st)

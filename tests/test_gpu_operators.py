@@ -758,3 +758,32 @@ def test_results_belong_to_the_stream_of_the_call(sv):
         for n in want:
             assert torch.equal(got[n], want[n]) and torch.equal(far[n], want[n]), n
     ver.close()
+
+
+@pytest.mark.parametrize("M,odd", [(1, 0), (3, 1), (130, 0)])
+@pytest.mark.parametrize("K", [65600, 1 << 20])
+def test_linear_bf16_results_of_very_long_sums(sv, M, odd, K):
+    # Sums of one sign.  Each step of 16 products cuts off up to 2^-23 of the sum so far for each of them and the sum
+    # itself; a sum grows evenly, so n steps are short of up to 17 n 2^-24 of it.  At most 2048 steps go into one sum, and
+    # the additions of the K / 512 segments' sums are off by half a step each; then comes the rounding to bf16, up to 2^-8.
+    g, N = _gen(M + K), 400
+    x = torch.rand(M, K + odd, generator=g, device="cuda").to(torch.bfloat16)[:, odd:]
+    w = torch.rand(N, K + odd, generator=g, device="cuda")
+    w = (w * torch.linspace(1, 2, N, device="cuda").unsqueeze(1)).to(torch.bfloat16)[:, odd:]
+    want = torch.cat([x.double() @ part.double().T for part in w.split(50)], 1)
+    off = (sv.linear(x, w).double() - want) / want
+    own = 17 * 2048 * 2.0 ** -24 + K / 512 * 2.0 ** -24
+    assert float(off.abs().max()) <= 2.0 ** -8 * (1 + own) + own
+    # the sums lie evenly over a binade, so their roundings have no side: within 4 deviations of a mean over N of them
+    assert abs(float(off.mean())) <= own + 4 * 2.0 ** -8 / 3 ** 0.5 / N ** 0.5, float(off.mean())
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_sums_that_take_seconds(sv, dtype, odd):
+    # a wait gives up after two seconds without an answer, not where a tile takes that long: all ones, so every sum of 512
+    # is exact, and so are the sums of these up to 2^33 (24 bits above 2^9); the last one is a single entry
+    K = (1 << 29) + 1
+    x = torch.ones(K + odd, dtype=torch.bfloat16, device="cuda")[odd:].unsqueeze(0)
+    y = sv.linear(x, x, out_dtype=dtype)
+    assert float(y) == float(torch.tensor(float(K)).to(dtype))
