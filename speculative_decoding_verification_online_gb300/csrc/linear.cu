@@ -108,30 +108,27 @@ __host__ __device__ constexpr bool long_code(int act) {
   return act == SV_ACT_GELU || act == SV_ACT_GELU_TANH || act == SV_ACT_SOFTCAP;
 }
 
-// y's type: fp32, bf16, or looked up for each entry
-enum YType { kYF32 = 0, kYBf16 = 1, kYEither = 2 };
+// What a kernel is made for: sums of all of K for results of either type, or sums in segments (see below) for one type
+enum Sums { kWhole = 0, kSegmentsF32 = 1, kSegmentsBf16 = 2 };
 
-// f with the activation and y's type as constants: code that a call does not use is not fetched either.  Where sums come in
-// segments (kEither) one code serves both types: those kernels are for fp32 results, and bf16 ones of very long K.
-template <int kAct, bool kEither, typename F>
+// f with the activation and y's type as constants: code that a call does not use is not fetched either
+template <int kAct, int kSums, typename F>
 __device__ __forceinline__ void with_type(int y_bf16, F&& f) {
-  if constexpr (kEither)
-    f(std::integral_constant<int, kAct>(), std::integral_constant<int, kYEither>());
-  else if (y_bf16)
-    f(std::integral_constant<int, kAct>(), std::integral_constant<int, kYBf16>());
+  if (kSums == kSegmentsBf16 || (kSums == kWhole && y_bf16))
+    f(std::integral_constant<int, kAct>(), std::bool_constant<kSums != kSegmentsF32>());
   else
-    f(std::integral_constant<int, kAct>(), std::integral_constant<int, kYF32>());
+    f(std::integral_constant<int, kAct>(), std::bool_constant<kSums == kSegmentsBf16>());
 }
 
-template <bool kEither, typename F>
+template <int kSums, typename F>
 __device__ __forceinline__ void with_epilogue(int act, int y_bf16, F&& f) {
   switch (act) {
-    case SV_ACT_RELU: with_type<SV_ACT_RELU, kEither>(y_bf16, f); break;
-    case SV_ACT_SILU: with_type<SV_ACT_SILU, kEither>(y_bf16, f); break;
-    case SV_ACT_GELU: with_type<SV_ACT_GELU, kEither>(y_bf16, f); break;
-    case SV_ACT_GELU_TANH: with_type<SV_ACT_GELU_TANH, kEither>(y_bf16, f); break;
-    case SV_ACT_SOFTCAP: with_type<SV_ACT_SOFTCAP, kEither>(y_bf16, f); break;
-    default: with_type<SV_ACT_NONE, kEither>(y_bf16, f);
+    case SV_ACT_RELU: with_type<SV_ACT_RELU, kSums>(y_bf16, f); break;
+    case SV_ACT_SILU: with_type<SV_ACT_SILU, kSums>(y_bf16, f); break;
+    case SV_ACT_GELU: with_type<SV_ACT_GELU, kSums>(y_bf16, f); break;
+    case SV_ACT_GELU_TANH: with_type<SV_ACT_GELU_TANH, kSums>(y_bf16, f); break;
+    case SV_ACT_SOFTCAP: with_type<SV_ACT_SOFTCAP, kSums>(y_bf16, f); break;
+    default: with_type<SV_ACT_NONE, kSums>(y_bf16, f);
   }
 }
 
@@ -144,10 +141,10 @@ __device__ __forceinline__ void prefetch_l2(const void* p, int64_t i, int bf16) 
 }
 
 // The sum's way out: the one rounding to bf16, where y is bf16, is the last step.
-template <int kAct, int kType>
+template <int kAct, bool kBf16>
 __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, float z, float bias, float res) {
   z = activate<kAct>(z + bias, P.cap, P.inv_cap) + res;
-  if (kType == kYBf16 || (kType == kYEither && P.y_bf16))
+  if constexpr (kBf16)
     static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16(z);
   else
     static_cast<float*>(P.y)[at] = z;
@@ -462,12 +459,12 @@ __device__ __forceinline__ const __nv_bfloat16* first_row(const MmaParams& P, co
   return p;
 }
 
-// kWeightsA: w is A, and the CTAs work in pairs.  kSegments: see above.  kLoad: rows at odd addresses.
-template <bool kWeightsA, bool kLoad, bool kSegments>
+// kWeightsA: w is A, and the CTAs work in pairs.  kSums, kSegments: see above.  kLoad: rows at odd addresses.
+template <bool kWeightsA, bool kLoad, int kSums>
 __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoadWarps : 0), 1)
     mma_kernel(const __grid_constant__ MmaParams P, const __grid_constant__ Maps<kLoad ? kMostMaps : 2> maps) {
   static_assert(!(kWeightsA && kLoad));
-  constexpr bool kPair = kWeightsA;
+  constexpr bool kPair = kWeightsA, kSegments = kSums != kWhole;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint64_t fronts[kLoad ? kMaxStages : 1];
@@ -717,7 +714,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
         const int rows_here = in ? static_cast<int>(min(static_cast<int64_t>(P.nt), P.L.M - m_tile)) : 0;
         const int shift = wide(P.L.res_bf16);
         if constexpr (kSegments) carry();
-        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto type) {
+        with_epilogue<kSums>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
           constexpr int kRun = long_code(act.value) ? 16 : kCols;
           uint32_t r_next[kRun] = {};
           auto residuals = [&](int c) {
@@ -740,7 +737,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
             residuals(c + 2 * kRun);
             int64_t to = at.g * P.L.y_group + (m_tile + c) * P.L.y_row + col;
             auto finish = [&](int i) {
-              finish_value<act.value, type.value>(P.L, to, sum(ok, __uint_as_float(v[i])), bias,
+              finish_value<act.value, y_bf16.value>(P.L, to, sum(ok, __uint_as_float(v[i])), bias,
                                                     __uint_as_float(r[i] << shift));
             };
             if (__all_sync(~0u, c + kRun <= rows_here)) {
@@ -780,7 +777,7 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
         if constexpr (kSegments) carry();
         bool ok = true;
         if (kLoad && cols <= 0) wait_sums();  // the last tile of a class with a row less
-        auto finish_tile = [&](auto act, auto type, auto width, auto batch) {
+        auto finish_tile = [&](auto act, auto y_bf16, auto width, auto batch) {
           constexpr int kWidth = width.value, kRows = kEpiWarps * 32 / kWidth, kBatch = batch.value;
           const int c = et % kWidth, row = et / kWidth;
           uint32_t r[kBatch] = {}, r_next[kBatch] = {};
@@ -828,25 +825,25 @@ __global__ void __launch_bounds__(kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoa
 #pragma unroll
               for (int i = 0; i < kBatch; ++i, to += kRows * P.L.y_row)
                 if (m0 + i * kRows < rows)
-                  finish_value<act.value, type.value>(P.L, to, v[i], bias, __uint_as_float(r[i] << shift));
+                  finish_value<act.value, y_bf16.value>(P.L, to, v[i], bias, __uint_as_float(r[i] << shift));
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
           }
         };
-        with_epilogue<kSegments>(P.L.act, P.L.y_bf16, [&](auto act, auto type) {
+        with_epilogue<kSums>(P.L.act, P.L.y_bf16, [&](auto act, auto y_bf16) {
           using Chunk = std::integral_constant<int, kStageCols>;
           using Tile = std::integral_constant<int, kEpiWarps * 32>;
           using Four = std::integral_constant<int, 4>;
           using Eight = std::integral_constant<int, 8>;
           using Most = std::integral_constant<int, kLoad && kSegments ? 8 : 16>;
           if (P.at_once && (tokens <= 4 || !P.L.res))
-            finish_tile(act, type, Tile(), Four());
+            finish_tile(act, y_bf16, Tile(), Four());
           else if (P.at_once)
-            finish_tile(act, type, Tile(), Eight());
+            finish_tile(act, y_bf16, Tile(), Eight());
           else if (tokens <= 16 || (!P.L.res && (kLoad || tokens <= 32)))
-            finish_tile(act, type, Chunk(), Four());
+            finish_tile(act, y_bf16, Chunk(), Four());
           else
-            finish_tile(act, type, Chunk(), Most());
+            finish_tile(act, y_bf16, Chunk(), Most());
         });
       }
       if (kSegments && P.halves) release(~n & 1);
@@ -949,9 +946,9 @@ bool map_classes(MmaParams* P, Maps<kMostMaps>* maps) {
 // how many steps of `stride` entries come back to the same place in 16 bytes
 int period(int64_t stride) { return stride % 8 == 0 ? 1 : stride % 4 == 0 ? 2 : stride % 2 == 0 ? 4 : 8; }
 
-template <bool kWeightsA, bool kLoad, bool kSegments>
+template <bool kWeightsA, bool kLoad, int kSums>
 sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st, bool map_w = true) {
-  constexpr bool kPair = kWeightsA;
+  constexpr bool kPair = kWeightsA, kSegments = kSums != kWhole;
   MmaParams P = {};
   P.L = L;
   P.every = P.classes = P.group_classes = 1;
@@ -982,14 +979,14 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   Maps<kLoad ? kMostMaps : 2> maps;
   if constexpr (kLoad) {
     P.b_groups = L.w_group > 0;
-    if (P.w_mapped && !map_classes(&P, &maps)) return launch_mma<false, true, kSegments>(L, device, sms, st, false);
+    if (P.w_mapped && !map_classes(&P, &maps)) return launch_mma<false, true, kSums>(L, device, sms, st, false);
   } else {
     CUtensorMap& map_x = maps.m[kWeightsA ? 1 : 0];
     CUtensorMap& map_w = maps.m[kWeightsA ? 0 : 1];
     int gx = 0, gw = 0;
     if (!make_map(&map_x, L.x, L.K, L.M, L.groups, L.x_row, L.x_group, kWeightsA ? b_rows : P.ra, &gx) ||
         !make_map(&map_w, L.w, L.K, L.N, L.groups, L.w_row, L.w_group, kWeightsA ? 128 : b_rows, &gw))
-      return launch_mma<false, true, kSegments>(L, device, sms, st);
+      return launch_mma<false, true, kSums>(L, device, sms, st);
     P.a_groups = kWeightsA ? gw : gx;
     P.b_groups = kWeightsA ? gx : gw;
   }
@@ -1021,14 +1018,14 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   // once a device
   static std::atomic<bool> opted_in[64];
   if (device >= 64 || !opted_in[device].load()) {
-    if (cudaFuncSetAttribute(mma_kernel<kWeightsA, kLoad, kSegments>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem) !=
+    if (cudaFuncSetAttribute(mma_kernel<kWeightsA, kLoad, kSums>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem) !=
         cudaSuccess)
       return SV_ECUDA;
     if (device < 64) opted_in[device].store(true);
   }
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, workers)) * (kPair ? 2 : 1);
   const unsigned threads = kMmaThreads + (kLoad ? 32 * kLoadGroups * kLoadWarps : 0);
-  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad, kSegments>, grid, threads, smem, kPair ? 2 : 1, st, P, maps);
+  const cudaError_t e = launch_waiting(mma_kernel<kWeightsA, kLoad, kSums>, grid, threads, smem, kPair ? 2 : 1, st, P, maps);
   return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
@@ -1091,10 +1088,13 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
-  if (K == 0) return sv::launch_mma<false, true, false>(P, device, sms, st);
-  if (K > (y_dt == SV_F32 ? sv::kLongF32 : sv::kLongBf16))
-    return M > 128 ? sv::launch_mma<true, false, true>(P, device, sms, st)
-                   : sv::launch_mma<false, false, true>(P, device, sms, st);
-  return M > 128 ? sv::launch_mma<true, false, false>(P, device, sms, st)
-                 : sv::launch_mma<false, false, false>(P, device, sms, st);
+  if (K == 0) return sv::launch_mma<false, true, sv::kWhole>(P, device, sms, st);
+  if (y_dt == SV_F32 && K > sv::kLongF32)
+    return M > 128 ? sv::launch_mma<true, false, sv::kSegmentsF32>(P, device, sms, st)
+                   : sv::launch_mma<false, false, sv::kSegmentsF32>(P, device, sms, st);
+  if (y_dt == SV_BF16 && K > sv::kLongBf16)
+    return M > 128 ? sv::launch_mma<true, false, sv::kSegmentsBf16>(P, device, sms, st)
+                   : sv::launch_mma<false, false, sv::kSegmentsBf16>(P, device, sms, st);
+  return M > 128 ? sv::launch_mma<true, false, sv::kWhole>(P, device, sms, st)
+                 : sv::launch_mma<false, false, sv::kWhole>(P, device, sms, st);
 }
