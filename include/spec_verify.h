@@ -377,8 +377,8 @@ sv_status spec_verify_run_noalloc(const void* target_logits, sv_dtype tdt,
  *   bias_dt, residual_dt, y_dt: SV_F32 or SV_BF16 each.
  *   Products are summed in fp32 (on the tensor cores, at most 768 entries of K
  *   in one sum where y is fp32), the epilogue is fp32, and y is rounded once.
- *   cap: the bound of SV_ACT_SOFTCAP (cap * tanh(z / cap)), finite and > 0;
- *     otherwise not used.
+ *   cap: the bound of SV_ACT_SOFTCAP (cap * tanh(z / cap)), above 2^-128 (its
+ *     reciprocal is finite) and finite; otherwise not used.
  * groups, M or N = 0 is a no-op; K = 0 sums nothing.  Any size, stride and
  * alignment of the element is taken; rows of x and w that start at multiples
  * of 16 bytes take the fast path.  SV_EUNSUPPORTED: a stride of 2^40 or more, or

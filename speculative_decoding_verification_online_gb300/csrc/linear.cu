@@ -72,14 +72,6 @@ __device__ __forceinline__ void load_entries(uint32_t (&r)[kCount], const void* 
   }
 }
 
-// tanh to about 8 half steps: its series below 1/4, 1 - 2 / (1 + exp 2x) above
-__device__ __forceinline__ float tanh_of(float x) {
-  const float a = fabsf(x), q = a * a;
-  const float low = a * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
-  const float high = 1.f - __fdividef(2.f, 1.f + __expf(2.f * a));
-  return copysignf(a < 0.25f ? low : high, x);
-}
-
 // (1 + erf(z / sqrt 2)) / 2.  The part beyond |z| is t p(t) exp(-z^2 / 2) with t = 1 / (1 + 0.3275911 |z| / sqrt 2) and a p
 // of degree 4, off by 7.5e-8 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, halved), and by as much
 // again with fp32's roundings.  GELU of 357 x 37248 bf16 results with bias and residual, K = 128: 33.7 us, 35.4 with erff.
@@ -90,14 +82,24 @@ __device__ __forceinline__ float normal_below(float z) {
   return z > 0.f ? 1.f - beyond : beyond;
 }
 
+// cap * tanh(z / cap) to about 8 half steps.  With x = z / cap: z times the series of tanh(x) / x below 1/4, so that z keeps
+// its digits where the quotient falls below the normal floats, and cap (1 - 2 / (1 + exp 2x)) above.  Above 2^126 the
+// reciprocal is below them and off by up to 2^-22.
+__device__ __forceinline__ float soft_cap(float z, const LinearParams& P) {
+  const float x = z * P.inv_cap, a = fabsf(x), q = a * a;
+  const float low = z * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float high = P.cap * (1.f - __fdividef(2.f, 1.f + __expf(2.f * a)));
+  return a < 0.25f ? low : copysignf(high, z);
+}
+
 template <int kAct>
-__device__ __forceinline__ float activate(float z, float cap, float inv_cap) {
+__device__ __forceinline__ float activate(float z, const LinearParams& P) {
   if constexpr (kAct == SV_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
   if constexpr (kAct == SV_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
   if constexpr (kAct == SV_ACT_GELU) return z * normal_below(z);
   // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
   if constexpr (kAct == SV_ACT_GELU_TANH) return __fdividef(z, 1.f + __expf(-1.59576912f * (z + 0.044715f * z * z * z)));
-  if constexpr (kAct == SV_ACT_SOFTCAP) return cap * tanh_of(z * inv_cap);
+  if constexpr (kAct == SV_ACT_SOFTCAP) return soft_cap(z, P);
   return z;
 }
 
@@ -143,7 +145,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p, int64_t i, int bf16) 
 // The sum's way out: the one rounding to bf16, where y is bf16, is the last step.
 template <int kAct, bool kBf16>
 __device__ __forceinline__ void finish_value(const LinearParams& P, int64_t at, float z, float bias, float res) {
-  z = activate<kAct>(z + bias, P.cap, P.inv_cap) + res;
+  z = activate<kAct>(z + bias, P) + res;
   if constexpr (kBf16)
     static_cast<__nv_bfloat16*>(P.y)[at] = __float2bfloat16(z);
   else
@@ -1054,7 +1056,7 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   if (!sv::valid_dtype(y_dt) || (bias && !sv::valid_dtype(bias_dt)) || (residual && !sv::valid_dtype(residual_dt)))
     return SV_EINVAL;
   if (act < SV_ACT_NONE || act > SV_ACT_SOFTCAP) return SV_EINVAL;
-  if (act == SV_ACT_SOFTCAP && !(cap > 0.f && std::isfinite(cap))) return SV_EINVAL;
+  if (act == SV_ACT_SOFTCAP && !(cap > 0.f && std::isfinite(cap) && std::isfinite(1.f / cap))) return SV_EINVAL;
   if (x_row < 0 || x_group < 0 || w_row < 0 || w_group < 0 || bias_group < 0 || residual_row < 0 ||
       residual_group < 0 || y_row < 0 || y_group < 0)
     return SV_EINVAL;

@@ -787,3 +787,31 @@ def test_linear_sums_that_take_seconds(sv, dtype, odd):
     x = torch.ones(K + odd, dtype=torch.bfloat16, device="cuda")[odd:].unsqueeze(0)
     y = sv.linear(x, x, out_dtype=dtype)
     assert float(y) == float(torch.tensor(float(K)).to(dtype))
+
+
+def _by_bias(sv, z, act, cap=1.0, dtype=torch.float32, M=1):
+    """An activation of z itself: without entries of K its argument is the bias."""
+    empty = torch.empty(M, 0, dtype=torch.bfloat16, device="cuda")
+    return sv.linear(empty, torch.empty(len(z), 0, dtype=torch.bfloat16, device="cuda"), bias=z, activation=act, cap=cap,
+                     out_dtype=dtype)[0]
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -128 * (1 + 2.0 ** -20), 5e-39, 1.2e-38, 1e-30, 1.0, 5.0, 1e30, 1e38, 3.4028234663852886e38])
+def test_linear_soft_cap_of_any_size(sv, cap):
+    # tanh's argument is off by 2 half steps and, of caps above 2^126, by 4 more (2^-22, as their reciprocals have fewer
+    # digits); tanh by 4 more, the product by 1; results below the normal floats by a step of those
+    cap = float(torch.tensor(cap))  # as an fp32 number has it
+    z = torch.cat([torch.tensor([0.0, -0.0, float("inf"), -float("inf")]), torch.logspace(-44.8, 38.5, 4000),
+                   -torch.logspace(-44.8, 38.5, 4000)])
+    near = torch.tensor(cap, dtype=torch.float64) * torch.logspace(-6, 2, 2000, dtype=torch.float64)
+    z = torch.cat([z, near.clamp(max=3.4e38).float(), -near.clamp(max=3.4e38).float()]).cuda()
+    got, want = _by_bias(sv, z, "softcap", cap).double(), ref.ACT["softcap"](z.double(), cap)
+    steps = 11 if cap > 2.0 ** 126 else 8
+    off = (got - want).abs()
+    bound = steps * 2.0 ** -24 * want.abs() + 2.0 ** -149
+    assert bool((off <= bound).all()), (float(z[(off / bound).argmax()]), float((off / bound).max()))
+    # a bf16 result: a rounding more.  The largest bf16 number is (2 - 2^-7) 2^127; what is nearer to 2^128 is infinite.
+    short = _by_bias(sv, z, "softcap", cap, torch.bfloat16).double()
+    there = want.abs() < (2 - 2.0 ** -8) * 2.0 ** 127 * (1 - 12 * 2.0 ** -24)
+    assert bool(((short - want).abs() <= (2.0 ** -8 + 12 * 2.0 ** -24) * want.abs() + 2.0 ** -133)[there].all())
+    assert torch.equal(short[~there].abs(), torch.full_like(short[~there], float("inf")))

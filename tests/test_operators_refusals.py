@@ -151,3 +151,11 @@ def test_python_softmax_and_tree_refuse_shapes_and_types():
                            ("draft_row", _OnGpu((5,), i32, device="cuda:1"), ValueError)):
         with pytest.raises(error):
             sv.verify_tree(**dict(good, **{name: t}))
+
+
+@pytest.mark.parametrize("cap", [1e-45, 1e-40, 2.0 ** -128])
+def test_linear_refuses_caps_without_a_finite_reciprocal(cap):
+    # no call of a cap that is taken: its groups are 0
+    assert _call(sv.spec_verify_linear, LINEAR, dict(act=5, cap=cap)) == m.SV_EINVAL
+    assert _call(sv.spec_verify_linear, LINEAR, dict(act=5, cap=cap, groups=0)) == m.SV_EINVAL
+    assert _call(sv.spec_verify_linear, LINEAR, dict(act=5, cap=2.0 ** -127, groups=0)) == m.SV_OK
