@@ -438,8 +438,9 @@ sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_t logits_st
  * At a node with rows p and q, with rest = p and Z = 1 at first, a child x is
  * accepted iff rest(x) > 0 and u * mu(x) <= rest(x) / Z, where u = u_accept of
  * that child, and mu = q (SV_WITH_REPLACEMENT: siblings drawn independently), q
- * renormalised without the siblings offered before (SV_WITHOUT_REPLACEMENT), or
- * 1 (certain).  A refusal leaves rest = the positive part of rest / Z - mu and Z
+ * renormalised without the tokens of the siblings offered before
+ * (SV_WITHOUT_REPLACEMENT; 0 for a token offered before, whose mass is taken out
+ * once), or 1 (certain).  A refusal leaves rest = the positive part of rest / Z - mu and Z
  * its sum.  Behind the last child refused (or where a node has none) the token
  * comes from rest by inverse CDF in token order: the smallest v whose inclusive
  * prefix sum exceeds u_pick[b] * Z; a rest with no mass falls back to p.  p and

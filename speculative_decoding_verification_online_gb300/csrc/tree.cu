@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
           break;
         }
         const int i = child;
-        const float qx = s.qx[i], px = s.px[i], u = s.u[i];
+        float qx = s.qx[i];
+        const float px = s.px[i], u = s.u[i];
         if (!(px >= 0.f && px < INFINITY && qx >= 0.f && qx < INFINITY)) {
           bad = 1, work = kTreeEnd;
           break;
@@ -474,6 +475,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
           alpha = qx > px ? px / qx : 1.f;
         } else {
           r = bare ? Pair{s.again[i] ? 0.f : px, 0.f} : rest_of(px, qx, c.s, c.l);
+          // a sibling offered before has no place in what is left of the proposal
+          if (!bare && !P.replacement && s.again[i]) qx = 0.f;
           if (!bare && !P.replacement) {
             w.add(-mass.s);
             w.l -= mass.l;

@@ -815,3 +815,51 @@ def test_linear_soft_cap_of_any_size(sv, cap):
     there = want.abs() < (2 - 2.0 ** -8) * 2.0 ** 127 * (1 - 12 * 2.0 ** -24)
     assert bool(((short - want).abs() <= (2.0 ** -8 + 12 * 2.0 ** -24) * want.abs() + 2.0 ** -133)[there].all())
     assert torch.equal(short[~there].abs(), torch.full_like(short[~there], float("inf")))
+
+
+@pytest.mark.parametrize("V,n", [(8, 4), (20, 7), (600, 12), (5000, 9)])
+def test_tree_siblings_offered_twice_without_replacement(sv, V, n):
+    """A sibling that was offered before has no place in what is left of the proposal: its mu is 0, and its mass is
+    taken out once.  Against the distributions themselves, candidate by candidate."""
+    B = 60
+    rng = np.random.default_rng(V)
+    logits = rng.standard_normal((B, V))
+    p = np.zeros((B * (n + 1), V), np.float32)
+    p[::n + 1] = ref._softmax(2 * logits)
+    p[p.sum(1) == 0] = 1.0 / V
+    q = ref._softmax(2 * logits + 1.5 * rng.standard_normal((B, V))).astype(np.float32)
+    few = [rng.choice(V, 1 + n // 2, replace=False, p=r / r.sum()) for r in q.astype(np.float64)]
+    tokens = np.stack([rng.choice(f, n) for f in few]).astype(np.int32)  # n places, half as many tokens
+    u, u_pick = rng.random((B, n)).astype(np.float32) * 0.999, rng.random(B).astype(np.float32) * 0.999
+    row = np.full((B, n + 1), -1, np.int32)
+    row[:, 0] = np.arange(B)
+    alpha, flags, tok = np.zeros((B, n)), np.zeros((B, n), np.int8), np.full((B, 2), -1, np.int32)
+    twice = 0
+    for b in range(B):
+        rest, prop, seen = p[b * (n + 1)].astype(np.float64), q[b].astype(np.float64), []
+        Z = 1.0
+        for i in range(n):
+            v = tokens[b, i]
+            twice += v in seen
+            mu = prop / (1.0 - prop[seen].sum())
+            mu[seen] = 0.0
+            alpha[b, i] = min(1.0, rest[v] / (Z * mu[v])) if mu[v] > 0 else float(rest[v] > 0)
+            if rest[v] > 0 and u[b, i] * mu[v] * Z <= rest[v]:
+                flags[b, i], tok[b] = ref.ACCEPT, (v, 0)
+                break
+            flags[b, i] = ref.REJECT
+            rest = np.maximum(rest / Z - mu, 0.0)
+            Z = rest.sum()
+            if v not in seen:
+                seen.append(v)
+        if flags[b].max() == ref.REJECT and not (flags[b] == ref.ACCEPT).any():
+            tok[b, 0] = ref.pick(rest if Z > 0 else p[b * (n + 1)].astype(np.float64), u_pick[b])
+        else:
+            tok[b, 1] = ref.pick(p[b * (n + 1) + 1 + int(np.argmax(flags[b] == ref.ACCEPT))].astype(np.float64), u_pick[b])
+    assert twice > B // 4
+    batch = dict(p=p, q=q, tokens=tokens.reshape(-1), parent=np.full(B * n, -1, np.int32), draft_row=row.reshape(-1),
+                 node_start=(np.arange(B + 1) * n).astype(np.int32), u_accept=u.reshape(-1), u_pick=u_pick)
+    got, _ = _run_tree(sv, batch, n, 1, False)
+    assert np.array_equal(got["flags"].reshape(B, n), flags)
+    np.testing.assert_allclose(got["accept_prob"].reshape(B, n), alpha, rtol=2.0 ** -24 + 1e-9, atol=1e-30)
+    assert np.array_equal(got["tokens"], tok)
