@@ -863,3 +863,12 @@ def test_tree_siblings_offered_twice_without_replacement(sv, V, n):
     assert np.array_equal(got["flags"].reshape(B, n), flags)
     np.testing.assert_allclose(got["accept_prob"].reshape(B, n), alpha, rtol=2.0 ** -24 + 1e-9, atol=1e-30)
     assert np.array_equal(got["tokens"], tok)
+
+
+@pytest.mark.parametrize("spread", [0.3, 1.0])
+def test_linear_fp32_gelu_is_as_good_as_its_roundings(sv, spread):
+    # The argument's rounding, the sum's and the product's two are even, of a third of a squared half step at most each,
+    # and erff's own error is taken for a fifth: sqrt(5 / 3) half steps in the 2-norm.
+    z = torch.randn(1000000, generator=_gen(81), device="cuda") * spread
+    got, want = _by_bias(sv, z, "gelu").double(), ref.ACT["gelu"](z.double(), 1.0)
+    assert float((got - want).norm() / want.norm()) <= (5 / 3) ** 0.5 * 2.0 ** -24
