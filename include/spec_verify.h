@@ -358,7 +358,11 @@ sv_status spec_verify_run_noalloc(const void* target_logits, sv_dtype tdt,
  * allocate nothing and keep nothing from one call to the next, so calls may
  * overlap and may be captured.  Every pointer is device memory on `device`
  * (made current for the call, whatever device is current before it); strides
- * count elements.  Host errors as spec_verify_run, before any launch. */
+ * count elements.  Host errors as spec_verify_run, before any launch.  No wait
+ * inside the kernels is endless: one that has no answer for two seconds (a GPU
+ * taken away for as long, say) gives up.  The status, that of the launch, does not
+ * show it: the entries of y or probs that depend on it become NaN, and a sequence
+ * of spec_verify_tree fails closed. */
 
 /* Grouped matrix products with bias, activation and residual in the epilogue:
  *   y[g, m, n] = act(sum_k x[g, m, k] * w[g, n, k] + bias[g, n]) + residual[g, m, n]

@@ -66,20 +66,30 @@ __device__ __forceinline__ unsigned long long now_ns() {
 }
 
 // Waits for a phase; gives up after two seconds, or when another wait of the CTA
-// has, and marks that in *dead.
+// has, and marks that in *dead.  Two seconds by the clock are not enough: a GPU that
+// was taken away for as long gets its answer in one of the next tries.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, volatile int* dead) {
   if (mbar_try(bar, parity)) return true;
   unsigned long long since = 0;
-  for (;;) {
+  for (int late = 0;;) {
     for (int i = 0; i < 64; ++i)
       if (mbar_try(bar, parity)) return true;
     const unsigned long long t = now_ns();
     if (since == 0) since = t;
-    if (*dead || t - since > 2000000000ull) {
+    if (*dead || (t - since > 2000000000ull && ++late > 16)) {
       *dead = 1;
       return false;
     }
   }
+}
+
+// The end of a CTA of which a wait gave up.  Its copies, and what the other CTAs of
+// its cluster write into its memory, may still be on their way.  It stays for more
+// than three waits, the most that another CTA can pass before it misses this one's
+// part and gives up too.
+__device__ __forceinline__ void stay_behind() {
+  const unsigned long long since = now_ns();
+  while (now_ns() - since < 8000000000ull) __nanosleep(1000000);
 }
 
 // the address of the same place in the shared memory of the cluster's CTA `rank`

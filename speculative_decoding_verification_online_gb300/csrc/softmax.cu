@@ -63,7 +63,7 @@ struct SoftShared {
   float m[2][kSoftCluster];      // (largest, its place) where T = 0
   int at[2][kSoftCluster];
   uint64_t arrived[2], copied[3];
-  int dead, copy_dead;  // two marks: a row whose exchange failed still waits for its copy
+  volatile int dead, copy_dead;  // two marks: a row whose exchange failed still waits for its copy
 };
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -303,12 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
     float* y = P.y + r * P.y_stride;
     const float t = P.t_row ? P.t_row[r] : P.t;
     // 1.44.. / t overflows below 1e-38, where every logit but the largest has no probability
-    const float c = t > 0.f ? fminf(1.4426950408889634f / t, 3.0e38f) : 1.f;
+    float c = t > 0.f ? fminf(1.4426950408889634f / t, 3.0e38f) : 1.f;
     Two e[2 * kSoftFours];
     float m, sum;
-    bool ok = true;
     if (held) {
-      ok = mbar_wait(&s.copied[stage], stage_phase, &s.copy_dead);
+      if (!mbar_wait(&s.copied[stage], stage_phase, &s.copy_dead)) c = NAN;  // what lies in the stage is not the row
       load_part<T, kVec, kThreads>(reinterpret_cast<const T*>(stages + stage * kStageBytes + shift_of(x + lo)), hi - lo, c, e,
                                    m, sum);
     } else {
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
     auto ahead = [&]() {
       if (!held) return;
       const int64_t next = r + static_cast<int64_t>(kStages) * clusters;
-      if (threadIdx.x == 0 && next < P.rows)
+      if (threadIdx.x == 0 && next < P.rows && !s.copy_dead)
         copy_part<T>(x0 + next * P.x_stride, lo, hi, stages + stage * kStageBytes, &s.copied[stage]);
       if (++stage == kStages) stage = 0, stage_phase ^= 1;
     };
@@ -350,14 +349,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
       for (int o = 16; o; o >>= 1) bs += __shfl_xor_sync(~0u, bs, o);
       // Every CTA writes its part into every other's memory, and the write itself counts there.  A cluster barrier
       // would first wait for the stores of the row before.
-      if (lane == 0) mbar_expect(&s.arrived[turn], ctas * sizeof(float2));
-      if (lane < ctas)
+      const bool heard = !s.dead;  // a phase that did not come is not begun again
+      if (lane == 0 && heard) mbar_expect(&s.arrived[turn], ctas * sizeof(float2));
+      if (lane < ctas && heard)
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
                          in_cta(&s.part[turn][rank], lane)),
                      "l"(two(bm, bs)), "r"(in_cta(&s.arrived[turn], lane))
                      : "memory");
     }
-    ok = mbar_wait(&s.arrived[turn], phases >> turn & 1, &s.dead) && ok;
+    const bool ok = mbar_wait(&s.arrived[turn], phases >> turn & 1, &s.dead);
     phases ^= 1u << turn;
     const float2 part = lane < ctas ? s.part[turn][lane] : make_float2(-INFINITY, 0.f);
     m = part.x;
@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) softmax_kernel(cons
       }
     }
   }
+  if (s.dead || s.copy_dead) stay_behind();
 }
 
 template <int kThreads>

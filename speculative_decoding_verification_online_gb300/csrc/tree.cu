@@ -69,7 +69,7 @@ struct TreeShared {
   // exchange between
   float2 slot[2][kTreeCluster];
   uint64_t arrived[2];
-  int dead;
+  volatile int dead;
   // what the first warp asks of the others
   const float* row_p;
   const float* row_q;  // null: c is 0
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
                          in_cta(&s.slot[pass & 1][rank], lane)),
                      "f"(t.s), "f"(t.l), "r"(in_cta(&s.arrived[pass & 1], lane))
                      : "memory");
-      if (!mbar_wait(&s.arrived[pass & 1], pass >> 1 & 1, &s.dead)) bad = 1;
+      if (!__all_sync(~0u, mbar_wait(&s.arrived[pass & 1], pass >> 1 & 1, &s.dead))) bad = 1;
     }
     ++pass;
   }
@@ -568,13 +568,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2) tree_kernel(const __grid_cons
       if (lane == 0) P.out_tokens[static_cast<int64_t>(b) * (P.max_depth + 1) + len] = v;
     }
   }
-  if (rank != 0) return;
+  // A CTA whose wait gave up stays behind, and then leaves the results of a sequence that failed, whatever others left.
+  if (s.dead) stay_behind();
+  else if (rank != 0) return;
   // rank 0 leaves the rest; its first warp knows how the walk went
   __shared__ int s_len, s_bad;
   if (tid == 0) {
     s_len = len, s_bad = bad;
     P.accepted_len[b] = bad ? -1 : len;
-    if (P.counters) {
+    if (P.counters && rank == 0) {
       if (bad) {
         atomicAdd(P.counters + SV_CNT_INVALID, 1ull);
       } else {
