@@ -977,7 +977,12 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
   P.nt = choose_width(kPair, kSegments && !P.halves ? 160 : 256, rows_b, others, P.ra, L.groups, blocks, workers);
   P.tiles_b = static_cast<int>((rows_b + P.nt - 1) / P.nt);
   const int64_t most_tiles = (int64_t{1} << 31) - 1;
-  if (others * P.tiles_b > most_tiles / L.groups) return SV_EUNSUPPORTED;
+  if (others * P.tiles_b > most_tiles / L.groups) {
+    // classes of rows cut the columns into up to eight times as many tiles; without them there are fewer than 2^31 for any
+    // y that memory holds (a tile's width is at least N as far as 256)
+    if (P.classes > 1) return launch_mma<false, true, kSums>(L, device, sms, st, false);
+    return SV_EUNSUPPORTED;
+  }
   const int64_t tiles = others * P.tiles_b * L.groups;
   P.tiles = static_cast<unsigned>(tiles);
   const int b_rows = kPair ? P.nt / 2 : P.nt;

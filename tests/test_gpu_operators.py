@@ -872,3 +872,14 @@ def test_linear_fp32_gelu_is_as_good_as_its_roundings(sv, spread):
     z = torch.randn(1000000, generator=_gen(81), device="cuda") * spread
     got, want = _by_bias(sv, z, "gelu").double(), ref.ACT["gelu"](z.double(), 1.0)
     assert float((got - want).norm() / want.norm()) <= (5 / 3) ** 0.5 * 2.0 ** -24
+
+
+def test_linear_as_many_groups_as_memory_holds(sv):
+    # 2^28 groups of eight odd rows: in classes of rows that start alike they would be 2^31 tiles
+    G, N, K = 1 << 28, 8, 3
+    g = _gen(91)
+    x = torch.randn(1, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(1, N, K, generator=g, device="cuda").to(torch.bfloat16)
+    y = sv.linear(x, w.expand(G, N, K))
+    ref.assert_linear(y[0], x, w[0], None, None, "none", 0.0)
+    assert bool((y == y[0]).all())
