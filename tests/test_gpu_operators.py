@@ -883,3 +883,106 @@ def test_linear_as_many_groups_as_memory_holds(sv):
     y = sv.linear(x, w.expand(G, N, K))
     ref.assert_linear(y[0], x, w[0], None, None, "none", 0.0)
     assert bool((y == y[0]).all())
+
+
+# ------------------------------------------------------------- the ends of the documented ranges
+
+def _far_rows(seed, rows, V, dtype, odd):
+    """Logits rows; `odd`: at odd addresses, NaN between them."""
+    g = _gen(seed)
+    if not odd:
+        return (torch.randn(rows, V, generator=g, device="cuda") * 4).to(dtype)
+    store = torch.full((1 + rows * (V + 3),), float("nan"), dtype=dtype, device="cuda")
+    x = store[1:].view(rows, V + 3)[:, :V]
+    x.copy_(torch.randn(rows, V, generator=g, device="cuda") * 4)
+    return x
+
+
+# a row in registers, clusters of sixteen that take several rows, rows longer than the registers of sixteen CTAs
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,V,odd", [(40, 140000, False), (40, 151936, True), (3, 262144, False), (3, 262145, False),
+                                        (2, 300001, True), (20, 300000, False), (3, 1 << 22, False), (2, (1 << 22) - 1, True)])
+def test_softmax_long_rows(sv, dtype, rows, V, odd):
+    x = _far_rows(rows + V, rows, V, dtype, odd)
+    t = torch.rand(rows, generator=_gen(V), device="cuda") + 0.3
+    t[rows // 2] = 0.0
+    out = torch.full((rows, V + 2), 9.0, device="cuda")
+    y = sv.softmax(x, t, out=out[:, 1:V + 1])
+    warm = t > 0
+    _assert_softmax(y[warm], x[warm], t[warm])
+    cold = x[rows // 2].float()
+    assert torch.equal(y[rows // 2], torch.nn.functional.one_hot(cold.argmax(), V).float())
+    assert bool((out[:, 0] == 9).all()) and bool((out[:, -1] == 9).all())
+
+
+@pytest.mark.parametrize("V", [262145, 300001, 1 << 22])
+def test_softmax_long_rows_in_place(sv, V):
+    x = _far_rows(V, 4, V, torch.float32, False)
+    x[2, V - 3] = x[2, 70000] = 60.0
+    before, t = x.clone(), torch.tensor([0.7, 1.3, 0.0, 1e-30], device="cuda")
+    sv.softmax(x, t, out=x)
+    _assert_softmax(x[:2], before[:2], t[:2])
+    want = torch.zeros_like(x[2:])
+    want[0, 70000] = 1
+    want[1, before[3].argmax()] = 1
+    assert torch.equal(x[2:], want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [262145, 1 << 22])
+def test_softmax_long_rows_without_a_distribution(sv, dtype, V):
+    x = _far_rows(V, 9, V, dtype, False)
+    x[1, V - 1] = float("nan")
+    x[2, V // 2] = float("inf")
+    x[3] = float("-inf")
+    x[4, : V - 1] = float("-inf")
+    x[5] = torch.finfo(dtype).min
+    t = torch.ones(9, device="cuda")
+    t[6], t[7], t[8] = -1.0, float("nan"), float("inf")
+    y = sv.softmax(x, t)
+    assert bool(torch.isnan(y[[1, 2, 3, 6, 7, 8]]).all())
+    assert float(y[4, V - 1]) == 1.0 and float(y[4].sum()) == 1.0
+    _assert_softmax(y[[0, 5]], x[[0, 5]], 1.0)
+    cold = sv.softmax(x, torch.where(t > 0, 0.0, t))
+    assert bool(torch.isnan(cold[[1, 2, 3, 6, 7]]).all())
+    assert torch.equal(cold[[0, 4, 5]].argmax(1), x[[0, 4, 5]].float().argmax(1))
+    assert bool((cold[[0, 4, 5]].sum(1) == 1).all())
+
+
+@pytest.mark.parametrize("V,kind", [(300001, "mixed"), (1 << 22, "sampled"), ((1 << 22) - 1, "certain")])
+def test_tree_the_longest_rows(sv, V, kind):
+    batch = ref.random_tree_batch(V, 2, V, 4, 3, True, kind, sharp=3.0, noise=1.0)
+    _check_tree(sv, batch, 4, 3)
+
+
+@pytest.mark.parametrize("V", [2200001, 1 << 22])
+def test_tree_one_cta_for_the_longest_rows(sv, V):
+    # so many sequences that each has one CTA, with more than 4096 sums of a row; all share one row of each side
+    B = 170
+    rng = np.random.default_rng(V)
+    logits = rng.standard_normal(V, dtype=np.float32) * 2
+    p = ref._softmax(logits[None].astype(np.float64)).astype(np.float32)
+    q = ref._softmax((logits + 0.4 * rng.standard_normal(V, dtype=np.float32))[None].astype(np.float64)).astype(np.float32)
+    sums = np.cumsum(q[0].astype(np.float64))
+    tokens = np.searchsorted(sums, rng.random(B) * sums[-1], side="right").clip(max=V - 1).astype(np.int32)
+    row = np.stack([np.zeros(B), np.full(B, -1)], 1).astype(np.int32).reshape(-1)
+    batch = dict(tokens=tokens, parent=np.full(B, -1, np.int32), draft_row=row, node_start=np.arange(B + 1, dtype=np.int32),
+                 u_accept=rng.random(B).astype(np.float32), u_pick=np.minimum(rng.random(B), 1 - 2.0 ** -24).astype(np.float32))
+    t = {k: torch.as_tensor(v).cuda() for k, v in batch.items()}
+    cnt = torch.zeros(8, dtype=torch.int64, device="cuda")
+    out = sv.verify_tree(torch.as_tensor(p).cuda().expand(2 * B, V), torch.as_tensor(q).cuda(), t["tokens"], t["parent"],
+                         t["draft_row"], t["node_start"], t["u_accept"], t["u_pick"], max_nodes=1, max_depth=1, counters=cnt)
+    # the tokens of either row by its sums, in 64 bits
+    p64, q64 = p[0].astype(np.float64), q[0].astype(np.float64)
+    alpha = np.minimum(1.0, p64[tokens] / q64[tokens])
+    yes = batch["u_accept"].astype(np.float64) * q64[tokens] <= p64[tokens]
+    rest_sums, p_sums = np.cumsum(np.maximum(p64 - q64, 0.0)), np.cumsum(p64)
+    u = batch["u_pick"].astype(np.float64)
+    assert 5 < (~yes).sum() < B - 5
+    pick = np.where(yes, np.searchsorted(p_sums, u * p_sums[-1], side="right"),
+                    np.searchsorted(rest_sums, u * rest_sums[-1], side="right"))
+    want = dict(accepted_len=yes.astype(np.int32), path=np.where(yes, 0, -1).astype(np.int32)[:, None],
+                tokens=np.stack([np.where(yes, tokens, pick), np.where(yes, pick, -1)], 1).astype(np.int32),
+                flags=np.where(yes, ref.ACCEPT, ref.REJECT).astype(np.int8), accept_prob=alpha)
+    counts = np.array([B, yes.sum(), 0, (~yes).sum(), yes.sum(), 0, 0, 0])
+    _assert_tree(({k: v.cpu().numpy() for k, v in out.items()}, cnt.cpu().numpy()), (want, counts))
