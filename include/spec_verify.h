@@ -377,7 +377,8 @@ sv_status spec_verify_run_noalloc(const void* target_logits, sv_dtype tdt,
  *     none): row (g, m) starts at g * residual_group + m * residual_row.
  *   y: rows at g * y_group + m * y_row, which must not overlap each other
  *     (SV_EINVAL); it may be the residual itself, with the same strides and
- *     type, and must not overlap any other input.
+ *     type, and must not overlap any other input (SV_EINVAL where that is
+ *     certain: operands that start at one place, or without gaps).
  *   bias_dt, residual_dt, y_dt: SV_F32 or SV_BF16 each.
  *   Products are summed in fp32 (on the tensor cores, at most 768 entries of K
  *   in one sum where y is fp32), the epilogue is fp32, and y is rounded once.
@@ -411,7 +412,8 @@ sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_group,
  *   T_r = temperature_per_row[r] (device, [rows]) or, where that is NULL,
  *     temperature: finite, >= 0.  0 puts 1 on the row's first largest logit.
  *   probs: rows at r * probs_stride >= V apart; it may be fp32 logits
- *     themselves with the same stride, and must not overlap them otherwise.
+ *     themselves with the same stride, and must not overlap them otherwise
+ *     (SV_EINVAL where that is certain, as above).
  * A row with a NaN or +inf logit, with every logit -inf, or with a temperature
  * of its own that is negative or not finite becomes NaN throughout (a verifying
  * call that reads it fails closed).  V up to SV_MAX_V; rows = 0 is a no-op. */

@@ -24,6 +24,26 @@ struct DeviceGuard {
   }
 };
 
+// Where an operand's entries lie: `groups` times `rows` rows of n entries of `size` bytes, strides counting entries.
+struct Extent {
+  const void* p;
+  int64_t size, n, row, rows, group, groups;
+  // bytes from the first entry to behind the last (strides below 2^40 times counts up to 2^30)
+  __int128 span() const {
+    return (static_cast<__int128>(row) * (rows - 1) + static_cast<__int128>(group) * (groups - 1) + n) * size;
+  }
+  // whether every byte between them is one of its own
+  bool dense() const { return span() == static_cast<__int128>(n) * rows * groups * size; }
+};
+
+// Whether two operands (neither of them empty) share memory for certain: they start at one place, or lie in parts of memory
+// that meet and have no gaps.  Rows that lie between another operand's rows are not told apart.
+inline bool sure_to_overlap(const Extent& a, const Extent& b) {
+  if (a.p == b.p) return true;
+  const __int128 pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  return pa < pb + b.span() && pb < pa + a.span() && a.dense() && b.dense();
+}
+
 // A kernel's first step: everything before it in the stream is done and visible.
 // Then the next kernel may come in as CTAs leave (it waits here in its turn).
 __device__ __forceinline__ void wait_for_stream() {

@@ -1079,6 +1079,16 @@ extern "C" sv_status spec_verify_linear(const void* x, int64_t x_row, int64_t x_
   if (!sv::rows_apart(y_row, y_group, M, groups, N)) return SV_EINVAL;
   sv::DeviceGuard guard(device);
   if (!guard.ok) return SV_ECUDA;
+  const int64_t rs = residual_dt == SV_BF16 ? 2 : 4;
+  const sv::Extent ey = {y, y_dt == SV_BF16 ? 2 : 4, N, y_row, M, y_group, groups};
+  const sv::Extent ex = {x, 2, K, x_row, M, x_group, groups}, ew = {w, 2, K, w_row, N, w_group, groups};
+  const sv::Extent er = {residual, rs, N, residual_row, M, residual_group, groups};
+  const sv::Extent eb = {bias, bias_dt == SV_BF16 ? 2 : 4, N, bias_group, groups, 0, 1};
+  if (K > 0 && (sv::sure_to_overlap(ey, ex) || sv::sure_to_overlap(ey, ew))) return SV_EINVAL;
+  if (bias && sv::sure_to_overlap(ey, eb)) return SV_EINVAL;
+  const bool own_residual = residual == y && residual_dt == y_dt && (M == 1 || residual_row == y_row) &&
+                            (groups == 1 || residual_group == y_group);
+  if (residual && !own_residual && sv::sure_to_overlap(ey, er)) return SV_EINVAL;
   sv::LinearParams P = {};
   P.x = static_cast<const __nv_bfloat16*>(x);
   P.w = static_cast<const __nv_bfloat16*>(w);

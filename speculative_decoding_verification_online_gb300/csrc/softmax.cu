@@ -407,6 +407,10 @@ extern "C" sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_
   if (rows > 1 && (logits_stride < 0 || probs_stride < V)) return SV_EINVAL;
   sv::DeviceGuard g(device);
   if (!g.ok) return SV_ECUDA;
+  const bool in_place = logits == probs && dt == SV_F32 && (rows == 1 || logits_stride == probs_stride);
+  if (!in_place && sv::sure_to_overlap({logits, static_cast<int64_t>(es), V, logits_stride, rows, 0, 1},
+                                       {probs, 4, V, probs_stride, rows, 0, 1}))
+    return SV_EINVAL;
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
   // enough CTAs a row to hold it, and more while the rows leave room beside two CTAs an SM

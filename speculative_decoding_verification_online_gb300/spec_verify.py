@@ -277,7 +277,7 @@ def linear(x, weight, bias=None, residual=None, activation="none", cap=0.0, out=
     rows have to be contiguous: ``out=logits.transpose(0, 1)`` writes heads
     straight into [M, G, N].  ``activation``: none, relu, silu, gelu, gelu_tanh,
     or softcap (``cap`` * tanh(z / ``cap``)).  ``out`` may be ``residual``
-    itself.  A new result takes ``out_dtype`` (default bfloat16).  No gradient
+    itself, but share no memory with ``x``, ``weight`` and ``bias``.  A new result takes ``out_dtype`` (default bfloat16).  No gradient
     is recorded."""
     dev = _cuda_device(x, "x")
     bf16 = torch.bfloat16

@@ -986,3 +986,35 @@ def test_tree_one_cta_for_the_longest_rows(sv, V):
                 flags=np.where(yes, ref.ACCEPT, ref.REJECT).astype(np.int8), accept_prob=alpha)
     counts = np.array([B, yes.sum(), 0, (~yes).sum(), yes.sum(), 0, 0, 0])
     _assert_tree(({k: v.cpu().numpy() for k, v in out.items()}, cnt.cpu().numpy()), (want, counts))
+
+
+def test_calls_that_would_write_over_their_inputs_are_refused(sv):
+    g = _gen(95)
+    h = torch.randn(6, 256, generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(256, 256, generator=g, device="cuda") / 16).to(torch.bfloat16)
+    before = h.clone()
+    shared = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+    f32 = torch.zeros(6, 256, device="cuda")
+    for kw in (dict(x=h, residual=h, out=h), dict(x=h, out=h), dict(x=h, out=w[:6]), dict(x=h, out=w[100:106]),
+               dict(x=shared[:1536].view(6, 256), out=shared[768:2304].view(6, 256)),
+               dict(x=h, bias=f32[2], out=f32), dict(x=h, residual=f32[:1].expand(6, 256), out=f32),
+               dict(x=h, residual=f32.view(torch.bfloat16)[:3].view(6, 256), out=f32)):
+        with pytest.raises(sv.SpecVerifyError):
+            sv.linear(kw.pop("x"), w, **kw)
+    for logits, out in ((f32, f32.view(-1)[:1530].view(6, 255)), (f32.view(torch.bfloat16)[:3].view(6, 256), f32),
+                        (f32.view(-1)[256:].view(5, 256), f32[:5])):
+        with pytest.raises((sv.SpecVerifyError, ValueError)):
+            sv.softmax(logits, 1.0, out=out)
+    assert torch.equal(h, before)
+    # rows that lie between another operand's rows, and neighbours, are taken
+    both = torch.zeros(6, 512, dtype=torch.bfloat16, device="cuda")
+    both[:, :256] = h
+    sv.linear(both[:, :256], w, residual=both[:, :256], out=both[:, 256:])
+    ref.assert_linear(both[:, 256:], h, w, None, h, "none", 0.0)
+    rows = torch.zeros(12, 256, dtype=torch.bfloat16, device="cuda")
+    rows[6:] = h
+    sv.linear(rows[6:], w, out=rows[:6])
+    ref.assert_linear(rows[:6], h, w, None, None, "none", 0.0)
+    wide = torch.randn(6, 300, generator=g, device="cuda")
+    p = sv.softmax(wide[:, :100], 1.0, out=wide[:, 100:200])
+    _assert_softmax(p, wide[:, :100], 1.0)
