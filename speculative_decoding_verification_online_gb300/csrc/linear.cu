@@ -10,12 +10,14 @@
 // What bounds it, measured on a GB300 (6.78 TB/s, 1.95 PFLOP/s bf16 measured with a
 // copy and a library product):
 //  * few tokens: reading w once.  M = 6, N = 151936, K = 2048: 99 us, 6.3 TB/s; five
-//    heads of M = 64, N = K = 4096 with bias, SiLU and residual: 34.4 us, 5.0 TB/s
+//    heads of M = 64, N = K = 4096 with bias, SiLU and residual: 34.7 us, 5.0 TB/s
 //    (one wave of tiles: its start and its end are not hidden).
 //  * many tokens: the tensor cores and the power limit.  M = 2304, N = 32000, K =
-//    4096: 298 us, 2.03 PFLOP/s alone, 1.79 under load; M = 384, N = 128256, K =
-//    4096: 248 us, 1.62 PFLOP/s (75 % of the cycles in products: 200 KB of stages in
-//    flight a SM do not cover what w takes to come from HBM).
+//    4096: 298 us, 2.03 PFLOP/s alone, 340 to 354 us, 1.71 to 1.78, back to back;
+//    M = 384, N = 128256, K = 4096 with a soft cap: 248 us, 1.62 PFLOP/s alone, 258 to
+//    262 us repeated on the same inputs, 296 to 300 us, 1.36, back to back on others
+//    (75 % of the cycles in products: 200 KB of stages in flight a SM do not cover what
+//    w takes to come from HBM).
 //  * rows at odd addresses: w's bytes where K is long (M = 77, N = 32001, K = 8001:
 //    103 us, 5.0 TB/s; 83 us for K = 8000), the start and the end of a tile where it is
 //    short (K = 1001: 27 us; 21 us for K = 1000; 42 us where warps load both operands).
@@ -74,8 +76,8 @@ __device__ __forceinline__ void load_entries(uint32_t (&r)[kCount], const void* 
 
 // (1 + erf(z / sqrt 2)) / 2 for results of bf16.  The part beyond |z| is t p(t) exp(-z^2 / 2) with t = 1 / (1 + 0.3275911 |z| /
 // sqrt 2) and a p of degree 4, off by 7.5e-8 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, halved), and
-// by as much again with fp32's roundings.  GELU of 357 x 37248 bf16 results with bias and residual, K = 128: 31.0 us, 35.4
-// with erff.
+// by as much again with fp32's roundings.  GELU of 357 x 37248 bf16 results with bias and residual, K = 128: 33.7 us, 35.4 with
+// erff.
 __device__ __forceinline__ float normal_below(float z) {
   const float a = fabsf(z), t = __fdividef(1.f, fmaf(0.231641888f, a, 1.f));
   const float p = fmaf(fmaf(fmaf(fmaf(0.5307027145f, t, -0.7265760135f), t, 0.7107068705f), t, -0.142248368f), t, 0.127414796f);

@@ -15,10 +15,12 @@
 // multiplication an entry.  Parts longer than the registers hold are read twice,
 // the second time from L2.
 //
-// Measured on a GB300: 384 rows of 128256 bf16 logits 57 to 61 us, 4.9 to 5.2 TB/s of
-// 6.78 (36 clusters of eight CTAs fit; a row's turn is its arithmetic, 17 warp
-// instructions for 32 entries, then an exchange that the other CTA of the SM has
-// to cover); 746 x 62236 49 us, 5.7 TB/s; seven rows of 262143 fp32 logits 5 us.
+// Measured on a GB300: 384 rows of 128256 bf16 logits 55 to 62 us repeated on the same
+// ones, 63 us on others each time, 4.7 to 5.4 TB/s of 6.78 (36 clusters of eight CTAs
+// fit; a row's turn is its arithmetic, 17 warp instructions for 32 entries, then an
+// exchange that the other CTA of the SM has to cover); 746 x 62236 49 us, 5.7 TB/s;
+// seven rows of 262143 fp32 logits 5.1 us; 64 rows of 400000 bf16 logits, read twice,
+// 48 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -413,7 +415,10 @@ extern "C" sv_status spec_verify_softmax(const void* logits, sv_dtype dt, int64_
     return SV_EINVAL;
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
-  // enough CTAs a row to hold it, and more while the rows leave room beside two CTAs an SM
+  // Enough CTAs a row to hold it, and more while the rows leave room beside two CTAs an SM.  Half as many, as chosen and twice
+  // as many: 7 x 262143 fp32 8.8, 5.1 us (no more than 16); 20 x 128256 bf16 7.4, 6.2, 8.8 us; 80 x 32000 7.4, 5.9, 7.4 us;
+  // 384 x 32000 18.1, 14.0, 24.2 us; 384 x 128256 67.8, 55.3, 108 us; 200 x 128256 fp32 43.0, 40.1, 56.7 us.  Above 131072
+  // entries holding a row takes 16, of which 14 clusters fit: 300 x 151936 bf16 86 us; read twice by 8 110 us, by 4 75 us.
   int ctas = 1;
   while (ctas < sv::kSoftCluster && (V > ctas * sv::kSoftPart || (static_cast<int64_t>(rows) * ctas * 2 <= 2ll * sms &&
                                                                   V > ctas * sv::kSoftThreads * 4)))

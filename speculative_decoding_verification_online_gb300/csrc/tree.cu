@@ -21,10 +21,10 @@
 // CTA's first warp takes the same walk, and a sum over a row is one exchange of
 // partial sums through the cluster's shared memory.
 //
-// Measured on a GB300: one chain of four drafts over 32000 tokens 7.0 us, of which
+// Measured on a GB300: one chain of four drafts over 32000 tokens 7.1 us, of which
 // a pass over the row pair takes 2 and the dependent loads in front of the walk 1.6;
-// 64 chains over 128256 tokens 17.9 us, their first pass at 8 TB/s from HBM and L2;
-// 32 trees of up to 21 drafts over 151936 tokens 32.5 us, bound by the sequence with
+// 64 chains over 128256 tokens 15.8 us, their first pass at 8 TB/s from HBM and L2;
+// 32 trees of up to 21 drafts over 151936 tokens 30.8 us, bound by the sequence with
 // the most refusals (about 5 us each: a pass of 1.2 MB by eight SMs, an exchange, a
 // step of the walk).
 #include <cooperative_groups.h>
@@ -643,7 +643,10 @@ extern "C" sv_status spec_verify_tree(const float* target_probs, int64_t target_
   P.counters = reinterpret_cast<unsigned long long*>(counters);
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return SV_ECUDA;
-  // as many CTAs a sequence as two per SM allow, each with a chunk for every other warp at least
+  // As many CTAs a sequence as two per SM allow, each with a chunk for every other warp at least.  Half as many, as chosen and
+  // twice as many, chains of four drafts: B = 1, V = 32000 8.2, 7.1, 6.8 us; B = 64, V = 128256 18.6, 16.2, 20.8 us; B = 100
+  // 31.4, 26.4, 29.4 us; B = 152 35.9, 30.9, 43.3 us; above 152 sequences one CTA each, or two: B = 160 45.4, 44.8 us, B = 256
+  // 48.2, 54.4 us.
   int ctas = 1;
   while (ctas < sv::kTreeCluster && static_cast<int64_t>(B) * ctas * 2 <= 2ll * sms &&
          ctas * sv::kTreeWarps < P.nchunk)
