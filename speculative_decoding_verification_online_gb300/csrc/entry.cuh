@@ -86,17 +86,16 @@ __device__ __forceinline__ unsigned long long now_ns() {
 }
 
 // Waits for a phase; gives up after two seconds, or when another wait of the CTA
-// has, and marks that in *dead.  Two seconds by the clock are not enough: a GPU that
-// was taken away for as long gets its answer in one of the next tries.
+// has, and marks that in *dead.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, volatile int* dead) {
   if (mbar_try(bar, parity)) return true;
   unsigned long long since = 0;
-  for (int late = 0;;) {
+  for (;;) {
     for (int i = 0; i < 64; ++i)
       if (mbar_try(bar, parity)) return true;
     const unsigned long long t = now_ns();
     if (since == 0) since = t;
-    if (*dead || (t - since > 2000000000ull && ++late > 16)) {
+    if (*dead || t - since > 2000000000ull) {
       *dead = 1;
       return false;
     }
