@@ -488,6 +488,146 @@ sv_status spec_verify_tree(const float* target_probs, int64_t target_stride,
                            float* accept_prob, int8_t* flags, uint64_t* counters,
                            int device, void* cuda_stream);
 
+/* Penalties for repeated tokens, biases and masks on logits rows, in front of
+ * the probabilities.  Rows lie as target_probs of spec_verify_tree does:
+ * sequence b's root row at node_start[b] + b, then its nodes' rows, so rows =
+ * total_nodes + B; a chain's [B, k+1, V] has node_start[b] = b * k.  The row of
+ * a node stands behind its path, the node and its ancestors.
+ *
+ * For token v of a row of sequence b, with n = how often v is among
+ * history[b, prompt_len[b] .. history_len[b]-1] and the path's tokens, and seen
+ * = n > 0 or v is among history[b, 0 .. prompt_len[b]-1]:
+ *   z = seen ? (l > 0 ? l / repetition[b] : l * repetition[b]) : l
+ *   z = z - frequency[b] * n - (n > 0 ? presence[b] : 0) + bias[b, v]
+ *   out = the row's mask allows v ? z : -inf
+ * in fp32, rounded once to out's type.  A masked logit may be anything; a mask
+ * that allows nothing leaves a row of -inf (a verifying call fails closed on it).
+ *
+ *   logits, out: rows of V entries of types dt and out_dt at r * stride; out
+ *     may be logits with the same type and stride (then only entries that change
+ *     are written), and must not overlap them otherwise (SV_EINVAL where that is
+ *     certain, as above).
+ *   history: row b at b * history_stride, of history_cap entries; tokens outside
+ *     [0, V) count nothing.  history_len[b] < 0: a padded sequence, whose rows
+ *     are left as they were (not written).  prompt_len (NULL = 0): taken as 0
+ *     to history_len[b].
+ *   node_tokens, parent [total_nodes]: as spec_verify_tree; parent NULL = chains.
+ *     Node tokens outside [0, V) count nothing.
+ *   repetition, frequency, presence [B]: NULL = 1, 0, 0.
+ *   bias_start [B+1], bias_tokens, bias_values [total_biases]: the biases of
+ *     sequence b are the entries bias_start[b] .. bias_start[b+1] - 1; of entries
+ *     for one token the last one counts.  NULL = none.
+ *   mask: mask_rows rows of words of 32 tokens (bit v % 32 of word v / 32: v is
+ *     allowed) at i * mask_stride; row r has the mask mask_row[r] (-1: none), or
+ *     r where mask_row is NULL (then mask_rows >= rows).  mask NULL = none.
+ * Rows become NaN whose path has a parent outside [-1, i) or whose mask_row is
+ * outside [-1, mask_rows), and all rows of a sequence with history_len[b] >
+ * history_cap, a repetition that is not positive and finite, a frequency or
+ * presence that is not finite, or a range of biases that leaves [0,
+ * total_biases].  A sequence whose node range leaves [0, total_nodes] or holds
+ * more than max_nodes nodes has no rows that are known: nothing is written.
+ * SV_EUNSUPPORTED beyond SV_MAX_V or SV_MAX_NODES; B = 0 is a no-op. */
+sv_status spec_verify_penalties(const void* logits, sv_dtype dt, int64_t logits_stride,
+                                void* out, sv_dtype out_dt, int64_t out_stride, int V,
+                                const int32_t* history, int64_t history_stride, int history_cap,
+                                const int32_t* history_len, const int32_t* prompt_len,
+                                const int32_t* node_tokens, const int32_t* parent,
+                                const int32_t* node_start, int B, int total_nodes, int max_nodes,
+                                const float* repetition, const float* frequency,
+                                const float* presence, const int32_t* bias_start,
+                                const int32_t* bias_tokens, const float* bias_values,
+                                int total_biases, const int32_t* mask, int64_t mask_stride,
+                                int mask_rows, const int32_t* mask_row, int device,
+                                void* cuda_stream);
+
+/* A cache of keys and values in pages, held in 8 bits (e4m3, "fn": no
+ * infinities, 0x7f and 0xff are NaN) with a scale for each block of tokens and
+ * head: the value of an entry is entry * scale.
+ *   k, v: entry (layer, page, head, token, d) at layer * layer_stride + page *
+ *     page_stride + head * head_stride + token * token_stride + d bytes; the
+ *     strides are multiples of 16, k and v on multiples of 16.
+ *   k_scale, v_scale: fp32, scale (layer, page, head, i) at layer *
+ *     scale_layer_stride + (page * heads + head) * (page_tokens / block) + i.
+ *   page_tokens: a power of two, 16 to 256; block: a power of two up to
+ *     page_tokens; dim: 64 or 128; layers: 1 for the calls that work on one.
+ * Sequence b's position p is token p % page_tokens of the page page_table[b,
+ * p / page_tokens] (rows of table_cols entries at b * table_stride).
+ * context [B] = positions that are committed.  A step's rows, as above, stand at
+ * context[b] (the root: the token sampled last) and context[b] + 1 + i (node i).
+ * context[b] < 0: a padded sequence, of which nothing is read or written. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t layer_stride, page_stride, head_stride, token_stride, scale_layer_stride;
+  int layers, pages, heads, page_tokens, block, dim;
+} sv_cache;
+
+/* Write a step's rows (or a prompt's: max_nodes is not bounded here) into the
+ * cache at the positions above.
+ *   k, v: fp32 or bf16 entries, row r, head h at r * row + h * head, dim
+ *     contiguous entries each.
+ * A block of tokens that holds no positions below context[b] gets the scale
+ * need = 2^ceil(log2(largest / 448)), 2^-100 at least, of its new rows' largest
+ * finite magnitude; another block gets max(its scale, need), and where that
+ * grows its older entries become round(entry * old / new).  A new entry is
+ * round(x / scale), to nearest, ties to even; an x that is not finite becomes NaN.
+ * Powers of two: growing moves no digits but those that fall below the smallest.
+ * Positions whose page is outside [0, pages) or whose column is outside the
+ * table are not written, nor is a sequence whose node range leaves [0,
+ * total_nodes] or holds more than max_nodes nodes.  No two sequences may share a
+ * page that the call writes to. */
+sv_status spec_verify_cache_write(const sv_cache* cache, const void* k, const void* v, sv_dtype dt,
+                                  int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
+                                  const int32_t* page_table, int64_t table_stride, int table_cols,
+                                  const int32_t* context, const int32_t* node_start, int B,
+                                  int total_nodes, int max_nodes, int device, void* cuda_stream);
+
+/* Keep the rows of the accepted path (accepted_len and path [B, max_depth] of
+ * spec_verify_tree) in every layer: position context[b] + 1 + t takes the entries
+ * of position context[b] + 1 + path[b, t], t < accepted_len[b], and what lies
+ * behind is free.  A block that receives rows gets the largest of the scales that
+ * its rows (the moved ones, and those in front of context[b] + 1 that stay) had;
+ * entries become round(entry * old / new).
+ *   new_context [B] (optional, not `context` itself): context[b] + 1 +
+ *     accepted_len[b]; context[b] where nothing was accepted because the
+ *     sequence is padded or invalid (accepted_len[b] outside [0, max_depth], a
+ *     path that does not rise from at least 0, a position without a page, as
+ *     above): then nothing of it moves.
+ * SV_EUNSUPPORTED beyond SV_MAX_NODES (max_depth). */
+sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t* path, int max_depth,
+                                 const int32_t* accepted_len, const int32_t* page_table,
+                                 int64_t table_stride, int table_cols, const int32_t* context,
+                                 int32_t* new_context, int B, int device, void* cuda_stream);
+
+/* Attention of a step's rows over the cache, which holds their own keys and
+ * values already:
+ *   out[r, h] = sum_p softmax_p(scale * q[r, h] . K[p, h / G]) V[p, h / G]
+ * over the positions p that row r sees: those below context[b], the root's, and
+ * those of its path (parent as spec_verify_tree; NULL = chains: everything up to
+ * itself).  G = q_heads / heads.  Plain decoding is node_start = 0 throughout.
+ *   q, out: bfloat16, row r, head h at r * row + h * head, dim contiguous entries
+ *     each; q_row, q_head multiples of 8, q on a multiple of 16 bytes.  out must not
+ *     overlap q or the cache.
+ *   scale: finite.
+ *   workspace: device memory of spec_verify_attend_workspace(...) bytes, on a
+ *     multiple of 16, that no other call uses meanwhile; it holds parts of long
+ *     contexts until they are joined, and nothing between calls.
+ * Softmax statistics and sums are fp32; weights are rounded to eight significant
+ * bits, as bf16 weights would be.  What lies behind a sequence's last row does
+ * not matter, whatever it is; a row that sees a NaN becomes NaN.  So do the rows of a
+ * sequence with a page outside [0, pages) or a column outside the table among
+ * its positions or with a parent outside [-1, i).  Rows of padded sequences, and of a
+ * node range that leaves [0, total_nodes] or holds more than max_nodes nodes, are
+ * not written.  SV_EUNSUPPORTED beyond SV_MAX_NODES. */
+size_t spec_verify_attend_workspace(int heads, int q_heads, int dim, int max_nodes, int device);
+
+sv_status spec_verify_attend(const sv_cache* cache, const void* q, int64_t q_row, int64_t q_head,
+                             void* out, int64_t out_row, int64_t out_head, int q_heads, float scale,
+                             const int32_t* page_table, int64_t table_stride, int table_cols,
+                             const int32_t* context, const int32_t* node_start,
+                             const int32_t* parent, int B, int total_nodes, int max_nodes,
+                             void* workspace, size_t workspace_bytes, int device, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

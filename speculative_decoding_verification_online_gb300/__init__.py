@@ -17,5 +17,7 @@ from .spec_verify import (  # noqa: F401
     spec_verify_set_filters, spec_verify_set_gate_policy, spec_verify_status_string, run_noalloc,
     spec_verify_launches_per_filtered_run, ACTIVATIONS, SV_MAX_NODES, SV_WITH_REPLACEMENT, SV_WITHOUT_REPLACEMENT,
     SV_ACT_GELU, SV_ACT_GELU_TANH, SV_ACT_NONE, SV_ACT_RELU, SV_ACT_SILU, SV_ACT_SOFTCAP,
-    linear, softmax, verify_tree, spec_verify_linear, spec_verify_softmax, spec_verify_tree)
+    linear, softmax, verify_tree, spec_verify_linear, spec_verify_softmax, spec_verify_tree,
+    PagedCache, SvCache, attend_tree, cache_keep, cache_write, penalize, spec_verify_attend, spec_verify_attend_workspace,
+    spec_verify_cache_keep, spec_verify_cache_write, spec_verify_penalties)
 from .metrics import acceptance_summary, rule_id, summary_line  # noqa: F401,E402

@@ -1,0 +1,340 @@
+// Rows into a cache of 8-bit entries, and the rows of an accepted path together:
+// spec_verify_cache_write, spec_verify_cache_keep.
+//
+// Both are bound by memory, and by latency for the few rows of a step.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "cache.cuh"
+#include "entry.cuh"
+#include "spec_verify.h"
+
+namespace sv {
+namespace {
+
+constexpr int kWriteThreads = 128;
+constexpr int kWriteHeld = 8;  // runs of eight entries that a thread keeps between its two passes
+
+struct WriteParams {
+  CacheView c;
+  const void* x[2];
+  int64_t row[2], head[2];
+  int vec[2];
+  const int32_t *context, *node_start;
+  int total, max_nodes, blocks;  // blocks: of a sequence at most
+};
+
+template <typename T>
+struct Run;  // eight neighbouring entries as they lie in memory
+template <>
+struct Run<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, bool vec) {
+    if (vec) {
+      a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    } else {
+      a = make_float4(p[0], p[1], p[2], p[3]), b = make_float4(p[4], p[5], p[6], p[7]);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Run<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec) {
+    if (vec) {
+      a = *reinterpret_cast<const uint4*>(p);
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+      a = make_uint4(q[0] | static_cast<uint32_t>(q[1]) << 16, q[2] | static_cast<uint32_t>(q[3]) << 16,
+                     q[4] | static_cast<uint32_t>(q[5]) << 16, q[6] | static_cast<uint32_t>(q[7]) << 16);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+};
+
+// the largest finite magnitude
+__device__ __forceinline__ float largest(const float (&v)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(v[i]);
+    m = a < INFINITY ? fmaxf(m, a) : m;
+  }
+  return m;
+}
+
+// 2^ceil(log2(a / 448)), 2^-100 at least.  448 is 0.875 * 2^9, and a = f * 2^e with f in [1/2, 1).
+__device__ __forceinline__ float scale_for(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int e = static_cast<int>(u >> 23) - 126;
+  const int k = max(-100, (u & 0x7fffffu) <= 0x600000u ? e - 9 : e - 8);
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+__device__ __forceinline__ uint2 pack8(const float (&v)[8]) {
+  return make_uint2(e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16, e4m3x2(v[4], v[5]) | e4m3x2(v[6], v[7]) << 16);
+}
+
+// A CTA writes one block of tokens of one head, of k or of v.
+template <typename T>
+__global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_constant__ WriteParams P) {
+  __shared__ float warp_most[kWriteThreads / 32];
+  wait_for_stream();
+  const CacheView& c = P.c;
+  int at = blockIdx.x;
+  const int which = at & 1;
+  at >>= 1;
+  const int h = at % c.heads;
+  at /= c.heads;
+  const int j = at % P.blocks, b = at / P.blocks;
+  const int64_t context = P.context[b];
+  const int start = P.node_start[b], stop = P.node_start[b + 1];
+  if (context < 0 || start < 0 || stop < start || stop > P.total || stop - start > P.max_nodes) return;
+  const int size = 1 << c.block_log;
+  const int64_t end = context + (stop - start) + 1;  // behind the new rows
+  const int64_t p0 = ((context >> c.block_log) + j) << c.block_log;
+  if (p0 >= end) return;
+  const int page = c.page_of(b, p0);
+  if (page < 0) return;
+  const int64_t from = max(p0, context), to = min(p0 + size, end);
+  const int runs = c.dim / 8, count = static_cast<int>(to - from) * runs;
+  const T* x = static_cast<const T*>(P.x[which]) + (start + b + (from - context)) * P.row[which] + h * P.head[which];
+  float* scale = c.scales[which] + c.scale_at(page, h, p0);
+  const float old = from > p0 ? *scale : 0.f;
+  auto source = [&](int i) { return x + i / runs * P.row[which] + i % runs * 8; };
+  Run<T> held[kWriteHeld];
+  float most = 0.f, v[8];
+#pragma unroll
+  for (int k = 0; k < kWriteHeld; ++k) {
+    const int i = threadIdx.x + k * kWriteThreads;
+    if (i < count) held[k].load(source(i), P.vec[which]);
+  }
+#pragma unroll
+  for (int k = 0; k < kWriteHeld; ++k)
+    if (static_cast<int>(threadIdx.x) + k * kWriteThreads < count) {
+      held[k].values(v);
+      most = largest(v, most);
+    }
+  for (int i = threadIdx.x + kWriteHeld * kWriteThreads; i < count; i += kWriteThreads) {
+    Run<T> r;
+    r.load(source(i), P.vec[which]);
+    r.values(v);
+    most = largest(v, most);
+  }
+  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+  if (threadIdx.x % 32 == 0) warp_most[threadIdx.x / 32] = most;
+  __syncthreads();
+  for (int w = 0; w < kWriteThreads / 32; ++w) most = fmaxf(most, warp_most[w]);
+  const float need = scale_for(most);
+  const float now = from > p0 ? (need > old ? need : old) : need;
+  uint8_t* entries = c.entries[which] + c.entry_at(page, h, p0);
+  const float inverse = 1.f / now;
+  if (from > p0 && now != old) {
+    const int older = static_cast<int>(from - p0) * runs;
+    for (int i = threadIdx.x; i < older; i += kWriteThreads) {
+      uint2* p = reinterpret_cast<uint2*>(entries + i / runs * c.token + i % runs * 8);
+      const uint2 e = *p;
+      const uint32_t two[4] = {e.x & 0xffffu, e.x >> 16, e.y & 0xffffu, e.y >> 16};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = from_e4m3x2(two[k]);
+        v[2 * k] = f.x * old * inverse, v[2 * k + 1] = f.y * old * inverse;
+      }
+      *p = pack8(v);
+    }
+  }
+  auto put = [&](int i, const Run<T>& r) {
+    r.values(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inverse : NAN;
+    *reinterpret_cast<uint2*>(entries + (from - p0 + i / runs) * c.token + i % runs * 8) = pack8(v);
+  };
+#pragma unroll
+  for (int k = 0; k < kWriteHeld; ++k) {
+    const int i = threadIdx.x + k * kWriteThreads;
+    if (i < count) put(i, held[k]);
+  }
+  for (int i = threadIdx.x + kWriteHeld * kWriteThreads; i < count; i += kWriteThreads) {
+    Run<T> r;
+    r.load(source(i), P.vec[which]);
+    put(i, r);
+  }
+  if (threadIdx.x == 0) *scale = now;
+}
+
+// ------------------------------------------------------------ accepted rows
+
+struct KeepParams {
+  CacheView c;
+  const int32_t *path, *accepted, *context;
+  int32_t* new_context;
+  int max_depth, layers, B;
+};
+
+constexpr int kKeepThreads = 128;
+
+// A warp moves the rows of one sequence, head and layer, of k or of v.  path[t] >= t rises, so that rows in rising order
+// never lie where an earlier one was put: a block's sources are in blocks from its own on, whose scales and entries are
+// still the old ones when its turn comes.
+__global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams P) {
+  wait_for_stream();
+  const CacheView& c = P.c;
+  const int lane = threadIdx.x & 31;
+  int64_t at = (static_cast<int64_t>(blockIdx.x) * kKeepThreads + threadIdx.x) / 32;
+  const int which = static_cast<int>(at & 1);
+  at >>= 1;
+  const int h = static_cast<int>(at % c.heads);
+  at /= c.heads;
+  const int layer = static_cast<int>(at % P.layers), b = static_cast<int>(at / P.layers);
+  if (b >= P.B) return;
+  const int64_t context = P.context[b], first = context + 1;
+  const int len = P.accepted[b];
+  const int32_t* path = P.path + static_cast<int64_t>(b) * P.max_depth;
+  bool good = context >= 0 && len >= 0 && len <= P.max_depth;
+  const int size = 1 << c.block_log;
+  const int64_t p0 = first >> c.block_log << c.block_log;  // the first block that may receive rows
+  if (good) {
+    for (int t = lane; t < len; t += 32) {
+      const int node = path[t];
+      good &= node > (t ? path[t - 1] : -1) && c.page_of(b, first + node) >= 0 && c.page_of(b, first + t) >= 0;
+    }
+    good = __all_sync(~0u, good);
+  }
+  if (which == 0 && h == 0 && layer == 0 && lane == 0 && P.new_context)
+    P.new_context[b] = static_cast<int32_t>(good ? first + len : context);
+  if (!good || len == 0) return;
+  uint8_t* entries = c.entries[which] + layer * c.layer;
+  float* scales = c.scales[which] + layer * c.scale_layer;
+  const int per_row = c.dim / 16, rows_at_once = 32 / per_row;
+  const int mine = lane / per_row, byte = lane % per_row * 16;
+  for (int64_t block = p0; block < first + len; block += size) {
+    // rows of the block: source position of destination d
+    const int rows = static_cast<int>(min(static_cast<int64_t>(size), first + len - block));
+    auto source = [&](int d) {
+      const int64_t pos = block + d;
+      return pos < first ? pos : first + path[pos - first];
+    };
+    float most = 0.f;
+    for (int d = lane; d < rows; d += 32) {
+      const int64_t pos = source(d);
+      most = fmaxf(most, scales[c.scale_at(c.page_of(b, pos), h, pos)]);
+    }
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+    const int page = c.page_of(b, block);
+    const float own = scales[c.scale_at(page, h, block)];
+    const int begin = most == own ? static_cast<int>(max(first - block, int64_t{0})) : 0;  // rows that stay as they are
+    for (int d0 = begin; d0 < rows; d0 += rows_at_once) {
+      const int d = d0 + mine;
+      uint4 e = make_uint4(0, 0, 0, 0);
+      float f = 1.f;
+      if (d < rows) {
+        const int64_t pos = source(d);
+        const int pg = c.page_of(b, pos);
+        e = *reinterpret_cast<const uint4*>(entries + c.entry_at(pg, h, pos) + byte);
+        const float s = scales[c.scale_at(pg, h, pos)];
+        f = most > 0.f ? s / most : 1.f;
+      }
+      __syncwarp();
+      if (d < rows) {
+        if (f != 1.f) {
+          uint32_t w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 lo = from_e4m3x2(w[k] & 0xffffu), hi = from_e4m3x2(w[k] >> 16);
+            w[k] = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
+          }
+          e = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(entries + c.entry_at(page, h, block) + d * c.token + byte) = e;
+      }
+      __syncwarp();
+    }
+    if (lane == 0 && most != own) scales[c.scale_at(page, h, block)] = most;
+    __syncwarp();
+  }
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" sv_status spec_verify_cache_write(const sv_cache* cache, const void* k, const void* v, sv_dtype dt, int64_t k_row,
+                                             int64_t k_head, int64_t v_row, int64_t v_head, const int32_t* page_table,
+                                             int64_t table_stride, int table_cols, const int32_t* context,
+                                             const int32_t* node_start, int B, int total_nodes, int max_nodes, int device,
+                                             void* cuda_stream) {
+  if (sv_status s = sv::check_cache(cache, 1); s != SV_OK) return s;
+  if (sv_status s = sv::check_table(page_table, table_stride, table_cols, B); s != SV_OK) return s;
+  if (dt != SV_F32 && dt != SV_BF16) return SV_EINVAL;
+  if (B < 0 || total_nodes < 0 || max_nodes < 0) return SV_EINVAL;
+  if (k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0) return SV_EINVAL;
+  for (const int64_t s : {k_row, k_head, v_row, v_head})
+    if (s >= (int64_t{1} << 40)) return SV_EUNSUPPORTED;
+  if (B == 0) return SV_OK;
+  if (static_cast<int64_t>(total_nodes) + B > INT32_MAX) return SV_EUNSUPPORTED;
+  if (!k || !v || !context || !node_start) return SV_EINVAL;
+  const size_t es = dt == SV_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(k) % es || reinterpret_cast<uintptr_t>(v) % es || reinterpret_cast<uintptr_t>(context) % 4 ||
+      reinterpret_cast<uintptr_t>(node_start) % 4)
+    return SV_EINVAL;
+  if (cache->pages == 0) return SV_OK;
+  // max_nodes + 1 rows from any place in a block on
+  const int blocks =
+      static_cast<int>((std::min(max_nodes, total_nodes) + static_cast<int64_t>(cache->block) - 1) / cache->block) + 1;
+  const __int128 grid = static_cast<__int128>(blocks) * B * cache->heads * 2;
+  if (grid > INT32_MAX) return SV_EUNSUPPORTED;
+  sv::DeviceGuard g(device);
+  if (!g.ok) return SV_ECUDA;
+  sv::WriteParams P = {};
+  P.c = sv::view_of(*cache, page_table, table_stride, table_cols);
+  P.x[0] = k, P.x[1] = v;
+  P.row[0] = k_row, P.row[1] = v_row, P.head[0] = k_head, P.head[1] = v_head;
+  for (int i = 0; i < 2; ++i)
+    P.vec[i] = reinterpret_cast<uintptr_t>(P.x[i]) % 16 == 0 && P.row[i] * es % 16 == 0 && P.head[i] * es % 16 == 0;
+  P.context = context, P.node_start = node_start;
+  P.total = total_nodes, P.max_nodes = max_nodes;
+  P.blocks = blocks;
+  const auto kernel = dt == SV_BF16 ? sv::write_kernel<__nv_bfloat16> : sv::write_kernel<float>;
+  return sv::launch_waiting(kernel, static_cast<unsigned>(grid), sv::kWriteThreads, 0, 1, static_cast<cudaStream_t>(cuda_stream),
+                            P) == cudaSuccess
+             ? SV_OK
+             : SV_ECUDA;
+}
+
+extern "C" sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t* path, int max_depth,
+                                            const int32_t* accepted_len, const int32_t* page_table, int64_t table_stride,
+                                            int table_cols, const int32_t* context, int32_t* new_context, int B, int device,
+                                            void* cuda_stream) {
+  if (sv_status s = sv::check_cache(cache, 0); s != SV_OK) return s;
+  if (sv_status s = sv::check_table(page_table, table_stride, table_cols, B); s != SV_OK) return s;
+  if (B < 0 || max_depth < 0) return SV_EINVAL;
+  if (max_depth > SV_MAX_NODES) return SV_EUNSUPPORTED;
+  if (B == 0) return SV_OK;
+  if ((max_depth > 0 && !path) || !accepted_len || !context || context == new_context) return SV_EINVAL;
+  for (const void* p : {static_cast<const void*>(path), static_cast<const void*>(accepted_len),
+                        static_cast<const void*>(context), static_cast<const void*>(new_context)})
+    if (reinterpret_cast<uintptr_t>(p) % 4) return SV_EINVAL;
+  const __int128 warps = static_cast<__int128>(B) * cache->layers * cache->heads * 2;
+  const __int128 grid = (warps * 32 + sv::kKeepThreads - 1) / sv::kKeepThreads;
+  if (grid > INT32_MAX) return SV_EUNSUPPORTED;
+  sv::DeviceGuard g(device);
+  if (!g.ok) return SV_ECUDA;
+  sv::KeepParams P = {};
+  P.c = sv::view_of(*cache, page_table, table_stride, table_cols);
+  P.path = path, P.accepted = accepted_len, P.context = context, P.new_context = new_context;
+  P.max_depth = max_depth, P.layers = cache->layers, P.B = B;
+  return sv::launch_waiting(sv::keep_kernel, static_cast<unsigned>(grid), sv::kKeepThreads, 0, 1,
+                            static_cast<cudaStream_t>(cuda_stream), P) == cudaSuccess
+             ? SV_OK
+             : SV_ECUDA;
+}

@@ -44,6 +44,15 @@ inline bool sure_to_overlap(const Extent& a, const Extent& b) {
   return pa < pb + b.span() && pb < pa + a.span() && a.dense() && b.dense();
 }
 
+// rows of N values at g * group + m * row that never share a place
+inline bool rows_apart(int64_t row, int64_t group, int64_t M, int64_t groups, int64_t N) {
+  if (M == 1) return groups == 1 || group >= N;
+  if (groups == 1) return row >= N;
+  // strides below 2^40 times counts up to 2^30
+  const __int128 rows = static_cast<__int128>(row) * (M - 1) + N, all = static_cast<__int128>(group) * (groups - 1) + N;
+  return row <= group ? row >= N && group >= rows : group >= N && row >= all;
+}
+
 // A kernel's first step: everything before it in the stream is done and visible.
 // Then the next kernel may come in as CTAs leave (it waits here in its turn).
 __device__ __forceinline__ void wait_for_stream() {

@@ -1044,15 +1044,6 @@ sv_status launch_mma(const LinearParams& L, int device, int sms, cudaStream_t st
 bool valid_dtype(int d) { return d == SV_F32 || d == SV_BF16; }
 bool aligned_to(const void* p, int d) { return reinterpret_cast<uintptr_t>(p) % (d == SV_BF16 ? 2 : 4) == 0; }
 
-// rows of N values at g * group + m * row that never share a place
-bool rows_apart(int64_t row, int64_t group, int64_t M, int64_t groups, int64_t N) {
-  if (M == 1) return groups == 1 || group >= N;
-  if (groups == 1) return row >= N;
-  // strides below 2^40 times counts up to 2^30
-  const __int128 rows = static_cast<__int128>(row) * (M - 1) + N, all = static_cast<__int128>(group) * (groups - 1) + N;
-  return row <= group ? row >= N && group >= rows : group >= N && row >= all;
-}
-
 }  // namespace
 }  // namespace sv
 

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -88,6 +89,18 @@ def load() -> ctypes.CDLL:
     L.spec_verify_softmax.restype = I
     L.spec_verify_tree.argtypes = [P, I64, P, I64, I, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, P, P, I, P]
     L.spec_verify_tree.restype = I
+    L.spec_verify_penalties.argtypes = [P, I, I64, P, I, I64, I, P, I64, I, P, P, P, P, P, I, I, I, P, P, P, P, P, P, I, P,
+                                        I64, I, P, I, P]
+    L.spec_verify_penalties.restype = I
+    L.spec_verify_cache_write.argtypes = [P, P, P, I, I64, I64, I64, I64, P, I64, I, P, P, I, I, I, I, P]
+    L.spec_verify_cache_write.restype = I
+    L.spec_verify_cache_keep.argtypes = [P, P, I, P, P, I64, I, P, P, I, I, P]
+    L.spec_verify_cache_keep.restype = I
+    L.spec_verify_attend_workspace.argtypes = [I, I, I, I, I]
+    L.spec_verify_attend_workspace.restype = ctypes.c_size_t
+    L.spec_verify_attend.argtypes = [P, P, I64, I64, P, I64, I64, I, F, P, I64, I, P, P, P, I, I, I, P, ctypes.c_size_t, I,
+                                     P]
+    L.spec_verify_attend.restype = I
     _lib = L
     return L
 
@@ -200,6 +213,54 @@ def spec_verify_tree(p, p_stride, q, q_stride, draft_rows, node_start, tokens, p
     return load().spec_verify_tree(p, p_stride, q, q_stride, draft_rows, node_start, tokens, parent, draft_row,
                                    u_accept, u_pick, B, total_nodes, max_nodes, max_depth, V, siblings, accepted_len,
                                    out_tokens, path, accept_prob, flags, counters, device, stream)
+
+
+class SvCache(ctypes.Structure):
+    """sv_cache of include/spec_verify.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("scale_layer_stride", ctypes.c_int64), ("layers", ctypes.c_int),
+                ("pages", ctypes.c_int), ("heads", ctypes.c_int), ("page_tokens", ctypes.c_int), ("block", ctypes.c_int),
+                ("dim", ctypes.c_int)]
+
+
+def spec_verify_penalties(logits, dt, logits_stride, out, out_dt, out_stride, V, history, history_stride, history_cap,
+                          history_len, prompt_len, node_tokens, parent, node_start, B, total_nodes, max_nodes, repetition,
+                          frequency, presence, bias_start, bias_tokens, bias_values, total_biases, mask, mask_stride,
+                          mask_rows, mask_row, device, stream) -> int:
+    """Raw call of the penalties, biases and masks on logits rows; returns the status."""
+    return load().spec_verify_penalties(logits, dt, logits_stride, out, out_dt, out_stride, V, history, history_stride,
+                                        history_cap, history_len, prompt_len, node_tokens, parent, node_start, B,
+                                        total_nodes, max_nodes, repetition, frequency, presence, bias_start, bias_tokens,
+                                        bias_values, total_biases, mask, mask_stride, mask_rows, mask_row, device, stream)
+
+
+def spec_verify_cache_write(cache, k, v, dt, k_row, k_head, v_row, v_head, page_table, table_stride, table_cols, context,
+                            node_start, B, total_nodes, max_nodes, device, stream) -> int:
+    """Raw call that writes a step's rows into a cache (a pointer to SvCache); returns the status."""
+    return load().spec_verify_cache_write(cache, k, v, dt, k_row, k_head, v_row, v_head, page_table, table_stride,
+                                          table_cols, context, node_start, B, total_nodes, max_nodes, device, stream)
+
+
+def spec_verify_cache_keep(cache, path, max_depth, accepted_len, page_table, table_stride, table_cols, context, new_context,
+                           B, device, stream) -> int:
+    """Raw call that keeps the rows of the accepted paths; returns the status."""
+    return load().spec_verify_cache_keep(cache, path, max_depth, accepted_len, page_table, table_stride, table_cols, context,
+                                         new_context, B, device, stream)
+
+
+def spec_verify_attend_workspace(heads, q_heads, dim, max_nodes, device) -> int:
+    """Bytes of workspace of an attention call."""
+    return load().spec_verify_attend_workspace(heads, q_heads, dim, max_nodes, device)
+
+
+def spec_verify_attend(cache, q, q_row, q_head, out, out_row, out_head, q_heads, scale, page_table, table_stride, table_cols,
+                       context, node_start, parent, B, total_nodes, max_nodes, workspace, workspace_bytes, device,
+                       stream) -> int:
+    """Raw call of a step's attention over a cache; returns the status."""
+    return load().spec_verify_attend(cache, q, q_row, q_head, out, out_row, out_head, q_heads, scale, page_table,
+                                     table_stride, table_cols, context, node_start, parent, B, total_nodes, max_nodes,
+                                     workspace, workspace_bytes, device, stream)
 
 
 # ------------------------------------------------------ torch marshalling
@@ -415,6 +476,238 @@ def verify_tree(target_probs, draft_probs, tokens, parent, draft_row, node_start
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_tree")
     return out
+
+
+def penalize(logits, history, history_len, tokens, parent, node_start, prompt_len=None, repetition=None, frequency=None,
+             presence=None, bias=None, mask=None, mask_row=None, max_nodes=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and masks on logits rows, as ``spec_verify_penalties`` has them.
+
+    ``logits`` [nodes + B, V] (bfloat16 or float32, rows contiguous) holds each
+    sequence's root row, then its nodes' rows, as ``verify_tree`` takes them; a
+    row counts the tokens of ``history`` [B, cap] (int32; ``history_len`` [B] of
+    them, the first ``prompt_len`` [B] for ``repetition`` only) and of its own
+    path: ``tokens``, ``parent`` [nodes] (None: chains), ``node_start`` [B + 1].
+    ``repetition``, ``frequency``, ``presence``: float32 [B] or None.  ``bias``:
+    (start [B + 1], tokens, values) with int32, int32 and float32 entries.
+    ``mask`` [masks, >= V / 32] int32, a bit for each allowed token, for the row
+    itself or the one that ``mask_row`` [nodes + B] names (-1: none).  ``out``: the
+    results' tensor, may be ``logits`` (then only what changes is written);
+    default: a new one of the same type."""
+    dev = _cuda_device(logits, "logits")
+    i32, f32 = torch.int32, torch.float32
+    x_stride = _check_rows(logits, "logits", 2, None, dev)[0]
+    rows, V = logits.shape
+    B, total = history_len.shape[0], tokens.shape[0]
+    if rows != total + B:
+        raise ValueError(f"logits: {rows} rows, expected {total + B}")
+    h_stride = _check_rows(history, "history", 2, i32, dev)[0]
+    if history.shape[0] != B:
+        raise ValueError(f"history: {history.shape[0]} rows, expected {B}")
+    _check(history_len, "history_len", (B,), i32, dev)
+    _check(tokens, "tokens", (total,), i32, dev)
+    _check(node_start, "node_start", (B + 1,), i32, dev)
+    if parent is not None:
+        _check(parent, "parent", (total,), i32, dev)
+    if prompt_len is not None:
+        _check(prompt_len, "prompt_len", (B,), i32, dev)
+    for name, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+        if t is not None:
+            _check(t, name, (B,), f32, dev)
+    b_start = b_tokens = b_values = None
+    biases = 0
+    if bias is not None:
+        start, b_t, b_v = bias
+        biases = b_t.shape[0]
+        _check(start, "bias start", (B + 1,), i32, dev)
+        _check(b_t, "bias tokens", (biases,), i32, dev)
+        _check(b_v, "bias values", (biases,), f32, dev)
+        b_start, b_tokens, b_values = start.data_ptr(), b_t.data_ptr(), b_v.data_ptr()
+    m_ptr, m_stride, m_rows = None, 0, 0
+    if mask is not None:
+        m_stride = _check_rows(mask, "mask", 2, i32, dev)[0]
+        m_rows = mask.shape[0]
+        if mask.shape[1] < (V + 31) // 32:
+            raise ValueError(f"mask: rows of {mask.shape[1]} words, expected {(V + 31) // 32}")
+        if mask_row is None and m_rows != rows:
+            raise ValueError(f"mask: {m_rows} rows, expected {rows}")
+        m_ptr = mask.data_ptr()
+        if mask_row is not None:
+            _check(mask_row, "mask_row", (rows,), i32, dev)
+    elif mask_row is not None:
+        raise ValueError("mask_row: there is no mask")
+    if max_nodes is None:
+        max_nodes = min(total, SV_MAX_NODES)
+    if out is None:
+        out = _new(dev, stream, lambda: torch.empty(rows, V, dtype=logits.dtype, device=dev))
+    y_stride = _check_rows(out, "out", 2, None, dev)[0]
+    if out.shape != logits.shape:
+        raise ValueError(f"out: shape {tuple(out.shape)} != {tuple(logits.shape)}")
+    rc = spec_verify_penalties(
+        logits.data_ptr(), _dt(logits), x_stride, out.data_ptr(), _dt(out), y_stride, V, history.data_ptr(), h_stride,
+        history.shape[1], history_len.data_ptr(), _ptr(prompt_len), tokens.data_ptr(), _ptr(parent), node_start.data_ptr(),
+        B, total, max_nodes, _ptr(repetition), _ptr(frequency), _ptr(presence), b_start, b_tokens, b_values, biases, m_ptr,
+        m_stride, m_rows, _ptr(mask_row), dev.index, _stream(dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_penalties")
+    return out
+
+
+class PagedCache(NamedTuple):
+    """Keys and values in pages of 8-bit entries, with a scale for each block of tokens and head.
+
+    ``k``, ``v``: float8_e4m3fn [pages, heads, page tokens, dim], or with the
+    layers of a model in front; only the entries of a token have to be
+    contiguous, so that either of heads and tokens may be the inner one.
+    ``k_scale``, ``v_scale``: float32 [pages, heads, page tokens / block] of the
+    same layers, contiguous but for the layers.  A sequence's pages are named by its row of a page table."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def new(cls, pages, heads, page_tokens, dim, block=None, layers=None, device=None):
+        """An empty cache (its memory is not set); ``block`` tokens share a scale, by default a page's."""
+        lead = () if layers is None else (layers,)
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        shape, blocks = lead + (pages, heads), page_tokens // (page_tokens if block is None else block)
+        entries = [torch.empty(*shape, page_tokens, dim, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
+        scales = [torch.empty(*shape, blocks, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*entries, *scales)
+
+    def layer(self, i):
+        """The cache of one layer."""
+        return PagedCache(*(t[i] for t in self))
+
+
+def _cache(cache, dev, layered):
+    """sv_cache of (k, v, k_scale, v_scale), checked."""
+    k, v, ks, vs = cache
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    dim = len(k.shape)
+    if dim != 4 and not (layered and dim == 5):
+        raise ValueError(f"cache k: {dim} dimensions, expected {'4 or 5' if layered else 4}")
+    st = _check_rows(k, "cache k", dim, f8, dev)
+    if _check_rows(v, "cache v", dim, f8, dev) != st or v.shape != k.shape:
+        raise ValueError("cache v: shape and strides differ from those of k")
+    pages, heads, tokens, d = k.shape[-4:]
+    per = ks.shape[-1]
+    ss = _check_rows(ks, "cache k_scale", dim - 1, f32, dev)
+    if _check_rows(vs, "cache v_scale", dim - 1, f32, dev) != ss or vs.shape != ks.shape:
+        raise ValueError("cache v_scale: shape and strides differ from those of k_scale")
+    if ks.shape[:-1] != k.shape[:-2] or per < 1 or tokens % per:
+        raise ValueError(f"cache k_scale: shape {tuple(ks.shape)} does not go with k {tuple(k.shape)}")
+    if (heads > 1 and ss[-2] != per) or (pages > 1 and ss[-3] != heads * per):
+        raise ValueError("cache k_scale must be contiguous")
+    # a stride over one entry may be anything: it is not used
+    layers = k.shape[0] if dim == 5 else 1
+    return SvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), st[0] if layers > 1 else 0,
+                   st[-4] if pages > 1 else 0, st[-3] if heads > 1 else 0, st[-2] if tokens > 1 else d,
+                   ss[0] if layers > 1 else 0, layers, pages, heads, tokens, tokens // per, d)
+
+
+def _step(dev, page_table, context, node_start):
+    """Checks of a step's page table, contexts and node ranges; returns the table's pointer, stride and columns and B."""
+    i32 = torch.int32
+    stride = _check_rows(page_table, "page_table", 2, i32, dev)[0]
+    B, cols = page_table.shape
+    _check(context, "context", (B,), i32, dev)
+    if node_start is not None:
+        _check(node_start, "node_start", (B + 1,), i32, dev)
+    return page_table.data_ptr(), stride, cols, B
+
+
+def cache_write(cache, k, v, page_table, context, node_start, max_nodes=None, stream=None):
+    """Write a step's (or a prompt's) keys and values into the pages of a ``PagedCache``, in 8 bits.
+
+    ``k``, ``v`` [nodes + B, heads, dim] (bfloat16 or float32, entries contiguous):
+    each sequence's root row, then its nodes' rows, as ``verify_tree`` takes them;
+    they go to the positions ``context[b]``, ``context[b] + 1``, ...  ``page_table``
+    [B, columns], ``context`` [B] and ``node_start`` [B + 1] are int32.  A prompt
+    of n tokens is a sequence with n - 1 nodes.  ``max_nodes`` bounds a sequence's
+    nodes (default: the number of nodes).  How scales follow the entries:
+    ``spec_verify_cache_write`` in include/spec_verify.h."""
+    dev = _cuda_device(k, "k")
+    c = _cache(cache, dev, False)
+    table, t_stride, cols, B = _step(dev, page_table, context, node_start)
+    ks = _check_rows(k, "k", 3, None, dev)
+    vs = _check_rows(v, "v", 3, k.dtype, dev)
+    rows = k.shape[0]
+    if rows < B or k.shape[1:] != (c.heads, c.dim) or v.shape != k.shape:
+        raise ValueError(f"k, v: shapes {tuple(k.shape)}, {tuple(v.shape)}, expected (nodes + {B}, {c.heads}, {c.dim})")
+    if max_nodes is None:
+        max_nodes = rows - B
+    rc = spec_verify_cache_write(ctypes.byref(c), k.data_ptr(), v.data_ptr(), _dt(k), ks[0], ks[1], vs[0], vs[1], table,
+                                 t_stride, cols, context.data_ptr(), node_start.data_ptr(), B, rows - B, max_nodes, dev.index,
+                                 _stream(dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_cache_write")
+
+
+def cache_keep(cache, path, accepted_len, page_table, context, out=None, stream=None):
+    """Keep the cache's rows of the accepted drafts: ``path`` and ``accepted_len`` as ``verify_tree`` returns them.
+
+    In every layer of the cache (``PagedCache``, with or without layers in front)
+    the rows of a sequence's path move to the positions behind its root; what
+    lies behind them is free.  Returns the new contexts (``out``, or a new
+    tensor): ``context + 1 + accepted_len``; they are unchanged where nothing
+    could be kept (``spec_verify_cache_keep`` in include/spec_verify.h)."""
+    dev = _cuda_device(path, "path")
+    c = _cache(cache, dev, True)
+    table, t_stride, cols, B = _step(dev, page_table, context, None)
+    i32 = torch.int32
+    _check(path, "path", (B, path.shape[-1]), i32, dev)
+    _check(accepted_len, "accepted_len", (B,), i32, dev)
+    if out is None:
+        out = _new(dev, stream, lambda: torch.empty(B, dtype=i32, device=dev))
+    else:
+        _check(out, "out", (B,), i32, dev)
+    rc = spec_verify_cache_keep(ctypes.byref(c), path.data_ptr(), path.shape[1], accepted_len.data_ptr(), table, t_stride,
+                                cols, context.data_ptr(), out.data_ptr(), B, dev.index, _stream(dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_cache_keep")
+    return out
+
+
+def attend_tree(q, cache, page_table, context, node_start, parent=None, scale=None, max_nodes=None, out=None, stream=None):
+    """Attention of drafted rows over a ``PagedCache`` that holds their keys and values already (``cache_write``).
+
+    ``q`` [nodes + B, query heads, dim] (bfloat16, entries contiguous): each
+    sequence's root row, then its nodes' rows, as ``verify_tree`` takes them.  A
+    row sees the ``context[b]`` committed positions, the root and its path
+    (``parent`` [nodes]; None: chains).  Plain decoding has a ``node_start`` of
+    zeros.  ``scale``: of the logits, by default dim ** -0.5.  ``max_nodes``
+    bounds a sequence's nodes (default: the number of nodes, as far as
+    SV_MAX_NODES).  Returns bfloat16 rows shaped as ``q`` (``out``, or a new
+    tensor).  No gradient is recorded."""
+    dev = _cuda_device(q, "q")
+    bf16 = torch.bfloat16
+    c = _cache(cache, dev, False)
+    table, t_stride, cols, B = _step(dev, page_table, context, node_start)
+    qs = _check_rows(q, "q", 3, bf16, dev)
+    rows, q_heads, d = q.shape
+    if d != c.dim or rows < B:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (nodes + {B}, query heads, {c.dim})")
+    total = rows - B
+    if parent is not None:
+        _check(parent, "parent", (total,), torch.int32, dev)
+    if max_nodes is None:
+        max_nodes = min(total, SV_MAX_NODES)
+    if out is not None:
+        _check_rows(out, "out", 3, bf16, dev)
+        if out.shape != q.shape:
+            raise ValueError(f"out: shape {tuple(out.shape)} != {tuple(q.shape)}")
+    size = spec_verify_attend_workspace(c.heads, q_heads, d, max_nodes, dev.index)
+    new, work = _new(dev, stream, lambda: (torch.empty(q.shape, dtype=bf16, device=dev) if out is None else out,
+                                           torch.empty(size, dtype=torch.uint8, device=dev)))
+    os = new.stride()
+    rc = spec_verify_attend(ctypes.byref(c), q.data_ptr(), qs[0], qs[1], new.data_ptr(), os[0], os[1], q_heads,
+                            d ** -0.5 if scale is None else float(scale), table, t_stride, cols, context.data_ptr(),
+                            node_start.data_ptr(), _ptr(parent), B, total, max_nodes, work.data_ptr(), size, dev.index,
+                            _stream(dev, stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_attend")
+    return new
 
 
 class SpecVerifier:
