@@ -24,6 +24,10 @@ inline sv_status check_cache(const sv_cache* c, int layers) {
     if (s % 16) return SV_EINVAL;
     if (s >= (int64_t{1} << 40)) return SV_EUNSUPPORTED;
   }
+  // pages and heads that share their place
+  if ((c->pages > 1 && c->page_stride < c->dim) || (c->heads > 1 && c->head_stride < c->dim) ||
+      (c->layers > 1 && c->layer_stride < c->dim))
+    return SV_EINVAL;
   if (c->pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return SV_EINVAL;
   if (reinterpret_cast<uintptr_t>(c->k) % 16 || reinterpret_cast<uintptr_t>(c->v) % 16 ||
       reinterpret_cast<uintptr_t>(c->k_scale) % 4 || reinterpret_cast<uintptr_t>(c->v_scale) % 4)

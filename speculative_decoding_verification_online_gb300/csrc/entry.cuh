@@ -152,10 +152,10 @@ cudaError_t prepare_waiting(K kernel, unsigned threads, size_t smem, unsigned ct
 // The launch of a kernel that calls wait_for_stream, in clusters of `ctas`: it may
 // become resident while its predecessor drains.
 template <typename K, typename... A>
-cudaError_t launch_waiting(K kernel, unsigned grid, unsigned threads, size_t smem, unsigned ctas, cudaStream_t st,
+cudaError_t launch_waiting(K kernel, dim3 grid, unsigned threads, size_t smem, unsigned ctas, cudaStream_t st,
                            const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -168,6 +168,11 @@ class Cache:
             got.append(np.stack(rows, 1))
         return got
 
+    def value_scales(self, b, n):
+        """The values' scales of the first n positions: [heads, n]."""
+        places = [self.at(b, p) for p in range(n)]
+        return np.stack([self.scale[1][g, :, a // self.block] for g, a in places], 1)
+
     def attend(self, q, context, node_start, parent, scale):
         """Rows [.., query heads, dim], and the bound of what a call may be off by, entry by entry.
 
@@ -175,8 +180,9 @@ class Cache:
         of which cuts off less than 2^-23 of the sum of the magnitudes for each of its products and itself; three fp32
         products with the scales (2^-24 each) and the difference to the largest x (2^-24 of the largest magnitude) follow;
         a query entry may be off by 2^-10 steps where the largest is 224 or more, 2^-17.8 of it.  The exponential is off
-        by 2^-22.  A weight is rounded to eight bits (2^-8), or to 2^-10 where its tile's largest is 256 (2^-18 of it).
-        The sum of the weights is off by 2^-24 an addition.  At last the result is rounded to bf16."""
+        by 2^-22.  A weight times its value's scale is rounded to eight bits (2^-8), or to 2^-10 where its tile's largest such
+        product (with a scale of 2^-12 of the tile's largest at least, taken up to the next power of two) is 256 or more: 2^-17
+        of the largest product over all positions, with a scale of 2^-12 of the largest at least.  The sum of the weights is off by 2^-24 an addition.  At last the result is rounded to bf16."""
         q = doubles(q)
         start = ints(node_start)
         par = None if parent is None else ints(parent)
@@ -188,6 +194,7 @@ class Cache:
             lo, n = start[b], start[b + 1] - start[b]
             chain = list(range(-1, n - 1)) if par is None else [int(p) for p in par[lo:lo + n]]
             k, v = self.sequence(b, c + 1 + n)
+            sizes = self.value_scales(b, c + 1 + n)
             for i in range(n + 1):
                 seen = np.r_[np.arange(c + 1), c + 1 + np.array(sorted(path_of(chain, i)), dtype=int)]
                 for h in range(q.shape[1]):
@@ -202,8 +209,10 @@ class Cache:
                     p = w / w.sum()
                     o = p @ vv
                     d = np.minimum(d, 1.0)
-                    lost = p * (2.0 * d + 2.0 ** -8 + 2.0 ** -21) + 2.0 ** -18 * p.max()
-                    err = lost @ np.abs(vv) + (p @ (2 * d) + len(p) * 2.0 ** -24) * np.abs(o)
+                    size = sizes[h // group][seen]
+                    lost = p * (2.0 * d + 2.0 ** -8 + 2.0 ** -21)
+                    least = 2.0 ** -17 * np.max(p * np.maximum(size, size.max() * 2.0 ** -12))
+                    err = lost @ np.abs(vv) + least * (np.abs(vv) / size[:, None]).sum(0) + (p @ (2 * d) + len(p) * 2.0 ** -24) * np.abs(o)
                     out[lo + b + i, h] = o
                     off[lo + b + i, h] = err * 1.01 + (np.abs(o) + err) * 2.0 ** -8
         return out, off
