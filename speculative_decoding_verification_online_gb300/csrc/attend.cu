@@ -9,15 +9,21 @@
 // at twice the rate of bf16's, and nothing is converted but queries and weights.
 //
 // A key head's query rows (all rows of the step times the query heads of its group) are
-// the columns: up to kN of them make a block.  Positions are rows, 128 to a tile: thread
+// the columns: up to kN of them make a block, and one or two blocks a unit.  Positions are rows, 128 to a tile: thread
 // t of a warpgroup has position t of every column, so that a position's scale and
-// visibility are the thread's own.  The softmax is per tile: weights times their value's
-// scale stand against the tile's own largest such product (times 2^8, of the 448 that
-// e4m3 holds), so that what is small against another tile's does not fall below e4m3's
-// range; the tiles' sums are joined in fp32 registers.
+// visibility are the thread's own.
+//
+// A weight times its value's scale stands against a reference of its column, the largest
+// such product of a tile.  It is taken anew where a tile has one that is more than 445
+// times as large, and at every 16th tile if that tile's are all below 1/32 of it: those
+// in between have at most lost digits that weigh 2^-15 of what has been added before, and
+// what is small against other tiles' does not fall below e4m3's range.  Else a tile needs
+// no reduction: sums of weights stay with the threads until a segment ends, and the
+// products' sums in tensor memory.  Those of hi and lo are apart there, so that lo can be
+// held 2^5 times as large.
 //
 // Work is cut evenly over the SMs, whatever the lengths: all tiles of all units (sequence, key
-// head, two blocks of columns) in a row, a CTA taking the n-th part of them.  A unit that
+// head, columns) in a row, a CTA taking the n-th part of them.  A unit that
 // is cut leaves its parts in the workspace, and a second kernel joins them.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -37,11 +43,12 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 128;  // positions
-constexpr int kGroupThreads = 128;
+constexpr int kGroupThreads = 256;  // of a tile's softmax: a thread has one position of half of the columns
 constexpr int kAttendThreads = 128 + 2 * kGroupThreads;
-constexpr int kMaxStages = 8;
-constexpr int kAttendSmem = 226 * 1024;
-constexpr float kTop = 8.f;  // log2 of a tile's largest weight
+constexpr float kMost = 8.8f;  // log2 of the largest weight over the reference; 448 is 2^8.807
+constexpr float kLow = -5.f;   // log2 of what a tile's largest may have fallen to where the reference stays
+constexpr int kRefresh = 16;   // tiles of a group after which that is looked at
+constexpr float kDeep = 60.f;  // log2 of how far a reference may fall below the highest: what is below adds nothing
 
 struct AttendParams {
   CacheView c;
@@ -52,7 +59,7 @@ struct AttendParams {
   float scale;  // times log2(e)
   const int32_t *context, *node_start, *parent;
   int B, total, max_nodes;
-  int stages, boxes, box_tokens;  // boxes of a tile
+  int boxes, box_tokens;  // boxes of a tile
   int grid;                       // CTAs that share the tiles
   float* parts;
 };
@@ -70,7 +77,7 @@ struct Sequence {
   int64_t units, work;
 };
 
-template <int kN>
+template <int kColumns>  // of a unit
 __device__ __forceinline__ Sequence sequence_of(const AttendParams& P, int b) {
   Sequence s = {};
   s.context = P.context[b];
@@ -81,7 +88,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttendParams& P, int b) {
   s.lost = s.end > static_cast<int64_t>(P.c.table_cols) << P.c.page_log;
   s.tiles = s.lost ? 1 : static_cast<int>((s.end + kTile - 1) / kTile);
   s.cols = (s.nodes + 1) * P.group;
-  s.pairs = (s.cols + 2 * kN - 1) / (2 * kN);
+  s.pairs = (s.cols + kColumns - 1) / kColumns;
   s.units = static_cast<int64_t>(P.c.heads) * s.pairs;
   s.work = s.units * s.tiles;
   return s;
@@ -96,13 +103,13 @@ struct Start {
 };
 
 // Where tile `at(total)` of all lies; every thread of the CTA calls it.
-template <int kN, typename F>
+template <int kColumns, typename F>
 __device__ __forceinline__ void find_tile(const AttendParams& P, F&& at, Start* s, int64_t* warp_sums) {
   const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (P.B + threads - 1) / threads;
   const int lo = min(P.B, static_cast<int>(threadIdx.x) * per), hi = min(P.B, lo + per);
   int64_t mine = 0;
-  for (int b = lo; b < hi; ++b) mine += sequence_of<kN>(P, b).work;
+  for (int b = lo; b < hi; ++b) mine += sequence_of<kColumns>(P, b).work;
   int64_t sum = mine;
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t u = __shfl_up_sync(~0u, sum, o);
@@ -120,7 +127,7 @@ __device__ __forceinline__ void find_tile(const AttendParams& P, F&& at, Start* 
   __syncthreads();
   if (tile >= base && tile < base + mine) {
     for (int b = lo; b < hi; ++b) {
-      const int64_t w = sequence_of<kN>(P, b).work;
+      const int64_t w = sequence_of<kColumns>(P, b).work;
       if (tile < base + w) {
         s->b = b, s->off = tile - base;
         break;
@@ -138,7 +145,7 @@ struct Segment {
   bool two, whole_front, whole;  // two blocks of columns; from the unit's first tile on; all of the unit's tiles
 };
 
-template <int kN>
+template <int kN, int kBlocks>
 struct Walk {
   const AttendParams& P;
   int64_t pos, hi, off;
@@ -154,17 +161,17 @@ struct Walk {
     while (!loaded || off >= s.work) {
       if (loaded) ++b, off = 0;
       if (b >= P.B) return false;
-      s = sequence_of<kN>(P, b);
+      s = sequence_of<kN * kBlocks>(P, b);
       loaded = true;
     }
     const int64_t unit = off / s.tiles;
     g.s = s, g.b = b;
     g.h = static_cast<int>(unit / s.pairs);
-    g.c0 = static_cast<int>(unit % s.pairs) * 2 * kN;
+    g.c0 = static_cast<int>(unit % s.pairs) * kN * kBlocks;
     g.t0 = static_cast<int>(off - unit * s.tiles);
     const int64_t left = hi - pos, here = s.tiles - g.t0, n = left < here ? left : here;
     g.t1 = g.t0 + static_cast<int>(n);
-    g.two = s.cols - g.c0 > kN;
+    g.two = kBlocks == 2 && s.cols - g.c0 > kN;
     g.whole_front = g.t0 == 0;
     g.whole = g.t0 == 0 && g.t1 == s.tiles;
     pos += n, off += n;
@@ -204,27 +211,69 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// kCols columns of this warp's 32 lanes
+// kCols columns (8, or a multiple of 16) of this warp's 32 lanes
 template <int kCols>
 __device__ __forceinline__ void tc_load(uint32_t addr, float (&f)[kCols]) {
-#pragma unroll
-  for (int c = 0; c < kCols; c += 16)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=f"(f[c]), "=f"(f[c + 1]), "=f"(f[c + 2]), "=f"(f[c + 3]), "=f"(f[c + 4]), "=f"(f[c + 5]), "=f"(f[c + 6]),
-          "=f"(f[c + 7]), "=f"(f[c + 8]), "=f"(f[c + 9]), "=f"(f[c + 10]), "=f"(f[c + 11]), "=f"(f[c + 12]),
-          "=f"(f[c + 13]), "=f"(f[c + 14]), "=f"(f[c + 15])
-        : "r"(addr + c)
-        : "memory");
-#pragma unroll
-  for (int c = 0; c < kCols; c += 16)
+  if constexpr (kCols == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                 : "r"(addr)
+                 : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(f[c]), "+f"(f[c + 1]), "+f"(f[c + 2]), "+f"(f[c + 3]), "+f"(f[c + 4]), "+f"(f[c + 5]),
-                   "+f"(f[c + 6]), "+f"(f[c + 7]), "+f"(f[c + 8]), "+f"(f[c + 9]), "+f"(f[c + 10]), "+f"(f[c + 11]),
-                   "+f"(f[c + 12]), "+f"(f[c + 13]), "+f"(f[c + 14]), "+f"(f[c + 15])
+                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7])
                  :
                  : "memory");
+  } else {
+#pragma unroll
+    for (int c = 0; c < kCols; c += 16)
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+          "%15}, [%16];"
+          : "=f"(f[c]), "=f"(f[c + 1]), "=f"(f[c + 2]), "=f"(f[c + 3]), "=f"(f[c + 4]), "=f"(f[c + 5]), "=f"(f[c + 6]),
+            "=f"(f[c + 7]), "=f"(f[c + 8]), "=f"(f[c + 9]), "=f"(f[c + 10]), "=f"(f[c + 11]), "=f"(f[c + 12]),
+            "=f"(f[c + 13]), "=f"(f[c + 14]), "=f"(f[c + 15])
+          : "r"(addr + c)
+          : "memory");
+#pragma unroll
+    for (int c = 0; c < kCols; c += 16)
+      asm volatile("tcgen05.wait::ld.sync.aligned;"
+                   : "+f"(f[c]), "+f"(f[c + 1]), "+f"(f[c + 2]), "+f"(f[c + 3]), "+f"(f[c + 4]), "+f"(f[c + 5]),
+                     "+f"(f[c + 6]), "+f"(f[c + 7]), "+f"(f[c + 8]), "+f"(f[c + 9]), "+f"(f[c + 10]), "+f"(f[c + 11]),
+                     "+f"(f[c + 12]), "+f"(f[c + 13]), "+f"(f[c + 14]), "+f"(f[c + 15])
+                   :
+                   : "memory");
+  }
+}
+
+// eight columns back
+__device__ __forceinline__ void tc_store(uint32_t addr, const float (&f)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(f[0]), "f"(f[1]), "f"(f[2]),
+               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "r"(addr)
+               : "memory");
+}
+
+// Two floats in a 64-bit register: one instruction for both, each rounded by itself.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void both(Two t, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(t)); }
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // Operands in shared memory (all of their offsets in units of 16 bytes).
@@ -242,14 +291,46 @@ __device__ __forceinline__ uint64_t weights_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (8ull << 16) | (128ull << 32) | (1ull << 46);
 }
 
+// mbar_wait in fewer instructions: the loops of all warps together should stay in the instruction caches.
+__device__ __forceinline__ void wait_for(uint64_t* bar, unsigned parity, volatile int* dead) {
+  if (mbar_try(bar, parity)) return;
+  unsigned since, t;
+  asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(since));
+#pragma unroll 1
+  while (!mbar_try(bar, parity)) {
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+    if (t - since > 2000000000u || *dead) {
+      *dead = 1;
+      return;
+    }
+  }
+}
+
 __device__ __forceinline__ float power(float x) {  // 2^x; results below 2^-126 become 0
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
-// Each column's largest, or sum, over a warp's lanes: halves of the columns change hands until a lane has its own.  Of 32
-// columns lane i gets column i; of 16 column i / 2.
+// Two numbers that are not negative, times 32, as e4m3 numbers hi + lo / 32: hi is the nearest one, lo what is left.  They pass
+// through fp16's eleven bits.
+__device__ __forceinline__ void split2(Two w, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  both(w, a, b);
+  uint32_t h, back, rest;
+  uint16_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(0x28002800u));  // 1 / 32
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(rest));
+  hi = r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(r));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(rest) : "r"(back), "r"(0xd000d000u), "r"(h));  // -32
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(rest));
+  lo = r;
+}
+
+// Each column's largest, or sum, over a warp's lanes: halves of the columns change hands until a lane has its own.  Of kCols
+// columns lane i gets column i / (32 / kCols).
 template <int kCols, bool kSum>
 __device__ __forceinline__ float over_lanes(const float* f) {
   const int lane = threadIdx.x & 31;
@@ -277,24 +358,27 @@ __device__ __forceinline__ float over_lanes(const float* f) {
   return v[0];
 }
 
-template <int kN>
+// Tiles of K and of V have rings of their own: K's is free after the first product, V's after the second.
+template <int kN, int kBlocks, int kD>
 struct AttendShared {
-  static constexpr int kWords = kN > 32 ? kN / 32 : 1;  // of a block's visibility
-  // of a position: the scale of K; a power of two c that is not below the scale of V over the tile's largest (but 2^-12 at
-  // least) as log2 c and 1 / c; the rest of that scale, over c
-  float4 factor[kMaxStages][kTile];
-  uint32_t seen[kMaxStages][kTile][2 * kWords];
-  float vmost[kMaxStages];
-  int special[kMaxStages];
-  float most[2][4][kN];                    // a warp's largest logits, and at last its sums
-  float ref[2][kN];                        // what a tile's logits stand against
-  float keep[2][kN], take[2][kN];          // factors of the sums so far and of the tile's
-  float row[2][kN];                        // of a query row: its power of two, the softmax's scale
+  static constexpr int kK = kD == 64 ? 10 : 5, kV = kD == 64 ? 12 : 6;
+  static constexpr int kWords = (kBlocks * kN + 31) / 32;  // of a unit's columns
+  // of a special tile's positions: the columns that see it; whether what they see is no number
+  uint32_t seen[kV][kTile][kWords];
+  uint32_t none[kV][kTile / 32];
+  float most[2][4][kN];  // a warp's largest logits, and at last its sums
+  float ref[2][kN];      // references, negative
+  float step[2][kN];     // how far a reference moved
+  float keep[2][kN];     // what the sums so far are worth against the new one
+  float take[kN];
+  float row[kBlocks][kN];    // of a query row: its power of two, the softmax's scale
+  int64_t out[kBlocks][kN];  // where its result goes
   float m[2][kN];
-  float lsum[kN];
-  uint32_t path[2][SV_MAX_NODES][2 * kWords];
-  int parent[2][SV_MAX_NODES];
-  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
+  uint32_t moved[2], unset[2];  // of a group: columns whose sums have to be multiplied, that have no reference yet
+  float anchors[2][4];  // of a group's warps
+  uint32_t path[SV_MAX_NODES][kWords];
+  int parent[SV_MAX_NODES];
+  uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV], ready[kV];
   uint64_t s_full[2], s_free[2], p_full[2], o_full[2], q_full;
   int64_t warp_sums[kAttendThreads / 32];
   Start start;
@@ -302,19 +386,30 @@ struct AttendShared {
   volatile int dead;
 };
 
-template <int kN, int kD>
+template <int kN, int kBlocks, int kD>
 struct Sizes {
-  static constexpr int kTileBytes = kTile * kD, kStageBytes = 2 * kTileBytes;
+  using Shared = AttendShared<kN, kBlocks, kD>;
+  static constexpr int kTileBytes = kTile * kD;
   static constexpr int kQ = kN * kD, kWeights = kTile * kN;  // one of the two numbers of a block's entries
-  static constexpr int kFixed = 1024 + 4 * kQ + 4 * kWeights;
-  static constexpr int kFits = (kAttendSmem - 1024 - static_cast<int>(sizeof(AttendShared<kN>)) - kFixed) / kStageBytes;
-  static constexpr int kStages = kFits < kMaxStages ? kFits : kMaxStages;
-  static constexpr int kPart = 2 * kN * (kD + 2);  // floats of a part in the workspace
-  static_assert(kStages >= 3);
+  static constexpr int kColumns = kBlocks * kN;              // of a unit
+  static constexpr int kSmem = static_cast<int>(sizeof(Shared)) + 1024 + (Shared::kK + Shared::kV) * kTileBytes +
+                               2 * kBlocks * kQ + 4 * kWeights;
+  static constexpr int kPart = kColumns * (kD + 2);  // floats of a part in the workspace
+  static_assert(kSmem <= 227 * 1024);
 };
 
-__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
-__device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory"); }
+// whether any thread of a group says so
+__device__ __forceinline__ bool group_any(int group, bool mine) {
+  unsigned any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"(static_cast<unsigned>(mine)), "r"(1 + group)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 3, 512;" ::: "memory"); }
 
 // smallest power of two that brings values of up to `a` to 448 at most (2^-100 at least)
 __device__ __forceinline__ float power_for(float a) {
@@ -330,43 +425,46 @@ __device__ __forceinline__ bool holds_nan(uint4 e) {
   return (hit(e.x) | hit(e.y) | hit(e.z) | hit(e.w)) != 0;
 }
 
-template <int kN, int kD>
+template <int kN, int kBlocks, int kD>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendParams P,
                                                                    const __grid_constant__ Maps maps) {
-  using Z = Sizes<kN, kD>;
-  using Shared = AttendShared<kN>;
-  constexpr int kWords = Shared::kWords, kWordCols = kN < 32 ? kN : 32;
-  extern __shared__ uint8_t raw[];
-  __shared__ __align__(16) Shared s;
-  uint8_t* const base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-  uint8_t* const tiles = base;                                   // stages: K, V
-  uint8_t* const queries = tiles + P.stages * Z::kStageBytes;    // [block][hi, lo]
-  uint8_t* const weights = queries + 4 * Z::kQ;                  // [warpgroup][hi, lo]
+  using Z = Sizes<kN, kBlocks, kD>;
+  using Shared = AttendShared<kN, kBlocks, kD>;
+  constexpr int kWords = Shared::kWords;
+  constexpr unsigned kK = Shared::kK, kV = Shared::kV;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& s = *reinterpret_cast<Shared*>(raw);
+  uint8_t* const base = raw + sizeof(Shared) + ((1024 - (smem_addr(raw + sizeof(Shared)) & 1023)) & 1023);
+  uint8_t* const tiles_k = base;
+  uint8_t* const tiles_v = tiles_k + kK * Z::kTileBytes;
+  uint8_t* const queries = tiles_v + kV * Z::kTileBytes;            // [block][hi, lo]
+  uint8_t* const weights = queries + 2 * kBlocks * Z::kQ;       // [warpgroup][hi, lo]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < P.stages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.ready[i], 1), mbar_init(&s.empty[i], 1);
+    for (unsigned i = 0; i < kK; ++i) mbar_init(&s.k_full[i], 1), mbar_init(&s.k_empty[i], 1);
+    for (unsigned i = 0; i < kV; ++i) mbar_init(&s.v_full[i], 1), mbar_init(&s.v_empty[i], 1), mbar_init(&s.ready[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&s.s_full[i], 1), mbar_init(&s.s_free[i], 4), mbar_init(&s.p_full[i], 4), mbar_init(&s.o_full[i], 1);
-    mbar_init(&s.q_full, 8);
+      mbar_init(&s.s_full[i], 1), mbar_init(&s.s_free[i], 8), mbar_init(&s.p_full[i], 8), mbar_init(&s.o_full[i], 1);
+    mbar_init(&s.q_full, 16);
     s.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)), "n"(4 * kN)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)), "n"(8 * kN)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   wait_for_stream();
   int64_t lo = 0;
-  find_tile<kN>(P, [&](int64_t total) { return cut(total, blockIdx.x, P.grid); }, &s.start, s.warp_sums);
+  find_tile<Z::kColumns>(P, [&](int64_t total) { return cut(total, blockIdx.x, P.grid); }, &s.start, s.warp_sums);
   tc_before();
   __syncthreads();
   tc_after();
   const Start start = s.start;
   lo = cut(start.total, blockIdx.x, P.grid);
   const int64_t hi = cut(start.total, blockIdx.x + 1, P.grid);
-  const uint32_t tmem = s.tmem;  // S of the two groups, then O
-  Walk<kN> walk(P, start, lo, hi);
+  const uint32_t tmem = s.tmem;  // S of the two groups (kN columns each), then O (2 kN: of hi, of lo)
+  Walk<kN, kBlocks> walk(P, start, lo, hi);
   Segment g;
   if (warp == 0) {
     // ---- tiles by TMA, a lane for each of a tile's boxes
@@ -380,196 +478,201 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       };
       int page = page_at(g.t0);
       for (int t = g.t0; t < g.t1; ++t, ++count) {
-        const int st = count % P.stages;
         const int next = page_at(t + 1);
-        if (count >= static_cast<unsigned>(P.stages)) mbar_wait(&s.empty[st], (count / P.stages - 1) & 1, &s.dead);
-        if (lane == 0) mbar_expect(&s.full[st], Z::kStageBytes);
+        const int token = static_cast<int>((static_cast<int64_t>(t) * kTile + lane * P.box_tokens) & ((1 << P.c.page_log) - 1));
+        const unsigned a = count % kK, b = count % kV;
+        if (count >= kK) wait_for(&s.k_empty[a], (count / kK - 1) & 1, &s.dead);
+        if (lane == 0) mbar_expect(&s.k_full[a], Z::kTileBytes);
         __syncwarp();
-        if (lane < P.boxes) {
-          const int token = static_cast<int>((static_cast<int64_t>(t) * kTile + lane * P.box_tokens) & ((1 << P.c.page_log) - 1));
-          const uint32_t to = smem_addr(tiles + st * Z::kStageBytes) + lane * P.box_tokens * kD;
-          tma_load(&maps.k, to, &s.full[st], token, g.h, page);
-          tma_load(&maps.v, to + Z::kTileBytes, &s.full[st], token, g.h, page);
-        }
+        if (lane < P.boxes)
+          tma_load(&maps.k, smem_addr(tiles_k + a * Z::kTileBytes) + lane * P.box_tokens * kD, &s.k_full[a], token, g.h, page);
+        if (count >= kV) wait_for(&s.v_empty[b], (count / kV - 1) & 1, &s.dead);
+        if (lane == 0) mbar_expect(&s.v_full[b], Z::kTileBytes);
+        __syncwarp();
+        if (lane < P.boxes)
+          tma_load(&maps.v, smem_addr(tiles_v + b * Z::kTileBytes) + lane * P.box_tokens * kD, &s.v_full[b], token, g.h, page);
         page = next;
       }
     }
   } else if (warp == 1) {
-    // ---- products
-    constexpr unsigned kQk = (1u << 4) | (static_cast<unsigned>(kN / 8) << 17) | (8u << 24);
-    constexpr unsigned kPv =
-        (1u << 4) | (1u << 15) | (1u << 16) | (static_cast<unsigned>(kN / 8) << 17) | (static_cast<unsigned>(kD / 16) << 24);
-    unsigned count = 0, segment = 0, done[2] = {0, 0}, asked[2] = {0, 0};
+    // ---- products with K
+    constexpr unsigned kShape = (1u << 4) | (static_cast<unsigned>(kN / 8) << 17) | (8u << 24);
+    unsigned count = 0, segment = 0, asked[2] = {0, 0};
     while (walk.next(g)) {
-      mbar_wait(&s.q_full, segment++ & 1, &s.dead);
+      wait_for(&s.q_full, segment++ & 1, &s.dead);
       const int items = (g.t1 - g.t0) << (g.two ? 1 : 0);
-      for (int i = 0; i <= items; ++i) {
-        if (i < items) {
-          const int w = i & 1, tile = g.two ? i / 2 : i;
-          const unsigned n = count + tile, st = n % P.stages;
-          if (!g.two || w == 0) {
-            mbar_wait(&s.full[st], n / P.stages & 1, &s.dead);
-            mbar_wait(&s.ready[st], n / P.stages & 1, &s.dead);
-          }
-          if (asked[w] > 0) mbar_wait(&s.s_free[w], (asked[w] - 1) & 1, &s.dead);
-          ++asked[w];
-          tc_after();
-          const uint64_t k = rows_desc<kD>(smem_addr(tiles + st * Z::kStageBytes));
-          const uint64_t q = rows_desc<kD>(smem_addr(queries + (g.two ? w : 0) * 2 * Z::kQ));
-          if (elect_one()) {
+      for (int i = 0; i < items; ++i) {
+        const int w = i & 1;
+        const unsigned n = count + (g.two ? i / 2 : i), st = n % kK;
+        if (!g.two || w == 0) wait_for(&s.k_full[st], n / kK & 1, &s.dead);
+        if (asked[w] > 0) wait_for(&s.s_free[w], (asked[w] - 1) & 1, &s.dead);
+        ++asked[w];
+        tc_after();
+        const uint64_t k = rows_desc<kD>(smem_addr(tiles_k + st * Z::kTileBytes));
+        const uint64_t q = rows_desc<kD>(smem_addr(queries + (g.two ? w : 0) * 2 * Z::kQ));
+        if (elect_one()) {
 #pragma unroll
-            for (int piece = 0; piece < 2; ++piece)
+          for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
-              for (int d = 0; d < kD / 32; ++d)
-                tc_mma(tmem + w * kN, k + 2 * d, q + piece * (Z::kQ / 16) + 2 * d, kQk, piece + d > 0);
-            tc_commit(&s.s_full[w]);
-          }
-          __syncwarp();
+            for (int d = 0; d < kD / 32; ++d)
+              tc_mma(tmem + w * kN, k + 2 * d, q + piece * (Z::kQ / 16) + 2 * d, kShape, piece + d > 0);
+          tc_commit(&s.s_full[w]);
+          if (!g.two || w == 1) tc_commit(&s.k_empty[st]);
         }
-        if (i > 0) {
-          const int j = i - 1, w = j & 1, tile = g.two ? j / 2 : j;
-          const unsigned n = count + tile, st = n % P.stages;
-          mbar_wait(&s.p_full[w], done[w]++ & 1, &s.dead);
-          tc_after();
-          const uint64_t v = rows_desc<kD>(smem_addr(tiles + st * Z::kStageBytes + Z::kTileBytes));
-          const uint64_t p = weights_desc(smem_addr(weights + w * 2 * Z::kWeights));
-          if (elect_one()) {
-#pragma unroll
-            for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-              for (int t = 0; t < kTile / 32; ++t)
-                tc_mma(tmem + (2 + w) * kN, v + t * (32 * kD / 16), p + piece * (Z::kWeights / 16) + t * 32, kPv, piece + t > 0);
-            tc_commit(&s.o_full[w]);
-            if (!g.two || w == 1) tc_commit(&s.empty[st]);
-          }
-          __syncwarp();
-        }
+        __syncwarp();
       }
       count += g.t1 - g.t0;
     }
-  } else if (warp < 4) {
-    // ---- scales and visibility of a tile's positions, by turns
-    const int me = warp - 2;
+  } else if (warp == 2) {
+    // ---- products with V
+    constexpr unsigned kShape =
+        (1u << 4) | (1u << 15) | (1u << 16) | (static_cast<unsigned>(2 * kN / 8) << 17) | (static_cast<unsigned>(kD / 16) << 24);
+    unsigned count = 0, done[2] = {0, 0};
+    while (walk.next(g)) {
+      const int items = (g.t1 - g.t0) << (g.two ? 1 : 0);
+      for (int i = 0; i < items; ++i) {
+        const int w = i & 1;
+        const unsigned n = count + (g.two ? i / 2 : i), st = n % kV;
+        if (!g.two || w == 0) wait_for(&s.v_full[st], n / kV & 1, &s.dead);
+        wait_for(&s.p_full[w], done[w]++ & 1, &s.dead);
+        tc_after();
+        const uint64_t v = rows_desc<kD>(smem_addr(tiles_v + st * Z::kTileBytes));
+        const uint64_t p = weights_desc(smem_addr(weights + w * 2 * Z::kWeights));
+        if (elect_one()) {
+#pragma unroll
+          for (int t = 0; t < kTile / 32; ++t)
+            tc_mma(tmem + (2 + 2 * w) * kN, v + t * (32 * kD / 16), p + t * 32, kShape,
+                   i > 1 || t > 0);  // a group's first item of a segment begins its sums
+          tc_commit(&s.o_full[w]);
+          if (!g.two || w == 1) tc_commit(&s.v_empty[st]);
+        }
+        __syncwarp();
+      }
+      count += g.t1 - g.t0;
+    }
+  } else if (warp == 3) {
+    // ---- visibility of the positions of special tiles, those with drafted positions or with the sequence's end
     unsigned count = 0;
     while (walk.next(g)) {
       bool built = false, bad = false;
       for (int t = g.t0; t < g.t1; ++t, ++count) {
-        if ((count & 1) != static_cast<unsigned>(me)) continue;
-        const int st = count % P.stages;
+        const unsigned st = count % kV;
         const int64_t p0 = static_cast<int64_t>(t) * kTile;
         const bool special = g.s.lost || p0 + kTile > g.s.context + 1;
-        float kf[4], vf[4];
-        bool none[4];  // no page
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t pos = p0 + lane + 32 * i;
-          kf[i] = vf[i] = 0.f;
-          none[i] = g.s.lost;
-          if (!g.s.lost && pos < g.s.end) {
-            const int page = P.c.page_of(g.b, pos);
-            none[i] = page < 0;
-            if (page >= 0) {
-              const int64_t at = P.c.scale_at(page, g.h, pos);
-              kf[i] = P.c.scales[0][at], vf[i] = P.c.scales[1][at];
-            }
-          }
-        }
-        float most = fmaxf(fmaxf(vf[0], vf[1]), fmaxf(vf[2], vf[3]));
-        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
         if (special && !built && !g.s.lost && P.parent) {
-          // rows of the path of each node's column
+          // the columns whose path a node is on
           built = true;
-          __syncwarp();
           for (int i = lane; i < g.s.nodes; i += 32) {
             const int up = P.parent[g.s.start + i];
             bad |= up < -1 || up >= i;
-            s.parent[me][i] = up;
+            s.parent[i] = up;
 #pragma unroll
-            for (int w = 0; w < 2 * kWords; ++w) s.path[me][i][w] = 0;
+            for (int w = 0; w < kWords; ++w) s.path[i][w] = 0;
           }
           bad = __any_sync(~0u, bad);
           __syncwarp();
-          const int last = min(g.s.nodes, (g.c0 + 2 * kN - 1) / P.group);
+          const int last = min(g.s.nodes, (g.c0 + Z::kColumns - 1) / P.group);
           for (int i = g.c0 / P.group + lane; !bad && i <= last; i += 32) {
             const int from = i * P.group - g.c0, to = from + P.group;
-            for (int node = i - 1; node >= 0; node = s.parent[me][node])
+            for (int node = i - 1; node >= 0; node = s.parent[node])
 #pragma unroll
-              for (int w = 0; w < 2 * kWords; ++w) {
-                const int a = max(0, from - w * kWordCols), e = min(kWordCols, to - w * kWordCols);
-                if (e > a) atomicOr(&s.path[me][node][w], (e - a == 32 ? ~0u : ((1u << (e - a)) - 1u)) << a);
+              for (int w = 0; w < kWords; ++w) {
+                const int a = max(0, from - w * 32), e = min(32, to - w * 32);
+                if (e > a) atomicOr(&s.path[node][w], (e - a == 32 ? ~0u : ((1u << (e - a)) - 1u)) << a);
               }
           }
           __syncwarp();
         }
-        if (count >= static_cast<unsigned>(P.stages)) mbar_wait(&s.empty[st], (count / P.stages - 1) & 1, &s.dead);
-        if (special) mbar_wait(&s.full[st], count / P.stages & 1, &s.dead);
-        uint8_t* const v = tiles + st * Z::kStageBytes + Z::kTileBytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = lane + 32 * i;
-          if (special) {
+        wait_for(&s.v_full[st], count / kV & 1, &s.dead);
+        if (special) {
+          uint8_t* const v = tiles_v + st * Z::kTileBytes;
+#pragma unroll 1
+          for (int i = 0; i < kTile / 32; ++i) {
+            const int at = lane + 32 * i;
             const int64_t pos = p0 + at, node = pos - g.s.context - 1;
-            uint32_t seen[2 * kWords];
+            bool none = g.s.lost;
+            uint32_t seen[kWords];
 #pragma unroll
-            for (int w = 0; w < 2 * kWords; ++w) seen[w] = ~0u;
+            for (int w = 0; w < kWords; ++w) seen[w] = ~0u;
             if (!g.s.lost && node >= 0) {
               // What a position holds that not every row sees goes through the product of every row: nothing but numbers
               // may stand there.
               uint4* row = reinterpret_cast<uint4*>(v + at * kD);
+              const bool behind = pos >= g.s.end;
               bool nan = false;
-              if (pos < g.s.end)
+              if (!behind)
                 for (int c = 0; c < kD / 16; ++c) nan |= holds_nan(row[c]);
-              if (nan || pos >= g.s.end)
+              if (nan || behind)
                 for (int c = 0; c < kD / 16; ++c) row[c] = make_uint4(0, 0, 0, 0);
-              if (nan || bad) kf[i] = NAN;
-              if (none[i]) {
-              } else if (pos >= g.s.end) {
+              none = nan || bad;
+              const bool lost = !behind && P.c.page_of(g.b, pos) < 0;  // every row of the sequence is
+              if (behind) {
 #pragma unroll
-                for (int w = 0; w < 2 * kWords; ++w) seen[w] = 0;
-              } else if (!bad && P.parent) {
+                for (int w = 0; w < kWords; ++w) seen[w] = 0;
+              } else if (!bad && !lost && P.parent) {
 #pragma unroll
-                for (int w = 0; w < 2 * kWords; ++w) seen[w] = s.path[me][node][w];
-              } else if (!bad) {
+                for (int w = 0; w < kWords; ++w) seen[w] = s.path[node][w];
+              } else if (!bad && !lost) {
                 const int from = static_cast<int>(node + 1) * P.group - g.c0;  // the first column that sees it
 #pragma unroll
-                for (int w = 0; w < 2 * kWords; ++w) {
-                  const int a = from - w * kWordCols;
+                for (int w = 0; w < kWords; ++w) {
+                  const int a = from - w * 32;
                   seen[w] = a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
                 }
               }
             }
 #pragma unroll
-            for (int w = 0; w < 2 * kWords; ++w) s.seen[st][at][w] = seen[w];
+            for (int w = 0; w < kWords; ++w) s.seen[st][at][w] = seen[w];
+            const uint32_t bits = __ballot_sync(~0u, none);
+            if (lane == 0) s.none[st][i] = bits;
           }
-          const float ratio = most > 0.f ? vf[i] / most : vf[i];
-          // ratio = f * 2^e, f in [1/2, 1): 2^e, or 2^(e - 1) where f is 1/2
-          const uint32_t u = __float_as_uint(ratio);
-          const int e = max(-12, min(0, static_cast<int>(u >> 23) - 126 - ((u & 0x7fffffu) == 0)));
-          s.factor[st][at] = make_float4(none[i] ? NAN : kf[i], e, __uint_as_float((127 - e) << 23),
-                                         ratio * __uint_as_float((127 - e) << 23));
+          async_fence();
         }
-        if (lane == 0) s.vmost[st] = most > 0.f ? most : 1.f, s.special[st] = special;
-        if (special) async_fence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.ready[st]);
       }
     }
   } else {
     // ---- softmax
-    const int me = (warp - 4) / 4, quad = warp & 3, t = threadIdx.x - 128 - me * kGroupThreads;
+    const int me = (warp - 4) / 8, half = (warp - 4) / 4 & 1, quad = warp & 3;
+    const int t = threadIdx.x - 128 - me * kGroupThreads, position = t & (kTile - 1);
+    constexpr int kC = kN / 2;  // columns of a thread
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // 32 lanes of tensor memory each
+    const uint32_t tmem_s = tmem + lanes + me * kN + half * kC, tmem_o = tmem + lanes + (2 + 2 * me) * kN + half * kC;
     unsigned count = 0, items = 0;
     uint8_t* const mine = weights + me * 2 * Z::kWeights;
     float* const others = reinterpret_cast<float*>(weights);  // the second group's sums at a segment's end
     while (walk.next(g)) {
+      const int step = g.two ? 1 : 2, first_tile = g.t0 + (g.two ? 0 : me);
+      // pages and scales of this thread's position, an item and two ahead.  (Positions are below 2^31 + SV_MAX_NODES.)
+      const int32_t* const table = P.c.table + g.b * P.c.table_stride;
+      const int64_t of_head = static_cast<int64_t>(g.h) << (P.c.page_log - P.c.block_log);
+      const float *const k_scales = P.c.scales[0] + of_head, *const v_scales = P.c.scales[1] + of_head;
+      const int page_scales = P.c.heads << (P.c.page_log - P.c.block_log);
+      const unsigned in_page = (1u << P.c.page_log) - 1u, end = g.s.lost ? 0u : static_cast<unsigned>(g.s.end);
+      auto page_at = [&](int tile) {
+        const unsigned pos = static_cast<unsigned>(tile) * kTile + position;
+        return tile < g.t1 && pos < end ? table[pos >> P.c.page_log] : -1;
+      };
+      auto scales_at = [&](int tile, int page) {
+        const unsigned pos = static_cast<unsigned>(tile) * kTile + position;
+        float2 f = make_float2(g.s.lost || pos < end ? NAN : 0.f, 0.f);
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(P.c.pages)) {
+          const int64_t at = static_cast<int64_t>(page) * page_scales + ((pos & in_page) >> P.c.block_log);
+          f.x = k_scales[at], f.y = v_scales[at];
+        }
+        return f;
+      };
+      int page_next = page_at(first_tile);
+      float2 scales_next = scales_at(first_tile, page_next);
+      page_next = page_at(first_tile + step);
       // the queries, a warp for each row: two e4m3 numbers an entry, of the entry over its row's power of two
       constexpr int kPer = kD / 32;
       const int rows = g.two ? 2 * kN : kN;
-      for (int r = warp - 4; r < rows; r += 8) {
-        const int col = g.c0 + r;
+      for (int r = warp - 4; r < rows; r += 16) {
+        const int col = g.c0 + r, i = col / P.group;
         float q[kPer] = {};
         if (col < g.s.cols) {
-          const int i = col / P.group;
           const __nv_bfloat16* p = P.q + (static_cast<int64_t>(g.s.start) + g.b + i) * P.q_row +
                                    (static_cast<int64_t>(g.h) * P.group + col - i * P.group) * P.q_head + lane * kPer;
           uint32_t u[kPer / 2];
@@ -608,123 +711,165 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           *reinterpret_cast<uint16_t*>(to + Z::kQ) = static_cast<uint16_t>(lo);
         }
         if (lane == 0) {
-          const float f = fine ? unit * P.scale : NAN;
-          s.row[block][row] = f;
+          s.row[block][row] = fine ? unit * P.scale : NAN;
+          s.out[block][row] = (static_cast<int64_t>(g.s.start) + g.b + i) * P.out_row +
+                              (static_cast<int64_t>(g.h) * P.group + col - i * P.group) * P.out_head;
         }
       }
+      if (t < kN) s.ref[me][t] = 0.f;
+      // the anchor of the group's value scales: a power of two near the first tile's largest, 2^-60 at least
+      float anchor = scales_next.y;
+      for (int o = 16; o; o >>= 1) anchor = fmaxf(anchor, __shfl_xor_sync(~0u, anchor, o));
+      if (lane == 0) s.anchors[me][quad] = anchor;
       async_fence();
       groups_sync();  // the rows' factors are there for both groups
       if (lane == 0) mbar_arrive(&s.q_full);
-      const float* const factors = s.row[g.two ? me : 0];
-      float o[kN], l[kN < 32 ? 1 : kN / 32], m = -INFINITY;
+      anchor = fmaxf(fmaxf(s.anchors[me][0], s.anchors[me][1]), fmaxf(s.anchors[me][2], s.anchors[me][3]));
+      anchor = __uint_as_float(__float_as_uint(fminf(fmaxf(anchor, 0x1p-60f), 0x1p100f)) & 0x7f800000u);
+      const float per_anchor = 1.f / anchor;
+      const float* const factors = s.row[g.two ? me : 0] + half * kC;
+      Two l[kC / 2];
 #pragma unroll
-      for (int c = 0; c < kN; ++c) o[c] = 0.f;
-#pragma unroll
-      for (int c = 0; c < (kN < 32 ? 1 : kN / 32); ++c) l[c] = 0.f;
-      constexpr int kChunk = kN < 32 ? kN : 32;
-      const int own = kN < 32 ? lane >> 1 : lane;  // this lane's column of a chunk
-      for (int tile = g.two ? 0 : me; tile < g.t1 - g.t0; tile += g.two ? 1 : 2) {
-        const unsigned n = count + tile, st = n % P.stages;
-        mbar_wait(&s.ready[st], n / P.stages & 1, &s.dead);
-        mbar_wait(&s.s_full[me], items & 1, &s.dead);
+      for (int c = 0; c < kC / 2; ++c) l[c] = 0;
+      float m = -INFINITY, top = -INFINITY;  // m: of column t, its reference
+      bool unset = true;
+      const unsigned begun = items;
+      const int own = half * kC + lane / (32 / kC);  // the column that reductions leave to this lane
+      for (int tile = first_tile; tile < g.t1; tile += step) {
+        const unsigned n = count + (tile - g.t0), st = n % kV;
+        const float2 scales = scales_next;
+        scales_next = scales_at(tile + step, page_next);
+        page_next = page_at(tile + 2 * step);
+        float kf = scales.x;
+        // V's scale over the anchor: rest * 2^e, rest in (1/2, 1], e -12 at least
+        const float ratio = scales.y * per_anchor;
+        const uint32_t u = __float_as_uint(ratio);
+        const int e = max(-12, min(100, static_cast<int>(u >> 23 & 0xff) - 126 - ((u & 0x7fffffu) == 0)));
+        const float inverse = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const bool special = g.s.lost || (static_cast<int64_t>(tile) + 1) * kTile > g.s.context + 1;
+        if (special) {
+          wait_for(&s.ready[st], n / kV & 1, &s.dead);
+          if (s.none[st][quad] >> lane & 1u) kf = NAN;
+        }
+        wait_for(&s.s_full[me], items & 1, &s.dead);
         tc_after();
-        float x[kN];
-        tc_load<kN>(tmem + lanes + me * kN, x);
+        float x[kC];
+        tc_load<kC>(tmem_s, x);
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.s_free[me]);
-        const float4 mul = s.factor[st][t];
+        // x becomes the logit, log2 of V's scale added, over the reference
+        {
+          const Two kf2 = two(kf, kf), shift = two(static_cast<float>(e), static_cast<float>(e));
+          const float* const refs = s.ref[me] + half * kC;
 #pragma unroll
-        for (int c = 0; c < kN; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(factors + c);
-          x[c] = fmaf(x[c] * f.x, mul.x, mul.y), x[c + 1] = fmaf(x[c + 1] * f.y, mul.x, mul.y);
-          x[c + 2] = fmaf(x[c + 2] * f.z, mul.x, mul.y), x[c + 3] = fmaf(x[c + 3] * f.w, mul.x, mul.y);
-        }
-        if (s.special[st]) {
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            const uint32_t seen = s.seen[st][t][(g.two ? me : 0) * kWords + w];
-#pragma unroll
-            for (int c = 0; c < kWordCols; ++c)
-              if (!(seen >> c & 1u)) x[w * kWordCols + c] = -INFINITY;
+          for (int c = 0; c < kC; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(factors + c), r = *reinterpret_cast<const float4*>(refs + c);
+            both(fma2(two(x[c], x[c + 1]), mul2(two(f.x, f.y), kf2), add2(shift, two(r.x, r.y))), x[c], x[c + 1]);
+            both(fma2(two(x[c + 2], x[c + 3]), mul2(two(f.z, f.w), kf2), add2(shift, two(r.z, r.w))), x[c + 2], x[c + 3]);
           }
         }
+        if (special) {
+          const int col = (g.two ? me * kN : 0) + half * kC;
+          const uint32_t seen = s.seen[st][position][col / 32] >> col % 32;
 #pragma unroll
-        for (int c = 0; c < kN; c += kChunk) s.most[me][quad][c + own] = over_lanes<kChunk, false>(x + c);
-        group_sync(me);
-        if (t < kN) {
-          const float mt = fmaxf(fmaxf(s.most[me][0][t], s.most[me][1][t]), fmaxf(s.most[me][2][t], s.most[me][3][t]));
-          const float to = fmaxf(m, mt);
-          s.ref[me][t] = (mt == -INFINITY ? 0.f : mt) - kTop;
-          s.keep[me][t] = m == to ? 1.f : power(m - to);
-          s.take[me][t] = mt == -INFINITY ? 0.f : power(mt - to);
-          m = to;
+          for (int c = 0; c < kC; ++c)
+            if (!(seen >> c & 1u)) x[c] = -INFINITY;
         }
-        group_sync(me);
+        float most = x[0];
 #pragma unroll
-        for (int c = 0; c < kN; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&s.ref[me][c]);
-          x[c] = power(x[c] - f.x), x[c + 1] = power(x[c + 1] - f.y), x[c + 2] = power(x[c + 2] - f.z),
-          x[c + 3] = power(x[c + 3] - f.w);
+        for (int c = 1; c < kC; ++c) most = fmaxf(most, x[c]);
+        if (group_any(me, most > kMost || unset || (items - begun) % kRefresh == 0)) {
+          s.most[me][quad][own] = over_lanes<kC, false>(x);
+          group_sync(me);
+          if (t < kN) {
+            const float zt = fmaxf(fmaxf(s.most[me][0][t], s.most[me][1][t]), fmaxf(s.most[me][2][t], s.most[me][3][t]));
+            const bool first = m == -INFINITY;
+            const float from = first ? 0.f : m;
+            float to = from, keep = 1.f;
+            if (zt != -INFINITY) {
+              if (first || !(zt <= kMost && zt >= kLow)) to = from + zt;
+              if (!first) to = fmaxf(to, top - kDeep), keep = power(from - to);
+              m = to, top = fmaxf(top, to);
+            }
+            s.ref[me][t] = -to, s.step[me][t] = from - to, s.keep[me][t] = keep;
+            const unsigned lanes_here = kN < 32 ? (1u << (kN & 31)) - 1u : ~0u;
+            const uint32_t moved = __ballot_sync(lanes_here, keep != 1.f), none = __ballot_sync(lanes_here, m == -INFINITY);
+            if (lane == 0) s.moved[me] = moved, s.unset[me] = none;
+          }
+          group_sync(me);
+          const bool moved = s.moved[me] != 0;
+          unset = s.unset[me] != 0;
+          const float *const steps = s.step[me] + half * kC, *const keeps = s.keep[me] + half * kC;
+#pragma unroll
+          for (int c = 0; c < kC; c += 2) {
+            const float2 d = *reinterpret_cast<const float2*>(steps + c), k = *reinterpret_cast<const float2*>(keeps + c);
+            x[c] += d.x, x[c + 1] += d.y;
+            l[c / 2] = mul2(l[c / 2], two(k.x, k.y));
+          }
+          if (moved && items != begun) {
+            wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < 2 * kC; c += 8) {
+              const int col = c % kC;
+              const uint32_t at = tmem_o + (c / kC) * kN + col;  // hi's sums, then lo's
+              float o[8];
+              tc_load<8>(at, o);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] *= keeps[col + k];
+              tc_store(at, o);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_before();
+          }
         }
+        const Two inverse2 = two(inverse, inverse), rest = two(32.f * ratio * inverse, 32.f * ratio * inverse);
+        if (items != begun) wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);  // the weights in front have been read
 #pragma unroll
-        for (int c = 0; c < kN; c += kChunk) {
-          float p[kChunk];
-#pragma unroll
-          for (int k = 0; k < kChunk; ++k) p[k] = x[c + k] * mul.z;
-          const float sum = over_lanes<kChunk, true>(p);
-          l[c / kChunk] = l[c / kChunk] * s.keep[me][c + own] + sum * s.take[me][c + own];
-        }
-#pragma unroll
-        for (int c = 0; c < kN; c += 16) {
+        for (int c = 0; c < kC; c += 8) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float a = x[c + 4 * k] * mul.w, b = x[c + 4 * k + 1] * mul.w, d = x[c + 4 * k + 2] * mul.w,
-                        e = x[c + 4 * k + 3] * mul.w;
-            const uint32_t h0 = e4m3x2(a, b), h1 = e4m3x2(d, e);
-            const float2 f0 = from_e4m3x2(h0), f1 = from_e4m3x2(h1);
-            hi[k] = h0 | h1 << 16;
-            lo[k] = e4m3x2(a - f0.x, b - f0.y) | e4m3x2(d - f1.x, e - f1.y) << 16;
+            const int at = c + 2 * k;
+            const Two p = two(power(x[at]), power(x[at + 1]));
+            l[at / 2] = fma2(p, inverse2, l[at / 2]);
+            split2(mul2(p, rest), hi[k], lo[k]);
           }
-          uint4* const to = reinterpret_cast<uint4*>(mine + c / 16 * (kTile * 16) + t * 16);
-          to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          to[Z::kWeights / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          // runs of 16 columns, 16 bytes a position
+          const int col = half * kC + c;
+          uint2* const to = reinterpret_cast<uint2*>(mine + col / 16 * (kTile * 16) + position * 16 + col % 16);
+          to[0] = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          to[Z::kWeights / 8] = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
-        const float vmost = s.vmost[st];  // behind the arrival the stage may be filled again
         async_fence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[me]);
-        mbar_wait(&s.o_full[me], items & 1, &s.dead);
-        tc_after();
         ++items;
-#pragma unroll
-        for (int c = 0; c < kN; c += 16) {
-          float u[16];
-          tc_load<16>(tmem + lanes + (2 + me) * kN + c, u);
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(&s.keep[me][c + k]),
-                         b = *reinterpret_cast<const float4*>(&s.take[me][c + k]);
-            o[c + k] = o[c + k] * a.x + u[k] * (b.x * vmost), o[c + k + 1] = o[c + k + 1] * a.y + u[k + 1] * (b.y * vmost);
-            o[c + k + 2] = o[c + k + 2] * a.z + u[k + 2] * (b.z * vmost);
-            o[c + k + 3] = o[c + k + 3] * a.w + u[k + 3] * (b.w * vmost);
-          }
-        }
-        tc_before();
       }
       count += g.t1 - g.t0;
       // ---- the segment's end.  Lane d of tensor memory is entry d: with 64 of them the first 16 lanes of each warp have one.
-      const int d = kD == 128 ? t : quad * 16 + lane;
-      const bool has = kD == 128 || lane < 16;
+      const int d = kD == 128 ? position : quad * 16 + lane;
+      const bool has = kD == 128 || lane < 16, any = items != begun;
+      if (any) wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
+      tc_after();
+      {
+        float v[kC];
 #pragma unroll
-      for (int c = 0; c < kN; c += kChunk) s.most[me][quad][c + own] = l[c / kChunk];
+        for (int k = 0; k < kC; k += 2) both(l[k / 2], v[k], v[k + 1]);
+        s.most[me][quad][own] = over_lanes<kC, true>(v);
+      }
       if (t < kN) s.m[me][t] = m;
       groups_sync();
       if (!g.two && me == 1) {
-        if (has)
+#pragma unroll 1
+        for (int c = 0; c < kC; c += 8) {
+          float o[8] = {}, u[8] = {};
+          if (any) tc_load<8>(tmem_o + c, o), tc_load<8>(tmem_o + kN + c, u);
+          if (has)
 #pragma unroll
-          for (int c = 0; c < kN; ++c) others[c * kD + d] = o[c];
+            for (int k = 0; k < 8; ++k) others[(half * kC + c + k) * kD + d] = fmaf(u[k], 0.03125f, o[k]) * anchor;
+        }
       }
       if (t < kN && (g.two || me == 0)) {
         float sum = s.most[me][0][t] + s.most[me][1][t] + s.most[me][2][t] + s.most[me][3][t], to = m, f1 = 0.f;
@@ -733,10 +878,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           f1 = s.m[1][t] == -INFINITY ? 0.f : power(s.m[1][t] - to);
           sum = sum * (m == to ? 1.f : power(m - to)) + f1 * (s.most[1][0][t] + s.most[1][1][t] + s.most[1][2][t] + s.most[1][3][t]);
         }
-        // (in the first group's places of a segment of one block)
-        s.keep[me][t] = m == to ? 1.f : power(m - to);
-        s.take[me][t] = f1;
-        s.ref[me][t] = sum;
+        s.keep[me][t] = (m == to ? 1.f : power(m - to)) * anchor;
+        if (!g.two) s.take[t] = f1;
+        s.step[me][t] = sum;
         m = to;
       }
       if (!g.two)
@@ -744,34 +888,32 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       else
         group_sync(me);
       if (g.two || me == 0) {
-        const int c0 = g.c0 + (g.two ? me * kN : 0), cols = min(kN, g.s.cols - c0);
+        const int cols = min(kN, g.s.cols - g.c0 - (g.two ? me * kN : 0)), first = g.two ? me * kN : 0;
         const bool ok = !s.dead;
-        if (g.whole) {
-          __nv_bfloat16* const to = P.out + (static_cast<int64_t>(g.s.start) + g.b) * P.out_row +
-                                    static_cast<int64_t>(g.h) * P.group * P.out_head + d;
+        float* const part = P.parts + (2 * static_cast<int64_t>(blockIdx.x) + g.whole_front) * Z::kPart;
+#pragma unroll 1
+        for (int c = 0; c < kC; c += 8) {
+          float o[8], u[8];
+          tc_load<8>(tmem_o + c, o), tc_load<8>(tmem_o + kN + c, u);
 #pragma unroll
-          for (int c = 0; c < kN; ++c) {
-            float v = o[c] * s.keep[me][c];
-            if (!g.two && has) v += others[c * kD + d] * s.take[me][c];
-            v = ok ? v / s.ref[me][c] : NAN;
-            const int i = (c0 + c) / P.group;
-            if (has && c < cols) to[i * P.out_row + (c0 + c - i * P.group) * P.out_head] = __float2bfloat16(v);
-          }
-        } else {
-          float* const to = P.parts + (2 * static_cast<int64_t>(blockIdx.x) + g.whole_front) * Z::kPart;
-          const int first = g.two ? me * kN : 0;
-#pragma unroll
-          for (int c = 0; c < kN; ++c) {
-            float v = o[c] * s.keep[me][c];
-            if (!g.two && has) v += others[c * kD + d] * s.take[me][c];
-            if (has && c < cols) to[(first + c) * kD + d] = v;
-          }
-          if (t < cols) {
-            to[2 * kN * kD + first + t] = m;
-            to[2 * kN * (kD + 1) + first + t] = ok ? s.ref[me][t] : NAN;
+          for (int k = 0; k < 8; ++k) {
+            const int col = half * kC + c + k;
+            float v = fmaf(u[k], 0.03125f, o[k]) * s.keep[me][col];
+            if (!g.two && has) v += others[col * kD + d] * s.take[col];
+            if (has && col < cols) {
+              if (g.whole)
+                P.out[s.out[g.two ? me : 0][col] + d] = __float2bfloat16(ok ? v / s.step[me][col] : NAN);
+              else
+                part[(first + col) * kD + d] = v;
+            }
           }
         }
+        if (!g.whole && t < cols) {
+          part[Z::kColumns * kD + first + t] = m;
+          part[Z::kColumns * (kD + 1) + first + t] = ok ? s.step[me][t] : NAN;
+        }
       }
+      tc_before();
       groups_sync();  // queries, weights and factors are free again
     }
   }
@@ -781,50 +923,51 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   if (s.dead) stay_behind();
   __syncwarp();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(4 * kN) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(8 * kN) : "memory");
 }
 
 // ---- parts of a unit together
 
 constexpr int kJoinThreads = 128;
 
-template <int kN, int kD>
+template <int kColumns, int kD>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendParams P) {
-  using Z = Sizes<kN, kD>;
+  constexpr int kPart = kColumns * (kD + 2);
   __shared__ Start start;
   __shared__ int64_t warp_sums[kJoinThreads / 32];
   wait_for_stream();
   // CTA i looks at the cut in front of the i + 1-st of the CTAs that shared the tiles
   const int at = blockIdx.x + 1;
   int64_t tile = 0;
-  find_tile<kN>(P, [&](int64_t total) { return cut(total, at, P.grid); }, &start, warp_sums);
+  find_tile<kColumns>(P, [&](int64_t total) { return cut(total, at, P.grid); }, &start, warp_sums);
   tile = cut(start.total, at, P.grid);
   if (start.b >= P.B) return;
-  const Sequence s = sequence_of<kN>(P, start.b);
+  const Sequence s = sequence_of<kColumns>(P, start.b);
   const int64_t unit = start.off / s.tiles, first = tile - (start.off - unit * s.tiles), last = first + s.tiles;
   // nothing is cut here, or an earlier cut is in this unit too
   if (tile == first || cut(start.total, at - 1, P.grid) > first) return;
   int parts = 1;
   while (at + parts - 1 < P.grid && cut(start.total, at + parts - 1, P.grid) < last) ++parts;
-  const int h = static_cast<int>(unit / s.pairs), c0 = static_cast<int>(unit % s.pairs) * 2 * kN, cols = min(2 * kN, s.cols - c0);
+  const int h = static_cast<int>(unit / s.pairs), c0 = static_cast<int>(unit % s.pairs) * kColumns,
+            cols = min(kColumns, s.cols - c0);
   const int lane = threadIdx.x & 31;
   const int64_t before = static_cast<int64_t>(at) - 1;  // the CTA with the first part
   // a CTA without tiles has no part: its place is skipped
-  auto part = [&](int k) { return P.parts + (2 * (before + k) + (k == 0)) * Z::kPart; };
+  auto part = [&](int k) { return P.parts + (2 * (before + k) + (k == 0)) * kPart; };
   auto empty = [&](int k) {
     return cut(start.total, static_cast<int>(before) + k, P.grid) == cut(start.total, static_cast<int>(before) + k + 1, P.grid);
   };
   for (int c = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; c < cols; c += gridDim.y * (kJoinThreads / 32)) {
     float m = -INFINITY;
     for (int k = lane; k < parts; k += 32)
-      if (!empty(k)) m = fmaxf(m, part(k)[2 * kN * kD + c]);
+      if (!empty(k)) m = fmaxf(m, part(k)[kColumns * kD + c]);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     float l = 0.f, v[kD / 32] = {};
     for (int k = 0; k < parts; ++k) {
       if (empty(k)) continue;
       const float* p = part(k);
-      const float mk = p[2 * kN * kD + c], f = mk == m ? 1.f : power(mk - m);
-      l += p[2 * kN * (kD + 1) + c] * f;
+      const float mk = p[kColumns * kD + c], f = mk == m ? 1.f : power(mk - m);
+      l += p[kColumns * (kD + 1) + c] * f;
 #pragma unroll
       for (int e = 0; e < kD / 32; ++e) v[e] += p[c * kD + lane + 32 * e] * f;
     }
@@ -873,35 +1016,33 @@ bool map_entries(CUtensorMap* map, const sv_cache& c, void* base, void* none, in
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// columns of a block: as few as hold a sequence's rows in one block, 64 at most
-int block_columns(int group, int max_nodes) {
+// Columns of a unit: as few as hold a sequence's rows, 64 at most (two blocks of 32).
+int unit_columns(int group, int max_nodes) {
   const int64_t cols = static_cast<int64_t>(max_nodes + 1) * group;
   return cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
 }
 
-template <int kN, int kD>
-sv_status launch_attend(AttendParams P, const Maps& maps, int device, cudaStream_t st) {
-  using Z = Sizes<kN, kD>;
-  P.stages = Z::kStages;
-  const int smem = Z::kFixed + Z::kStages * Z::kStageBytes;
+template <int kN, int kBlocks, int kD>
+sv_status launch_attend(const AttendParams& P, const Maps& maps, int device, cudaStream_t st) {
+  constexpr int smem = Sizes<kN, kBlocks, kD>::kSmem;
+  const auto kernel = attend_kernel<kN, kBlocks, kD>;
   static std::atomic<bool> opted_in[64];
   if (device >= 64 || !opted_in[device].load()) {
-    if (cudaFuncSetAttribute(attend_kernel<kN, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return SV_ECUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SV_ECUDA;
     if (device < 64) opted_in[device].store(true);
   }
-  if (launch_waiting(attend_kernel<kN, kD>, P.grid, kAttendThreads, smem, 1, st, P, maps) != cudaSuccess) return SV_ECUDA;
-  if (P.grid > 1 &&
-      launch_waiting(join_kernel<kN, kD>, dim3(P.grid - 1, kN / 8), kJoinThreads, 0, 1, st, P) != cudaSuccess)
+  if (launch_waiting(kernel, P.grid, kAttendThreads, smem, 1, st, P, maps) != cudaSuccess) return SV_ECUDA;
+  if (P.grid > 1 && launch_waiting(join_kernel<kN * kBlocks, kD>, dim3(P.grid - 1, kN * kBlocks / 8), kJoinThreads, 0, 1, st, P) !=
+                        cudaSuccess)
     return SV_ECUDA;
   return SV_OK;
 }
 
 template <int kD>
 sv_status launch_attend(const AttendParams& P, const Maps& maps, int columns, int device, cudaStream_t st) {
-  return columns == 16   ? launch_attend<16, kD>(P, maps, device, st)
-         : columns == 32 ? launch_attend<32, kD>(P, maps, device, st)
-                         : launch_attend<64, kD>(P, maps, device, st);
+  return columns == 16   ? launch_attend<16, 1, kD>(P, maps, device, st)
+         : columns == 32 ? launch_attend<32, 1, kD>(P, maps, device, st)
+                         : launch_attend<32, 2, kD>(P, maps, device, st);
 }
 
 int sms_of(int device) {
@@ -914,8 +1055,7 @@ int sms_of(int device) {
 
 extern "C" size_t spec_verify_attend_workspace(int heads, int q_heads, int dim, int max_nodes, int device) {
   if (heads < 1 || q_heads < 1 || dim < 1 || max_nodes < 0 || max_nodes > SV_MAX_NODES) return 0;
-  const int columns = sv::block_columns(q_heads / heads, max_nodes);
-  return static_cast<size_t>(2 * sv::sms_of(device)) * 2 * columns * (dim + 2) * sizeof(float);
+  return static_cast<size_t>(2 * sv::sms_of(device)) * sv::unit_columns(q_heads / heads, max_nodes) * (dim + 2) * sizeof(float);
 }
 
 extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, int64_t q_row, int64_t q_head, void* out,
@@ -966,7 +1106,7 @@ extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, in
   if (!sv::map_entries(&maps.k, *cache, cache->k, workspace, P.box_tokens) ||
       !sv::map_entries(&maps.v, *cache, cache->v, workspace, P.box_tokens))
     return SV_ECUDA;
-  const int columns = sv::block_columns(P.group, max_nodes);
+  const int columns = sv::unit_columns(P.group, max_nodes);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   return cache->dim == 128 ? sv::launch_attend<128>(P, maps, columns, device, st)
                            : sv::launch_attend<64>(P, maps, columns, device, st);

@@ -180,9 +180,10 @@ class Cache:
         of which cuts off less than 2^-23 of the sum of the magnitudes for each of its products and itself; three fp32
         products with the scales (2^-24 each) and the difference to the largest x (2^-24 of the largest magnitude) follow;
         a query entry may be off by 2^-10 steps where the largest is 224 or more, 2^-17.8 of it.  The exponential is off
-        by 2^-22.  A weight times its value's scale is rounded to eight bits (2^-8), or to 2^-10 where its tile's largest such
-        product (with a scale of 2^-12 of the tile's largest at least, taken up to the next power of two) is 256 or more: 2^-17
-        of the largest product over all positions, with a scale of 2^-12 of the largest at least.  The sum of the weights is off by 2^-24 an addition.  At last the result is rounded to bf16."""
+        by 2^-22.  A weight times its value's scale is rounded to eight bits (2^-8), or to 2^-15 where the largest such product
+        of a tile (this one or one before it; with a scale of 2^-12 of some tile's largest at least, taken up to the next power
+        of two) is 1 or more: 2^-14 of the largest product over all positions, with a scale of 2^-12 of the largest at least.
+        The products with V are summed like those with K, in steps of 32 positions, twice.  The sum of the weights is off by 2^-24 an addition.  At last the result is rounded to bf16."""
         q = doubles(q)
         start = ints(node_start)
         par = None if parent is None else ints(parent)
@@ -210,8 +211,8 @@ class Cache:
                     o = p @ vv
                     d = np.minimum(d, 1.0)
                     size = sizes[h // group][seen]
-                    lost = p * (2.0 * d + 2.0 ** -8 + 2.0 ** -21)
-                    least = 2.0 ** -17 * np.max(p * np.maximum(size, size.max() * 2.0 ** -12))
+                    lost = p * (2.0 * d + 2.0 ** -8 + 2.0 ** -21 + (len(p) / 16 + 8) * 33 * 2.0 ** -23)
+                    least = 2.0 ** -14 * np.max(p * np.maximum(size, size.max() * 2.0 ** -12))
                     err = lost @ np.abs(vv) + least * (np.abs(vv) / size[:, None]).sum(0) + (p @ (2 * d) + len(p) * 2.0 ** -24) * np.abs(o)
                     out[lo + b + i, h] = o
                     off[lo + b + i, h] = err * 1.01 + (np.abs(o) + err) * 2.0 ** -8
