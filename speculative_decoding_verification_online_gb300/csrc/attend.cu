@@ -60,6 +60,8 @@ struct AttendParams {
   const int32_t *context, *node_start, *parent;
   int B, total, max_nodes;
   int boxes, box_tokens;  // boxes of a tile
+  int page_scales;        // scales of a page
+  unsigned in_page;       // a mask of positions in a page
   int grid;                       // CTAs that share the tiles
   float* parts;
 };
@@ -138,11 +140,13 @@ __device__ __forceinline__ void find_tile(const AttendParams& P, F&& at, Start* 
   __syncthreads();
 }
 
-// A run of tiles of one unit.
+// A run of tiles of one unit.  (Positions are below 2^31 + SV_MAX_NODES.)
 struct Segment {
-  Sequence s;
-  int b, h, c0, t0, t1;  // c0: the first column
-  bool two, whole_front, whole;  // two blocks of columns; from the unit's first tile on; all of the unit's tiles
+  int b, h, c0, t0, t1;  // c0: the first column; t1 = 0: there are no more
+  int start, nodes, cols;
+  unsigned root, end;    // the root's position, and behind the last one
+  bool two, lost;        // two blocks of columns; positions without a place in the table
+  bool front, whole;     // from the unit's first tile on; all of the unit's tiles
 };
 
 template <int kN, int kBlocks>
@@ -156,26 +160,30 @@ struct Walk {
   __device__ __forceinline__ Walk(const AttendParams& P, const Start& at, int64_t lo, int64_t hi)
       : P(P), pos(lo), hi(hi), off(at.off), b(at.b) {}
 
-  __device__ __forceinline__ bool next(Segment& g) {
-    if (pos >= hi) return false;
+  __device__ __forceinline__ Segment next() {
+    Segment g = {};
+    if (pos >= hi) return g;
     while (!loaded || off >= s.work) {
       if (loaded) ++b, off = 0;
-      if (b >= P.B) return false;
+      if (b >= P.B) return g;
       s = sequence_of<kN * kBlocks>(P, b);
       loaded = true;
     }
     const int64_t unit = off / s.tiles;
-    g.s = s, g.b = b;
+    g.b = b;
     g.h = static_cast<int>(unit / s.pairs);
     g.c0 = static_cast<int>(unit % s.pairs) * kN * kBlocks;
     g.t0 = static_cast<int>(off - unit * s.tiles);
     const int64_t left = hi - pos, here = s.tiles - g.t0, n = left < here ? left : here;
     g.t1 = g.t0 + static_cast<int>(n);
+    g.start = s.start, g.nodes = s.nodes, g.cols = s.cols;
+    g.root = static_cast<unsigned>(s.context), g.end = s.lost ? 0u : static_cast<unsigned>(s.end);
     g.two = kBlocks == 2 && s.cols - g.c0 > kN;
-    g.whole_front = g.t0 == 0;
+    g.lost = s.lost;
+    g.front = g.t0 == 0;
     g.whole = g.t0 == 0 && g.t1 == s.tiles;
     pos += n, off += n;
-    return true;
+    return g;
   }
 };
 
@@ -367,19 +375,24 @@ struct AttendShared {
   uint32_t seen[kV][kTile][kWords];
   uint32_t none[kV][kTile / 32];
   float most[2][4][kN];  // a warp's largest logits, and at last its sums
-  float ref[2][kN];      // references, negative
-  float step[2][kN];     // how far a reference moved
-  float keep[2][kN];     // what the sums so far are worth against the new one
-  float take[kN];
-  float row[kBlocks][kN];    // of a query row: its power of two, the softmax's scale
-  int64_t out[kBlocks][kN];  // where its result goes
+  // (read in fours)
+  alignas(16) float zero[kN];  // references of a segment's first items
+  alignas(16) float ref[2][kN];   // references, negative
+  alignas(16) float step[2][kN];  // how far a reference moved
+  alignas(16) float keep[2][kN];  // what the sums so far are worth against the new one
   float m[2][kN];
   uint32_t moved[2], unset[2];  // of a group: columns whose sums have to be multiplied, that have no reference yet
-  float anchors[2][4];  // of a group's warps
+  // at a segment's end: factors of the groups' sums (of the blocks' in a segment of two) and of the result
+  float worth[2][kN], whole[2][kN], last[2][kN];
+  alignas(16) float row[kBlocks][kN];  // of a query row: its power of two, the softmax's scale
+  int64_t out[kBlocks][kN];            // where its result goes
+  float anchors[2][4], second_anchor;  // of a group's warps; of the second group
   uint32_t path[SV_MAX_NODES][kWords];
   int parent[SV_MAX_NODES];
+  Segment segment[4];  // the first warp walks ahead
+  uint64_t g_full[4], g_free[4];
   uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV], ready[kV];
-  uint64_t s_full[2], s_free[2], p_full[2], o_full[2], q_full;
+  uint64_t s_full[2], s_free[2], p_full[2], o_full[2], q_full, o_read;
   int64_t warp_sums[kAttendThreads / 32];
   Start start;
   uint32_t tmem;
@@ -406,6 +419,16 @@ __device__ __forceinline__ bool group_any(int group, bool mine) {
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(any)
       : "r"(static_cast<unsigned>(mine)), "r"(1 + group)
+      : "memory");
+  return any != 0;
+}
+// the same of both groups
+__device__ __forceinline__ bool groups_any(bool mine) {
+  unsigned any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 3, 512, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"(static_cast<unsigned>(mine))
       : "memory");
   return any != 0;
 }
@@ -445,7 +468,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     for (unsigned i = 0; i < kV; ++i) mbar_init(&s.v_full[i], 1), mbar_init(&s.v_empty[i], 1), mbar_init(&s.ready[i], 1);
     for (int i = 0; i < 2; ++i)
       mbar_init(&s.s_full[i], 1), mbar_init(&s.s_free[i], 8), mbar_init(&s.p_full[i], 8), mbar_init(&s.o_full[i], 1);
-    mbar_init(&s.q_full, 16);
+    for (int i = 0; i < 4; ++i) mbar_init(&s.g_full[i], 1), mbar_init(&s.g_free[i], 19);
+    mbar_init(&s.q_full, 16), mbar_init(&s.o_read, 16);
+    for (int c = 0; c < kN; ++c) s.zero[c] = 0.f;
+    for (int c = 0; c < kN; ++c) s.zero[c] = 0.f;
     s.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -464,22 +490,40 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   lo = cut(start.total, blockIdx.x, P.grid);
   const int64_t hi = cut(start.total, blockIdx.x + 1, P.grid);
   const uint32_t tmem = s.tmem;  // S of the two groups (kN columns each), then O (2 kN: of hi, of lo)
-  Walk<kN, kBlocks> walk(P, start, lo, hi);
-  Segment g;
+  // The next segment of a warp that takes them from the first; false behind the last, and where a wait gave up.
+  auto next_segment = [&](unsigned n, Segment& g) {
+    wait_for(&s.g_full[n & 3], n >> 2 & 1, &s.dead);
+    g = s.segment[n & 3];
+    return g.t1 > 0 && !s.dead;
+  };
+  auto free_segment = [&](unsigned n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.g_free[n & 3]);
+  };
   if (warp == 0) {
-    // ---- tiles by TMA, a lane for each of a tile's boxes
+    // ---- segments, and their tiles by TMA, a lane for each of a tile's boxes
+    Walk<kN, kBlocks> walk(P, start, lo, hi);
     unsigned count = 0;
-    while (walk.next(g)) {
+    for (unsigned n = 0;; ++n) {
+      const Segment g = walk.next();
+      if (n > 3) wait_for(&s.g_free[n & 3], (n >> 2) - 1 & 1, &s.dead);
+      if (s.dead) break;
+      if (lane == 0) {
+        s.segment[n & 3] = g;
+        mbar_arrive(&s.g_full[n & 3]);
+      }
+      __syncwarp();
+      if (g.t1 == 0) break;
       auto page_at = [&](int t) {
-        const int64_t pos = static_cast<int64_t>(t) * kTile + lane * P.box_tokens;
+        const unsigned pos = static_cast<unsigned>(t) * kTile + lane * P.box_tokens;
         int page = -1;
-        if (lane < P.boxes && !g.s.lost && t < g.t1 && pos < g.s.end) page = P.c.page_of(g.b, pos);
+        if (lane < P.boxes && t < g.t1 && pos < g.end) page = P.c.page_of(g.b, pos);
         return page < 0 ? max(1, P.c.pages) : page;  // (behind the last page: zeros)
       };
       int page = page_at(g.t0);
       for (int t = g.t0; t < g.t1; ++t, ++count) {
         const int next = page_at(t + 1);
-        const int token = static_cast<int>((static_cast<int64_t>(t) * kTile + lane * P.box_tokens) & ((1 << P.c.page_log) - 1));
+        const int token = (t * kTile + lane * P.box_tokens) & ((1 << P.c.page_log) - 1);
         const unsigned a = count % kK, b = count % kV;
         if (count >= kK) wait_for(&s.k_empty[a], (count / kK - 1) & 1, &s.dead);
         if (lane == 0) mbar_expect(&s.k_full[a], Z::kTileBytes);
@@ -497,9 +541,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   } else if (warp == 1) {
     // ---- products with K
     constexpr unsigned kShape = (1u << 4) | (static_cast<unsigned>(kN / 8) << 17) | (8u << 24);
-    unsigned count = 0, segment = 0, asked[2] = {0, 0};
-    while (walk.next(g)) {
-      wait_for(&s.q_full, segment++ & 1, &s.dead);
+    unsigned count = 0, asked[2] = {0, 0};
+    Segment g;
+    for (unsigned segment = 0; next_segment(segment, g); free_segment(segment++)) {
+      wait_for(&s.q_full, segment & 1, &s.dead);
       const int items = (g.t1 - g.t0) << (g.two ? 1 : 0);
       for (int i = 0; i < items; ++i) {
         const int w = i & 1;
@@ -528,7 +573,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     constexpr unsigned kShape =
         (1u << 4) | (1u << 15) | (1u << 16) | (static_cast<unsigned>(2 * kN / 8) << 17) | (static_cast<unsigned>(kD / 16) << 24);
     unsigned count = 0, done[2] = {0, 0};
-    while (walk.next(g)) {
+    Segment g;
+    for (unsigned segment = 0; next_segment(segment, g); free_segment(segment++)) {
       const int items = (g.t1 - g.t0) << (g.two ? 1 : 0);
       for (int i = 0; i < items; ++i) {
         const int w = i & 1;
@@ -553,17 +599,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   } else if (warp == 3) {
     // ---- visibility of the positions of special tiles, those with drafted positions or with the sequence's end
     unsigned count = 0;
-    while (walk.next(g)) {
+    Segment g;
+    for (unsigned segment = 0; next_segment(segment, g); free_segment(segment++)) {
       bool built = false, bad = false;
       for (int t = g.t0; t < g.t1; ++t, ++count) {
         const unsigned st = count % kV;
-        const int64_t p0 = static_cast<int64_t>(t) * kTile;
-        const bool special = g.s.lost || p0 + kTile > g.s.context + 1;
-        if (special && !built && !g.s.lost && P.parent) {
+        const unsigned p0 = static_cast<unsigned>(t) * kTile;
+        if (!(g.lost || p0 + kTile > g.root + 1)) {
+          wait_for(&s.v_full[st], count / kV & 1, &s.dead);  // a parity tells a phase only from the one next to it
+          continue;
+        }
+        if (!built && !g.lost && P.parent) {
           // the columns whose path a node is on
           built = true;
-          for (int i = lane; i < g.s.nodes; i += 32) {
-            const int up = P.parent[g.s.start + i];
+          for (int i = lane; i < g.nodes; i += 32) {
+            const int up = P.parent[g.start + i];
             bad |= up < -1 || up >= i;
             s.parent[i] = up;
 #pragma unroll
@@ -571,7 +621,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           }
           bad = __any_sync(~0u, bad);
           __syncwarp();
-          const int last = min(g.s.nodes, (g.c0 + Z::kColumns - 1) / P.group);
+          const int last = min(g.nodes, (g.c0 + Z::kColumns - 1) / P.group);
           for (int i = g.c0 / P.group + lane; !bad && i <= last; i += 32) {
             const int from = i * P.group - g.c0, to = from + P.group;
             for (int node = i - 1; node >= 0; node = s.parent[node])
@@ -584,21 +634,22 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           __syncwarp();
         }
         wait_for(&s.v_full[st], count / kV & 1, &s.dead);
-        if (special) {
+        {
           uint8_t* const v = tiles_v + st * Z::kTileBytes;
 #pragma unroll 1
           for (int i = 0; i < kTile / 32; ++i) {
             const int at = lane + 32 * i;
-            const int64_t pos = p0 + at, node = pos - g.s.context - 1;
-            bool none = g.s.lost;
+            const unsigned pos = p0 + at;
+            const int node = static_cast<int>(pos - g.root - 1);
+            bool none = g.lost;
             uint32_t seen[kWords];
 #pragma unroll
             for (int w = 0; w < kWords; ++w) seen[w] = ~0u;
-            if (!g.s.lost && node >= 0) {
+            if (!g.lost && node >= 0) {
               // What a position holds that not every row sees goes through the product of every row: nothing but numbers
               // may stand there.
               uint4* row = reinterpret_cast<uint4*>(v + at * kD);
-              const bool behind = pos >= g.s.end;
+              const bool behind = pos >= g.end;
               bool nan = false;
               if (!behind)
                 for (int c = 0; c < kD / 16; ++c) nan |= holds_nan(row[c]);
@@ -613,7 +664,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) seen[w] = s.path[node][w];
               } else if (!bad && !lost) {
-                const int from = static_cast<int>(node + 1) * P.group - g.c0;  // the first column that sees it
+                const int from = (node + 1) * P.group - g.c0;  // the first column that sees it
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
                   const int a = from - w * 32;
@@ -639,95 +690,109 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     constexpr int kC = kN / 2;  // columns of a thread
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // 32 lanes of tensor memory each
     const uint32_t tmem_s = tmem + lanes + me * kN + half * kC, tmem_o = tmem + lanes + (2 + 2 * me) * kN + half * kC;
-    unsigned count = 0, items = 0;
+    unsigned count = 0, items = 0, ready = 0;  // ready: a bit for each stage, its barrier's parity
     uint8_t* const mine = weights + me * 2 * Z::kWeights;
-    float* const others = reinterpret_cast<float*>(weights);  // the second group's sums at a segment's end
-    while (walk.next(g)) {
-      const int step = g.two ? 1 : 2, first_tile = g.t0 + (g.two ? 0 : me);
-      // pages and scales of this thread's position, an item and two ahead.  (Positions are below 2^31 + SV_MAX_NODES.)
+    // A query row is read by kLanes lanes, eight entries each, kRows rows a warp at once.  The rows of a segment and the page of
+    // its first tile are on their way while the segment in front is finished.
+    constexpr int kLanes = kD / 8, kRows = 32 / kLanes, kPasses = (Z::kColumns + 16 * kRows - 1) / (16 * kRows);
+    uint4 ahead[kPasses] = {};
+    int page_ahead = -1;
+    auto look_ahead = [&](unsigned n) {
+      wait_for(&s.g_full[n & 3], n >> 2 & 1, &s.dead);
+      page_ahead = -1;
+      if (s.dead) return;
+      const Segment& g = s.segment[n & 3];
+      const unsigned pos = static_cast<unsigned>(g.t0 + (g.two ? 0 : me)) * kTile + position;
+      page_ahead = pos < g.end && g.t0 + (g.two ? 0 : me) < g.t1 ? P.c.table[g.b * P.c.table_stride + (pos >> P.c.page_log)] : -1;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int col = g.c0 + ((warp - 4) + 16 * p) * kRows + lane / kLanes, i = col / P.group;
+        ahead[p] = make_uint4(0, 0, 0, 0);
+        if (g.t1 > 0 && col < g.cols)
+          ahead[p] = *reinterpret_cast<const uint4*>(P.q + (static_cast<int64_t>(g.start) + g.b + i) * P.q_row +
+                                                     (static_cast<int64_t>(g.h) * P.group + col - i * P.group) * P.q_head +
+                                                     lane % kLanes * 8);
+      }
+    };
+    look_ahead(0);
+    for (unsigned segment = 0;; ++segment) {
+      const Segment& g = s.segment[segment & 3];
+      const int t0 = g.t0, t1 = g.t1;
+      const bool two_blocks = g.two;
+      // all of the warps that meet at barriers go on, or none
+      if (groups_any(t1 == 0 || s.dead)) break;
+      const int step = two_blocks ? 1 : 2, first_tile = t0 + (two_blocks ? 0 : me);
+      // pages and scales of this thread's position, an item and two ahead
       const int32_t* const table = P.c.table + g.b * P.c.table_stride;
-      const int64_t of_head = static_cast<int64_t>(g.h) << (P.c.page_log - P.c.block_log);
-      const float *const k_scales = P.c.scales[0] + of_head, *const v_scales = P.c.scales[1] + of_head;
-      const int page_scales = P.c.heads << (P.c.page_log - P.c.block_log);
-      const unsigned in_page = (1u << P.c.page_log) - 1u, end = g.s.lost ? 0u : static_cast<unsigned>(g.s.end);
+      const int of_head = g.h << (P.c.page_log - P.c.block_log);
+      const unsigned end = g.end;
+      const bool lost = g.lost;
       auto page_at = [&](int tile) {
         const unsigned pos = static_cast<unsigned>(tile) * kTile + position;
-        return tile < g.t1 && pos < end ? table[pos >> P.c.page_log] : -1;
+        return tile < t1 && pos < end ? table[pos >> P.c.page_log] : -1;
       };
       auto scales_at = [&](int tile, int page) {
         const unsigned pos = static_cast<unsigned>(tile) * kTile + position;
-        float2 f = make_float2(g.s.lost || pos < end ? NAN : 0.f, 0.f);
+        float2 f = make_float2(lost || pos < end ? NAN : 0.f, 0.f);
         if (static_cast<unsigned>(page) < static_cast<unsigned>(P.c.pages)) {
-          const int64_t at = static_cast<int64_t>(page) * page_scales + ((pos & in_page) >> P.c.block_log);
-          f.x = k_scales[at], f.y = v_scales[at];
+          const int64_t at = static_cast<int64_t>(page) * P.page_scales + of_head + ((pos & P.in_page) >> P.c.block_log);
+          f.x = P.c.scales[0][at], f.y = P.c.scales[1][at];
         }
         return f;
       };
-      int page_next = page_at(first_tile);
-      float2 scales_next = scales_at(first_tile, page_next);
-      page_next = page_at(first_tile + step);
-      // the queries, a warp for each row: two e4m3 numbers an entry, of the entry over its row's power of two
-      constexpr int kPer = kD / 32;
-      const int rows = g.two ? 2 * kN : kN;
-      for (int r = warp - 4; r < rows; r += 16) {
-        const int col = g.c0 + r, i = col / P.group;
-        float q[kPer] = {};
-        if (col < g.s.cols) {
-          const __nv_bfloat16* p = P.q + (static_cast<int64_t>(g.s.start) + g.b + i) * P.q_row +
-                                   (static_cast<int64_t>(g.h) * P.group + col - i * P.group) * P.q_head + lane * kPer;
-          uint32_t u[kPer / 2];
-          if constexpr (kPer == 4) {
-            const uint2 e = *reinterpret_cast<const uint2*>(p);
-            u[0] = e.x, u[1] = e.y;
-          } else {
-            u[0] = *reinterpret_cast<const uint32_t*>(p);
-          }
+      float2 scales_next = scales_at(first_tile, page_ahead);
+      int page_next = page_at(first_tile + step);
+      // the queries over a power of two for each row, as two e4m3 numbers an entry
 #pragma unroll
-          for (int k = 0; k < kPer / 2; ++k)
-            q[2 * k] = __uint_as_float(u[k] << 16), q[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = ((warp - 4) + 16 * p) * kRows + lane / kLanes, col = g.c0 + r, block = r / kN, row = r % kN;
+        if (r - lane / kLanes >= (two_blocks ? 2 : 1) * kN) break;
+        const uint32_t w[4] = {ahead[p].x, ahead[p].y, ahead[p].z, ahead[p].w};
+        float most = 0.f, q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          q[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+          most = fabsf(q[e]) < INFINITY ? fmaxf(most, fabsf(q[e])) : INFINITY;
         }
-        float most = 0.f;
-        bool fine = true;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) most = fmaxf(most, fabsf(q[k])), fine &= fabsf(q[k]) < INFINITY;
-        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-        fine = __all_sync(~0u, fine);
+        for (int o = kLanes / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+        const bool fine = most < INFINITY;
         const float unit = fine ? power_for(most) : 1.f, inverse = 1.f / unit;
-        uint32_t hi = 0, lo = 0;
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < kPer / 2; ++k) {
-          const float a = q[2 * k] * inverse, b = q[2 * k + 1] * inverse;
+        for (int e = 0; e < 8; e += 2) {
+          const float a = q[e] * inverse, b = q[e + 1] * inverse;
           const uint32_t h = e4m3x2(a, b);
           const float2 f = from_e4m3x2(h);
-          hi |= h << (16 * k), lo |= e4m3x2(a - f.x, b - f.y) << (16 * k);
+          hi[e / 4] |= h << (e % 4 * 8), lo[e / 4] |= e4m3x2(a - f.x, b - f.y) << (e % 4 * 8);
         }
-        const int block = r / kN, row = r % kN, byte = lane * kPer, chunk = byte / 16;
-        const int swizzled = kD == 128 ? chunk ^ (row & 7) : chunk ^ (row >> 1 & 3);
-        uint8_t* const to = queries + block * 2 * Z::kQ + row * kD + swizzled * 16 + byte % 16;
-        if constexpr (kPer == 4) {
-          *reinterpret_cast<uint32_t*>(to) = hi, *reinterpret_cast<uint32_t*>(to + Z::kQ) = lo;
-        } else {
-          *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(hi);
-          *reinterpret_cast<uint16_t*>(to + Z::kQ) = static_cast<uint16_t>(lo);
-        }
-        if (lane == 0) {
-          s.row[block][row] = fine ? unit * P.scale : NAN;
-          s.out[block][row] = (static_cast<int64_t>(g.s.start) + g.b + i) * P.out_row +
-                              (static_cast<int64_t>(g.h) * P.group + col - i * P.group) * P.out_head;
+        if (r < (two_blocks ? 2 : 1) * kN) {
+          const int byte = lane % kLanes * 8, chunk = byte / 16;
+          const int swizzled = kD == 128 ? chunk ^ (row & 7) : chunk ^ (row >> 1 & 3);
+          uint8_t* const to = queries + block * 2 * Z::kQ + row * kD + swizzled * 16 + byte % 16;
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to + Z::kQ) = make_uint2(lo[0], lo[1]);
+          if (lane % kLanes == 0) {
+            const int i = col / P.group;
+            s.row[block][row] = fine ? unit * P.scale : NAN;
+            s.out[block][row] = (static_cast<int64_t>(g.start) + g.b + i) * P.out_row +
+                                (static_cast<int64_t>(g.h) * P.group + col - i * P.group) * P.out_head;
+          }
         }
       }
-      if (t < kN) s.ref[me][t] = 0.f;
       // the anchor of the group's value scales: a power of two near the first tile's largest, 2^-60 at least
       float anchor = scales_next.y;
       for (int o = 16; o; o >>= 1) anchor = fmaxf(anchor, __shfl_xor_sync(~0u, anchor, o));
       if (lane == 0) s.anchors[me][quad] = anchor;
       async_fence();
-      groups_sync();  // the rows' factors are there for both groups
+      __syncwarp();
       if (lane == 0) mbar_arrive(&s.q_full);
+      // the first tile with drafted positions or the sequence's end
+      const int first_special = lost ? 0 : static_cast<int>(min((g.root + 1) / kTile, static_cast<unsigned>(t1)));
+      wait_for(&s.q_full, segment & 1, &s.dead);
       anchor = fmaxf(fmaxf(s.anchors[me][0], s.anchors[me][1]), fmaxf(s.anchors[me][2], s.anchors[me][3]));
       anchor = __uint_as_float(__float_as_uint(fminf(fmaxf(anchor, 0x1p-60f), 0x1p100f)) & 0x7f800000u);
       const float per_anchor = 1.f / anchor;
-      const float* const factors = s.row[g.two ? me : 0] + half * kC;
+      const float* const factors = s.row[two_blocks ? me : 0] + half * kC;
       Two l[kC / 2];
 #pragma unroll
       for (int c = 0; c < kC / 2; ++c) l[c] = 0;
@@ -735,8 +800,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       bool unset = true;
       const unsigned begun = items;
       const int own = half * kC + lane / (32 / kC);  // the column that reductions leave to this lane
-      for (int tile = first_tile; tile < g.t1; tile += step) {
-        const unsigned n = count + (tile - g.t0), st = n % kV;
+      for (int tile = first_tile; tile < t1; tile += step) {
+        const unsigned st = (count + (tile - t0)) % kV;
         const float2 scales = scales_next;
         scales_next = scales_at(tile + step, page_next);
         page_next = page_at(tile + 2 * step);
@@ -746,10 +811,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const uint32_t u = __float_as_uint(ratio);
         const int e = max(-12, min(100, static_cast<int>(u >> 23 & 0xff) - 126 - ((u & 0x7fffffu) == 0)));
         const float inverse = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const bool special = g.s.lost || (static_cast<int64_t>(tile) + 1) * kTile > g.s.context + 1;
-        if (special) {
-          wait_for(&s.ready[st], n / kV & 1, &s.dead);
+        uint32_t seen = ~0u;
+        if (tile >= first_special) {
+          wait_for(&s.ready[st], ready >> st & 1u, &s.dead);
           if (s.none[st][quad] >> lane & 1u) kf = NAN;
+          const int col = (two_blocks ? me * kN : 0) + half * kC;
+          seen = s.seen[st][position][col / 32] >> col % 32;
         }
         wait_for(&s.s_full[me], items & 1, &s.dead);
         tc_after();
@@ -758,74 +825,76 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.s_free[me]);
-        // x becomes the logit, log2 of V's scale added, over the reference
         {
+          // x becomes the logit, log2 of V's scale added, over the reference
           const Two kf2 = two(kf, kf), shift = two(static_cast<float>(e), static_cast<float>(e));
-          const float* const refs = s.ref[me] + half * kC;
+          const float* const refs = (items == begun ? s.zero : s.ref[me]) + half * kC;
 #pragma unroll
           for (int c = 0; c < kC; c += 4) {
             const float4 f = *reinterpret_cast<const float4*>(factors + c), r = *reinterpret_cast<const float4*>(refs + c);
             both(fma2(two(x[c], x[c + 1]), mul2(two(f.x, f.y), kf2), add2(shift, two(r.x, r.y))), x[c], x[c + 1]);
             both(fma2(two(x[c + 2], x[c + 3]), mul2(two(f.z, f.w), kf2), add2(shift, two(r.z, r.w))), x[c + 2], x[c + 3]);
           }
-        }
-        if (special) {
-          const int col = (g.two ? me * kN : 0) + half * kC;
-          const uint32_t seen = s.seen[st][position][col / 32] >> col % 32;
+          if (tile >= first_special) {
 #pragma unroll
-          for (int c = 0; c < kC; ++c)
-            if (!(seen >> c & 1u)) x[c] = -INFINITY;
-        }
-        float most = x[0];
+            for (int c = 0; c < kC; ++c)
+              if (!(seen >> c & 1u)) x[c] = -INFINITY;
+          }
+          float most = x[0];
 #pragma unroll
-        for (int c = 1; c < kC; ++c) most = fmaxf(most, x[c]);
-        if (group_any(me, most > kMost || unset || (items - begun) % kRefresh == 0)) {
-          s.most[me][quad][own] = over_lanes<kC, false>(x);
-          group_sync(me);
-          if (t < kN) {
-            const float zt = fmaxf(fmaxf(s.most[me][0][t], s.most[me][1][t]), fmaxf(s.most[me][2][t], s.most[me][3][t]));
-            const bool first = m == -INFINITY;
-            const float from = first ? 0.f : m;
-            float to = from, keep = 1.f;
-            if (zt != -INFINITY) {
-              if (first || !(zt <= kMost && zt >= kLow)) to = from + zt;
-              if (!first) to = fmaxf(to, top - kDeep), keep = power(from - to);
-              m = to, top = fmaxf(top, to);
+          for (int c = 1; c < kC; ++c) most = fmaxf(most, x[c]);
+          // with a weight that is too large in any thread, or for a new reference, the tile's largest are found
+          if (group_any(me, most > kMost || unset || (items - begun) % kRefresh == 0)) {
+            s.most[me][quad][own] = over_lanes<kC, false>(x);
+            group_sync(me);
+            if (t < kN) {
+              const float zt = fmaxf(fmaxf(s.most[me][0][t], s.most[me][1][t]), fmaxf(s.most[me][2][t], s.most[me][3][t]));
+              const bool first = m == -INFINITY;
+              const float from = first ? 0.f : m;
+              float to = from, keep = 1.f;
+              if (zt != -INFINITY) {
+                if (first || !(zt <= kMost && zt >= kLow)) to = from + zt;
+                if (!first) to = fmaxf(to, top - kDeep), keep = power(from - to);
+                m = to, top = fmaxf(top, to);
+              }
+              s.ref[me][t] = -to, s.step[me][t] = from - to, s.keep[me][t] = keep;
+              const unsigned lanes_here = kN < 32 ? (1u << (kN & 31)) - 1u : ~0u;
+              const uint32_t moved = __ballot_sync(lanes_here, keep != 1.f), none = __ballot_sync(lanes_here, m == -INFINITY);
+              if (lane == 0) s.moved[me] = moved, s.unset[me] = none;
             }
-            s.ref[me][t] = -to, s.step[me][t] = from - to, s.keep[me][t] = keep;
-            const unsigned lanes_here = kN < 32 ? (1u << (kN & 31)) - 1u : ~0u;
-            const uint32_t moved = __ballot_sync(lanes_here, keep != 1.f), none = __ballot_sync(lanes_here, m == -INFINITY);
-            if (lane == 0) s.moved[me] = moved, s.unset[me] = none;
-          }
-          group_sync(me);
-          const bool moved = s.moved[me] != 0;
-          unset = s.unset[me] != 0;
-          const float *const steps = s.step[me] + half * kC, *const keeps = s.keep[me] + half * kC;
+            group_sync(me);
+            unset = s.unset[me] != 0;
+            const float *const steps = s.step[me] + half * kC, *const keeps = s.keep[me] + half * kC;
 #pragma unroll
-          for (int c = 0; c < kC; c += 2) {
-            const float2 d = *reinterpret_cast<const float2*>(steps + c), k = *reinterpret_cast<const float2*>(keeps + c);
-            x[c] += d.x, x[c + 1] += d.y;
-            l[c / 2] = mul2(l[c / 2], two(k.x, k.y));
-          }
-          if (moved && items != begun) {
-            wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
-            tc_after();
+            for (int c = 0; c < kC; c += 2) {
+              const float2 d = *reinterpret_cast<const float2*>(steps + c), k = *reinterpret_cast<const float2*>(keeps + c);
+              x[c] += d.x, x[c + 1] += d.y;
+              l[c / 2] = mul2(l[c / 2], two(k.x, k.y));
+            }
+            if (s.moved[me] != 0 && items != begun) {
+              wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
+              tc_after();
 #pragma unroll 1
-            for (int c = 0; c < 2 * kC; c += 8) {
-              const int col = c % kC;
-              const uint32_t at = tmem_o + (c / kC) * kN + col;  // hi's sums, then lo's
-              float o[8];
-              tc_load<8>(at, o);
+              for (int c = 0; c < 2 * kC; c += 8) {
+                const int col = c % kC;
+                const uint32_t at = tmem_o + (c / kC) * kN + col;  // hi's sums, then lo's
+                float o[8];
+                tc_load<8>(at, o);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= keeps[col + k];
-              tc_store(at, o);
+                for (int k = 0; k < 8; ++k) o[k] *= keeps[col + k];
+                tc_store(at, o);
+              }
+              asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+              tc_before();
             }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            tc_before();
           }
         }
         const Two inverse2 = two(inverse, inverse), rest = two(32.f * ratio * inverse, 32.f * ratio * inverse);
-        if (items != begun) wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);  // the weights in front have been read
+        // the weights in front have been read; the sums of the segment in front too
+        if (items != begun)
+          wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
+        else if (segment > 0)
+          wait_for(&s.o_read, (segment - 1) & 1, &s.dead);
 #pragma unroll
         for (int c = 0; c < kC; c += 8) {
           uint32_t hi[4], lo[4];
@@ -847,12 +916,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (lane == 0) mbar_arrive(&s.p_full[me]);
         ++items;
       }
-      count += g.t1 - g.t0;
+      for (int tile = max(t0, first_special); tile < t1; ++tile) ready ^= 1u << (count + (tile - t0)) % kV;
+      count += t1 - t0;
+      look_ahead(segment + 1);
       // ---- the segment's end.  Lane d of tensor memory is entry d: with 64 of them the first 16 lanes of each warp have one.
-      const int d = kD == 128 ? position : quad * 16 + lane;
-      const bool has = kD == 128 || lane < 16, any = items != begun;
-      if (any) wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
-      tc_after();
+      if (items != begun) wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
       {
         float v[kC];
 #pragma unroll
@@ -860,61 +928,67 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         s.most[me][quad][own] = over_lanes<kC, true>(v);
       }
       if (t < kN) s.m[me][t] = m;
-      groups_sync();
-      if (!g.two && me == 1) {
-#pragma unroll 1
-        for (int c = 0; c < kC; c += 8) {
-          float o[8] = {}, u[8] = {};
-          if (any) tc_load<8>(tmem_o + c, o), tc_load<8>(tmem_o + kN + c, u);
-          if (has)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) others[(half * kC + c + k) * kD + d] = fmaf(u[k], 0.03125f, o[k]) * anchor;
-        }
+      if (me == 1 && t == 0) s.second_anchor = anchor;
+      auto sync = [&]() {
+        if (two_blocks)
+          group_sync(me);
+        else
+          groups_sync();
+      };
+      sync();
+      if (t < kN && (two_blocks || me == 0)) {
+        auto sum = [&](int group) {
+          return s.most[group][0][t] + s.most[group][1][t] + s.most[group][2][t] + s.most[group][3][t];
+        };
+        const float m1 = two_blocks ? -INFINITY : s.m[1][t], to = fmaxf(m, m1);
+        const float f0 = m == to ? 1.f : power(m - to), f1 = m1 == -INFINITY ? 0.f : m1 == to ? 1.f : power(m1 - to);
+        float all = sum(me) * f0;
+        if (!two_blocks && f1 != 0.f) all += sum(1) * f1;
+        const float over = s.dead ? NAN : g.whole ? 1.f / all : 1.f;
+        s.worth[me][t] = f0 * over * anchor;
+        if (!two_blocks) s.worth[1][t] = f1 * over * s.second_anchor;
+        s.whole[me][t] = s.dead ? NAN : all;
+        s.last[me][t] = to;
       }
-      if (t < kN && (g.two || me == 0)) {
-        float sum = s.most[me][0][t] + s.most[me][1][t] + s.most[me][2][t] + s.most[me][3][t], to = m, f1 = 0.f;
-        if (!g.two) {
-          to = fmaxf(m, s.m[1][t]);
-          f1 = s.m[1][t] == -INFINITY ? 0.f : power(s.m[1][t] - to);
-          sum = sum * (m == to ? 1.f : power(m - to)) + f1 * (s.most[1][0][t] + s.most[1][1][t] + s.most[1][2][t] + s.most[1][3][t]);
-        }
-        s.keep[me][t] = (m == to ? 1.f : power(m - to)) * anchor;
-        if (!g.two) s.take[t] = f1;
-        s.step[me][t] = sum;
-        m = to;
-      }
-      if (!g.two)
-        groups_sync();
-      else
-        group_sync(me);
-      if (g.two || me == 0) {
-        const int cols = min(kN, g.s.cols - g.c0 - (g.two ? me * kN : 0)), first = g.two ? me * kN : 0;
-        const bool ok = !s.dead;
-        float* const part = P.parts + (2 * static_cast<int64_t>(blockIdx.x) + g.whole_front) * Z::kPart;
+      sync();
+      tc_after();
+      {
+        const int d = kD == 128 ? position : quad * 16 + lane;
+        const bool has = kD == 128 || lane < 16;
+        const int block = two_blocks ? me : 0, cols = min(kN, g.cols - g.c0 - block * kN);
+        float* const part = P.parts + (2 * static_cast<int64_t>(blockIdx.x) + g.front) * Z::kPart;
+        const bool others = !two_blocks && t1 - t0 > 1;  // the second group has sums too
+        // of one block eight columns a warp, which reads both groups' sums; of two each group's own
+        const int from = two_blocks ? half * kC : (me * 2 + half) * 8, to = two_blocks ? from + kC : min(kN, from + 8);
 #pragma unroll 1
-        for (int c = 0; c < kC; c += 8) {
-          float o[8], u[8];
-          tc_load<8>(tmem_o + c, o), tc_load<8>(tmem_o + kN + c, u);
+        for (int c = from; c < to; c += 8) {
+          const uint32_t at = tmem + lanes + (2 + 2 * block) * kN + c;
+          float o[8], u[8], v[8];
+          tc_load<8>(at, o), tc_load<8>(at + kN, u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int col = half * kC + c + k;
-            float v = fmaf(u[k], 0.03125f, o[k]) * s.keep[me][col];
-            if (!g.two && has) v += others[col * kD + d] * s.take[col];
-            if (has && col < cols) {
-              if (g.whole)
-                P.out[s.out[g.two ? me : 0][col] + d] = __float2bfloat16(ok ? v / s.step[me][col] : NAN);
-              else
-                part[(first + col) * kD + d] = v;
-            }
+          for (int k = 0; k < 8; ++k) v[k] = fmaf(u[k], 0.03125f, o[k]) * s.worth[block][c + k];
+          if (others) {
+            tc_load<8>(at + 2 * kN, o), tc_load<8>(at + 3 * kN, u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = fmaf(fmaf(u[k], 0.03125f, o[k]), s.worth[1][c + k], v[k]);
           }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (has && c + k < cols) {
+              if (g.whole)
+                P.out[s.out[block][c + k] + d] = __float2bfloat16(v[k]);
+              else
+                part[(block * kN + c + k) * kD + d] = v[k];
+            }
         }
-        if (!g.whole && t < cols) {
-          part[Z::kColumns * kD + first + t] = m;
-          part[Z::kColumns * (kD + 1) + first + t] = ok ? s.step[me][t] : NAN;
+        if (!g.whole && t < cols && (two_blocks || me == 0)) {
+          part[Z::kColumns * kD + block * kN + t] = s.last[me][t];
+          part[Z::kColumns * (kD + 1) + block * kN + t] = s.whole[me][t];
         }
       }
       tc_before();
-      groups_sync();  // queries, weights and factors are free again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.o_read), mbar_arrive(&s.g_free[segment & 3]);
     }
   }
   tc_before();
@@ -1100,6 +1174,7 @@ extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, in
   P.B = B, P.total = total_nodes, P.max_nodes = max_nodes;
   P.box_tokens = std::min(cache->page_tokens, sv::kTile);
   P.boxes = sv::kTile / P.box_tokens;
+  P.page_scales = cache->heads * (cache->page_tokens / cache->block), P.in_page = static_cast<unsigned>(cache->page_tokens) - 1u;
   P.grid = sms;
   P.parts = static_cast<float*>(workspace);
   sv::Maps maps;

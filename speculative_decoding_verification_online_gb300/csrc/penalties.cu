@@ -27,6 +27,7 @@ namespace {
 constexpr int kPenWarps = 8, kPenThreads = 32 * kPenWarps;
 constexpr int kPenRange = 8192;      // tokens of a CTA at most
 constexpr int kPenLeast = 1024;      // and at least
+constexpr int kAhead = 4;
 constexpr uint32_t kAsked = 1u << 31, kBiased = 1u << 30, kCount = kBiased - 1;
 
 struct PenaltyParams {
@@ -55,17 +56,29 @@ __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __b
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16(v); }
 
-// eight neighbouring logits at a multiple of 16 bytes
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// eight neighbouring logits at a multiple of 16 bytes, as they lie in memory
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-}
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -179,14 +192,29 @@ __global__ void __launch_bounds__(kPenThreads) penalties_kernel(const __grid_con
     if (mask || !P.in_place) {
       const bool vec = P.x_vec && P.y_vec;
       const int whole = vec ? from + (to - from) / 8 * 8 : from;
-      for (int v = from + 8 * lane; v < whole; v += 256) {
-        const uint32_t bits = mask ? mask[v / 32] >> (v % 32) & 0xffu : 0xffu;
-        if (P.in_place && bits == 0xffu) continue;
-        float e[8];
-        if (bits != 0) load8(x + v, e);
+      // runs of eight, kAhead of a lane's on their way at once
+#pragma unroll 1
+      for (int v0 = from + 8 * lane; v0 < whole; v0 += 256 * kAhead) {
+        uint32_t bits[kAhead];
+        Raw8<X> raw[kAhead];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = bits >> k & 1u ? e[k] : -INFINITY;
-        store8(y + v, e);
+        for (int j = 0; j < kAhead; ++j) {
+          const int v = v0 + 256 * j;
+          bits[j] = v < whole ? mask ? mask[v / 32] >> (v % 32) & 0xffu : 0xffu : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (bits[j] != 0 && !(P.in_place && bits[j] == 0xffu)) raw[j].load(x + v0 + 256 * j);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int v = v0 + 256 * j;
+          if (v >= whole || (P.in_place && bits[j] == 0xffu)) continue;
+          float e[8];
+          raw[j].values(e);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) e[k] = bits[j] >> k & 1u ? e[k] : -INFINITY;
+          store8(y + v, e);
+        }
       }
       for (int v = whole + lane; v < to; v += 32) {
         const bool ok = allowed(v);
