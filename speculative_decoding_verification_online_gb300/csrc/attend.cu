@@ -50,6 +50,13 @@ constexpr float kLow = -5.f;   // log2 of what a tile's largest may have fallen 
 constexpr int kRefresh = 16;   // tiles of a group after which that is looked at
 constexpr float kDeep = 60.f;  // log2 of how far a reference may fall below the highest: what is below adds nothing
 
+// where a tile lies among all
+struct Start {
+  int64_t total;
+  int b;
+  int64_t off;  // in sequence b's work
+};
+
 struct AttendParams {
   CacheView c;
   const __nv_bfloat16* q;
@@ -62,7 +69,8 @@ struct AttendParams {
   int boxes, box_tokens;  // boxes of a tile
   int page_scales;        // scales of a page
   unsigned in_page;       // a mask of positions in a page
-  int grid;                       // CTAs that share the tiles
+  int grid;      // CTAs that share the tiles
+  Start* cuts;   // where a CTA's first tile lies: for the second kernel
   float* parts;
 };
 
@@ -96,13 +104,12 @@ __device__ __forceinline__ Sequence sequence_of(const AttendParams& P, int b) {
   return s;
 }
 
-__device__ __forceinline__ int64_t cut(int64_t total, int i, int n) { return total / n * i + total % n * i / n; }
-
-struct Start {
-  int64_t total;
-  int b;
-  int64_t off;  // in sequence b's work
-};
+// the first tile of the i-th of n parts of all tiles
+__device__ __forceinline__ int64_t cut(int64_t total, int i, int n) {
+  if (total < 1 << 22) return static_cast<unsigned>(total) * static_cast<unsigned>(i) / static_cast<unsigned>(n);  // (n below 2^10)
+  const int64_t each = total / n;
+  return each * i + static_cast<unsigned>(total - each * n) * static_cast<unsigned>(i) / static_cast<unsigned>(n);
+}
 
 // Where tile `at(total)` of all lies; every thread of the CTA calls it.
 template <int kColumns, typename F>
@@ -140,6 +147,11 @@ __device__ __forceinline__ void find_tile(const AttendParams& P, F&& at, Start* 
   __syncthreads();
 }
 
+// short where it can be
+__device__ __forceinline__ int64_t divide(int64_t a, int b) {
+  return a < INT32_MAX ? static_cast<int64_t>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+}
+
 // A run of tiles of one unit.  (Positions are below 2^31 + SV_MAX_NODES.)
 struct Segment {
   int b, h, c0, t0, t1;  // c0: the first column; t1 = 0: there are no more
@@ -169,10 +181,10 @@ struct Walk {
       s = sequence_of<kN * kBlocks>(P, b);
       loaded = true;
     }
-    const int64_t unit = off / s.tiles;
+    const int64_t unit = divide(off, s.tiles);
     g.b = b;
-    g.h = static_cast<int>(unit / s.pairs);
-    g.c0 = static_cast<int>(unit % s.pairs) * kN * kBlocks;
+    g.h = static_cast<int>(divide(unit, s.pairs));
+    g.c0 = static_cast<int>(unit - static_cast<int64_t>(g.h) * s.pairs) * kN * kBlocks;
     g.t0 = static_cast<int>(off - unit * s.tiles);
     const int64_t left = hi - pos, here = s.tiles - g.t0, n = left < here ? left : here;
     g.t1 = g.t0 + static_cast<int>(n);
@@ -487,6 +499,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   __syncthreads();
   tc_after();
   const Start start = s.start;
+  if (threadIdx.x == 0) P.cuts[blockIdx.x] = start;
   lo = cut(start.total, blockIdx.x, P.grid);
   const int64_t hi = cut(start.total, blockIdx.x + 1, P.grid);
   const uint32_t tmem = s.tmem;  // S of the two groups (kN columns each), then O (2 kN: of hi, of lo)
@@ -1007,17 +1020,14 @@ constexpr int kJoinThreads = 128;
 template <int kColumns, int kD>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttendParams P) {
   constexpr int kPart = kColumns * (kD + 2);
-  __shared__ Start start;
-  __shared__ int64_t warp_sums[kJoinThreads / 32];
   wait_for_stream();
   // CTA i looks at the cut in front of the i + 1-st of the CTAs that shared the tiles
   const int at = blockIdx.x + 1;
-  int64_t tile = 0;
-  find_tile<kColumns>(P, [&](int64_t total) { return cut(total, at, P.grid); }, &start, warp_sums);
-  tile = cut(start.total, at, P.grid);
+  const Start start = P.cuts[at];
+  const int64_t tile = cut(start.total, at, P.grid);
   if (start.b >= P.B) return;
   const Sequence s = sequence_of<kColumns>(P, start.b);
-  const int64_t unit = start.off / s.tiles, first = tile - (start.off - unit * s.tiles), last = first + s.tiles;
+  const int64_t unit = divide(start.off, s.tiles), first = tile - (start.off - unit * s.tiles), last = first + s.tiles;
   // nothing is cut here, or an earlier cut is in this unit too
   if (tile == first || cut(start.total, at - 1, P.grid) > first) return;
   int parts = 1;
@@ -1032,19 +1042,29 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     return cut(start.total, static_cast<int>(before) + k, P.grid) == cut(start.total, static_cast<int>(before) + k + 1, P.grid);
   };
   for (int c = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; c < cols; c += gridDim.y * (kJoinThreads / 32)) {
+    // a lane has the factors of every 32nd part
     float m = -INFINITY;
     for (int k = lane; k < parts; k += 32)
       if (!empty(k)) m = fmaxf(m, part(k)[kColumns * kD + c]);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     float l = 0.f, v[kD / 32] = {};
-    for (int k = 0; k < parts; ++k) {
-      if (empty(k)) continue;
-      const float* p = part(k);
-      const float mk = p[kColumns * kD + c], f = mk == m ? 1.f : power(mk - m);
-      l += p[kColumns * (kD + 1) + c] * f;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      float f = 0.f;
+      if (k0 + lane < parts && !empty(k0 + lane)) {
+        const float mk = part(k0 + lane)[kColumns * kD + c];
+        f = mk == m ? 1.f : power(mk - m);
+        l += part(k0 + lane)[kColumns * (kD + 1) + c] * f;
+      }
+#pragma unroll 4
+      for (int k = 0; k < min(32, parts - k0); ++k) {
+        const float fk = __shfl_sync(~0u, f, k);
+        const float* p = part(k0 + k) + c * kD + lane;
+        if (fk != 0.f)
 #pragma unroll
-      for (int e = 0; e < kD / 32; ++e) v[e] += p[c * kD + lane + 32 * e] * f;
+          for (int e = 0; e < kD / 32; ++e) v[e] += p[32 * e] * fk;
+      }
     }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
     const int i = (c0 + c) / P.group;
     __nv_bfloat16* const to = P.out + (static_cast<int64_t>(s.start) + start.b + i) * P.out_row +
                               (static_cast<int64_t>(h) * P.group + c0 + c - i * P.group) * P.out_head;
@@ -1129,7 +1149,8 @@ int sms_of(int device) {
 
 extern "C" size_t spec_verify_attend_workspace(int heads, int q_heads, int dim, int max_nodes, int device) {
   if (heads < 1 || q_heads < 1 || dim < 1 || max_nodes < 0 || max_nodes > SV_MAX_NODES) return 0;
-  return static_cast<size_t>(2 * sv::sms_of(device)) * sv::unit_columns(q_heads / heads, max_nodes) * (dim + 2) * sizeof(float);
+  const size_t sms = sv::sms_of(device);
+  return (sms + sms % 2) * sizeof(sv::Start) + 2 * sms * sv::unit_columns(q_heads / heads, max_nodes) * (dim + 2) * sizeof(float);
 }
 
 extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, int64_t q_row, int64_t q_head, void* out,
@@ -1176,7 +1197,8 @@ extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, in
   P.boxes = sv::kTile / P.box_tokens;
   P.page_scales = cache->heads * (cache->page_tokens / cache->block), P.in_page = static_cast<unsigned>(cache->page_tokens) - 1u;
   P.grid = sms;
-  P.parts = static_cast<float*>(workspace);
+  P.cuts = static_cast<sv::Start*>(workspace);
+  P.parts = reinterpret_cast<float*>(P.cuts + sms + (sms & 1));
   sv::Maps maps;
   if (!sv::map_entries(&maps.k, *cache, cache->k, workspace, P.box_tokens) ||
       !sv::map_entries(&maps.v, *cache, cache->v, workspace, P.box_tokens))

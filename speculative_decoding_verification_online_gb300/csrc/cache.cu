@@ -105,13 +105,9 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
   const int64_t end = context + (stop - start) + 1;  // behind the new rows
   const int64_t p0 = ((context >> c.block_log) + j) << c.block_log;
   if (p0 >= end) return;
-  const int page = c.page_of(b, p0);
-  if (page < 0) return;
   const int64_t from = max(p0, context), to = min(p0 + size, end);
   const int runs = c.dim / 8, count = static_cast<int>(to - from) * runs;
   const T* x = static_cast<const T*>(P.x[which]) + (start + b + (from - context)) * P.row[which] + h * P.head[which];
-  float* scale = c.scales[which] + c.scale_at(page, h, p0);
-  const float old = from > p0 ? *scale : 0.f;
   auto source = [&](int i) { return x + i / runs * P.row[which] + i % runs * 8; };
   Run<T> held[kWriteHeld];
   float most = 0.f, v[8];
@@ -120,6 +116,11 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
     const int i = threadIdx.x + k * kWriteThreads;
     if (i < count) held[k].load(source(i), P.vec[which]);
   }
+  // (the page is looked up while the rows are on their way)
+  const int page = c.page_of(b, p0);
+  if (page < 0) return;
+  float* scale = c.scales[which] + c.scale_at(page, h, p0);
+  const float old = from > p0 ? *scale : 0.f;
 #pragma unroll
   for (int k = 0; k < kWriteHeld; ++k)
     if (static_cast<int>(threadIdx.x) + k * kWriteThreads < count) {
@@ -179,89 +180,106 @@ struct KeepParams {
   CacheView c;
   const int32_t *path, *accepted, *context;
   int32_t* new_context;
-  int max_depth, layers, B;
+  int max_depth, layers, parts, tasks;  // tasks: of a CTA at most
 };
 
-constexpr int kKeepThreads = 128;
+constexpr int kKeepThreads = 256;
 
-// A warp moves the rows of one sequence, head and layer, of k or of v.  path[t] >= t rises, so that rows in rising order
-// never lie where an earlier one was put: a block's sources are in blocks from its own on, whose scales and entries are
-// still the old ones when its turn comes.
+struct KeepShared {
+  // of a moved row: its entries before and after, and its scale before (of head 0)
+  int64_t from[SV_MAX_NODES], to[SV_MAX_NODES], scale[SV_MAX_NODES];
+  int bad;
+};
+
+// A CTA looks up where the rows of one sequence lie, and its warps move them, each in every n-th of its tasks: a head of a
+// layer, of k or of v.  path[t] >= t rises, so that rows in rising order never lie where an earlier one was put: a block's
+// sources are in blocks from its own on, whose scales and entries are still the old ones when its turn comes.
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams P) {
+  __shared__ KeepShared s;
   wait_for_stream();
   const CacheView& c = P.c;
-  const int lane = threadIdx.x & 31;
-  int64_t at = (static_cast<int64_t>(blockIdx.x) * kKeepThreads + threadIdx.x) / 32;
-  const int which = static_cast<int>(at & 1);
-  at >>= 1;
-  const int h = static_cast<int>(at % c.heads);
-  at /= c.heads;
-  const int layer = static_cast<int>(at % P.layers), b = static_cast<int>(at / P.layers);
-  if (b >= P.B) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x / P.parts, part = blockIdx.x % P.parts;
   const int64_t context = P.context[b], first = context + 1;
   const int len = P.accepted[b];
   const int32_t* path = P.path + static_cast<int64_t>(b) * P.max_depth;
-  bool good = context >= 0 && len >= 0 && len <= P.max_depth;
   const int size = 1 << c.block_log;
   const int64_t p0 = first >> c.block_log << c.block_log;  // the first block that may receive rows
-  if (good) {
-    for (int t = lane; t < len; t += 32) {
+  bool good = context >= 0 && len >= 0 && len <= P.max_depth;
+  if (threadIdx.x == 0) s.bad = 0;
+  __syncthreads();
+  if (good)
+    for (int t = threadIdx.x; t < len; t += kKeepThreads) {
       const int node = path[t];
-      good &= node > (t ? path[t - 1] : -1) && c.page_of(b, first + node) >= 0 && c.page_of(b, first + t) >= 0;
+      const int page_to = c.page_of(b, first + t);
+      int page_from = -1;
+      if (node > (t ? path[t - 1] : -1)) page_from = c.page_of(b, first + node);
+      if (page_from < 0 || page_to < 0) {
+        s.bad = 1;
+      } else {
+        s.from[t] = c.entry_at(page_from, 0, first + node), s.to[t] = c.entry_at(page_to, 0, first + t);
+        s.scale[t] = c.scale_at(page_from, 0, first + node);
+      }
     }
-    good = __all_sync(~0u, good);
-  }
-  if (which == 0 && h == 0 && layer == 0 && lane == 0 && P.new_context)
+  __syncthreads();
+  good = good && !s.bad;
+  if (part == 0 && threadIdx.x == 0 && P.new_context)
     P.new_context[b] = static_cast<int32_t>(good ? first + len : context);
   if (!good || len == 0) return;
-  uint8_t* entries = c.entries[which] + layer * c.layer;
-  float* scales = c.scales[which] + layer * c.scale_layer;
-  const int per_row = c.dim / 16, rows_at_once = 32 / per_row;
+  const int per_page = c.page_log - c.block_log, per_row = c.dim / 16, rows_at_once = 32 / per_row;
   const int mine = lane / per_row, byte = lane % per_row * 16;
-  for (int64_t block = p0; block < first + len; block += size) {
-    // rows of the block: source position of destination d
-    const int rows = static_cast<int>(min(static_cast<int64_t>(size), first + len - block));
-    auto source = [&](int d) {
-      const int64_t pos = block + d;
-      return pos < first ? pos : first + path[pos - first];
-    };
-    float most = 0.f;
-    for (int d = lane; d < rows; d += 32) {
-      const int64_t pos = source(d);
-      most = fmaxf(most, scales[c.scale_at(c.page_of(b, pos), h, pos)]);
-    }
-    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-    const int page = c.page_of(b, block);
-    const float own = scales[c.scale_at(page, h, block)];
-    const int begin = most == own ? static_cast<int>(max(first - block, int64_t{0})) : 0;  // rows that stay as they are
-    for (int d0 = begin; d0 < rows; d0 += rows_at_once) {
-      const int d = d0 + mine;
-      uint4 e = make_uint4(0, 0, 0, 0);
-      float f = 1.f;
-      if (d < rows) {
-        const int64_t pos = source(d);
-        const int pg = c.page_of(b, pos);
-        e = *reinterpret_cast<const uint4*>(entries + c.entry_at(pg, h, pos) + byte);
-        const float s = scales[c.scale_at(pg, h, pos)];
-        f = most > 0.f ? s / most : 1.f;
-      }
-      __syncwarp();
-      if (d < rows) {
-        if (f != 1.f) {
-          uint32_t w[4] = {e.x, e.y, e.z, e.w};
+  const int tasks = min(P.tasks, P.layers * c.heads * 2 - part * P.tasks);
+#pragma unroll 1
+  for (int i = warp; i < tasks; i += kKeepThreads / 32) {
+    const int task = part * P.tasks + i, which = task & 1, h = (task >> 1) % c.heads, layer = (task >> 1) / c.heads;
+    uint8_t* const entries = c.entries[which] + layer * c.layer + h * c.head;
+    float* const scales = c.scales[which] + layer * c.scale_layer + (static_cast<int64_t>(h) << per_page);
+#pragma unroll 1
+    for (int64_t block = p0; block < first + len; block += size) {
+      // rows of the block: `stay` from its beginning on, then the moved ones t0 .. t1 - 1
+      const int stay = static_cast<int>(max(first - block, int64_t{0})), t0 = static_cast<int>(max(block - first, int64_t{0}));
+      const int t1 = static_cast<int>(min(block + size - first, static_cast<int64_t>(len)));
+      const int64_t at = s.to[t0] - stay * c.token;  // the block's first row
+      // the block's own scale lies with that of its first moved row's destination
+      const int64_t own_at = c.scale_at(c.page_of(b, block), 0, block);
+      // the first rows' entries are on their way with the scales
+      auto load = [&](int t) {
+        return t < t1 ? *reinterpret_cast<const uint4*>(entries + s.from[t] + byte) : make_uint4(0, 0, 0, 0);
+      };
+      uint4 e = load(t0 + mine);
+      const float own = scales[own_at];
+      float most = stay > 0 ? own : 0.f;
+      for (int t = t0 + lane; t < t1; t += 32) most = fmaxf(most, scales[s.scale[t]]);
+      for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+      auto rescaled = [&](uint4 v, float f) {
+        if (f == 1.f) return v;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 lo = from_e4m3x2(w[k] & 0xffffu), hi = from_e4m3x2(w[k] >> 16);
-            w[k] = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
-          }
-          e = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < 4; ++k) {
+          const float2 lo = from_e4m3x2(w[k] & 0xffffu), hi = from_e4m3x2(w[k] >> 16);
+          w[k] = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
         }
-        *reinterpret_cast<uint4*>(entries + c.entry_at(page, h, block) + d * c.token + byte) = e;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      // rows that stay follow a scale that grows
+      if (stay > 0 && most != own)
+        for (int d = mine; d < stay; d += rows_at_once) {
+          uint4* const p = reinterpret_cast<uint4*>(entries + at + d * c.token + byte);
+          *p = rescaled(*p, most > 0.f ? own / most : 1.f);
+        }
+#pragma unroll 1
+      for (int t = t0 + mine; t - mine < t1; t += rows_at_once) {
+        const float f = t < t1 && most > 0.f ? scales[s.scale[t]] / most : 1.f;
+        const uint4 v = rescaled(e, f);
+        const bool moves = t < t1 && (f != 1.f || s.from[t] != s.to[t]);
+        e = load(t + rows_at_once);
+        __syncwarp();
+        if (moves) *reinterpret_cast<uint4*>(entries + s.to[t] + byte) = v;
+        __syncwarp();
       }
+      if (lane == 0 && most != own) scales[own_at] = most;
       __syncwarp();
     }
-    if (lane == 0 && most != own) scales[c.scale_at(page, h, block)] = most;
-    __syncwarp();
   }
 }
 
@@ -324,16 +342,19 @@ extern "C" sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t
   for (const void* p : {static_cast<const void*>(path), static_cast<const void*>(accepted_len),
                         static_cast<const void*>(context), static_cast<const void*>(new_context)})
     if (reinterpret_cast<uintptr_t>(p) % 4) return SV_EINVAL;
-  const __int128 warps = static_cast<__int128>(B) * cache->layers * cache->heads * 2;
-  const __int128 grid = (warps * 32 + sv::kKeepThreads - 1) / sv::kKeepThreads;
-  if (grid > INT32_MAX) return SV_EUNSUPPORTED;
+  // A CTA has eight tasks at least, one a warp, and more where there are CTAs enough without
+  const int64_t all = static_cast<int64_t>(cache->layers) * cache->heads * 2;
+  if (static_cast<__int128>(all) * B > INT32_MAX) return SV_EUNSUPPORTED;
+  const int64_t tasks = std::max<int64_t>(8, std::min<int64_t>(64, (all * B / 1024 + 7) / 8 * 8));
+  const int64_t parts = (all + tasks - 1) / tasks;
   sv::DeviceGuard g(device);
   if (!g.ok) return SV_ECUDA;
   sv::KeepParams P = {};
   P.c = sv::view_of(*cache, page_table, table_stride, table_cols);
   P.path = path, P.accepted = accepted_len, P.context = context, P.new_context = new_context;
-  P.max_depth = max_depth, P.layers = cache->layers, P.B = B;
-  return sv::launch_waiting(sv::keep_kernel, static_cast<unsigned>(grid), sv::kKeepThreads, 0, 1,
+  P.max_depth = max_depth, P.layers = cache->layers;
+  P.parts = static_cast<int>(parts), P.tasks = static_cast<int>(tasks);
+  return sv::launch_waiting(sv::keep_kernel, static_cast<unsigned>(parts * B), sv::kKeepThreads, 0, 1,
                             static_cast<cudaStream_t>(cuda_stream), P) == cudaSuccess
              ? SV_OK
              : SV_ECUDA;
