@@ -34,6 +34,7 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "entry.cuh"
@@ -231,44 +232,42 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// kCols columns (8, or a multiple of 16) of this warp's 32 lanes
+// kCols columns (a multiple of 4) of this warp's 32 lanes
 template <int kCols>
 __device__ __forceinline__ void tc_load(uint32_t addr, float (&f)[kCols]) {
-  if constexpr (kCols == 8) {
+  constexpr int k16 = kCols / 16 * 16, k8 = k16 + (kCols - k16) / 8 * 8;
+#pragma unroll
+  for (int c = 0; c < k16; c += 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(f[c]), "=f"(f[c + 1]), "=f"(f[c + 2]), "=f"(f[c + 3]), "=f"(f[c + 4]), "=f"(f[c + 5]), "=f"(f[c + 6]),
+          "=f"(f[c + 7]), "=f"(f[c + 8]), "=f"(f[c + 9]), "=f"(f[c + 10]), "=f"(f[c + 11]), "=f"(f[c + 12]),
+          "=f"(f[c + 13]), "=f"(f[c + 14]), "=f"(f[c + 15])
+        : "r"(addr + c)
+        : "memory");
+#pragma unroll
+  for (int c = k16; c < k8; c += 8)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-                 : "r"(addr)
+                 : "=f"(f[c]), "=f"(f[c + 1]), "=f"(f[c + 2]), "=f"(f[c + 3]), "=f"(f[c + 4]), "=f"(f[c + 5]), "=f"(f[c + 6]),
+                   "=f"(f[c + 7])
+                 : "r"(addr + c)
                  : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7])
-                 :
+#pragma unroll
+  for (int c = k8; c < kCols; c += 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(f[c]), "=f"(f[c + 1]), "=f"(f[c + 2]), "=f"(f[c + 3])
+                 : "r"(addr + c)
                  : "memory");
-  } else {
+  // the registers pass through the wait, so that nothing reads them in front of it
 #pragma unroll
-    for (int c = 0; c < kCols; c += 16)
-      asm volatile(
-          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-          "%15}, [%16];"
-          : "=f"(f[c]), "=f"(f[c + 1]), "=f"(f[c + 2]), "=f"(f[c + 3]), "=f"(f[c + 4]), "=f"(f[c + 5]), "=f"(f[c + 6]),
-            "=f"(f[c + 7]), "=f"(f[c + 8]), "=f"(f[c + 9]), "=f"(f[c + 10]), "=f"(f[c + 11]), "=f"(f[c + 12]),
-            "=f"(f[c + 13]), "=f"(f[c + 14]), "=f"(f[c + 15])
-          : "r"(addr + c)
-          : "memory");
-#pragma unroll
-    for (int c = 0; c < kCols; c += 16)
-      asm volatile("tcgen05.wait::ld.sync.aligned;"
-                   : "+f"(f[c]), "+f"(f[c + 1]), "+f"(f[c + 2]), "+f"(f[c + 3]), "+f"(f[c + 4]), "+f"(f[c + 5]),
-                     "+f"(f[c + 6]), "+f"(f[c + 7]), "+f"(f[c + 8]), "+f"(f[c + 9]), "+f"(f[c + 10]), "+f"(f[c + 11]),
-                     "+f"(f[c + 12]), "+f"(f[c + 13]), "+f"(f[c + 14]), "+f"(f[c + 15])
-                   :
-                   : "memory");
-  }
+  for (int c = 0; c < kCols; c += 4)
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(f[c]), "+f"(f[c + 1]), "+f"(f[c + 2]), "+f"(f[c + 3]) : : "memory");
 }
 
-// eight columns back
-__device__ __forceinline__ void tc_store(uint32_t addr, const float (&f)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(f[0]), "f"(f[1]), "f"(f[2]),
-               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "r"(addr)
+// four columns back
+__device__ __forceinline__ void tc_store(uint32_t addr, const float (&f)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "r"(addr)
                : "memory");
 }
 
@@ -423,6 +422,42 @@ struct Sizes {
   static_assert(kSmem <= 227 * 1024);
 };
 
+// a stage of a ring, and how often it has been passed modulo 2
+template <int kStages>
+struct Ring {
+  int at = 0;
+  unsigned phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++at == kStages) at = 0, phase ^= 1;
+  }
+};
+
+// The pages of a segment's tiles, a lane's of its box, looked up a tile ahead.
+struct Pages {
+  const AttendParams& P;
+  const int32_t* table;
+  unsigned end, box;  // box: the first position of this lane's box in a tile, or far behind
+  int t1, ahead;
+  __device__ __forceinline__ Pages(const AttendParams& P, const Segment& g, int lane)
+      : P(P), table(P.c.table + g.b * P.c.table_stride), end(g.end), t1(g.t1) {
+    box = lane < P.boxes ? lane * P.box_tokens : ~0u;
+    ahead = look(g.t0);
+  }
+  __device__ __forceinline__ int look(int t) const {
+    const unsigned pos = static_cast<unsigned>(t) * kTile + box;
+    return box != ~0u && t < t1 && pos < end ? table[pos >> P.c.page_log] : -1;
+  }
+  // of tile t, the one after the last asked for; behind the last page (zeros) where there is none
+  __device__ __forceinline__ int next(int t) {
+    const int page = ahead;
+    ahead = look(t + 1);
+    return static_cast<unsigned>(page) < static_cast<unsigned>(P.c.pages) ? page : max(1, P.c.pages);
+  }
+  __device__ __forceinline__ int token(int t) const {
+    return static_cast<int>((static_cast<unsigned>(t) * kTile + box) & P.in_page);
+  }
+};
+
 __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 256;" ::"r"(1 + group) : "memory"); }
 // whether any thread of a group says so
 __device__ __forceinline__ bool group_any(int group, bool mine) {
@@ -460,7 +495,8 @@ __device__ __forceinline__ bool holds_nan(uint4 e) {
   return (hit(e.x) | hit(e.y) | hit(e.z) | hit(e.w)) != 0;
 }
 
-template <int kN, int kBlocks, int kD>
+// kC: columns of a thread, half of those of a block that are used.
+template <int kN, int kBlocks, int kC, int kD>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendParams P,
                                                                    const __grid_constant__ Maps maps) {
   using Z = Sizes<kN, kBlocks, kD>;
@@ -487,6 +523,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     s.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // columns that are not used have weights too
+  for (int i = threadIdx.x; i < 4 * Z::kWeights / 16; i += kAttendThreads)
+    reinterpret_cast<uint4*>(weights)[i] = make_uint4(0, 0, 0, 0);
+  async_fence();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)), "n"(8 * kN)
                  : "memory");
@@ -513,10 +553,22 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.g_free[n & 3]);
   };
+  // A tile of K or of V by TMA, a lane for each of its boxes.  (One warp for K, one for V: with one for both 1500 cycles a tile,
+  // more than anything else of it.)
+  auto copy_tile = [&](Pages& pages, int t, const CUtensorMap* map, uint8_t* tiles, uint64_t* full, uint64_t* empty, int st,
+                       unsigned phase, int h) {
+    const int page = pages.next(t);
+    wait_for(&empty[st], phase ^ 1, &s.dead);
+    if (lane == 0) mbar_expect(&full[st], Z::kTileBytes);
+    if (lane < P.boxes)
+      tma_load(map, smem_addr(tiles) + st * Z::kTileBytes + lane * P.box_tokens * kD, &full[st], pages.token(t), h, page);
+  };
   if (warp == 0) {
-    // ---- segments, and their tiles by TMA, a lane for each of a tile's boxes
+    // ---- segments; their tiles of K; the visibility of the positions of special tiles, those with drafted positions or with
+    // the sequence's end
     Walk<kN, kBlocks> walk(P, start, lo, hi);
-    unsigned count = 0;
+    Ring<kK> ring;
+    Ring<kV> ring_v;
     for (unsigned n = 0;; ++n) {
       const Segment g = walk.next();
       if (n > 3) wait_for(&s.g_free[n & 3], (n >> 2) - 1 & 1, &s.dead);
@@ -527,28 +579,88 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       }
       __syncwarp();
       if (g.t1 == 0) break;
-      auto page_at = [&](int t) {
-        const unsigned pos = static_cast<unsigned>(t) * kTile + lane * P.box_tokens;
-        int page = -1;
-        if (lane < P.boxes && t < g.t1 && pos < g.end) page = P.c.page_of(g.b, pos);
-        return page < 0 ? max(1, P.c.pages) : page;  // (behind the last page: zeros)
-      };
-      int page = page_at(g.t0);
-      for (int t = g.t0; t < g.t1; ++t, ++count) {
-        const int next = page_at(t + 1);
-        const int token = (t * kTile + lane * P.box_tokens) & ((1 << P.c.page_log) - 1);
-        const unsigned a = count % kK, b = count % kV;
-        if (count >= kK) wait_for(&s.k_empty[a], (count / kK - 1) & 1, &s.dead);
-        if (lane == 0) mbar_expect(&s.k_full[a], Z::kTileBytes);
+      Pages pages(P, g, lane);
+      bool built = false, bad = false;
+#pragma unroll 1
+      for (int t = g.t0; t < g.t1; ++t, ring.step(), ring_v.step()) {
+        copy_tile(pages, t, &maps.k, tiles_k, s.k_full, s.k_empty, ring.at, ring.phase, g.h);
+        const unsigned p0 = static_cast<unsigned>(t) * kTile;
+        const int st = ring_v.at;
+        if (!(g.lost || p0 + kTile > g.root + 1)) continue;
+        if (!built && !g.lost && P.parent) {
+          // the columns whose path a node is on
+          built = true;
+          for (int i = lane; i < g.nodes; i += 32) {
+            const int up = P.parent[g.start + i];
+            bad |= up < -1 || up >= i;
+            s.parent[i] = up;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) s.path[i][w] = 0;
+          }
+          bad = __any_sync(~0u, bad);
+          __syncwarp();
+          const int last = min(g.nodes, (g.c0 + Z::kColumns - 1) / P.group);
+          for (int i = g.c0 / P.group + lane; !bad && i <= last; i += 32) {
+            const int from = i * P.group - g.c0, to = from + P.group;
+            for (int node = i - 1; node >= 0; node = s.parent[node])
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                const int a = max(0, from - w * 32), e = min(32, to - w * 32);
+                if (e > a) atomicOr(&s.path[node][w], (e - a == 32 ? ~0u : ((1u << (e - a)) - 1u)) << a);
+              }
+          }
+          __syncwarp();
+        }
+        // (a parity tells a phase only from the one next to it: not before the tile that was there has been used)
+        wait_for(&s.v_empty[st], ring_v.phase ^ 1, &s.dead);
+        wait_for(&s.v_full[st], ring_v.phase, &s.dead);
+        {
+          uint8_t* const v = tiles_v + st * Z::kTileBytes;
+#pragma unroll 1
+          for (int i = 0; i < kTile / 32; ++i) {
+            const int at = lane + 32 * i;
+            const unsigned pos = p0 + at;
+            const int node = static_cast<int>(pos - g.root - 1);
+            bool none = g.lost;
+            uint32_t seen[kWords];
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) seen[w] = ~0u;
+            if (!g.lost && node >= 0) {
+              // What a position holds that not every row sees goes through the product of every row: nothing but numbers
+              // may stand there.
+              uint4* row = reinterpret_cast<uint4*>(v + at * kD);
+              const bool behind = pos >= g.end;
+              bool nan = false;
+              if (!behind)
+                for (int c = 0; c < kD / 16; ++c) nan |= holds_nan(row[c]);
+              if (nan || behind)
+                for (int c = 0; c < kD / 16; ++c) row[c] = make_uint4(0, 0, 0, 0);
+              none = nan || bad;
+              const bool lost = !behind && P.c.page_of(g.b, pos) < 0;  // every row of the sequence is
+              if (behind) {
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) seen[w] = 0;
+              } else if (!bad && !lost && P.parent) {
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) seen[w] = s.path[node][w];
+              } else if (!bad && !lost) {
+                const int from = (node + 1) * P.group - g.c0;  // the first column that sees it
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                  const int a = from - w * 32;
+                  seen[w] = a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
+                }
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) s.seen[st][at][w] = seen[w];
+            const uint32_t bits = __ballot_sync(~0u, none);
+            if (lane == 0) s.none[st][i] = bits;
+          }
+          async_fence();
+        }
         __syncwarp();
-        if (lane < P.boxes)
-          tma_load(&maps.k, smem_addr(tiles_k + a * Z::kTileBytes) + lane * P.box_tokens * kD, &s.k_full[a], token, g.h, page);
-        if (count >= kV) wait_for(&s.v_empty[b], (count / kV - 1) & 1, &s.dead);
-        if (lane == 0) mbar_expect(&s.v_full[b], Z::kTileBytes);
-        __syncwarp();
-        if (lane < P.boxes)
-          tma_load(&maps.v, smem_addr(tiles_v + b * Z::kTileBytes) + lane * P.box_tokens * kD, &s.v_full[b], token, g.h, page);
-        page = next;
+        if (lane == 0) mbar_arrive(&s.ready[st]);
       }
     }
   } else if (warp == 1) {
@@ -610,97 +722,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       count += g.t1 - g.t0;
     }
   } else if (warp == 3) {
-    // ---- visibility of the positions of special tiles, those with drafted positions or with the sequence's end
-    unsigned count = 0;
+    // ---- tiles of V
     Segment g;
+    Ring<kV> ring;
     for (unsigned segment = 0; next_segment(segment, g); free_segment(segment++)) {
-      bool built = false, bad = false;
-      for (int t = g.t0; t < g.t1; ++t, ++count) {
-        const unsigned st = count % kV;
-        const unsigned p0 = static_cast<unsigned>(t) * kTile;
-        if (!(g.lost || p0 + kTile > g.root + 1)) {
-          wait_for(&s.v_full[st], count / kV & 1, &s.dead);  // a parity tells a phase only from the one next to it
-          continue;
-        }
-        if (!built && !g.lost && P.parent) {
-          // the columns whose path a node is on
-          built = true;
-          for (int i = lane; i < g.nodes; i += 32) {
-            const int up = P.parent[g.start + i];
-            bad |= up < -1 || up >= i;
-            s.parent[i] = up;
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) s.path[i][w] = 0;
-          }
-          bad = __any_sync(~0u, bad);
-          __syncwarp();
-          const int last = min(g.nodes, (g.c0 + Z::kColumns - 1) / P.group);
-          for (int i = g.c0 / P.group + lane; !bad && i <= last; i += 32) {
-            const int from = i * P.group - g.c0, to = from + P.group;
-            for (int node = i - 1; node >= 0; node = s.parent[node])
-#pragma unroll
-              for (int w = 0; w < kWords; ++w) {
-                const int a = max(0, from - w * 32), e = min(32, to - w * 32);
-                if (e > a) atomicOr(&s.path[node][w], (e - a == 32 ? ~0u : ((1u << (e - a)) - 1u)) << a);
-              }
-          }
-          __syncwarp();
-        }
-        wait_for(&s.v_full[st], count / kV & 1, &s.dead);
-        {
-          uint8_t* const v = tiles_v + st * Z::kTileBytes;
-#pragma unroll 1
-          for (int i = 0; i < kTile / 32; ++i) {
-            const int at = lane + 32 * i;
-            const unsigned pos = p0 + at;
-            const int node = static_cast<int>(pos - g.root - 1);
-            bool none = g.lost;
-            uint32_t seen[kWords];
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) seen[w] = ~0u;
-            if (!g.lost && node >= 0) {
-              // What a position holds that not every row sees goes through the product of every row: nothing but numbers
-              // may stand there.
-              uint4* row = reinterpret_cast<uint4*>(v + at * kD);
-              const bool behind = pos >= g.end;
-              bool nan = false;
-              if (!behind)
-                for (int c = 0; c < kD / 16; ++c) nan |= holds_nan(row[c]);
-              if (nan || behind)
-                for (int c = 0; c < kD / 16; ++c) row[c] = make_uint4(0, 0, 0, 0);
-              none = nan || bad;
-              const bool lost = !behind && P.c.page_of(g.b, pos) < 0;  // every row of the sequence is
-              if (behind) {
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) seen[w] = 0;
-              } else if (!bad && !lost && P.parent) {
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) seen[w] = s.path[node][w];
-              } else if (!bad && !lost) {
-                const int from = (node + 1) * P.group - g.c0;  // the first column that sees it
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) {
-                  const int a = from - w * 32;
-                  seen[w] = a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
-                }
-              }
-            }
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) s.seen[st][at][w] = seen[w];
-            const uint32_t bits = __ballot_sync(~0u, none);
-            if (lane == 0) s.none[st][i] = bits;
-          }
-          async_fence();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.ready[st]);
-      }
+      Pages pages(P, g, lane);
+      for (int t = g.t0; t < g.t1; ++t, ring.step())
+        copy_tile(pages, t, &maps.v, tiles_v, s.v_full, s.v_empty, ring.at, ring.phase, g.h);
     }
   } else {
     // ---- softmax
     const int me = (warp - 4) / 8, half = (warp - 4) / 4 & 1, quad = warp & 3;
     const int t = threadIdx.x - 128 - me * kGroupThreads, position = t & (kTile - 1);
-    constexpr int kC = kN / 2;  // columns of a thread
+    constexpr int kPad = kC == 12 ? 16 : kC, kUsed = 2 * kC;
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // 32 lanes of tensor memory each
     const uint32_t tmem_s = tmem + lanes + me * kN + half * kC, tmem_o = tmem + lanes + (2 + 2 * me) * kN + half * kC;
     unsigned count = 0, items = 0, ready = 0;  // ready: a bit for each stage, its barrier's parity
@@ -812,7 +846,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       float m = -INFINITY, top = -INFINITY;  // m: of column t, its reference
       bool unset = true;
       const unsigned begun = items;
-      const int own = half * kC + lane / (32 / kC);  // the column that reductions leave to this lane
+      const int own = lane / (32 / kPad);  // the column of its half that reductions leave to this lane
+      // each column's largest, or sum, over this warp's positions
+      auto post = [&](const float (&v)[kC], auto sum) {
+        float r;
+        if constexpr (kPad == kC) {
+          r = over_lanes<kC, sum.value>(v);
+        } else {
+          float w[kPad];
+#pragma unroll
+          for (int c = 0; c < kPad; ++c) w[c] = c < kC ? v[c < kC ? c : 0] : sum.value ? 0.f : -INFINITY;
+          r = over_lanes<kPad, sum.value>(w);
+        }
+        if (own < kC) s.most[me][quad][half * kC + own] = r;
+      };
       for (int tile = first_tile; tile < t1; tile += step) {
         const unsigned st = (count + (tile - t0)) % kV;
         const float2 scales = scales_next;
@@ -858,9 +905,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           for (int c = 1; c < kC; ++c) most = fmaxf(most, x[c]);
           // with a weight that is too large in any thread, or for a new reference, the tile's largest are found
           if (group_any(me, most > kMost || unset || (items - begun) % kRefresh == 0)) {
-            s.most[me][quad][own] = over_lanes<kC, false>(x);
+            post(x, std::false_type());
             group_sync(me);
-            if (t < kN) {
+            if (t < kUsed) {
               const float zt = fmaxf(fmaxf(s.most[me][0][t], s.most[me][1][t]), fmaxf(s.most[me][2][t], s.most[me][3][t]));
               const bool first = m == -INFINITY;
               const float from = first ? 0.f : m;
@@ -871,7 +918,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 m = to, top = fmaxf(top, to);
               }
               s.ref[me][t] = -to, s.step[me][t] = from - to, s.keep[me][t] = keep;
-              const unsigned lanes_here = kN < 32 ? (1u << (kN & 31)) - 1u : ~0u;
+              const unsigned lanes_here = kUsed < 32 ? (1u << (kUsed & 31)) - 1u : ~0u;
               const uint32_t moved = __ballot_sync(lanes_here, keep != 1.f), none = __ballot_sync(lanes_here, m == -INFINITY);
               if (lane == 0) s.moved[me] = moved, s.unset[me] = none;
             }
@@ -888,13 +935,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
               wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
               tc_after();
 #pragma unroll 1
-              for (int c = 0; c < 2 * kC; c += 8) {
+              for (int c = 0; c < 2 * kC; c += 4) {
                 const int col = c % kC;
                 const uint32_t at = tmem_o + (c / kC) * kN + col;  // hi's sums, then lo's
-                float o[8];
-                tc_load<8>(at, o);
+                float o[4];
+                tc_load<4>(at, o);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] *= keeps[col + k];
+                for (int k = 0; k < 4; ++k) o[k] *= keeps[col + k];
                 tc_store(at, o);
               }
               asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -908,21 +955,33 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
         else if (segment > 0)
           wait_for(&s.o_read, (segment - 1) & 1, &s.dead);
+        // runs of 16 columns, 16 bytes a position
+        uint32_t hi[kC / 4], lo[kC / 4];
 #pragma unroll
-        for (int c = 0; c < kC; c += 8) {
-          uint32_t hi[4], lo[4];
+        for (int c = 0; c < kC; c += 2) {
+          const Two p = two(power(x[c]), power(x[c + 1]));
+          l[c / 2] = fma2(p, inverse2, l[c / 2]);
+          uint32_t h, r;
+          split2(mul2(p, rest), h, r);
+          if (c % 4 == 0)
+            hi[c / 4] = h, lo[c / 4] = r;
+          else
+            hi[c / 4] |= h << 16, lo[c / 4] |= r << 16;
+        }
+        uint8_t* const to = mine + position * 16;
+        auto run = [&](int col) { return to + col / 16 * (kTile * 16) + col % 16; };
+        if constexpr (kC == 16) {
+          *reinterpret_cast<uint4*>(run(half * kC)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(run(half * kC) + Z::kWeights) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        } else if constexpr (kC == 8) {
+          *reinterpret_cast<uint2*>(run(half * kC)) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(run(half * kC) + Z::kWeights) = make_uint2(lo[0], lo[1]);
+        } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = c + 2 * k;
-            const Two p = two(power(x[at]), power(x[at + 1]));
-            l[at / 2] = fma2(p, inverse2, l[at / 2]);
-            split2(mul2(p, rest), hi[k], lo[k]);
+          for (int c = 0; c < kC; c += 4) {
+            *reinterpret_cast<uint32_t*>(run(half * kC + c)) = hi[c / 4];
+            *reinterpret_cast<uint32_t*>(run(half * kC + c) + Z::kWeights) = lo[c / 4];
           }
-          // runs of 16 columns, 16 bytes a position
-          const int col = half * kC + c;
-          uint2* const to = reinterpret_cast<uint2*>(mine + col / 16 * (kTile * 16) + position * 16 + col % 16);
-          to[0] = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          to[Z::kWeights / 8] = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
         async_fence();
         __syncwarp();
@@ -938,9 +997,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         float v[kC];
 #pragma unroll
         for (int k = 0; k < kC; k += 2) both(l[k / 2], v[k], v[k + 1]);
-        s.most[me][quad][own] = over_lanes<kC, true>(v);
+        post(v, std::true_type());
       }
-      if (t < kN) s.m[me][t] = m;
+      if (t < kUsed) s.m[me][t] = m;
       if (me == 1 && t == 0) s.second_anchor = anchor;
       auto sync = [&]() {
         if (two_blocks)
@@ -949,7 +1008,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           groups_sync();
       };
       sync();
-      if (t < kN && (two_blocks || me == 0)) {
+      if (t < kUsed && (two_blocks || me == 0)) {
         auto sum = [&](int group) {
           return s.most[group][0][t] + s.most[group][1][t] + s.most[group][2][t] + s.most[group][3][t];
         };
@@ -972,7 +1031,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         float* const part = P.parts + (2 * static_cast<int64_t>(blockIdx.x) + g.front) * Z::kPart;
         const bool others = !two_blocks && t1 - t0 > 1;  // the second group has sums too
         // of one block eight columns a warp, which reads both groups' sums; of two each group's own
-        const int from = two_blocks ? half * kC : (me * 2 + half) * 8, to = two_blocks ? from + kC : min(kN, from + 8);
+        const int from = two_blocks ? half * kC : (me * 2 + half) * 8, to = two_blocks ? from + kC : min(kUsed, from + 8);
 #pragma unroll 1
         for (int c = from; c < to; c += 8) {
           const uint32_t at = tmem + lanes + (2 + 2 * block) * kN + c;
@@ -1116,10 +1175,10 @@ int unit_columns(int group, int max_nodes) {
   return cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
 }
 
-template <int kN, int kBlocks, int kD>
+template <int kN, int kBlocks, int kC, int kD>
 sv_status launch_attend(const AttendParams& P, const Maps& maps, int device, cudaStream_t st) {
   constexpr int smem = Sizes<kN, kBlocks, kD>::kSmem;
-  const auto kernel = attend_kernel<kN, kBlocks, kD>;
+  const auto kernel = attend_kernel<kN, kBlocks, kC, kD>;
   static std::atomic<bool> opted_in[64];
   if (device >= 64 || !opted_in[device].load()) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SV_ECUDA;
@@ -1133,10 +1192,12 @@ sv_status launch_attend(const AttendParams& P, const Maps& maps, int device, cud
 }
 
 template <int kD>
-sv_status launch_attend(const AttendParams& P, const Maps& maps, int columns, int device, cudaStream_t st) {
-  return columns == 16   ? launch_attend<16, 1, kD>(P, maps, device, st)
-         : columns == 32 ? launch_attend<32, 1, kD>(P, maps, device, st)
-                         : launch_attend<32, 2, kD>(P, maps, device, st);
+sv_status launch_attend(const AttendParams& P, const Maps& maps, int columns, int64_t used, int device, cudaStream_t st) {
+  // a thread takes half of the columns that there are, in fours
+  if (columns == 16) return used <= 8 ? launch_attend<16, 1, 4, kD>(P, maps, device, st) : launch_attend<16, 1, 8, kD>(P, maps, device, st);
+  if (columns == 32)
+    return used <= 24 ? launch_attend<32, 1, 12, kD>(P, maps, device, st) : launch_attend<32, 1, 16, kD>(P, maps, device, st);
+  return launch_attend<32, 2, 16, kD>(P, maps, device, st);
 }
 
 int sms_of(int device) {
@@ -1205,6 +1266,7 @@ extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, in
     return SV_ECUDA;
   const int columns = sv::unit_columns(P.group, max_nodes);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  return cache->dim == 128 ? sv::launch_attend<128>(P, maps, columns, device, st)
-                           : sv::launch_attend<64>(P, maps, columns, device, st);
+  const int64_t used = static_cast<int64_t>(max_nodes + 1) * P.group;
+  return cache->dim == 128 ? sv::launch_attend<128>(P, maps, columns, used, device, st)
+                           : sv::launch_attend<64>(P, maps, columns, used, device, st);
 }
