@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   uint8_t* const base = raw + sizeof(Shared) + ((1024 - (smem_addr(raw + sizeof(Shared)) & 1023)) & 1023);
   uint8_t* const tiles_k = base;
   uint8_t* const tiles_v = tiles_k + kK * Z::kTileBytes;
-  uint8_t* const queries = tiles_v + kV * Z::kTileBytes;            // [block][hi, lo]
+  uint8_t* const queries = tiles_v + kV * Z::kTileBytes;            // [hi, lo][block]
   uint8_t* const weights = queries + 2 * kBlocks * Z::kQ;       // [warpgroup][hi, lo]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -664,30 +664,34 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       }
     }
   } else if (warp == 1) {
-    // ---- products with K
-    constexpr unsigned kShape = (1u << 4) | (static_cast<unsigned>(kN / 8) << 17) | (8u << 24);
-    unsigned count = 0, asked[2] = {0, 0};
+    // ---- products with K; of two blocks at once, whose sums lie side by side
+    constexpr unsigned kShape = (1u << 4) | (8u << 24);
+    unsigned count = 0, asked = 0, begun = 0;  // asked: a bit for each group, how often modulo 2
+    const uint64_t q = rows_desc<kD>(smem_addr(queries));
     Segment g;
     for (unsigned segment = 0; next_segment(segment, g); free_segment(segment++)) {
       wait_for(&s.q_full, segment & 1, &s.dead);
-      const int items = (g.t1 - g.t0) << (g.two ? 1 : 0);
-      for (int i = 0; i < items; ++i) {
-        const int w = i & 1;
-        const unsigned n = count + (g.two ? i / 2 : i), st = n % kK;
-        if (!g.two || w == 0) wait_for(&s.k_full[st], n / kK & 1, &s.dead);
-        if (asked[w] > 0) wait_for(&s.s_free[w], (asked[w] - 1) & 1, &s.dead);
-        ++asked[w];
+      const unsigned shape = kShape | static_cast<unsigned>((g.two ? 2 * kN : kN) / 8) << 17;
+      for (int i = 0; i < g.t1 - g.t0; ++i) {
+        const unsigned n = count + i, st = n % kK;
+        wait_for(&s.k_full[st], n / kK & 1, &s.dead);
+        const unsigned groups = g.two ? 3u : 1u << (i & 1);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (groups & begun & 1u << w) wait_for(&s.s_free[w], ~asked >> w & 1u, &s.dead);
+        asked ^= groups, begun |= groups;
         tc_after();
         const uint64_t k = rows_desc<kD>(smem_addr(tiles_k + st * Z::kTileBytes));
-        const uint64_t q = rows_desc<kD>(smem_addr(queries + (g.two ? w : 0) * 2 * Z::kQ));
+        const uint32_t to = tmem + (groups == 2u ? kN : 0);
         if (elect_one()) {
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
             for (int d = 0; d < kD / 32; ++d)
-              tc_mma(tmem + w * kN, k + 2 * d, q + piece * (Z::kQ / 16) + 2 * d, kShape, piece + d > 0);
-          tc_commit(&s.s_full[w]);
-          if (!g.two || w == 1) tc_commit(&s.k_empty[st]);
+              tc_mma(to, k + 2 * d, q + piece * (kBlocks * Z::kQ / 16) + 2 * d, shape, piece + d > 0);
+          if (groups & 1u) tc_commit(&s.s_full[0]);
+          if (groups & 2u) tc_commit(&s.s_full[1]);
+          tc_commit(&s.k_empty[st]);
         }
         __syncwarp();
       }
@@ -815,9 +819,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (r < (two_blocks ? 2 : 1) * kN) {
           const int byte = lane % kLanes * 8, chunk = byte / 16;
           const int swizzled = kD == 128 ? chunk ^ (row & 7) : chunk ^ (row >> 1 & 3);
-          uint8_t* const to = queries + block * 2 * Z::kQ + row * kD + swizzled * 16 + byte % 16;
+          uint8_t* const to = queries + block * Z::kQ + row * kD + swizzled * 16 + byte % 16;
           *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(to + Z::kQ) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(to + kBlocks * Z::kQ) = make_uint2(lo[0], lo[1]);
           if (lane % kLanes == 0) {
             const int i = col / P.group;
             s.row[block][row] = fine ? unit * P.scale : NAN;
@@ -826,7 +830,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           }
         }
       }
-      // the anchor of the group's value scales: a power of two near the first tile's largest, 2^-60 at least
+      // the anchor of the group's value scales: a power of two near the first tile's largest, 2^-110 at least
       float anchor = scales_next.y;
       for (int o = 16; o; o >>= 1) anchor = fmaxf(anchor, __shfl_xor_sync(~0u, anchor, o));
       if (lane == 0) s.anchors[me][quad] = anchor;
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       const int first_special = lost ? 0 : static_cast<int>(min((g.root + 1) / kTile, static_cast<unsigned>(t1)));
       wait_for(&s.q_full, segment & 1, &s.dead);
       anchor = fmaxf(fmaxf(s.anchors[me][0], s.anchors[me][1]), fmaxf(s.anchors[me][2], s.anchors[me][3]));
-      anchor = __uint_as_float(__float_as_uint(fminf(fmaxf(anchor, 0x1p-60f), 0x1p100f)) & 0x7f800000u);
+      anchor = __uint_as_float(__float_as_uint(fminf(fmaxf(anchor, 0x1p-110f), 0x1p100f)) & 0x7f800000u);
       const float per_anchor = 1.f / anchor;
       const float* const factors = s.row[two_blocks ? me : 0] + half * kC;
       Two l[kC / 2];
@@ -869,7 +873,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         // V's scale over the anchor: rest * 2^e, rest in (1/2, 1], e -12 at least
         const float ratio = scales.y * per_anchor;
         const uint32_t u = __float_as_uint(ratio);
-        const int e = max(-12, min(100, static_cast<int>(u >> 23 & 0xff) - 126 - ((u & 0x7fffffu) == 0)));
+        const int e = max(-12, min(120, static_cast<int>(u >> 23 & 0xff) - 126 - ((u & 0x7fffffu) == 0)));
         const float inverse = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         uint32_t seen = ~0u;
         if (tile >= first_special) {

@@ -584,23 +584,28 @@ def _cache(cache, dev, layered):
     """sv_cache of (k, v, k_scale, v_scale), checked."""
     k, v, ks, vs = cache
     f8, f32 = torch.float8_e4m3fn, torch.float32
-    dim = len(k.shape)
+    st, shape, ss, scales = k.stride(), k.shape, ks.stride(), ks.shape
+    dim = len(shape)
     if dim != 4 and not (layered and dim == 5):
         raise ValueError(f"cache k: {dim} dimensions, expected {'4 or 5' if layered else 4}")
-    st = _check_rows(k, "cache k", dim, f8, dev)
-    if _check_rows(v, "cache v", dim, f8, dev) != st or v.shape != k.shape:
+    if k.dtype != f8 or v.dtype != f8 or ks.dtype != f32 or vs.dtype != f32:
+        raise TypeError(f"cache: dtypes {k.dtype}, {v.dtype}, {ks.dtype}, {vs.dtype}, expected {f8} twice and {f32} twice")
+    if k.device != dev or v.device != dev or ks.device != dev or vs.device != dev:
+        raise ValueError(f"cache: on {k.device}, {v.device}, {ks.device}, {vs.device}, expected {dev}")
+    if v.stride() != st or v.shape != shape:
         raise ValueError("cache v: shape and strides differ from those of k")
-    pages, heads, tokens, d = k.shape[-4:]
-    per = ks.shape[-1]
-    ss = _check_rows(ks, "cache k_scale", dim - 1, f32, dev)
-    if _check_rows(vs, "cache v_scale", dim - 1, f32, dev) != ss or vs.shape != ks.shape:
+    if vs.stride() != ss or vs.shape != scales:
         raise ValueError("cache v_scale: shape and strides differ from those of k_scale")
-    if ks.shape[:-1] != k.shape[:-2] or per < 1 or tokens % per:
-        raise ValueError(f"cache k_scale: shape {tuple(ks.shape)} does not go with k {tuple(k.shape)}")
-    if (heads > 1 and ss[-2] != per) or (pages > 1 and ss[-3] != heads * per):
+    pages, heads, tokens, d = shape[-4:]
+    per = scales[-1]
+    if scales[:-1] != shape[:-2] or per < 1 or tokens % per:
+        raise ValueError(f"cache k_scale: shape {tuple(scales)} does not go with k {tuple(shape)}")
+    if st[-1] != 1 and d > 1:
+        raise ValueError("cache k: the entries of a token must be contiguous")
+    if (per > 1 and ss[-1] != 1) or (heads > 1 and ss[-2] != per) or (pages > 1 and ss[-3] != heads * per):
         raise ValueError("cache k_scale must be contiguous")
     # a stride over one entry may be anything: it is not used
-    layers = k.shape[0] if dim == 5 else 1
+    layers = shape[0] if dim == 5 else 1
     return SvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), st[0] if layers > 1 else 0,
                    st[-4] if pages > 1 else 0, st[-3] if heads > 1 else 0, st[-2] if tokens > 1 else d,
                    ss[0] if layers > 1 else 0, layers, pages, heads, tokens, tokens // per, d)
@@ -805,14 +810,19 @@ class SpecVerifier:
         return o
 
     def run_hidden(self, target_hidden, target_head, draft_hidden, draft_head, D, temperature, target_bias=None,
-                   draft_bias=None, cap=None, logits_dtype=torch.bfloat16, **kw):
-        """Verify from hidden states: the output heads' products, then ``run``.
+                   draft_bias=None, cap=None, logits_dtype=torch.bfloat16, penalties=None, **kw):
+        """Verify from hidden states: the output heads' products, penalties on the logits, then ``run``.
 
         ``target_hidden`` [B, k+1, H] with ``target_head`` [V, H];
         ``draft_hidden`` [B, k, H'] with ``draft_head`` [V, H'], or [k, V, H']
         for a head per position (all bfloat16), and biases [V] (or [k, V]).
-        ``cap`` bounds both sides' logits (cap * tanh(z / cap)).  ``kw`` goes to
-        ``run``; the result also holds target_logits and draft_logits."""
+        ``cap`` bounds both sides' logits (cap * tanh(z / cap)).  ``penalties``: what
+        ``penalize`` takes by these names -- history, history_len, prompt_len,
+        repetition, frequency, presence, bias -- for the rows of both sides, row j
+        of which stands behind D[:, :j]; mask and mask_row for the target's [B *
+        (k+1)] rows, draft_mask and draft_mask_row for the draft's [B * k].  ``kw``
+        goes to ``run``; the result also holds target_logits and draft_logits, as
+        they were verified."""
         B, k, V, dev = target_hidden.shape[0], self.k, self.V, self.device
         _check(target_hidden, "target_hidden", (B, k + 1, target_hidden.shape[-1]), torch.bfloat16, dev)
         _check(draft_hidden, "draft_hidden", (B, k, draft_hidden.shape[-1]), torch.bfloat16, dev)
@@ -826,6 +836,17 @@ class SpecVerifier:
         else:
             linear(draft_hidden.view(B * k, draft_hidden.shape[-1]), draft_head, bias=draft_bias,
                    out=Ld.view(B * k, V), **act)
+        if penalties is not None:
+            _check(D, "draft_tokens", (B, k), torch.int32, dev)
+            both = {name: t for name, t in penalties.items() if "mask" not in name}
+            tokens, start = _new(dev, stream, lambda: (D[:, :k - 1].reshape(-1), [
+                torch.arange(B + 1, dtype=torch.int32, device=dev) * n for n in (k, k - 1)]))
+            penalize(Lt.view(B * (k + 1), V), tokens=D.view(-1), parent=None, node_start=start[0], max_nodes=k,
+                     mask=penalties.get("mask"), mask_row=penalties.get("mask_row"), out=Lt.view(B * (k + 1), V),
+                     stream=stream, **both)
+            penalize(Ld.view(B * k, V), tokens=tokens, parent=None, node_start=start[1], max_nodes=k - 1,
+                     mask=penalties.get("draft_mask"), mask_row=penalties.get("draft_mask_row"), out=Ld.view(B * k, V),
+                     stream=stream, **both)
         out = self.run(Lt, Ld, D, temperature, **kw)
         out["target_logits"], out["draft_logits"] = Lt, Ld
         return out

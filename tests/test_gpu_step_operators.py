@@ -742,3 +742,56 @@ def test_steps_captured_and_on_other_streams(sv):
                 assert torch.equal(torch.nan_to_num(want[name].float()), torch.nan_to_num(got[name].float())), name
         for a, b in zip(eager_cache, caches[0][0]):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("k", [1, 4])
+def test_run_hidden_with_penalties_is_its_parts(sv, k):
+    B, V, H = 6, 1500, 128
+    g = gen(31)
+    th, dh = (torch.randn(B, n, H, generator=g, device="cuda").to(bf16) for n in (k + 1, k))
+    head = (torch.randn(V, H, generator=g, device="cuda") * 0.2).to(bf16)
+    D = torch.randint(0, 40, (B, k), generator=g, device="cuda").to(i32)
+    pen = dict(history=torch.randint(0, 60, (B, 50), generator=g, device="cuda").to(i32),
+               history_len=torch.randint(0, 51, (B,), generator=g, device="cuda").to(i32),
+               repetition=1.0 + torch.rand(B, generator=g, device="cuda"), presence=torch.rand(B, generator=g, device="cuda"))
+    masks = [torch.full((B * n, (V + 31) // 32), -1, dtype=i32, device="cuda") for n in (k + 1, k)]
+    for m in masks:
+        m[:, 7] = 0
+    ver = sv.SpecVerifier(B, k, V, device=0)
+    try:
+        got = ver.run_hidden(th, head, dh, head, D, 0.9, seed=3, logits_dtype=f32,
+                             penalties=dict(pen, mask=masks[0], draft_mask=masks[1]))
+        for name, hidden, n, m in (("target_logits", th, k + 1, masks[0]), ("draft_logits", dh, k, masks[1])):
+            z = sv.linear(hidden.reshape(B * n, H), head, out_dtype=f32)
+            nodes = D[:, :n - 1].contiguous()
+            start = ints(*range(0, B * (n - 1) + 1, n - 1)) if n > 1 else torch.zeros(B + 1, dtype=i32, device="cuda")
+            want, size = ref.penalties(z, tokens=nodes.view(-1), parent=None, node_start=start, mask=m, **pen)
+            have = ref.doubles(got[name].view(B * n, V))
+            fine = np.isfinite(want)
+            assert np.array_equal(fine, np.isfinite(have)) and not fine[:, 7 * 32].any()
+            assert np.all(np.abs(have[fine] - want[fine]) <= 20 * 2.0 ** -24 * (size + np.abs(want))[fine])
+        again = ver.run(got["target_logits"], got["draft_logits"], D, 0.9, seed=3)
+        assert torch.equal(again["tokens"], got["tokens"])
+    finally:
+        ver.close()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group,nodes", [(1, 3), (4, 0), (8, 0), (3, 2), (4, 3), (5, 4), (8, 2), (6, 4), (8, 4), (4, 12), (7, 8)])
+def test_attend_as_many_columns_as_a_call_may_need(sv, dim, group, nodes):
+    # 4 to 64 columns of a key head: each of the kernel's widths, with sequences that fill it and others that do not
+    sizes = [nodes, 0, max(0, nodes - 1), nodes]
+    c = attend_case(group * 31 + nodes, [700, 1, 130, 3000], sizes, 2, group, dim, 64, 32)
+    assert_attends(sv.attend_tree(**c), c)
+
+
+def test_attend_values_scales_of_any_size(sv):
+    # scales that differ from position to position, a million times, zeros among them; and blocks whose values are all zero
+    c = attend_case(17, [900, 40], [5, 2], 1, 4, 128, 64, 1)
+    g = gen(8)
+    vs = c["cache"][3]
+    vs.mul_(torch.exp(torch.randn(vs.shape, generator=g, device="cuda") * 3))
+    vs[torch.rand(vs.shape, generator=g, device="cuda") < 0.1] = 2.0 ** -100
+    assert_attends(sv.attend_tree(**c), c)
+    vs.fill_(2.0 ** -100)
+    assert_attends(sv.attend_tree(**c), c)
