@@ -25,6 +25,16 @@
 // Work is cut evenly over the SMs, whatever the lengths: all tiles of all units (sequence, key
 // head, columns) in a row, a CTA taking the n-th part of them.  A unit that
 // is cut leaves its parts in the workspace, and a second kernel joins them.
+//
+// Measured (with the joining kernel):
+//   64 chains of five drafts after up to 8192 positions, 8 key heads of 128, 4 query heads
+//     to each: 144.9 us, 5.6 TB/s (reading alone takes 121)
+//   the same with one row and 4096 positions each: 77.2 us (60.3)
+//   2 chains of four after 131071, 8 key heads of 64, 5 query heads to each: 93.8 us (40.1);
+//     the weights' arithmetic bounds it: entries of 64 are half the bytes of a weight
+//   32 trees of up to 21 nodes after up to 4000, 4 key heads of 128, 8 query heads to each:
+//     99.7 us (16.0); 176 columns are three units of 64, and the weights bound it
+//   one row after 1000 positions: 16.2 us, two launches and a chain of waits
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -1,7 +1,19 @@
 // Rows into a cache of 8-bit entries, and the rows of an accepted path together:
 // spec_verify_cache_write, spec_verify_cache_keep.
 //
-// Both are bound by memory, and by latency for the few rows of a step.
+// Writing: a CTA has the new rows of one block of entries, of keys or of values, and keeps
+// them in registers between the search for the largest magnitude and the rounding: rows
+// are read once.  Rows of 64 trees of up to 21 nodes, 8 heads of 128, bf16: 6.0 us; 32
+// prompts of up to 2048 tokens: 54.1 us, 5.6 TB/s.  What bounds that one is instructions as much as memory:
+// the largest magnitude is therefore looked for among the bits, two bf16 at once, and
+// finiteness is one question for the whole block (80.8 us with a test and a float
+// maximum for every entry).  128 threads with 8 runs each were the best: 256 with 4 take
+// 67.5 us, several blocks a CTA with the next one's rows on their way 133 us.
+//
+// Keeping: a CTA has some of a sequence's rows, and a warp moves one row of one head with
+// its scale; where the rows lie is looked up once for all.  64 accepted paths in 16 layers
+// of 8 heads of 128: 8.0 us, which is latency: the path, the pages, the scales, the rows,
+// each known from the one before.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,6 +56,14 @@ struct Run<float> {
   __device__ __forceinline__ void values(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
+  // the largest bits of a magnitude (as whole numbers: those of infinities and NaN are above all others), and them as fp32's
+  __device__ __forceinline__ uint32_t most(uint32_t m) const {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t top(uint32_t m) { return m; }
 };
 template <>
 struct Run<__nv_bfloat16> {
@@ -62,6 +82,13 @@ struct Run<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+  __device__ __forceinline__ uint32_t most(uint32_t m) const {  // of both halves
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[i] & 0x7fff7fffu));
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t top(uint32_t m) { return max(m & 0xffffu, m >> 16) << 16; }
 };
 
 // the largest finite magnitude
@@ -89,7 +116,7 @@ __device__ __forceinline__ uint2 pack8(const float (&v)[8]) {
 // A CTA writes one block of tokens of one head, of k or of v.
 template <typename T>
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_constant__ WriteParams P) {
-  __shared__ float warp_most[kWriteThreads / 32];
+  __shared__ uint32_t warp_most[kWriteThreads / 32];
   wait_for_stream();
   const CacheView& c = P.c;
   int at = blockIdx.x;
@@ -106,11 +133,10 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
   const int64_t p0 = ((context >> c.block_log) + j) << c.block_log;
   if (p0 >= end) return;
   const int64_t from = max(p0, context), to = min(p0 + size, end);
-  const int runs = c.dim / 8, count = static_cast<int>(to - from) * runs;
+  const int runs_log = c.dim == 128 ? 4 : 3, runs = 1 << runs_log, count = static_cast<int>(to - from) << runs_log;
   const T* x = static_cast<const T*>(P.x[which]) + (start + b + (from - context)) * P.row[which] + h * P.head[which];
-  auto source = [&](int i) { return x + i / runs * P.row[which] + i % runs * 8; };
+  auto source = [&](int i) { return x + (i >> runs_log) * P.row[which] + (i & (runs - 1)) * 8; };
   Run<T> held[kWriteHeld];
-  float most = 0.f, v[8];
 #pragma unroll
   for (int k = 0; k < kWriteHeld; ++k) {
     const int i = threadIdx.x + k * kWriteThreads;
@@ -121,30 +147,47 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
   if (page < 0) return;
   float* scale = c.scales[which] + c.scale_at(page, h, p0);
   const float old = from > p0 ? *scale : 0.f;
+  // f of every run, held or not
+  auto each = [&](auto f) {
 #pragma unroll
-  for (int k = 0; k < kWriteHeld; ++k)
-    if (static_cast<int>(threadIdx.x) + k * kWriteThreads < count) {
-      held[k].values(v);
-      most = largest(v, most);
+    for (int k = 0; k < kWriteHeld; ++k)
+      if (static_cast<int>(threadIdx.x) + k * kWriteThreads < count) f(threadIdx.x + k * kWriteThreads, held[k]);
+    for (int i = threadIdx.x + kWriteHeld * kWriteThreads; i < count; i += kWriteThreads) {
+      Run<T> r;
+      r.load(source(i), P.vec[which]);
+      f(i, r);
     }
-  for (int i = threadIdx.x + kWriteHeld * kWriteThreads; i < count; i += kWriteThreads) {
-    Run<T> r;
-    r.load(source(i), P.vec[which]);
-    r.values(v);
-    most = largest(v, most);
+  };
+  auto over_all = [&](uint32_t bits) {
+    bits = __reduce_max_sync(~0u, bits);
+    if (threadIdx.x % 32 == 0) warp_most[threadIdx.x / 32] = bits;
+    __syncthreads();
+    for (int w = 0; w < kWriteThreads / 32; ++w) bits = max(bits, warp_most[w]);
+    return bits;
+  };
+  uint32_t bits = 0;
+  each([&](int, const Run<T>& r) { bits = r.most(bits); });
+  bits = over_all(Run<T>::top(bits));
+  float v[8];
+  const bool finite = bits < 0x7f800000u;
+  if (!finite) {  // once more, without what is not
+    float most = 0.f;
+    each([&](int, const Run<T>& r) {
+      r.values(v);
+      most = largest(v, most);
+    });
+    __syncthreads();
+    bits = over_all(__float_as_uint(most));
   }
-  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-  if (threadIdx.x % 32 == 0) warp_most[threadIdx.x / 32] = most;
-  __syncthreads();
-  for (int w = 0; w < kWriteThreads / 32; ++w) most = fmaxf(most, warp_most[w]);
+  const float most = __uint_as_float(bits);
   const float need = scale_for(most);
   const float now = from > p0 ? (need > old ? need : old) : need;
   uint8_t* entries = c.entries[which] + c.entry_at(page, h, p0);
   const float inverse = 1.f / now;
   if (from > p0 && now != old) {
-    const int older = static_cast<int>(from - p0) * runs;
+    const int older = static_cast<int>(from - p0) << runs_log;
     for (int i = threadIdx.x; i < older; i += kWriteThreads) {
-      uint2* p = reinterpret_cast<uint2*>(entries + i / runs * c.token + i % runs * 8);
+      uint2* p = reinterpret_cast<uint2*>(entries + (i >> runs_log) * c.token + (i & (runs - 1)) * 8);
       const uint2 e = *p;
       const uint32_t two[4] = {e.x & 0xffffu, e.x >> 16, e.y & 0xffffu, e.y >> 16};
 #pragma unroll
@@ -155,22 +198,12 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
       *p = pack8(v);
     }
   }
-  auto put = [&](int i, const Run<T>& r) {
+  each([&](int i, const Run<T>& r) {
     r.values(v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < INFINITY ? v[k] * inverse : NAN;
-    *reinterpret_cast<uint2*>(entries + (from - p0 + i / runs) * c.token + i % runs * 8) = pack8(v);
-  };
-#pragma unroll
-  for (int k = 0; k < kWriteHeld; ++k) {
-    const int i = threadIdx.x + k * kWriteThreads;
-    if (i < count) put(i, held[k]);
-  }
-  for (int i = threadIdx.x + kWriteHeld * kWriteThreads; i < count; i += kWriteThreads) {
-    Run<T> r;
-    r.load(source(i), P.vec[which]);
-    put(i, r);
-  }
+    for (int k = 0; k < 8; ++k) v[k] = finite || fabsf(v[k]) < INFINITY ? v[k] * inverse : NAN;
+    *reinterpret_cast<uint2*>(entries + (from - p0 + (i >> runs_log)) * c.token + (i & (runs - 1)) * 8) = pack8(v);
+  });
   if (threadIdx.x == 0) *scale = now;
 }
 
