@@ -588,7 +588,8 @@ sv_status spec_verify_cache_write(const sv_cache* cache, const void* k, const vo
  * behind is free.  A block that receives rows gets the largest of the scales that
  * its rows (the moved ones, and those in front of context[b] + 1 that stay) had;
  * entries become round(entry * old / new).
- *   new_context [B] (optional, not `context` itself): context[b] + 1 +
+ *   No two sequences may share a page that holds a step's rows.
+ *   new_context [B] (optional; must not overlap context, accepted_len or path): context[b] + 1 +
  *     accepted_len[b]; context[b] where nothing was accepted because the
  *     sequence is padded or invalid (accepted_len[b] outside [0, max_depth], a
  *     path that does not rise from at least 0, a position without a page, as
@@ -608,7 +609,7 @@ sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t* path, int
  *   q, out: bfloat16, row r, head h at r * row + h * head, dim contiguous entries
  *     each; q_row, q_head multiples of 8, q on a multiple of 16 bytes.  out must not
  *     overlap q or the cache.
- *   scale: finite.
+ *   scale: finite (SV_EUNSUPPORTED beyond 2^126).
  *   workspace: device memory of spec_verify_attend_workspace(...) bytes, on a
  *     multiple of 16, that no other call uses meanwhile; it holds parts of long
  *     contexts until they are joined, and nothing between calls.

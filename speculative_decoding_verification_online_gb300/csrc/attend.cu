@@ -1237,6 +1237,7 @@ extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, in
   if (sv_status s = sv::check_cache(cache, 1); s != SV_OK) return s;
   if (sv_status s = sv::check_table(page_table, table_stride, table_cols, B); s != SV_OK) return s;
   if (q_heads < 1 || q_heads % cache->heads || !std::isfinite(scale)) return SV_EINVAL;
+  if (std::fabs(scale) > 0x1p126f) return SV_EUNSUPPORTED;  // (in base 2 it is 1.44 times as large)
   if (B < 0 || total_nodes < 0 || max_nodes < 0) return SV_EINVAL;
   if (max_nodes > SV_MAX_NODES) return SV_EUNSUPPORTED;
   if (q_row < 0 || q_head < 0 || out_row < 0 || out_head < 0) return SV_EINVAL;

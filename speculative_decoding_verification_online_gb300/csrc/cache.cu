@@ -375,9 +375,16 @@ extern "C" sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t
   for (const void* p : {static_cast<const void*>(path), static_cast<const void*>(accepted_len),
                         static_cast<const void*>(context), static_cast<const void*>(new_context)})
     if (reinterpret_cast<uintptr_t>(p) % 4) return SV_EINVAL;
-  // A CTA has eight tasks at least, one a warp, and more where there are CTAs enough without
   const int64_t all = static_cast<int64_t>(cache->layers) * cache->heads * 2;
   if (static_cast<__int128>(all) * B > INT32_MAX) return SV_EUNSUPPORTED;
+  // CTAs read while another one writes its sequence's
+  if (new_context) {
+    const sv::Extent to = {new_context, 4, B, 0, 1, 0, 1};
+    if (sv::sure_to_overlap({context, 4, B, 0, 1, 0, 1}, to) || sv::sure_to_overlap({accepted_len, 4, B, 0, 1, 0, 1}, to) ||
+        (max_depth > 0 && sv::sure_to_overlap({path, 4, max_depth, max_depth, B, 0, 1}, to)))
+      return SV_EINVAL;
+  }
+  // A CTA has eight tasks at least, one a warp, and more where there are CTAs enough without
   const int64_t tasks = std::max<int64_t>(8, std::min<int64_t>(64, (all * B / 1024 + 7) / 8 * 8));
   const int64_t parts = (all + tasks - 1) / tasks;
   sv::DeviceGuard g(device);

@@ -630,7 +630,8 @@ def cache_write(cache, k, v, page_table, context, node_start, max_nodes=None, st
     they go to the positions ``context[b]``, ``context[b] + 1``, ...  ``page_table``
     [B, columns], ``context`` [B] and ``node_start`` [B + 1] are int32.  A prompt
     of n tokens is a sequence with n - 1 nodes.  ``max_nodes`` bounds a sequence's
-    nodes (default: the number of nodes).  How scales follow the entries:
+    nodes (default: the number of nodes; blocks of threads are launched for as many
+    in every sequence, so that a batch of prompts should name its longest).  How scales follow the entries:
     ``spec_verify_cache_write`` in include/spec_verify.h."""
     dev = _cuda_device(k, "k")
     c = _cache(cache, dev, False)

@@ -111,6 +111,19 @@ def test_attend_refuses(change, status):
     assert _cached(sv.spec_verify_attend, ATTEND, change) == status
 
 
+@pytest.mark.parametrize("change", [
+    dict(new_context=A + 4), dict(context=A + FAR, new_context=A), dict(context=A + FAR, new_context=A + 4),
+    dict(context=A + FAR, accepted_len=A + FAR, new_context=A + 12),
+    dict(context=A + FAR, accepted_len=A + FAR, new_context=A - 4)])
+def test_cache_keep_refuses_new_contexts_over_what_it_reads(change):
+    assert _cached(sv.spec_verify_cache_keep, KEEP, change) == m.SV_EINVAL
+
+
+@pytest.mark.parametrize("scale", [1.01 * 2.0 ** 126, -3e38])
+def test_attend_refuses_scales_that_leave_fp32(scale):
+    assert _cached(sv.spec_verify_attend, ATTEND, dict(scale=scale)) == m.SV_EUNSUPPORTED
+
+
 def test_batches_of_nothing_are_no_ops():
     assert _call(sv.spec_verify_penalties, PENALTIES, dict(B=0, logits=None, out=None)) == m.SV_OK
     assert _cached(sv.spec_verify_cache_write, WRITE, dict(B=0, k=None)) == m.SV_OK
