@@ -4,7 +4,7 @@
 //
 // Keys and values go from memory to the tensor cores as they are, in 8 bits.  A query of
 // eight significant bits is the exact sum of two e4m3 numbers (times a power of two for
-// its row), and a weight is rounded to two: hi = e4m3(w), lo = e4m3(w - hi), as good as
+// its row; an entry below 2^-11 of the row's largest is off by 2^-17.8 of it at most), and a weight is rounded to two: hi = e4m3(w), lo = e4m3(w - hi), as good as
 // a rounding to bf16.  So S = K (Qhi + Qlo)^T and O = V^T (Phi + Plo), two products each
 // at twice the rate of bf16's, and nothing is converted but queries and weights.
 //
