@@ -332,6 +332,27 @@ def test_cache_write_values_that_are_none_and_zeros(sv):
         assert_cache(cache, want)
 
 
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_cache_write_values_that_are_none_anywhere_in_a_large_block(sv, dtype, offset):
+    # in every quarter of a block, in every place of a run of eight, of either sign; rows without a finite value
+    heads, dim, tokens, block, n = 2, 128, 256, 256, 250
+    none = [float("nan"), float("inf"), float("-inf")]
+    for at in range(0, n, 31):
+        cache = make_cache(at, 2, heads, tokens, dim, block)
+        table, g = ints(1).view(1, 1), gen(at)
+        k, v = (torch.randn(n, heads, dim + offset, generator=g, device="cuda").to(dtype)[:, :, offset:] for _ in range(2))
+        k[at, 0, at % dim] = none[at % 3]
+        k[n - 1 - at, 1, (3 * at) % dim] = none[(at + 1) % 3]
+        k[at, 1, 5] = -1e30
+        v[:, 0] = none[at % 3]
+        v[at] = none[(at + 2) % 3]
+        want = ref.Cache(cache, table)
+        want.write(k, v, ints(3), ints(0, n - 1))
+        sv.cache_write(cache, k, v, table, ints(3), ints(0, n - 1))
+        assert_cache(cache, want, at)
+
+
 def test_cache_write_leaves_what_is_not_its_own(sv):
     # padded and invalid sequences, positions without pages
     heads, dim, tokens, block = 2, 64, 16, 8
@@ -617,6 +638,29 @@ def test_attend_long_contexts_are_split_and_joined(sv):
     context, sizes = [30000, 3, 9001], [4, 2, 0]
     c = attend_case(12, context, sizes, 1, 4, 64, 64, 64)
     assert_attends(sv.attend_tree(**c), c)
+
+
+def test_attend_sequences_that_share_the_pages_of_a_prefix(sv):
+    c = attend_case(12, [150, 131, 128, 400], [3, 0, 5, 2], 2, 4, 128, 64, 16)
+    c["page_table"][:, :2] = c["page_table"][:1, :2].clone()
+    assert_attends(sv.attend_tree(**c), c)
+
+
+def test_attend_two_calls_at_once_with_the_same_inputs(sv):
+    # on two streams, again and again: each has a workspace of its own
+    c = attend_case(13, [3000, 77, 900], [9, 4, 0], 4, 4, 128, 64, 64)
+    alone = sv.attend_tree(**c)
+    assert_attends(alone, c)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(sv.attend_tree(**c))
+    torch.cuda.synchronize()
+    for out in outs[0] + outs[1]:
+        assert torch.equal(out.view(torch.int16), alone.view(torch.int16))
 
 
 def test_attend_is_deterministic(sv):
