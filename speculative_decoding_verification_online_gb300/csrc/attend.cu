@@ -4,8 +4,9 @@
 //
 // Keys and values go from memory to the tensor cores as they are, in 8 bits.  A query of
 // eight significant bits is the exact sum of two e4m3 numbers (times a power of two for
-// its row; an entry below 2^-11 of the row's largest is off by 2^-17.8 of it at most), and a weight is rounded to two: hi = e4m3(w), lo = e4m3(w - hi), as good as
-// a rounding to bf16.  So S = K (Qhi + Qlo)^T and O = V^T (Phi + Plo), two products each
+// its row; an entry below 2^-11 of the row's largest is off by 2^-17.8 of it at most), and
+// a weight is rounded to two: hi = e4m3(w), lo = e4m3(w - hi), as good as a rounding to
+// bf16.  So S = K (Qhi + Qlo)^T and O = V^T (Phi + Plo), two products each
 // at twice the rate of bf16's, and nothing is converted but queries and weights.
 //
 // A key head's query rows (all rows of the step times the query heads of its group) are
@@ -28,8 +29,8 @@
 //
 // Measured (with the joining kernel):
 //   64 chains of five drafts after up to 8192 positions, 8 key heads of 128, 4 query heads
-//     to each: 144.9 us, 5.6 TB/s (reading alone takes 121)
-//   the same with one row and 4096 positions each: 77.2 us (60.3)
+//     to each: 143.4 us, 5.65 TB/s (reading alone takes 121)
+//   the same with one row and 4096 positions each: 76.6 us (60.3)
 //   2 chains of four after 131071, 8 key heads of 64, 5 query heads to each: 93.8 us (40.1);
 //     the weights' arithmetic bounds it: entries of 64 are half the bytes of a weight
 //   32 trees of up to 21 nodes after up to 4000, 4 key heads of 128, 8 query heads to each:
@@ -637,14 +638,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             for (int w = 0; w < kWords; ++w) seen[w] = ~0u;
             if (!g.lost && node >= 0) {
               // What a position holds that not every row sees goes through the product of every row: nothing but numbers
-              // may stand there.
+              // may stand there.  (Lanes begin at different places of their rows: at the same one all of them would meet
+              // in four banks.  256 contexts of 300 positions 97.8 us, 92.9 so.)
               uint4* row = reinterpret_cast<uint4*>(v + at * kD);
               const bool behind = pos >= g.end;
               bool nan = false;
               if (!behind)
-                for (int c = 0; c < kD / 16; ++c) nan |= holds_nan(row[c]);
+                for (int c = 0; c < kD / 16; ++c) nan |= holds_nan(row[(c + lane) % (kD / 16)]);
               if (nan || behind)
-                for (int c = 0; c < kD / 16; ++c) row[c] = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < kD / 16; ++c) row[(c + lane) % (kD / 16)] = make_uint4(0, 0, 0, 0);
               none = nan || bad;
               const bool lost = !behind && P.c.page_of(g.b, pos) < 0;  // every row of the sequence is
               if (behind) {
