@@ -613,8 +613,10 @@ sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t* path, int
  *   workspace: device memory of spec_verify_attend_workspace(...) bytes, on a
  *     multiple of 16, that no other call uses meanwhile; it holds parts of long
  *     contexts until they are joined, and nothing between calls.
- * Softmax statistics and sums are fp32; weights are rounded to eight significant
- * bits, as bf16 weights would be.  What lies behind a sequence's last row does
+ * Softmax statistics and sums are fp32.  A weight times its value's scale is
+ * rounded as fp16 numbers are: to eleven significant bits where it is at least
+ * 2^-20 of the row's largest, by 2^-31 of the largest at most where it is smaller
+ * (a scale counting as 2^-12 of the others' at least).  What lies behind a sequence's last row does
  * not matter, whatever it is; a row that sees a NaN becomes NaN.  So do the rows of a
  * sequence with a page outside [0, pages) or a column outside the table among
  * its positions or with a parent outside [-1, i).  Rows of padded sequences, and of a

@@ -2,40 +2,45 @@
 //
 //   out[r, h] = sum_p softmax_p(scale q[r, h] . K[p]) V[p],  p over the committed positions and the row's path
 //
-// Keys and values go from memory to the tensor cores as they are, in 8 bits.  A query of
-// eight significant bits is the exact sum of two e4m3 numbers (times a power of two for
-// its row; an entry below 2^-11 of the row's largest is off by 2^-17.8 of it at most), and
-// a weight is rounded to two: hi = e4m3(w), lo = e4m3(w - hi), as good as a rounding to
-// bf16.  So S = K (Qhi + Qlo)^T and O = V^T (Phi + Plo), two products each
-// at twice the rate of bf16's, and nothing is converted but queries and weights.
+// Keys go from memory to the tensor cores as they are, in 8 bits: a query of eight
+// significant bits is the exact sum of two e4m3 numbers (times a power of two for its
+// row; an entry below 2^-11 of the row's largest is off by 2^-17.8 of it at most), so
+// S = K (Qhi + Qlo)^T is two products at twice the rate of bf16's.  O = V^T P is a product
+// of fp16 numbers: values become that exactly, and weights are rounded to it.
 //
 // A key head's query rows (all rows of the step times the query heads of its group) are
 // the columns: up to kN of them make a block, and one or two blocks a unit.  Positions are rows, 128 to a tile: thread
 // t of a warpgroup has position t of every column, so that a position's scale and
 // visibility are the thread's own.
 //
-// A weight times its value's scale stands against a reference of its column, the largest
-// such product of a tile.  It is taken anew where a tile has one that is more than 445
-// times as large, and at every 16th tile if that tile's are all below 1/32 of it: those
-// in between have at most lost digits that weigh 2^-15 of what has been added before, and
-// what is small against other tiles' does not fall below e4m3's range.  Else a tile needs
-// no reduction: sums of weights stay with the threads until a segment ends, and the
-// products' sums in tensor memory.  Those of hi and lo are apart there, so that lo can be
-// held 2^5 times as large.
+// A weight times its value's scale stands against a reference of its column, under which
+// the largest such product of some tile was 2^6.  It is taken anew where a tile has one
+// that is above 2^15, and at every 16th tile if that tile's are all below 2.  Else a tile
+// needs no reduction: sums of weights stay with the threads until a segment ends, and the
+// products' sums in tensor memory.
+//
+// Weights in fp16 have eleven bits down to 2^-14, 2^-20 of that tile's largest, and are off
+// by 2^-25 at most below: eight bits down to 2^-23 of the largest, 16 below its logit.  That
+// range is needed: a few positions may tower above all others, as a model's first tokens
+// do, with values near zero, and then the others are the result.  Two e4m3 numbers, hi + lo / 32,
+// have eight bits over 2^15 only: a first position 11 above 4000 others took half of the
+// others' weight.  (A reference for each tile, and two rounds for tiles with such
+// positions, mended that too; on blocks whose scales differ it cost more: 64 chains 202 us, 166 so, and
+// trees 149, 113.)  A group of softmax threads widens its tile's values itself, where two blocks of columns
+// share a tile each group half of it.
 //
 // Work is cut evenly over the SMs, whatever the lengths: all tiles of all units (sequence, key
 // head, columns) in a row, a CTA taking the n-th part of them.  A unit that
 // is cut leaves its parts in the workspace, and a second kernel joins them.
 //
-// Measured (with the joining kernel):
+// Measured (with the joining kernel; in brackets what the bytes take at the rate of a copy):
 //   64 chains of five drafts after up to 8192 positions, 8 key heads of 128, 4 query heads
-//     to each: 143.4 us, 5.65 TB/s (reading alone takes 121)
-//   the same with one row and 4096 positions each: 76.6 us (60.3)
-//   2 chains of four after 131071, 8 key heads of 64, 5 query heads to each: 93.8 us (40.1);
-//     the weights' arithmetic bounds it: entries of 64 are half the bytes of a weight
+//     to each: 166 us (121); widening V takes 20 of them
+//   the same with one row and 4096 positions each: 83.7 us (60.3)
+//   2 chains of four after 131071, 8 key heads of 64, 5 query heads to each: 94.6 us (40.1)
 //   32 trees of up to 21 nodes after up to 4000, 4 key heads of 128, 8 query heads to each:
-//     99.7 us (16.0); 176 columns are three units of 64, and the weights bound it
-//   one row after 1000 positions: 16.2 us, two launches and a chain of waits
+//     114 us (16.0); 176 columns are three units of 64
+//   one row after 1000 positions: 16.5 us, two launches and a chain of waits
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,8 +62,9 @@ namespace {
 constexpr int kTile = 128;  // positions
 constexpr int kGroupThreads = 256;  // of a tile's softmax: a thread has one position of half of the columns
 constexpr int kAttendThreads = 128 + 2 * kGroupThreads;
-constexpr float kMost = 8.8f;  // log2 of the largest weight over the reference; 448 is 2^8.807
-constexpr float kLow = -5.f;   // log2 of what a tile's largest may have fallen to where the reference stays
+constexpr float kMost = 15.f;  // log2 of the largest weight over the reference; fp16 ends at 2^16
+constexpr float kNew = 6.f;    // log2 of the largest one under a new reference
+constexpr float kLow = 1.f;    // log2 of what a tile's largest may have fallen to where the reference stays
 constexpr int kRefresh = 16;   // tiles of a group after which that is looked at
 constexpr float kDeep = 60.f;  // log2 of how far a reference may fall below the highest: what is below adds nothing
 
@@ -235,6 +241,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, unsig
       : "memory");
 }
 
+__device__ __forceinline__ void tc_mma_half(uint32_t d, uint64_t a, uint64_t b, unsigned idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(add))
+      : "memory");
+}
+
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -307,16 +321,19 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
 }
 
 // Operands in shared memory (all of their offsets in units of 16 bytes).
-// Tiles of K and V: rows of kD bytes, 128- or 64-byte swizzle, groups of 8 rows behind one another.  As they lie they are K-major
-// for K (its rows are the rows of the product, kD its inner dimension), and for V, whose rows are the inner dimension,
-// transposed.  Q's rows lie like K's.
+// Tiles of K: rows of kD bytes, 128- or 64-byte swizzle, groups of 8 rows behind one another.  Q's rows lie like K's.
 template <int kD>
 __device__ __forceinline__ uint64_t rows_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (1ull << 16) | (static_cast<uint64_t>(kD * 8 / 16) << 32) | (1ull << 46) |
          (kD == 128 ? 2ull << 61 : 4ull << 61);
 }
-// Weights: runs of 16 columns, 16 bytes for each position, a run's 128 positions behind one another; no swizzle.  Eight positions
-// on: 128 bytes; a run on: 2048.
+// V in fp16: runs of 64 entries, 128 bytes for each position, 128-byte swizzle, a run's 128 positions behind one another.  The
+// positions are the inner dimension, so that it lies transposed.  Eight positions on: 1024 bytes; a run on: 16384.
+__device__ __forceinline__ uint64_t values_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// Weights: runs of 8 columns, 16 bytes for each position, a run's 128 positions behind one another; no swizzle; transposed like
+// V.  Eight positions on: 128 bytes; a run on: 2048.
 __device__ __forceinline__ uint64_t weights_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (8ull << 16) | (128ull << 32) | (1ull << 46);
 }
@@ -336,27 +353,35 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, unsigned parity, volatil
   }
 }
 
+__device__ __forceinline__ uint4 shared_load(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void shared_store(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 __device__ __forceinline__ float power(float x) {  // 2^x; results below 2^-126 become 0
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
-// Two numbers that are not negative, times 32, as e4m3 numbers hi + lo / 32: hi is the nearest one, lo what is left.  They pass
-// through fp16's eleven bits.
-__device__ __forceinline__ void split2(Two w, uint32_t& hi, uint32_t& lo) {
+// two weights to fp16, to nearest
+__device__ __forceinline__ uint32_t half2_of(Two w) {
   float a, b;
   both(w, a, b);
-  uint32_t h, back, rest;
-  uint16_t r;
+  uint32_t h;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(0x28002800u));  // 1 / 32
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(rest));
-  hi = r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(r));
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(rest) : "r"(back), "r"(0xd000d000u), "r"(h));  // -32
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(rest));
-  lo = r;
+  return h;
+}
+
+// two e4m3 entries as fp16 (exact)
+__device__ __forceinline__ uint32_t half2_of(uint16_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+  return h;
 }
 
 // Each column's largest, or sum, over a warp's lanes: halves of the columns change hands until a lane has its own.  Of kCols
@@ -388,10 +413,13 @@ __device__ __forceinline__ float over_lanes(const float* f) {
   return v[0];
 }
 
-// Tiles of K and of V have rings of their own: K's is free after the first product, V's after the second.
+// Tiles of K and of V have rings of their own: K's is free after the first product, V's where it is widened.
 template <int kN, int kBlocks, int kD>
 struct AttendShared {
-  static constexpr int kK = kD == 64 ? 10 : 5, kV = kD == 64 ? 12 : 6;
+  static constexpr int kK = kD == 64 ? 10 : kBlocks == 2 ? 3 : 4, kV = kD == 64 ? 8 : 4;
+  // Waits tell a phase only from the one next to it.  The first warp, kK tiles ahead of a product of which up to four tiles
+  // may be in use, looks at V's stages: two rounds of them are more than that.  And a group's next tile in a stage is its own.
+  static_assert(2 * kV >= kK + 4 && kV % 2 == 0);
   static constexpr int kWords = (kBlocks * kN + 31) / 32;  // of a unit's columns
   // of a special tile's positions: the columns that see it; whether what they see is no number
   uint32_t seen[kV][kTile][kWords];
@@ -414,7 +442,7 @@ struct AttendShared {
   Segment segment[4];  // the first warp walks ahead
   uint64_t g_full[4], g_free[4];
   uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV], ready[kV];
-  uint64_t s_full[2], s_free[2], p_full[2], o_full[2], q_full, o_read;
+  uint64_t s_full[2], s_free[2], wide_full[2], p_full[2], o_full[2], q_full, o_read;
   int64_t warp_sums[kAttendThreads / 32];
   Start start;
   uint32_t tmem;
@@ -425,10 +453,11 @@ template <int kN, int kBlocks, int kD>
 struct Sizes {
   using Shared = AttendShared<kN, kBlocks, kD>;
   static constexpr int kTileBytes = kTile * kD;
-  static constexpr int kQ = kN * kD, kWeights = kTile * kN;  // one of the two numbers of a block's entries
+  static constexpr int kQ = kN * kD;  // one of the two numbers of a block's entries
+  static constexpr int kWide = kTile * kD * 2, kWeights = kTile * kN * 2;  // fp16
   static constexpr int kColumns = kBlocks * kN;              // of a unit
   static constexpr int kSmem = static_cast<int>(sizeof(Shared)) + 1024 + (Shared::kK + Shared::kV) * kTileBytes +
-                               2 * kBlocks * kQ + 4 * kWeights;
+                               2 * kBlocks * kQ + 2 * kWide + 2 * kWeights;
   static constexpr int kPart = kColumns * (kD + 2);  // floats of a part in the workspace
   static_assert(kSmem <= 227 * 1024);
 };
@@ -520,26 +549,27 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   uint8_t* const tiles_k = base;
   uint8_t* const tiles_v = tiles_k + kK * Z::kTileBytes;
   uint8_t* const queries = tiles_v + kV * Z::kTileBytes;            // [hi, lo][block]
-  uint8_t* const weights = queries + 2 * kBlocks * Z::kQ;       // [warpgroup][hi, lo]
+  uint8_t* const wides = queries + 2 * kBlocks * Z::kQ;         // of a group's tile; with two blocks of every other tile
+  uint8_t* const weights = wides + 2 * Z::kWide;                // [group]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (unsigned i = 0; i < kK; ++i) mbar_init(&s.k_full[i], 1), mbar_init(&s.k_empty[i], 1);
-    for (unsigned i = 0; i < kV; ++i) mbar_init(&s.v_full[i], 1), mbar_init(&s.v_empty[i], 1), mbar_init(&s.ready[i], 1);
+    for (unsigned i = 0; i < kV; ++i) mbar_init(&s.v_full[i], 1), mbar_init(&s.v_empty[i], 16), mbar_init(&s.ready[i], 1);
     for (int i = 0; i < 2; ++i)
-      mbar_init(&s.s_full[i], 1), mbar_init(&s.s_free[i], 8), mbar_init(&s.p_full[i], 8), mbar_init(&s.o_full[i], 1);
+      mbar_init(&s.s_full[i], 1), mbar_init(&s.s_free[i], 8), mbar_init(&s.wide_full[i], 16), mbar_init(&s.p_full[i], 8),
+          mbar_init(&s.o_full[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&s.g_full[i], 1), mbar_init(&s.g_free[i], 19);
     mbar_init(&s.q_full, 16), mbar_init(&s.o_read, 16);
-    for (int c = 0; c < kN; ++c) s.zero[c] = 0.f;
     for (int c = 0; c < kN; ++c) s.zero[c] = 0.f;
     s.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // columns that are not used have weights too
-  for (int i = threadIdx.x; i < 4 * Z::kWeights / 16; i += kAttendThreads)
+  for (int i = threadIdx.x; i < 2 * Z::kWeights / 16; i += kAttendThreads)
     reinterpret_cast<uint4*>(weights)[i] = make_uint4(0, 0, 0, 0);
   async_fence();
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)), "n"(8 * kN)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)), "n"(4 * kN)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -553,7 +583,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   if (threadIdx.x == 0) P.cuts[blockIdx.x] = start;
   lo = cut(start.total, blockIdx.x, P.grid);
   const int64_t hi = cut(start.total, blockIdx.x + 1, P.grid);
-  const uint32_t tmem = s.tmem;  // S of the two groups (kN columns each), then O (2 kN: of hi, of lo)
+  const uint32_t tmem = s.tmem;  // S of the two groups (kN columns each), then O
   // The next segment of a warp that takes them from the first; false behind the last, and where a wait gave up.
   auto next_segment = [&](unsigned n, Segment& g) {
     wait_for(&s.g_full[n & 3], n >> 2 & 1, &s.dead);
@@ -712,26 +742,25 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   } else if (warp == 2) {
     // ---- products with V
     constexpr unsigned kShape =
-        (1u << 4) | (1u << 15) | (1u << 16) | (static_cast<unsigned>(2 * kN / 8) << 17) | (static_cast<unsigned>(kD / 16) << 24);
-    unsigned count = 0, done[2] = {0, 0};
+        (1u << 4) | (1u << 15) | (1u << 16) | (static_cast<unsigned>(kN / 8) << 17) | (static_cast<unsigned>(kD / 16) << 24);
+    unsigned count = 0, done = 0, used = 0;  // done, used: a bit for each group and each tile of wide values, how often modulo 2
     Segment g;
     for (unsigned segment = 0; next_segment(segment, g); free_segment(segment++)) {
       const int items = (g.t1 - g.t0) << (g.two ? 1 : 0);
       for (int i = 0; i < items; ++i) {
-        const int w = i & 1;
-        const unsigned n = count + (g.two ? i / 2 : i), st = n % kV;
-        if (!g.two || w == 0) wait_for(&s.v_full[st], n / kV & 1, &s.dead);
-        wait_for(&s.p_full[w], done[w]++ & 1, &s.dead);
+        const int w = i & 1, b = kBlocks == 2 && g.two ? (count + i / 2) & 1 : w;
+        if (kBlocks == 2 && g.two && w == 0) wait_for(&s.wide_full[b], used >> b & 1u, &s.dead), used ^= 1u << b;
+        wait_for(&s.p_full[w], done >> w & 1u, &s.dead);
+        done ^= 1u << w;
         tc_after();
-        const uint64_t v = rows_desc<kD>(smem_addr(tiles_v + st * Z::kTileBytes));
-        const uint64_t p = weights_desc(smem_addr(weights + w * 2 * Z::kWeights));
+        const uint64_t v = values_desc(smem_addr(wides + b * Z::kWide));
+        const uint64_t p = weights_desc(smem_addr(weights + w * Z::kWeights));
         if (elect_one()) {
 #pragma unroll
-          for (int t = 0; t < kTile / 32; ++t)
-            tc_mma(tmem + (2 + 2 * w) * kN, v + t * (32 * kD / 16), p + t * 32, kShape,
-                   i > 1 || t > 0);  // a group's first item of a segment begins its sums
+          for (int t = 0; t < kTile / 16; ++t)
+            tc_mma_half(tmem + (2 + w) * kN, v + t * (16 * 128 / 16), p + t * 16, kShape,
+                        i > 1 || t > 0);  // a group's first item of a segment begins its sums
           tc_commit(&s.o_full[w]);
-          if (!g.two || w == 1) tc_commit(&s.v_empty[st]);
         }
         __syncwarp();
       }
@@ -752,9 +781,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     const int t = threadIdx.x - 128 - me * kGroupThreads, position = t & (kTile - 1);
     constexpr int kPad = kC == 12 ? 16 : kC, kUsed = 2 * kC;
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // 32 lanes of tensor memory each
-    const uint32_t tmem_s = tmem + lanes + me * kN + half * kC, tmem_o = tmem + lanes + (2 + 2 * me) * kN + half * kC;
+    const uint32_t tmem_s = tmem + lanes + me * kN + half * kC, tmem_o = tmem + lanes + (2 + me) * kN + half * kC;
     unsigned count = 0, items = 0, ready = 0;  // ready: a bit for each stage, its barrier's parity
-    uint8_t* const mine = weights + me * 2 * Z::kWeights;
+    uint8_t* const mine = weights + me * Z::kWeights;
     // A query row is read by kLanes lanes, eight entries each, kRows rows a warp at once.  The rows of a segment and the page of
     // its first tile are on their way while the segment in front is finished.
     constexpr int kLanes = kD / 8, kRows = 32 / kLanes, kPasses = (Z::kColumns + 16 * kRows - 1) / (16 * kRows);
@@ -781,7 +810,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     for (unsigned segment = 0;; ++segment) {
       const Segment& g = s.segment[segment & 3];
       const int t0 = g.t0, t1 = g.t1;
-      const bool two_blocks = g.two;
+      const bool two_blocks = kBlocks == 2 && g.two;
       // all of the warps that meet at barriers go on, or none
       if (groups_any(t1 == 0 || s.dead)) break;
       const int step = two_blocks ? 1 : 2, first_tile = t0 + (two_blocks ? 0 : me);
@@ -877,7 +906,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (own < kC) s.most[me][quad][half * kC + own] = r;
       };
       for (int tile = first_tile; tile < t1; tile += step) {
-        const unsigned st = (count + (tile - t0)) % kV;
+        const unsigned n = count + (tile - t0), st = n % kV;
         const float2 scales = scales_next;
         scales_next = scales_at(tile + step, page_next);
         page_next = page_at(tile + 2 * step);
@@ -929,7 +958,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
               const float from = first ? 0.f : m;
               float to = from, keep = 1.f;
               if (zt != -INFINITY) {
-                if (first || !(zt <= kMost && zt >= kLow)) to = from + zt;
+                if (first || !(zt <= kMost && zt >= kLow)) to = from + (zt - kNew);
                 if (!first) to = fmaxf(to, top - kDeep), keep = power(from - to);
                 m = to, top = fmaxf(top, to);
               }
@@ -951,53 +980,83 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
               wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
               tc_after();
 #pragma unroll 1
-              for (int c = 0; c < 2 * kC; c += 4) {
-                const int col = c % kC;
-                const uint32_t at = tmem_o + (c / kC) * kN + col;  // hi's sums, then lo's
+              for (int c = 0; c < kC; c += 4) {
                 float o[4];
-                tc_load<4>(at, o);
+                tc_load<4>(tmem_o + c, o);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] *= keeps[col + k];
-                tc_store(at, o);
+                for (int k = 0; k < 4; ++k) o[k] *= keeps[c + k];
+                tc_store(tmem_o + c, o);
               }
               asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
               tc_before();
             }
           }
         }
-        const Two inverse2 = two(inverse, inverse), rest = two(32.f * ratio * inverse, 32.f * ratio * inverse);
-        // the weights in front have been read; the sums of the segment in front too
+        const Two inverse2 = two(inverse, inverse), rest = two(ratio * inverse, ratio * inverse);
+        // the weights in front and their values have been read; the sums of the segment in front too
         if (items != begun)
           wait_for(&s.o_full[me], (items - 1) & 1, &s.dead);
         else if (segment > 0)
           wait_for(&s.o_read, (segment - 1) & 1, &s.dead);
-        // runs of 16 columns, 16 bytes a position
-        uint32_t hi[kC / 4], lo[kC / 4];
+        // This thread's part of its position's values becomes fp16: half of them, or, where both groups need them, a quarter.
+        wait_for(&s.v_full[st], n / kV & 1, &s.dead);
+        {
+          // 16 entries at once, the i-th of a row; chunks are mixed by exclusive or, in the tile and in the runs
+          const uint32_t row =
+              smem_addr(tiles_v) + st * Z::kTileBytes + position * kD + (kD == 128 ? position & 7 : position >> 1 & 3) * 16;
+          const uint32_t to_row = smem_addr(wides) + (two_blocks ? n & 1 : me) * Z::kWide + position * 128 + (position & 7) * 16;
+          auto store = [&](int i, uint4 e) {
+            const uint32_t four[4] = {e.x, e.y, e.z, e.w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              h[2 * k] = half2_of(static_cast<uint16_t>(four[k]));
+              h[2 * k + 1] = half2_of(static_cast<uint16_t>(four[k] >> 16));
+            }
+            const uint32_t to = to_row + i / 4 * (kTile * 128);
+            shared_store(to ^ (2 * i & 7) * 16, make_uint4(h[0], h[1], h[2], h[3]));
+            shared_store(to ^ (2 * i + 1 & 7) * 16, make_uint4(h[4], h[5], h[6], h[7]));
+          };
+          constexpr int kQuarter = kD / 64;
+          if (two_blocks) {
+            const int first = (me * 2 + half) * kQuarter;
+            uint4 e[kQuarter];
+#pragma unroll
+            for (int c = 0; c < kQuarter; ++c) e[c] = shared_load(row ^ (first + c) * 16);
+#pragma unroll
+            for (int c = 0; c < kQuarter; ++c) store(first + c, e[c]);
+            async_fence();
+          } else {
+            const int first = half * 2 * kQuarter;
+            uint4 e[2 * kQuarter];
+#pragma unroll
+            for (int c = 0; c < 2 * kQuarter; ++c) e[c] = shared_load(row ^ (first + c) * 16);
+#pragma unroll
+            for (int c = 0; c < 2 * kQuarter; ++c) store(first + c, e[c]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s.v_empty[st], two_blocks ? 1 : 2);
+          if (two_blocks) mbar_arrive(&s.wide_full[n & 1]);
+        }
+        uint32_t w[kC / 2];
 #pragma unroll
         for (int c = 0; c < kC; c += 2) {
           const Two p = two(power(x[c]), power(x[c + 1]));
           l[c / 2] = fma2(p, inverse2, l[c / 2]);
-          uint32_t h, r;
-          split2(mul2(p, rest), h, r);
-          if (c % 4 == 0)
-            hi[c / 4] = h, lo[c / 4] = r;
-          else
-            hi[c / 4] |= h << 16, lo[c / 4] |= r << 16;
+          w[c / 2] = half2_of(mul2(p, rest));
         }
+        // runs of 8 columns, 16 bytes a position
         uint8_t* const to = mine + position * 16;
-        auto run = [&](int col) { return to + col / 16 * (kTile * 16) + col % 16; };
-        if constexpr (kC == 16) {
-          *reinterpret_cast<uint4*>(run(half * kC)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(run(half * kC) + Z::kWeights) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        } else if constexpr (kC == 8) {
-          *reinterpret_cast<uint2*>(run(half * kC)) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(run(half * kC) + Z::kWeights) = make_uint2(lo[0], lo[1]);
+        auto run = [&](int col) { return to + col / 8 * (kTile * 16) + col % 8 * 2; };
+        if constexpr (kC % 8 == 0) {
+#pragma unroll
+          for (int c = 0; c < kC; c += 8)
+            *reinterpret_cast<uint4*>(run(half * kC + c)) = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
         } else {
 #pragma unroll
-          for (int c = 0; c < kC; c += 4) {
-            *reinterpret_cast<uint32_t*>(run(half * kC + c)) = hi[c / 4];
-            *reinterpret_cast<uint32_t*>(run(half * kC + c) + Z::kWeights) = lo[c / 4];
-          }
+          for (int c = 0; c < kC; c += 4) *reinterpret_cast<uint2*>(run(half * kC + c)) = make_uint2(w[c / 2], w[c / 2 + 1]);
         }
         async_fence();
         __syncwarp();
@@ -1050,15 +1109,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int from = two_blocks ? half * kC : (me * 2 + half) * 8, to = two_blocks ? from + kC : min(kUsed, from + 8);
 #pragma unroll 1
         for (int c = from; c < to; c += 8) {
-          const uint32_t at = tmem + lanes + (2 + 2 * block) * kN + c;
-          float o[8], u[8], v[8];
-          tc_load<8>(at, o), tc_load<8>(at + kN, u);
+          const uint32_t at = tmem + lanes + (2 + block) * kN + c;
+          float o[8], v[8];
+          tc_load<8>(at, o);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = fmaf(u[k], 0.03125f, o[k]) * s.worth[block][c + k];
+          for (int k = 0; k < 8; ++k) v[k] = o[k] * s.worth[block][c + k];
           if (others) {
-            tc_load<8>(at + 2 * kN, o), tc_load<8>(at + 3 * kN, u);
+            tc_load<8>(at + kN, o);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = fmaf(fmaf(u[k], 0.03125f, o[k]), s.worth[1][c + k], v[k]);
+            for (int k = 0; k < 8; ++k) v[k] = fmaf(o[k], s.worth[1][c + k], v[k]);
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -1085,7 +1144,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   if (s.dead) stay_behind();
   __syncwarp();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(8 * kN) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(4 * kN) : "memory");
 }
 
 // ---- parts of a unit together
