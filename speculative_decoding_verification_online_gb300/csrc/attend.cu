@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
       }
       // the anchor of the group's value scales: a power of two near the first tile's largest, 2^-110 at least
-      float anchor = scales_next.y;
+      float anchor = scales_next.y < INFINITY ? scales_next.y : 0.f;
       for (int o = 16; o; o >>= 1) anchor = fmaxf(anchor, __shfl_xor_sync(~0u, anchor, o));
       if (lane == 0) s.anchors[me][quad] = anchor;
       async_fence();
@@ -907,9 +907,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       };
       for (int tile = first_tile; tile < t1; tile += step) {
         const unsigned n = count + (tile - t0), st = n % kV;
-        const float2 scales = scales_next;
+        float2 scales = scales_next;
         scales_next = scales_at(tile + step, page_next);
         page_next = page_at(tile + 2 * step);
+        // a scale of values that is no number: the rows that see it become NaN by their logits, a weight of 0 stays one (looked at
+        // here, where it has come: 185 us for 64 chains behind the load, 166 so)
+        if (!(fabsf(scales.y) < INFINITY)) scales = make_float2(NAN, 0.f);
         float kf = scales.x;
         // V's scale over the anchor: rest * 2^e, rest in (1/2, 1], e -12 at least
         const float ratio = scales.y * per_anchor;

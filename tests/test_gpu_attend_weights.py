@@ -1,5 +1,5 @@
 """How far the attention's weights are kept (``spec_verify_attend``): rows in which a few positions tower above all others, as
-a model's first tokens do, levels that change along a context, weights of every size.
+a model's first tokens do, levels that change along a context, weights of every size, scales that are no numbers.
 
 Everything is compared with 64 bits.  The bound of an output entry is that of weights of eight significant bits, plus 2^-31 of
 the row's largest weight for each position."""
@@ -9,7 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_step_operators import gen, sv  # noqa: F401  (sv is a fixture)
+from tests import step_reference as ref
+from tests.test_gpu_step_operators import attend_case, gen, sv  # noqa: F401  (sv is a fixture)
 
 pytestmark = pytest.mark.gpu
 i32, f32, bf16, f8, f64 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.float64
@@ -176,3 +177,27 @@ def test_attend_weights_of_every_size_above_the_reference(sv):
     # 2^-8 for the weight, 2^-16 for all else, half a bf16 step
     half = torch.exp2(torch.floor(torch.log2(got)) - 8)
     assert bool(((got - want).abs() <= want * (2.0 ** -8 + 2.0 ** -16) + half).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("which", [2, 3])
+def test_attend_scales_that_are_no_numbers_reach_the_rows_that_see_them(sv, bad, which):
+    context, sizes = [100, 127, 60], [7, 3, 0]
+    c = attend_case(21, context, sizes, 2, 2, 64, 16, 1)
+    want = sv.attend_tree(**c).clone()
+    table = c["page_table"].tolist()
+    for b, (n, m) in enumerate(zip(context, sizes)):  # behind the last row: nobody
+        for p in range(n + 1 + m, 16 * len(table[b])):
+            c["cache"][which][table[b][p // 16], :, p % 16] = bad
+    assert torch.equal(sv.attend_tree(**c), want)
+    p = context[0] + 1 + 2  # node 2, key head 1
+    c["cache"][which][table[0][p // 16], 1, p % 16] = bad
+    got = sv.attend_tree(**c)
+    parent = c["parent"].tolist()
+    lost = [i for i in range(8) if 2 in ref.path_of(parent, i)]
+    assert 3 in lost and len(lost) < 7
+    keep = torch.ones(got.shape[:2], dtype=torch.bool, device="cuda")
+    keep[lost, 2:4] = False
+    assert torch.equal(got[keep], want[keep])
+    if bad != bad or which == 3:
+        assert bool(torch.isnan(got[~keep]).all())
