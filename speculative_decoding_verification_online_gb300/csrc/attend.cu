@@ -1186,7 +1186,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     float l = 0.f, v[kD / 32] = {};
     for (int k0 = 0; k0 < parts; k0 += 32) {
-      float f = 0.f;
+      float f = -1.f;  // there is none.  (A factor of 0 counts: what a part far below the others holds may be NaN.)
       if (k0 + lane < parts && !empty(k0 + lane)) {
         const float mk = part(k0 + lane)[kColumns * kD + c];
         f = mk == m ? 1.f : power(mk - m);
@@ -1196,7 +1196,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       for (int k = 0; k < min(32, parts - k0); ++k) {
         const float fk = __shfl_sync(~0u, f, k);
         const float* p = part(k0 + k) + c * kD + lane;
-        if (fk != 0.f)
+        if (!(fk < 0.f))
 #pragma unroll
           for (int e = 0; e < kD / 32; ++e) v[e] += p[32 * e] * fk;
       }

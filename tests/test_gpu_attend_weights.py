@@ -201,3 +201,17 @@ def test_attend_scales_that_are_no_numbers_reach_the_rows_that_see_them(sv, bad,
     assert torch.equal(got[keep], want[keep])
     if bad != bad or which == 3:
         assert bool(torch.isnan(got[~keep]).all())
+
+
+def test_attend_a_nan_far_below_the_others_is_not_lost(sv):
+    # Two tiles at the end whose logits lie 100 below all others': the last one's only positions have a page that is none.
+    # However the tiles are cut, the row becomes NaN.
+    for n in range(20, 320, 7):
+        c, total = flat_case(1, 1, 1, 64, 128 * n + 10, 0, tokens=128)
+        k = torch.zeros(1, 1, total, 64, device="cuda")
+        k[:, :, 128 * (n - 1):, 0] = -100.0
+        put(c, 0, k)
+        c["q"][..., 0] = 8.0
+        assert not bool(torch.isnan(sv.attend_tree(**c)).any())
+        c["page_table"][0, n] = -1
+        assert bool(torch.isnan(sv.attend_tree(**c)).all()), n
