@@ -33,6 +33,7 @@ constexpr int kPenWarps = 8, kPenThreads = 32 * kPenWarps;
 constexpr int kPenRange = 8192;      // tokens of a CTA at most
 constexpr int kPenCopied = 4096;     // where rows are copied
 constexpr int kPenLeast = 1024;      // and at least
+constexpr int kPenMostShared = kPenRange * (4 + 4 + 2);  // bytes of a table, of places of biases, of a list
 constexpr int kPenLong = 8192;       // histories from here on have their list in order
 constexpr int kSingle = 8;           // logits of a lane on their way at once where they are not loaded in runs
 constexpr int kTokens = 16;          // of the history on a thread's way at once
@@ -437,8 +438,9 @@ extern "C" sv_status spec_verify_penalties(const void* logits, sv_dtype dt, int6
   P.in_place = in_place;
   const auto kernel = history_cap >= sv::kPenLong ? sv::penalties_variant<true>(dt, out_dt) : sv::penalties_variant<false>(dt, out_dt);
   const size_t smem = static_cast<size_t>(range) * ((bias_start ? 8 : 4) + 2);
+  // (always the same limit: one for this call alone could be lowered by another host thread in front of the launch)
   if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sv::kPenMostShared) != cudaSuccess)
     return SV_ECUDA;
   return sv::launch_waiting(kernel, static_cast<unsigned>(P.ranges) * static_cast<unsigned>(B), sv::kPenThreads, smem, 1, static_cast<cudaStream_t>(cuda_stream), P) == cudaSuccess
              ? SV_OK
