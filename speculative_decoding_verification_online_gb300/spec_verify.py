@@ -35,6 +35,8 @@ SV_MAX_NODES = 256
 ACTIVATIONS = {"none": SV_ACT_NONE, "relu": SV_ACT_RELU, "silu": SV_ACT_SILU, "gelu": SV_ACT_GELU,
                "gelu_tanh": SV_ACT_GELU_TANH, "softcap": SV_ACT_SOFTCAP}
 SV_WITH_REPLACEMENT, SV_WITHOUT_REPLACEMENT = 0, 1
+RUN_HIDDEN_PENALTIES = frozenset(("history", "history_len", "prompt_len", "repetition", "frequency", "presence", "bias", "mask",
+                                  "mask_row", "draft_mask", "draft_mask_row"))
 
 _lib = None
 
@@ -821,9 +823,14 @@ class SpecVerifier:
         ``penalize`` takes by these names -- history, history_len, prompt_len,
         repetition, frequency, presence, bias -- for the rows of both sides, row j
         of which stands behind D[:, :j]; mask and mask_row for the target's [B *
-        (k+1)] rows, draft_mask and draft_mask_row for the draft's [B * k].  ``kw``
+        (k+1)] rows, draft_mask and draft_mask_row for the draft's [B * k] (a side
+        without a mask is not masked); other names are refused.  ``kw``
         goes to ``run``; the result also holds target_logits and draft_logits, as
         they were verified."""
+        if penalties is not None:
+            unknown = set(penalties) - RUN_HIDDEN_PENALTIES
+            if unknown:
+                raise TypeError(f"penalties: unknown names {sorted(unknown)}, expected some of {sorted(RUN_HIDDEN_PENALTIES)}")
         B, k, V, dev = target_hidden.shape[0], self.k, self.V, self.device
         _check(target_hidden, "target_hidden", (B, k + 1, target_hidden.shape[-1]), torch.bfloat16, dev)
         _check(draft_hidden, "draft_hidden", (B, k, draft_hidden.shape[-1]), torch.bfloat16, dev)
