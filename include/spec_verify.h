@@ -607,7 +607,8 @@ sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t* path, int
  * those of its path (parent as spec_verify_tree; NULL = chains: everything up to
  * itself).  G = q_heads / heads.  Plain decoding is node_start = 0 throughout.
  *   q, out: bfloat16, row r, head h at r * row + h * head, dim contiguous entries
- *     each; q_row, q_head multiples of 8, q on a multiple of 16 bytes.  out must not
+ *     each; q_row, q_head (where there are several) multiples of 8, q on a multiple of
+ *     16 bytes.  out must not
  *     overlap q or the cache.
  *   scale: finite (SV_EUNSUPPORTED beyond 2^126).
  *   workspace: device memory of spec_verify_attend_workspace(...) bytes, on a

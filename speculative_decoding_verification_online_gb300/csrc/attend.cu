@@ -1310,11 +1310,14 @@ extern "C" sv_status spec_verify_attend(const sv_cache* cache, const void* q, in
   if (B == 0) return SV_OK;
   if (static_cast<int64_t>(total_nodes) + B > INT32_MAX || q_heads / cache->heads > (1 << 20)) return SV_EUNSUPPORTED;
   if (!q || !out || !context || !node_start) return SV_EINVAL;
-  if (q_row % 8 || q_head % 8 || reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 2) return SV_EINVAL;
+  const int rows = total_nodes + B;
+  // (the stride of a dimension of one is not used)
+  if ((rows > 1 && q_row % 8) || (q_heads > 1 && q_head % 8) || reinterpret_cast<uintptr_t>(q) % 16 ||
+      reinterpret_cast<uintptr_t>(out) % 2)
+    return SV_EINVAL;
   for (const void* p : {static_cast<const void*>(context), static_cast<const void*>(node_start),
                         static_cast<const void*>(parent)})
     if (reinterpret_cast<uintptr_t>(p) % 4) return SV_EINVAL;
-  const int rows = total_nodes + B;
   if (!sv::rows_apart(out_head, out_row, q_heads, rows, cache->dim)) return SV_EINVAL;
   if (sv::sure_to_overlap({q, 2, cache->dim, q_head, q_heads, q_row, rows},
                           {out, 2, cache->dim, out_head, q_heads, out_row, rows}))

@@ -582,6 +582,11 @@ class PagedCache(NamedTuple):
         return PagedCache(*(t[i] for t in self))
 
 
+def _strides_differ(a, b):
+    """Of two tensors of one shape, those that are used."""
+    return any(n > 1 and i != j for n, i, j in zip(a.shape, a.stride(), b.stride()))
+
+
 def _cache(cache, dev, layered):
     """sv_cache of (k, v, k_scale, v_scale), checked."""
     k, v, ks, vs = cache
@@ -594,9 +599,9 @@ def _cache(cache, dev, layered):
         raise TypeError(f"cache: dtypes {k.dtype}, {v.dtype}, {ks.dtype}, {vs.dtype}, expected {f8} twice and {f32} twice")
     if k.device != dev or v.device != dev or ks.device != dev or vs.device != dev:
         raise ValueError(f"cache: on {k.device}, {v.device}, {ks.device}, {vs.device}, expected {dev}")
-    if v.stride() != st or v.shape != shape:
+    if v.shape != shape or (v.stride() != st and _strides_differ(v, k)):
         raise ValueError("cache v: shape and strides differ from those of k")
-    if vs.stride() != ss or vs.shape != scales:
+    if vs.shape != scales or (vs.stride() != ss and _strides_differ(vs, ks)):
         raise ValueError("cache v_scale: shape and strides differ from those of k_scale")
     pages, heads, tokens, d = shape[-4:]
     per = scales[-1]
@@ -680,8 +685,9 @@ def cache_keep(cache, path, accepted_len, page_table, context, out=None, stream=
 def attend_tree(q, cache, page_table, context, node_start, parent=None, scale=None, max_nodes=None, out=None, stream=None):
     """Attention of drafted rows over a ``PagedCache`` that holds their keys and values already (``cache_write``).
 
-    ``q`` [nodes + B, query heads, dim] (bfloat16, entries contiguous): each
-    sequence's root row, then its nodes' rows, as ``verify_tree`` takes them.  A
+    ``q`` [nodes + B, query heads, dim] (bfloat16, entries contiguous, rows and
+    heads on multiples of 16 bytes): each sequence's root row, then its nodes'
+    rows, as ``verify_tree`` takes them.  A
     row sees the ``context[b]`` committed positions, the root and its path
     (``parent`` [nodes]; None: chains).  Plain decoding has a ``node_start`` of
     zeros.  ``scale``: of the logits, by default dim ** -0.5.  ``max_nodes``
