@@ -548,6 +548,8 @@ sv_status spec_verify_penalties(const void* logits, sv_dtype dt, int64_t logits_
  *     strides are multiples of 16, k and v on multiples of 16.
  *   k_scale, v_scale: fp32, scale (layer, page, head, i) at layer *
  *     scale_layer_stride + (page * heads + head) * (page_tokens / block) + i.
+ *     Calls that write refuse strides by which entries or scales lie over one another
+ *     (SV_EINVAL), those of a view that repeats its layers, say.
  *   page_tokens: a power of two, 16 to 256; block: a power of two up to
  *     page_tokens; dim: 64 or 128; layers: 1 for the calls that work on one.
  * Sequence b's position p is token p % page_tokens of the page page_table[b,

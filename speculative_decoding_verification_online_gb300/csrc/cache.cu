@@ -344,6 +344,7 @@ extern "C" sv_status spec_verify_cache_write(const sv_cache* cache, const void* 
       static_cast<int>((std::min(max_nodes, total_nodes) + static_cast<int64_t>(cache->block) - 1) / cache->block) + 1;
   const __int128 grid = static_cast<__int128>(blocks) * B * cache->heads * 2;
   if (grid > INT32_MAX) return SV_EUNSUPPORTED;
+  if (!sv::lies_apart(cache)) return SV_EINVAL;
   sv::DeviceGuard g(device);
   if (!g.ok) return SV_ECUDA;
   sv::WriteParams P = {};
@@ -377,6 +378,7 @@ extern "C" sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t
     if (reinterpret_cast<uintptr_t>(p) % 4) return SV_EINVAL;
   const int64_t all = static_cast<int64_t>(cache->layers) * cache->heads * 2;
   if (static_cast<__int128>(all) * B > INT32_MAX) return SV_EUNSUPPORTED;
+  if (!sv::lies_apart(cache)) return SV_EINVAL;
   // CTAs read while another one writes its sequence's
   if (new_context) {
     const sv::Extent to = {new_context, 4, B, 0, 1, 0, 1};

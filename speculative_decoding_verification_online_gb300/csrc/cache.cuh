@@ -3,8 +3,10 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <initializer_list>
+#include <iterator>
 
 #include "spec_verify.h"
 
@@ -33,6 +35,22 @@ inline sv_status check_cache(const sv_cache* c, int layers) {
       reinterpret_cast<uintptr_t>(c->k_scale) % 4 || reinterpret_cast<uintptr_t>(c->v_scale) % 4)
     return SV_EINVAL;
   return SV_OK;
+}
+
+// whether no two entries of a cache that is written, and no two scales, share their place (as far as strides tell)
+inline bool lies_apart(const sv_cache* c) {
+  struct Dimension {
+    int64_t stride, count;
+  } d[] = {{c->layer_stride, c->layers}, {c->page_stride, c->pages}, {c->head_stride, c->heads}, {c->token_stride, c->page_tokens}};
+  std::sort(std::begin(d), std::end(d), [](const Dimension& a, const Dimension& b) { return a.stride < b.stride; });
+  __int128 span = c->dim;
+  for (const Dimension& one : d) {
+    if (one.count <= 1) continue;
+    if (one.stride < span) return false;
+    span += static_cast<__int128>(one.stride) * (one.count - 1);
+  }
+  const __int128 scales = static_cast<__int128>(c->pages) * c->heads * (c->page_tokens / c->block);
+  return c->layers == 1 || c->scale_layer_stride >= scales;
 }
 
 inline sv_status check_table(const int32_t* page_table, int64_t table_stride, int table_cols, int B) {
