@@ -619,12 +619,15 @@ sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t* path, int
  * Softmax statistics and sums are fp32.  A weight times its value's scale is
  * rounded as fp16 numbers are: to eleven significant bits where it is at least
  * 2^-20 of the row's largest, by 2^-31 of the largest at most where it is smaller
- * (a scale counting as 2^-12 of the others' at least).  What lies behind a sequence's last row does
- * not matter, whatever it is; a row that sees a NaN, or a scale of values
- * that is not finite, becomes NaN.  So do the rows of a sequence with a page outside [0, pages) or a column outside the table among
- * its positions or with a parent outside [-1, i).  Rows of padded sequences, and of a
- * node range that leaves [0, total_nodes] or holds more than max_nodes nodes, are
- * not written.  SV_EUNSUPPORTED beyond SV_MAX_NODES. */
+ * (a scale counting as 2^-12 of the others' at least).  What lies behind a
+ * sequence's last row does not matter, whatever it is.  A row that sees a NaN, a
+ * scale of values that is not finite, or one more than 2^120 times as large as
+ * those of the tile of 128 positions that its part of the context begins with,
+ * becomes NaN.  So do the rows of a sequence with a page outside [0, pages) or a
+ * column outside the table among its positions or with a parent outside [-1, i).
+ * Rows of padded sequences, and of a node range that leaves [0, total_nodes] or
+ * holds more than max_nodes nodes, are not written.  SV_EUNSUPPORTED beyond
+ * SV_MAX_NODES. */
 size_t spec_verify_attend_workspace(int heads, int q_heads, int dim, int max_nodes, int device);
 
 sv_status spec_verify_attend(const sv_cache* cache, const void* q, int64_t q_row, int64_t q_head,

@@ -907,15 +907,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       };
       for (int tile = first_tile; tile < t1; tile += step) {
         const unsigned n = count + (tile - t0), st = n % kV;
-        float2 scales = scales_next;
+        const float2 scales = scales_next;
         scales_next = scales_at(tile + step, page_next);
         page_next = page_at(tile + 2 * step);
-        // a scale of values that is no number: the rows that see it become NaN by their logits, a weight of 0 stays one (looked at
-        // here, where it has come: 185 us for 64 chains behind the load, 166 so)
-        if (!(fabsf(scales.y) < INFINITY)) scales = make_float2(NAN, 0.f);
-        float kf = scales.x;
-        // V's scale over the anchor: rest * 2^e, rest in (1/2, 1], e -12 at least
-        const float ratio = scales.y * per_anchor;
+        // V's scale over the anchor: rest * 2^e, rest in (1/2, 1], e -12 at least.  One that is no number, or too large for that:
+        // the rows that see it become NaN by their logits, and a weight of 0 stays one.  (Looked at here, where it has come: 185 us
+        // for 64 chains behind the load, 166 so.)
+        float kf = scales.x, ratio = scales.y * per_anchor;
+        if (!(fabsf(ratio) <= 0x1p120f)) kf = NAN, ratio = 0.f;
         const uint32_t u = __float_as_uint(ratio);
         const int e = max(-12, min(120, static_cast<int>(u >> 23 & 0xff) - 126 - ((u & 0x7fffffu) == 0)));
         const float inverse = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);

@@ -215,3 +215,24 @@ def test_attend_a_nan_far_below_the_others_is_not_lost(sv):
         assert not bool(torch.isnan(sv.attend_tree(**c)).any())
         c["page_table"][0, n] = -1
         assert bool(torch.isnan(sv.attend_tree(**c)).all()), n
+
+
+def test_attend_scales_too_far_apart_are_told(sv):
+    # The first tile's values have the least scale that there is.  Others 2^110 times as large are added as they should be, and
+    # 2^125 times as large make a row NaN, or, where its units are cut behind that tile, are added as they should be too.
+    c, n = flat_case(40, 8, 4, 64, 700, 1)
+    g = gen(9)
+    put(c, 0, torch.randn(40, 8, n, 64, generator=g, device="cuda"))
+    put(c, 1, 1.0 + torch.rand(40, 8, n, 64, generator=g, device="cuda"))
+    c["q"].copy_(torch.randn(c["q"].shape, generator=g, device="cuda"))
+    first, others = c["page_table"][:, :2].long(), c["page_table"][:, 2:].long()
+    c["cache"][3][first] = 0.0
+    want = sv.attend_tree(**c).float()
+    c["cache"][3][first] = 2.0 ** -100
+    for power in (10, 25):
+        c["cache"][3][others] = 2.0 ** power
+        got = sv.attend_tree(**c).float() * 2.0 ** -power
+        none = torch.isnan(got)
+        assert bool((none.any(-1) == none.all(-1)).all()) and bool(none.any()) == (power == 25)
+        # two results of the same weights, each rounded to bf16, and fp16 weights
+        assert bool((((got - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -10)) | none).all())
