@@ -354,8 +354,8 @@ sv_status spec_verify_run_noalloc(const void* target_logits, sv_dtype tdt,
                                   void* cuda_stream);
 
 /* ---------------------------------------------------------------------------
- * Operators around a verifying call.  They take no handle and no workspace,
- * allocate nothing and keep nothing from one call to the next, so calls may
+ * Operators around a verifying call.  They take no handle and no workspace (but
+ * spec_verify_attend, its caller's), allocate nothing and keep nothing from one call to the next, so calls may
  * overlap and may be captured.  Every pointer is device memory on `device`
  * (made current for the call, whatever device is current before it); strides
  * count elements.  Host errors as spec_verify_run, before any launch.  No wait

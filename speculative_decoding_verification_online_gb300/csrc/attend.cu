@@ -25,8 +25,8 @@
 // do, with values near zero, and then the others are the result.  Two e4m3 numbers, hi + lo / 32,
 // have eight bits over 2^15 only: a first position 11 above 4000 others took half of the
 // others' weight.  (A reference for each tile, and two rounds for tiles with such
-// positions, mended that too; on blocks whose scales differ it cost more: 64 chains 202 us, 166 so, and
-// trees 149, 113.)  A group of softmax threads widens its tile's values itself, where two blocks of columns
+// positions, mended that too; on blocks whose scales differ it cost more: 64 chains 202 us, 167 so, and
+// trees 149, 114.)  A group of softmax threads widens its tile's values itself, where two blocks of columns
 // share a tile each group half of it.
 //
 // Work is cut evenly over the SMs, whatever the lengths: all tiles of all units (sequence, key
@@ -35,12 +35,12 @@
 //
 // Measured (with the joining kernel; in brackets what the bytes take at the rate of a copy):
 //   64 chains of five drafts after up to 8192 positions, 8 key heads of 128, 4 query heads
-//     to each: 166 us (121); widening V takes 20 of them
-//   the same with one row and 4096 positions each: 83.7 us (60.3)
-//   2 chains of four after 131071, 8 key heads of 64, 5 query heads to each: 94.6 us (40.1)
+//     to each: 167 us (121); widening V takes 20 of them
+//   the same with one row and 4096 positions each: 83.6 us (60.2)
+//   2 chains of four after 131071, 8 key heads of 64, 5 query heads to each: 95.0 us (40.1)
 //   32 trees of up to 21 nodes after up to 4000, 4 key heads of 128, 8 query heads to each:
 //     114 us (16.0); 176 columns are three units of 64
-//   one row after 1000 positions: 16.5 us, two launches and a chain of waits
+//   one row after 1000 positions: 16.6 us, two launches and a chain of waits
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -521,14 +521,6 @@ __device__ __forceinline__ bool groups_any(bool mine) {
 }
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 3, 512;" ::: "memory"); }
 
-// smallest power of two that brings values of up to `a` to 448 at most (2^-100 at least)
-__device__ __forceinline__ float power_for(float a) {
-  const uint32_t u = __float_as_uint(a);
-  const int e = static_cast<int>(u >> 23) - 126;
-  const int k = max(-100, (u & 0x7fffffu) <= 0x600000u ? e - 9 : e - 8);
-  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-}
-
 __device__ __forceinline__ bool holds_nan(uint4 e) {
   // 0x7f in the low seven bits of a byte
   const auto hit = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
@@ -669,7 +661,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             if (!g.lost && node >= 0) {
               // What a position holds that not every row sees goes through the product of every row: nothing but numbers
               // may stand there.  (Lanes begin at different places of their rows: at the same one all of them would meet
-              // in four banks.  256 contexts of 300 positions 97.8 us, 92.9 so.)
+              // in four banks: 5 % of 256 contexts of 300 positions.)
               uint4* row = reinterpret_cast<uint4*>(v + at * kD);
               const bool behind = pos >= g.end;
               bool nan = false;
@@ -848,7 +840,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
         for (int o = kLanes / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
         const bool fine = most < INFINITY;
-        const float unit = fine ? power_for(most) : 1.f, inverse = 1.f / unit;
+        const float unit = fine ? scale_for(most) : 1.f, inverse = 1.f / unit;
         uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -912,7 +904,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         page_next = page_at(tile + 2 * step);
         // V's scale over the anchor: rest * 2^e, rest in (1/2, 1], e -12 at least.  One that is no number, or too large for that:
         // the rows that see it become NaN by their logits, and a weight of 0 stays one.  (Looked at here, where it has come: 185 us
-        // for 64 chains behind the load, 166 so.)
+        // for 64 chains behind the load, 167 so.)
         float kf = scales.x, ratio = scales.y * per_anchor;
         if (!(fabsf(ratio) <= 0x1p120f)) kf = NAN, ratio = 0.f;
         const uint32_t u = __float_as_uint(ratio);

@@ -3,8 +3,8 @@
 //
 // Writing: a CTA has the new rows of one block of entries, of keys or of values, and keeps
 // them in registers between the search for the largest magnitude and the rounding: rows
-// are read once.  Rows of 64 trees of up to 21 nodes, 8 heads of 128, bf16: 6.0 us; 32
-// prompts of up to 2048 tokens: 54.1 us, 5.6 TB/s.  What bounds that one is instructions as much as memory:
+// are read once.  Rows of 64 trees of up to 21 nodes, 8 heads of 128, bf16: 5.9 us; 32
+// prompts of up to 2048 tokens: 54.3 us, 5.6 TB/s (in fp32 77.5 us).  What bounds that one is instructions as much as memory:
 // the largest magnitude is therefore looked for among the bits, two bf16 at once, and
 // finiteness is one question for the whole block (80.8 us with a test and a float
 // maximum for every entry).  128 threads with 8 runs each were the best: 256 with 4 take
@@ -99,14 +99,6 @@ __device__ __forceinline__ float largest(const float (&v)[8], float m) {
     m = a < INFINITY ? fmaxf(m, a) : m;
   }
   return m;
-}
-
-// 2^ceil(log2(a / 448)), 2^-100 at least.  448 is 0.875 * 2^9, and a = f * 2^e with f in [1/2, 1).
-__device__ __forceinline__ float scale_for(float a) {
-  const uint32_t u = __float_as_uint(a);
-  const int e = static_cast<int>(u >> 23) - 126;
-  const int k = max(-100, (u & 0x7fffffu) <= 0x600000u ? e - 9 : e - 8);
-  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
 __device__ __forceinline__ uint2 pack8(const float (&v)[8]) {

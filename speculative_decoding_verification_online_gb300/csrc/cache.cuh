@@ -103,6 +103,14 @@ inline CacheView view_of(const sv_cache& c, const int32_t* table, int64_t table_
   return v;
 }
 
+// 2^ceil(log2(a / 448)), 2^-100 at least.  448 is 0.875 * 2^9, and a = f * 2^e with f in [1/2, 1).
+__device__ __forceinline__ float scale_for(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int e = static_cast<int>(u >> 23) - 126;
+  const int k = max(-100, (u & 0x7fffffu) <= 0x600000u ? e - 9 : e - 8);
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
 // two values to e4m3, to nearest, ties to even, 448 at most; the first one in the low byte
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
