@@ -355,8 +355,8 @@ sv_status spec_verify_run_noalloc(const void* target_logits, sv_dtype tdt,
 
 /* ---------------------------------------------------------------------------
  * Operators around a verifying call.  They take no handle and no workspace (but
- * spec_verify_attend, its caller's), allocate nothing and keep nothing from one call to the next, so calls may
- * overlap and may be captured.  Every pointer is device memory on `device`
+ * spec_verify_attend, its caller's), allocate nothing and keep nothing from one
+ * call to the next, so calls may overlap and may be captured.  Every pointer is device memory on `device`
  * (made current for the call, whatever device is current before it); strides
  * count elements.  Host errors as spec_verify_run, before any launch.  No wait
  * inside the kernels is endless: one that has no answer for two seconds (a GPU
@@ -609,9 +609,8 @@ sv_status spec_verify_cache_keep(const sv_cache* cache, const int32_t* path, int
  * those of its path (parent as spec_verify_tree; NULL = chains: everything up to
  * itself).  G = q_heads / heads.  Plain decoding is node_start = 0 throughout.
  *   q, out: bfloat16, row r, head h at r * row + h * head, dim contiguous entries
- *     each; q_row, q_head (where there are several) multiples of 8, q on a multiple of
- *     16 bytes.  out must not
- *     overlap q or the cache.
+ *     each; q_row, q_head (where there are several) multiples of 8, q on a multiple
+ *     of 16 bytes.  out must not overlap q or the cache.
  *   scale: finite (SV_EUNSUPPORTED beyond 2^126).
  *   workspace: device memory of spec_verify_attend_workspace(...) bytes, on a
  *     multiple of 16, that no other call uses meanwhile; it holds parts of long
