@@ -27,7 +27,7 @@ def test_entries(cache, apart):
 
 @pytest.mark.parametrize("cache,apart", [
     ({}, True), (dict(scale_layer_stride=0), False), (dict(scale_layer_stride=71), False), (dict(layer_stride=9 * 4096 - 16), False),
-    (dict(layer_stride=64, token_stride=64 * 3, head_stride=3072, page_stride=12288), True), (dict(layers=1, scale_layer_stride=0), True)])
+    (dict(layer_stride=64, token_stride=64 * 3, head_stride=4096, page_stride=16384), True), (dict(layers=1, scale_layer_stride=0), True)])
 def test_layers(cache, apart):
     assert _cached(sv.spec_verify_cache_keep, KEEP, dict(device=NO_DEVICE), dict(LAYERS, **cache)) == (
         m.SV_ECUDA if apart else m.SV_EINVAL)
